@@ -2,8 +2,9 @@
 
     python -m gated_delta_rule_86_amd.build
 
-Compiles csrc/kda_kernels.hip, csrc/kda_recurrent.hip, csrc/kda_noalloc.hip and
-csrc/kda_backward.hip (device code) and csrc/kda_api.cpp (host C ABI) into
+Compiles csrc/kda_kernels.hip, csrc/kda_recurrent.hip, csrc/kda_noalloc.hip,
+csrc/kda_backward.hip, csrc/lin_attn.hip and csrc/qk_rope.hip (device code) and
+csrc/kda_api.cpp, csrc/lin_api.cpp and csrc/rope_api.cpp (host C ABI) into
 gated_delta_rule_86_amd/libkda.so.  Always rebuilds.
 """
 from __future__ import annotations
@@ -43,7 +44,9 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     srcs = [os.path.join(CSRC, "kda_kernels.hip"), os.path.join(CSRC, "kda_recurrent.hip"),
             os.path.join(CSRC, "kda_noalloc.hip"), os.path.join(CSRC, "kda_backward.hip"),
-            os.path.join(CSRC, "kda_api.cpp")]
+            os.path.join(CSRC, "lin_attn.hip"), os.path.join(CSRC, "qk_rope.hip"),
+            os.path.join(CSRC, "kda_api.cpp"), os.path.join(CSRC, "lin_api.cpp"),
+            os.path.join(CSRC, "rope_api.cpp")]
     tmp = LIB + ".tmp"
     cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *srcs]
     if verbose:

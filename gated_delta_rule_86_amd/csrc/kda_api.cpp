@@ -118,7 +118,7 @@ kda_status validate(const void *q, const void *k, const void *v, const void *g, 
 
 extern "C" {
 
-int kda_version(void) { return 100; }
+int kda_version(void) { return 200; }
 
 const char *kda_status_string(int s)
 {
@@ -137,6 +137,9 @@ const char *kda_status_string(int s)
     case KDA_ERR_ALIAS: return "KDA_ERR_ALIAS: an output overlaps an input";
     case KDA_ERR_FLAGS: return "KDA_ERR_FLAGS: unknown activation switch bits";
     case KDA_ERR_SCRATCH: return "KDA_ERR_SCRATCH: the call needs more than kda_fwd_noalloc's static scratch";
+    case KDA_ERR_HEADS: return "KDA_ERR_HEADS: H must be a multiple of Hk";
+    case KDA_ERR_STRIDE: return "KDA_ERR_STRIDE: a stride is negative, not a multiple of 16 bytes, or too large";
+    case KDA_ERR_ROTARY: return "KDA_ERR_ROTARY: head size or rotary_dim not supported";
     default: return "KDA_ERR_UNKNOWN";
     }
 }

@@ -1,0 +1,1225 @@
+// lin_attn.hip -- linear attention with a decay for each head, gfx950.
+//
+// Per (sequence, head), state S [V = 128][K = 128], natural-log decay g_t <= 0:
+//   S_t = e^{g_t} S_{t-1} + v_t k_t^T,     out_t = scale * S_t q_t.
+// In chunks of C = 64 tokens, with b the inclusive running sum of g inside the chunk and L
+// its last entry:
+//   out_t = scale * ( sum_{s <= t} e^{b_t - b_s} (q_t.k_s) v_s  +  e^{b_t} S q_t ),
+//   S    <- e^{L} S + sum_s e^{L - b_s} v_s k_s^T.
+// All three gradients are walks of the same form on other operands: dq takes (dO, v, k) in
+// the place of (q, k, v), forwards, with the transposed state; dv takes (k, q, dO) and dk
+// (v, dO, q) with the sources behind the token, the state dL/dS running from the end:
+//   out_s = scale * sum_{t >= s} e^{b_t - b_s} (k_s.q_t) dO_t  +  e^{L - b_s} dS k_s,
+//   dS   <- e^{L} dS + scale * sum_t e^{b_t} dO_t q_t^T.
+// The decay's gradient follows from the others: with db_t = q_t.dq_t - k_t.dk_t,
+//   dg_t = sum_{u >= t} db_u + <S_end, dS_end>, the sum up to the end of the segment.
+// A token's own pair (t = s) adds the same to q.dq and k.dk and is left out of both.
+//
+// Numbers: decays are used as min(max(g, -1000), 0) (below -1000 the factor is 0 in fp32 long
+// since, so -inf means "forget").  Running sums of logarithms are fp64 and kept as pairs of
+// floats; a factor is the exponential of a difference, at most 1.  The products run on
+// bf16 MFMA with fp32 accumulation; factors that are not bf16 inputs are cut into bf16 terms
+// (hi + lo: 16 significant bits; hi + mid + lo: 24).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lin_internal.h"
+
+namespace kda {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kBf16 = 1, kFp32 = 2;  // kda_state_dtype
+constexpr float kLowest = -1000.0f;
+constexpr double kLog2e64 = 1.4426950408889634;
+
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    bf16x2 p;
+    p[0] = (__bf16)a;
+    p[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, p);
+}
+__device__ __forceinline__ uint16_t to_bf16(float a) { return __builtin_bit_cast(uint16_t, (__bf16)a); }
+
+__device__ __forceinline__ float clamp_decay(float g)
+{
+    return g < kLowest ? kLowest : (g > 0.0f ? 0.0f : g);  // NaN stays NaN
+}
+
+// v_mfma_f32_32x32x16_bf16: A[m][k] in lane m + 32*(k/8), element k%8; B[k][n] in lane
+// n + 32*(k/8), element k%8; D[m][n] in lane n + 32*((m/4)%2), element 4*(m/8) + m%4.
+__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                   0, 0, 0);
+}
+
+// Barrier for LDS hand-offs: global loads and stores stay in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+}
+
+// LDS tiles are rows of 256 bytes (64 tokens x 128 channels); the 16-byte pieces of a row are
+// XORed with its number so that both 8 rows of one piece (the row-wise reads) and 4 rows
+// of two neighbouring pieces (the transposing reads) lie in different banks.
+__device__ __forceinline__ int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+__device__ __forceinline__ int tile_at(int row, int piece) { return row * 256 + ((piece ^ swz(row)) << 4); }
+
+__device__ __forceinline__ u32x4 lds_b128(const unsigned char *p) { return *reinterpret_cast<const u32x4 *>(p); }
+// Transposing read: lane i of each 16 lanes gives the address of 4 channels of token i / 4
+// and gets channel i of the 16 for the 4 tokens.
+__device__ __forceinline__ u32x2 lds_tr(const unsigned char *p)
+{
+    typedef __attribute__((address_space(3))) s16x4 lds_s4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 buf_b128(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// ------------------------------------------------------------------ sequences and pieces
+
+constexpr int kPieceStart = 1, kPieceEnd = 2, kFromSlot = 4, kToFinal = 8;
+
+struct Chunk {
+    int64_t t0;   // first token (in its row)
+    int64_t seq;
+    int len;      // 0: no chunk
+    int flags;
+};
+
+// The chunks that a workgroup walks: the pieces of sequences inside tokens [r0, r1) of its
+// row, in the walk's direction.  Sequences are cut into chunks from their first token in
+// the range on; a reverse walk takes the same chunks from the last to the first.
+struct Walk {
+    const int64_t *cu;
+    int64_t row, T, r0, r1;
+    int64_t first, last;   // sequences to visit
+    int64_t i;             // the current one
+    int64_t p0, p1;        // its piece
+    int64_t c, nc;         // chunk of it, chunks
+    int pflags;
+    bool rev;
+
+    __device__ int64_t start(int64_t n) const { return cu ? cu[n] : 0; }
+    __device__ int64_t end(int64_t n) const { return cu ? cu[n + 1] : T; }
+
+    // first index with cu[index] >= x
+    __device__ int64_t lower(int64_t N, int64_t x) const
+    {
+        int64_t lo = 0, hi = N + 1;
+        while (lo < hi) {
+            const int64_t m = (lo + hi) >> 1;
+            if (cu[m] < x)
+                lo = m + 1;
+            else
+                hi = m;
+        }
+        return lo;
+    }
+    __device__ void init(const LinArgs &a, int64_t row_, int64_t j, bool rev_)
+    {
+        cu = a.cu;
+        row = row_;
+        T = a.T;
+        rev = rev_;
+        r0 = j * a.len;
+        r1 = r0 + a.len < T ? r0 + a.len : T;
+        if (!cu) {
+            first = last = 0;
+        } else {
+            const int64_t m = lower(a.N, r0);
+            first = m > 0 && (m > a.N || cu[m] > r0) ? m - 1 : m;
+            if (first > a.N - 1)
+                first = a.N - 1;
+            last = r1 == T ? a.N - 1 : lower(a.N, r1) - 1;
+            if (last > a.N - 1)
+                last = a.N - 1;
+        }
+        i = rev ? last + 1 : first - 1;
+        c = nc = 0;
+    }
+    __device__ int64_t seq_index() const { return cu ? i : row; }
+    __device__ void set_piece()
+    {
+        const int64_t s0 = start(i), s1 = end(i);
+        p0 = s0 > r0 ? s0 : r0;
+        p1 = s1 < r1 ? s1 : r1;
+        nc = p1 > p0 ? (p1 - p0 + kLC - 1) / kLC : 0;
+        pflags = 0;
+        if (rev)
+            pflags = (s1 > r1 ? kFromSlot : 0) | (s0 >= r0 ? kToFinal : 0);
+        else
+            pflags = (s0 < r0 ? kFromSlot : 0) | (s1 <= r1 ? kToFinal : 0);
+    }
+    __device__ Chunk next()
+    {
+        Chunk k;
+        ++c;
+        while (c >= nc) {
+            i += rev ? -1 : 1;
+            if (rev ? i < first : i > last) {
+                nc = 0;
+                c = 0;
+                k.len = 0;
+                k.t0 = 0;
+                k.seq = 0;
+                k.flags = 0;
+                return k;
+            }
+            set_piece();
+            c = 0;
+        }
+        const int64_t n = rev ? nc - 1 - c : c;
+        k.t0 = p0 + n * kLC;
+        k.len = (int)(p1 - k.t0 < kLC ? p1 - k.t0 : kLC);
+        k.seq = seq_index();
+        k.flags = pflags | (c == 0 ? kPieceStart : 0) | (c == nc - 1 ? kPieceEnd : 0);
+        return k;
+    }
+};
+
+// ------------------------------------------------------------------------- state in registers
+//
+// Wave w of 4 holds columns 32w .. 32w+31 of the role's v channels, all 128 k channels:
+// S[kt][r], kt = 0..3, lane = column + 32 * half: channel 32 kt + 16 (r / 8) + 8 half + r % 8.
+// A lane's registers 8m .. 8m+7 of a tile are then 8 neighbouring channels, as the operand of a
+// 16-channel MFMA step wants them; the K operand of the update is read with its rows in
+// the matching order.
+
+struct State {
+    f32x16 t[4];
+};
+
+__device__ __forceinline__ const void *matrix_of(const void *base, int64_t n, size_t bytes)
+{
+    return base ? static_cast<const unsigned char *>(base) + (size_t)n * bytes : nullptr;
+}
+
+// One 128 x 128 matrix at `base` (dt: 1 bf16, 2 fp32; NULL: zeros) into registers or back.  Buffer
+// instructions: one lane offset serves all 64 entries, the rest sits in the instruction.
+__device__ __forceinline__ void state_load(State &S, const void *base, int dt, bool tr, int wave, int lane)
+{
+    const int col = 32 * wave + (lane & 31), half = lane >> 5;
+    const int size = dt == kBf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t r = rsrc(base, base ? (uint32_t)(kD * kD * size) : 0u);
+    const int vo = (tr ? 8 * half * kD + col : col * kD + 8 * half) * size;
+    if (dt == kBf16) {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int ch = 32 * kt + 16 * m;
+                if (tr) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        S.t[kt][8 * m + e] = __uint_as_float(
+                            (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, vo, (ch + e) * kD * 2, 0) << 16);
+                } else {
+                    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, ch * 2, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S.t[kt][8 * m + 2 * e] = lo_f(x[e]);
+                        S.t[kt][8 * m + 2 * e + 1] = hi_f(x[e]);
+                    }
+                }
+            }
+    } else {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int ch = 32 * kt + 16 * (n >> 1) + 4 * (n & 1);
+                if (tr) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S.t[kt][4 * n + e] =
+                            __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, vo, (ch + e) * kD * 4, 0));
+                } else {
+                    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, ch * 4, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S.t[kt][4 * n + e] = __uint_as_float(x[e]);
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ void state_store(const State &S, void *base, int dt, bool tr, int wave, int lane)
+{
+    typedef unsigned int u4 __attribute__((vector_size(16)));
+    const int col = 32 * wave + (lane & 31), half = lane >> 5;
+    const int size = dt == kBf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t r = rsrc(base, (uint32_t)(kD * kD * size));
+    const int vo = (tr ? 8 * half * kD + col : col * kD + 8 * half) * size;
+    if (dt == kBf16) {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int ch = 32 * kt + 16 * m;
+                if (tr) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        __builtin_amdgcn_raw_buffer_store_b16((short)to_bf16(S.t[kt][8 * m + e]), r, vo,
+                                                              (ch + e) * kD * 2, 0);
+                } else {
+                    u32x4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = pack2(S.t[kt][8 * m + 2 * e], S.t[kt][8 * m + 2 * e + 1]);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), r, vo, ch * 2, 0);
+                }
+            }
+    } else {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int ch = 32 * kt + 16 * (n >> 1) + 4 * (n & 1);
+                if (tr) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S.t[kt][4 * n + e]), r, vo,
+                                                              (ch + e) * kD * 4, 0);
+                } else {
+                    const f32x4 x = {S.t[kt][4 * n], S.t[kt][4 * n + 1], S.t[kt][4 * n + 2], S.t[kt][4 * n + 3]};
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), r, vo, ch * 4, 0);
+                }
+            }
+    }
+}
+
+// <S, X> over the workgroup's 128 x 128 entries (X fp32), this thread's share
+__device__ __forceinline__ float state_dot(const State &S, const float *base, bool tr, int wave, int lane)
+{
+    const int col = 32 * wave + (lane & 31), half = lane >> 5;
+    const __amdgpu_buffer_rsrc_t r = rsrc(base, (uint32_t)kLinStateBytes);
+    const int vo = (tr ? 8 * half * kD + col : col * kD + 8 * half) * 4, step = (tr ? kD : 1) * 4;
+    float d = 0.0f;
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+            d = fmaf(S.t[kt][n],
+                     __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                         r, vo, (32 * kt + 16 * (n >> 3) + (n & 7)) * step, 0)),
+                     d);
+    return d;
+}
+
+// S *= 2^l2.  The factor of slow decays is close to 1 and the same rounding of it in every
+// chunk would add up over a long sequence, so it is applied as S + S (2^l2 - 1).
+__device__ __forceinline__ void state_decay(State &S, float l2)
+{
+    if (l2 > -0.5f) {
+        const float f = expm1f(l2 * 0.6931471805599453f);
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                S.t[kt][r] = fmaf(S.t[kt][r], f, S.t[kt][r]);
+    } else {
+        const float f = __builtin_amdgcn_exp2f(l2);
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                S.t[kt][r] *= f;
+    }
+}
+
+// ------------------------------------------------------------------------------- LDS
+
+struct Decays {           // of one chunk, natural order of tokens
+    float bh[kLC], bl[kLC];  // running sum of log2 decays, as a pair
+    float wout[kLC];         // factor of the state's share of an output row
+    float win[kLC];          // factor of a source row on its way into the state
+    float last, pad[3];      // sum over the chunk, log2
+};
+
+constexpr int kTile = kLC * 256;
+constexpr int kPRow = 128;  // bytes per row of the 64 x 64 weight matrix
+
+struct LdsWalk {
+    unsigned char k[kTile], v[kTile], q[kTile];
+    unsigned char p[2][kLC * kPRow];  // weights, hi and lo terms, [out token][source token]
+    Decays d[2];
+};
+struct LdsWalkDots {
+    LdsWalk w;
+    unsigned char p3[kLC * kPRow];  // third term of the weights
+    float red[4][kLC];
+    float own[kLC];                 // weights of the tokens' own pairs
+};
+struct LdsStates {
+    unsigned char k[kTile], v[kTile];
+    Decays d[2];
+};
+
+// One wave: lane = token.
+__device__ __forceinline__ void make_decays(Decays &d, float g, int len, int lane, bool rev, float scale)
+{
+    double b = lane < len ? (double)clamp_decay(g) * kLog2e64 : 0.0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double u = __shfl_up(b, o);
+        if (lane >= o)
+            b += u;
+    }
+    const double last = __shfl(b, 63);
+    const float bh = (float)b;
+    d.bh[lane] = bh;
+    d.bl[lane] = (float)(b - (double)bh);
+    const float head = __builtin_amdgcn_exp2f(bh), tail = __builtin_amdgcn_exp2f((float)(last - b));
+    d.wout[lane] = rev ? tail : scale * head;
+    d.win[lane] = rev ? scale * head : tail;
+    if (lane == 0)
+        d.last = (float)last;
+}
+
+__device__ __forceinline__ float load_decay(const LinArgs &a, int64_t row, int64_t h, const Chunk &c, int lane)
+{
+    if (!a.per_token)
+        return a.decay[h];
+    const int t = lane < c.len ? lane : c.len - 1;
+    return a.decay[(row * a.T + c.t0 + t) * a.H + h];
+}
+
+struct TileLoad {
+    u32x4 r[4];
+};
+// 64 rows of 256 bytes; rows behind the chunk read as zeros (beyond the descriptor)
+__device__ __forceinline__ void tile_fetch(TileLoad &f, const LinTensor &x, int64_t row, int64_t h, const Chunk &c, int tid)
+{
+    const uint16_t *base = x.p + row * x.sb + c.t0 * x.st + (h / x.share) * x.sh;
+    const uint32_t stride = (uint32_t)(x.st * 2);
+    const __amdgpu_buffer_rsrc_t r = rsrc(base, (uint32_t)(c.len - 1) * stride + 256u);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int at = tid + 256 * n, tok = at >> 4;
+        // a stride of 0 or less than a row would let a row behind the chunk lie inside the descriptor
+        f.r[n] = buf_b128(r, tok < c.len ? (uint32_t)tok * stride + (uint32_t)(at & 15) * 16u : 0xffffff00u);
+    }
+}
+__device__ __forceinline__ void tile_put(const TileLoad &f, unsigned char *lds, int tid)
+{
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int at = tid + 256 * n;
+        *reinterpret_cast<u32x4 *>(lds + tile_at(at >> 4, at & 15)) = f.r[n];
+    }
+}
+
+// 8 tokens x this lane's channel of an operand whose channel group (of 4) the lane names
+__device__ __forceinline__ u32x4 tr_frag(const unsigned char *tile, int token, int channel)
+{
+    const u32x2 x = lds_tr(tile + tile_at(token, channel >> 3) + (channel & 7) * 2);
+    const u32x2 y = lds_tr(tile + tile_at(token + 4, channel >> 3) + (channel & 7) * 2);
+    return u32x4{x[0], x[1], y[0], y[1]};
+}
+
+// cut 8 floats into bf16 terms
+struct Terms3 {
+    u32x4 h, m, l;
+};
+__device__ __forceinline__ void cut2(const float *x, u32x4 &h, u32x4 &l)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = pack2(x[2 * e], x[2 * e + 1]);
+        l[e] = pack2(x[2 * e] - lo_f(h[e]), x[2 * e + 1] - hi_f(h[e]));
+    }
+}
+__device__ __forceinline__ void cut3(const float *x, Terms3 &t)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1];
+        t.h[e] = pack2(a, b);
+        const float a1 = a - lo_f(t.h[e]), b1 = b - hi_f(t.h[e]);
+        t.m[e] = pack2(a1, b1);
+        t.l[e] = pack2(a1 - lo_f(t.m[e]), b1 - hi_f(t.m[e]));
+    }
+}
+
+// S += sum over the chunk's tokens of (win v) k^T.  Source rows are weighted on the way in,
+// in fp32, and go into the product as three bf16 terms (24 bits), so that an fp32 state keeps
+// fp32's accuracy.
+__device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const Decays &d,
+                                             int len, int lane)
+{
+    const int half = lane >> 5, i = lane & 15, g2 = (lane >> 4) & 1;
+    const int cg = i & 3;
+    const int fg = ((cg & 1) << 1) | (cg >> 1);  // rows of the K operand in the order of the state's registers
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (16 * j < len) {
+            const int tok = 16 * j + 8 * half;
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.win[tok]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.win[tok + 4]);
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float w_a = e < 2 ? w0[2 * e] : w1[2 * e - 4], w_b = e < 2 ? w0[2 * e + 1] : w1[2 * e - 3];
+                x[2 * e] = lo_f(vf[j][e]) * w_a;
+                x[2 * e + 1] = hi_f(vf[j][e]) * w_b;
+            }
+            Terms3 t;
+            cut3(x, t);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                const u32x4 kf = tr_frag(ktile, tok + (i >> 2), 32 * kt + 16 * g2 + 4 * fg);
+                S.t[kt] = mfma(kf, t.l, S.t[kt]);
+                S.t[kt] = mfma(kf, t.m, S.t[kt]);
+                S.t[kt] = mfma(kf, t.h, S.t[kt]);
+            }
+        }
+    }
+}
+
+// Block -> (segment, head): the blocks of one XCD (every eighth) take neighbouring heads, so that
+// heads that share q/k rows, and the lines of per-token decays, meet in one L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total)
+{
+    const int64_t per = (total + 7) >> 3;
+    return (id & 7) * per + (id >> 3);
+}
+
+__device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a.status != 0; }
+
+// ------------------------------------------------------------------------- states pass
+//
+// Each segment's share of the state at its boundary: the last sequence of a forward walk if it
+// goes on behind the segment, the first one of a reverse walk if it began before it.  lam:
+// the factor on the state at the segment's other boundary, or -1 when the share is the whole
+// state (the sequence starts inside), -2 when there is none.
+__global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0, int lead1)
+{
+    __shared__ __attribute__((aligned(16))) LdsStates lds;
+    const int64_t total = a.rows * a.P * a.H;
+    const int64_t at = xcd_order(blockIdx.x, total);
+    if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
+        return;
+    const int64_t seg = at / a.H, h = at - seg * a.H;
+    const int64_t row = seg / a.P, j = seg - row * a.P;
+    const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
+    const bool rev = ro.rev != 0;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t slot = seg * a.H + h;
+    float *lam = ro.lam + slot;
+    const bool edge = rev ? j == 0 : j == a.P - 1;  // nothing beyond this boundary
+    if (edge || device_bad(a)) {
+        if (tid == 0)
+            *lam = -2.0f;
+        return;
+    }
+    Walk w;
+    w.init(a, row, j, rev);
+    // only the piece that crosses the boundary
+    if (rev)
+        w.i = w.first + 1;
+    else
+        w.i = w.last - 1;
+    w.first = rev ? w.first : w.last;
+    w.last = w.first;
+    Chunk c = w.next();
+    if (c.len == 0 || (c.flags & kToFinal)) {
+        if (tid == 0)
+            *lam = -2.0f;
+        return;
+    }
+    State S;
+    const bool whole = !(c.flags & kFromSlot);
+    state_load(S, whole ? matrix_of(ro.init, c.seq * a.H + h, kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1)) : nullptr,
+               ro.init_dt, ro.transposed != 0, wave, lane);
+    double sum = 0.0;
+    TileLoad fk, fv;
+    tile_fetch(fk, ro.k, row, h, c, tid);
+    tile_fetch(fv, ro.v, row, h, c, tid);
+    float g = load_decay(a, row, h, c, lane);
+    int buf = 0;
+    const int half = lane >> 5, i = lane & 15, g2 = (lane >> 4) & 1;
+    while (c.len > 0) {
+        tile_put(fk, lds.k, tid);
+        tile_put(fv, lds.v, tid);
+        if (wave == 3)
+            make_decays(lds.d[buf], g, c.len, lane, rev, a.scale);
+        const Chunk n = w.next();
+        if (n.len > 0) {
+            tile_fetch(fk, ro.k, row, h, n, tid);
+            tile_fetch(fv, ro.v, row, h, n, tid);
+            g = load_decay(a, row, h, n, lane);
+        }
+        lds_barrier();
+        const Decays &d = lds.d[buf];
+        u32x4 vf[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+            if (16 * jj < c.len)
+                vf[jj] = tr_frag(lds.v, 16 * jj + 8 * half + (i >> 2), 32 * wave + 16 * g2 + 4 * (i & 3));
+        state_decay(S, d.last);
+        sum += (double)d.last;
+        state_update(S, lds.k, vf, d, c.len, lane);
+        lds_barrier();
+        c = n;
+        buf ^= 1;
+    }
+    state_store(S, ro.slots + (size_t)slot * kD * kD, kFp32, ro.transposed != 0, wave, lane);
+    if (tid == 0)
+        *lam = whole ? -1.0f : __builtin_amdgcn_exp2f((float)sum);
+}
+
+// ---------------------------------------------------------------------------- scan
+//
+// slot_j <- share_j + lam_j * slot_{j-1} (forwards; backwards from the other end), so that slot
+// j is the state at the boundary behind (before) segment j.
+__global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int lead1)
+{
+    const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
+    constexpr unsigned kParts = kD * kD / 1024;  // workgroups per matrix
+    const int64_t rh = blockIdx.x / kParts, row = rh / a.H, h = rh - row * a.H;
+    const int e = ((blockIdx.x % kParts) * 256 + threadIdx.x) * 4;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t step = ro.rev ? -1 : 1;
+    int64_t j = ro.rev ? a.P - 1 : 0;
+    for (int64_t n = 0; n + 1 < a.P; ++n, j += step) {
+        const int64_t slot = (row * a.P + j) * a.H + h;
+        const float lam = ro.lam[slot];
+        if (lam == -2.0f)
+            continue;
+        f32x4 *p = reinterpret_cast<f32x4 *>(ro.slots + (size_t)slot * kD * kD + e);
+        f32x4 f = *p;
+        if (lam > 0.0f) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                f[x] = fmaf(lam, s[x], f[x]);
+            *p = f;
+        }
+        s = f;
+    }
+}
+
+// ---------------------------------------------------------------------------- output pass
+
+// kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
+// out.  Their sums over many tokens cancel, so weights and states then go into the products
+// as three terms, and the own pairs are added to the rows outside the matrix product.
+template <bool kDots>
+__global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(lds_raw);
+    LdsWalkDots &ldx = *reinterpret_cast<LdsWalkDots *>(lds_raw);  // behind lds only with kDots
+    const int64_t total = a.rows * a.P * a.H;
+    const int64_t at = xcd_order(blockIdx.x, total);
+    if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
+        return;
+    const int64_t seg = at / a.H, h = at - seg * a.H;
+    const int64_t row = seg / a.P, j = seg - row * a.P;
+    const LinRole &ro = a.role[blockIdx.y];
+    const bool rev = ro.rev != 0, tr = ro.transposed != 0;
+    const bool dots = kDots && ro.dots != nullptr;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = lane >> 5, l32 = lane & 31, i = lane & 15, g2 = (lane >> 4) & 1;
+    const size_t init_bytes = kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1);
+    const size_t fin_bytes = kLinStateBytes / (ro.fin_dt == kBf16 ? 2 : 1);
+    State S;
+    if (!a.cu && a.status && at == 0 && blockIdx.y == 0 && tid == 0)
+        *a.status = 0;
+
+    Walk w;
+    const bool bad = device_bad(a);
+    if (!bad)
+        w.init(a, row, j, rev);
+    // sequences without tokens keep their state
+    if (ro.fin && (a.cu || a.T == 0)) {
+        const int64_t lo = bad ? 0 : w.first, hi = bad ? (seg == 0 ? a.N - 1 : -1) : w.last;
+        for (int64_t n = lo; n <= hi; ++n) {
+            const int64_t s0 = a.cu && !bad ? a.cu[n] : 0, s1 = a.cu && !bad ? a.cu[n + 1] : 0;
+            if (s0 != s1 || (!bad && s0 < w.r0))
+                continue;
+            const int64_t sq = a.cu ? n : row;
+            state_load(S, matrix_of(ro.init, sq * a.H + h, init_bytes), ro.init_dt, tr, wave, lane);
+            state_store(S, static_cast<unsigned char *>(ro.fin) + (size_t)(sq * a.H + h) * fin_bytes, ro.fin_dt, tr,
+                        wave, lane);
+        }
+    }
+    if (bad)
+        return;
+
+    Chunk c = w.next();
+    if (c.len == 0)
+        return;
+    TileLoad fq, fk, fv;
+    tile_fetch(fq, ro.q, row, h, c, tid);
+    tile_fetch(fk, ro.k, row, h, c, tid);
+    tile_fetch(fv, ro.v, row, h, c, tid);
+    float g = load_decay(a, row, h, c, lane);
+    if (wave == 3)
+        make_decays(lds.d[0], g, c.len, lane, rev, a.scale);
+    int buf = 0;
+    while (c.len > 0) {
+        tile_put(fq, lds.q, tid);
+        tile_put(fk, lds.k, tid);
+        tile_put(fv, lds.v, tid);
+        const Chunk n = w.next();
+        if (n.len > 0) {
+            tile_fetch(fq, ro.q, row, h, n, tid);
+            tile_fetch(fk, ro.k, row, h, n, tid);
+            tile_fetch(fv, ro.v, row, h, n, tid);
+            g = load_decay(a, row, h, n, lane);
+        }
+        if (c.flags & kPieceStart) {
+            const bool slot = (c.flags & kFromSlot) != 0;
+            state_load(S,
+                       slot ? matrix_of(ro.slots, (seg + (rev ? 1 : -1)) * a.H + h, kLinStateBytes)
+                            : matrix_of(ro.init, c.seq * a.H + h, init_bytes),
+                       slot ? (int)kFp32 : ro.init_dt, tr, wave, lane);
+        }
+        lds_barrier();
+        const Decays &d = lds.d[buf];
+        const int nt = c.len > 32 ? 2 : 1;
+
+        // weights of one 32 x 32 block (sources sb, outputs ob) per wave 0..2, bf16 hi + lo
+        if (wave < (nt == 2 ? 3 : 1)) {
+            const int sb = wave == 0 ? 0 : (wave == 2 ? 1 : (rev ? 1 : 0));
+            const int ob = wave == 0 ? 0 : (wave == 2 ? 1 : (rev ? 0 : 1));
+            f32x16 p;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                p[r] = 0.0f;
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj)
+                p = mfma(lds_b128(lds.k + tile_at(32 * sb + l32, 2 * jj + half)),
+                         lds_b128(lds.q + tile_at(32 * ob + l32, 2 * jj + half)), p);
+            const int to = 32 * ob + l32;
+            const float bho = d.bh[to], blo = d.bl[to];
+#pragma unroll
+            for (int a4 = 0; a4 < 4; ++a4) {
+                const int s = 32 * sb + 8 * a4 + 4 * half;
+                const f32x4 bhs = *reinterpret_cast<const f32x4 *>(&d.bh[s]);
+                const f32x4 bls = *reinterpret_cast<const f32x4 *>(&d.bl[s]);
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float df = (bho - bhs[e]) + (blo - bls[e]);
+                    df = rev ? -df : df;
+                    const bool on = rev ? s + e >= to : s + e <= to;
+                    x[e] = on ? p[4 * a4 + e] * (a.scale * __builtin_amdgcn_exp2f(df)) : 0.0f;
+                    if (dots && s + e == to) {
+                        ldx.own[to] = x[e];
+                        x[e] = 0.0f;
+                    }
+                }
+                const u32x2 hi = {pack2(x[0], x[1]), pack2(x[2], x[3])};
+                const float y[4] = {x[0] - lo_f(hi[0]), x[1] - hi_f(hi[0]), x[2] - lo_f(hi[1]), x[3] - hi_f(hi[1])};
+                const u32x2 lo = {pack2(y[0], y[1]), pack2(y[2], y[3])};
+                const int off = to * kPRow + (((4 * sb + a4) ^ (to & 7)) << 4) + 8 * half;
+                *reinterpret_cast<u32x2 *>(lds.p[0] + off) = hi;
+                *reinterpret_cast<u32x2 *>(lds.p[1] + off) = lo;
+                if (dots)
+                    *reinterpret_cast<u32x2 *>(ldx.p3 + off) =
+                        u32x2{pack2(y[0] - lo_f(lo[0]), y[1] - hi_f(lo[0])), pack2(y[2] - lo_f(lo[1]), y[3] - hi_f(lo[1]))};
+            }
+        }
+        if (wave == 3 && n.len > 0)
+            make_decays(lds.d[buf ^ 1], g, n.len, lane, rev, a.scale);
+
+        u32x4 vf[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+            if (16 * jj < c.len)
+                vf[jj] = tr_frag(lds.v, 16 * jj + 8 * half + (i >> 2), 32 * wave + 16 * g2 + 4 * (i & 3));
+
+        // the state's share of the outputs: O^T[v][t], the state in bf16 hi + lo
+        f32x16 O[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                O[tt][r] = 0.0f;
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
+            Terms3 s;
+            cut3(x, s);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+                if (tt < nt) {
+                    const u32x4 qf = lds_b128(lds.q + tile_at(32 * tt + l32, 2 * jj + half));
+                    if (dots)
+                        O[tt] = mfma(s.l, qf, O[tt]);
+                    O[tt] = mfma(s.m, qf, O[tt]);
+                    O[tt] = mfma(s.h, qf, O[tt]);
+                }
+        }
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const float wo = d.wout[32 * tt + l32];
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                O[tt][r] *= wo;
+        }
+        lds_barrier();  // the weights are there
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const bool inside = rev ? (jj >> 1) >= tt : (jj >> 1) <= tt;
+                if (tt < nt && inside && 16 * jj < c.len) {
+                    const int to = 32 * tt + l32, off = to * kPRow + (((2 * jj + half) ^ (to & 7)) << 4);
+                    if (dots)
+                        O[tt] = mfma(vf[jj], lds_b128(ldx.p3 + off), O[tt]);
+                    O[tt] = mfma(vf[jj], lds_b128(lds.p[1] + off), O[tt]);
+                    O[tt] = mfma(vf[jj], lds_b128(lds.p[0] + off), O[tt]);
+                }
+            }
+
+        state_decay(S, d.last);
+        state_update(S, lds.k, vf, d, c.len, lane);
+
+        // rows out
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const int t = 32 * tt + l32;
+            float dot = 0.0f;
+            if (t < c.len) {
+                const int64_t tok = row * a.T + c.t0 + t;
+                const int64_t o = (tok * a.H + h) * kD + 32 * wave + 4 * half;
+                const float own = dots ? ldx.own[t] : 0.0f;
+#pragma unroll
+                for (int a4 = 0; a4 < 4; ++a4) {
+                    f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
+                    if (dots) {
+                        const u32x2 xr = *reinterpret_cast<const u32x2 *>(
+                            ro.x.p + row * ro.x.sb + (c.t0 + t) * ro.x.st + (h / ro.x.share) * ro.x.sh + 32 * wave +
+                            4 * half + 8 * a4);
+                        dot += (lo_f(xr[0]) * y[0] + hi_f(xr[0]) * y[1]) + (lo_f(xr[1]) * y[2] + hi_f(xr[1]) * y[3]);
+                        const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(t, 4 * wave + a4) + 8 * half);
+                        y[0] = fmaf(own, lo_f(vr[0]), y[0]);
+                        y[1] = fmaf(own, hi_f(vr[0]), y[1]);
+                        y[2] = fmaf(own, lo_f(vr[1]), y[2]);
+                        y[3] = fmaf(own, hi_f(vr[1]), y[3]);
+                    }
+                    if (ro.out_f32)
+                        *reinterpret_cast<f32x4 *>(static_cast<float *>(ro.out) + o + 8 * a4) = y;
+                    else
+                        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(ro.out) + o + 8 * a4) =
+                            u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+                }
+            }
+            if (dots) {
+                dot += __shfl_xor(dot, 32);
+                if (half == 0)
+                    ldx.red[wave][t] = dot;
+            }
+        }
+        lds_barrier();  // every read of this chunk's tiles is done
+        if (dots && tid < c.len)
+            ro.dots[(row * a.T + c.t0 + tid) * a.H + h] =
+                (ldx.red[0][tid] + ldx.red[1][tid]) + (ldx.red[2][tid] + ldx.red[3][tid]);
+        if ((c.flags & kPieceEnd) && (c.flags & kToFinal)) {
+            if (ro.fin && ro.defer && (c.flags & kFromSlot))
+                state_store(S, ro.slots + (size_t)((seg - 1) * a.H + h) * kD * kD, kFp32, tr, wave, lane);
+            else if (ro.fin)
+                state_store(S, static_cast<unsigned char *>(ro.fin) + (size_t)(c.seq * a.H + h) * fin_bytes, ro.fin_dt,
+                            tr, wave, lane);
+            if (kDots && ro.xfin) {
+                float x = state_dot(S, ro.xst + (size_t)(c.seq * a.H + h) * kD * kD, tr, wave, lane);
+#pragma unroll
+                for (int o = 32; o > 0; o >>= 1)
+                    x += __shfl_xor(x, o);
+                lds_barrier();
+                if (lane == 0)
+                    ldx.red[wave][0] = x;
+                lds_barrier();
+                if (tid == 0)
+                    ro.xfin[c.seq * a.H + h] =
+                        (ldx.red[0][0] + ldx.red[1][0]) + (ldx.red[2][0] + ldx.red[3][0]);
+                lds_barrier();
+            }
+        }
+        c = n;
+        buf ^= 1;
+    }
+}
+
+// In-place state carry with cut rows: the workgroup that ends a sequence may finish before the one
+// that starts it has read the initial state.  Final states of sequences that cross a
+// boundary therefore wait in the slot that their last segment started from (it has been read,
+// by the same threads) and move to their place here.
+__global__ __launch_bounds__(256) void lin_final_kernel(LinArgs a)
+{
+    const LinRole &ro = a.role[0];
+    const int64_t seg = blockIdx.x / a.H, h = blockIdx.x - seg * a.H;
+    const int64_t row = seg / a.P, j = seg - row * a.P;
+    if (j == 0 || device_bad(a))
+        return;
+    Walk w;
+    w.init(a, row, j, false);
+    w.i = w.first;
+    w.set_piece();
+    if (w.nc == 0 || !(w.pflags & kFromSlot) || !(w.pflags & kToFinal))
+        return;
+    const f32x4 *x = reinterpret_cast<const f32x4 *>(ro.slots + (size_t)((seg - 1) * a.H + h) * kD * kD);
+    const size_t at = (size_t)(w.seq_index() * a.H + h) * kD * kD;
+    for (int e = threadIdx.x; e < kD * kD / 4; e += 256) {
+        const f32x4 y = x[e];
+        if (ro.fin_dt == kFp32)
+            reinterpret_cast<f32x4 *>(static_cast<float *>(ro.fin) + at)[e] = y;
+        else
+            reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(ro.fin) + at)[e] = u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+    }
+}
+
+// ------------------------------------------------------------------- cu_seqlens, checked once
+
+__global__ __launch_bounds__(1024) void lin_check_kernel(const int64_t *cu, int64_t N, int64_t T, int32_t *status)
+{
+    __shared__ int bits;
+    if (threadIdx.x == 0)
+        bits = (cu[0] != 0 ? 1 : 0) | (cu[N] != T ? 4 : 0);
+    __syncthreads();
+    int mine = 0;
+    for (int64_t n = threadIdx.x; n < N; n += 1024)
+        if (cu[n + 1] < cu[n])
+            mine = 2;
+    if (mine)
+        atomicOr(&bits, mine);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *status = bits;
+}
+
+// ------------------------------------------------------------------- backward pass, tail
+
+// Sum of the value heads that share a q/k head, in head order, rounded once.  One thread per 4 channels.
+__global__ __launch_bounds__(256) void lin_fold_kernel(const float *xq, const float *xk, uint16_t *yq, uint16_t *yk,
+                                                       int64_t rows, int64_t Hk, int64_t G, const int32_t *status)
+{
+    if (status && *status != 0)
+        return;
+    const float *x = blockIdx.y ? xk : xq;
+    uint16_t *y = blockIdx.y ? yk : yq;
+    const int64_t n = rows * Hk * (kD / 4);
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
+        const int64_t r = at / (kD / 4);  // (token, q/k head)
+        const float *p = x + r * G * kD + (at - r * (kD / 4)) * 4;
+        f32x4 s = *reinterpret_cast<const f32x4 *>(p);
+        for (int64_t g = 1; g < G; ++g)
+            s += *reinterpret_cast<const f32x4 *>(p + g * kD);
+        *reinterpret_cast<u32x2 *>(y + at * 4) = u32x2{pack2(s[0], s[1]), pack2(s[2], s[3])};
+    }
+}
+
+// Sum over the 256 threads of a workgroup, in a fixed order; every thread gets it.
+__device__ __forceinline__ double wg_sum(double x, double *red, int tid)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        x += __shfl_xor(x, o);
+    __syncthreads();
+    if ((tid & 63) == 0)
+        red[tid >> 6] = x;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// dg of one segment and head: from the segment's end, where <S, dS> is known, back to its start
+__global__ __launch_bounds__(256) void lin_ddecay_kernel(LinArgs a, float *ddecay, double *part)
+{
+    __shared__ double red[4];
+    const int64_t seg = blockIdx.x / a.H, h = blockIdx.x - seg * a.H;
+    const int64_t row = seg / a.P, j = seg - row * a.P;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (device_bad(a)) {
+        if (!a.per_token && tid == 0)
+            part[seg * a.H + h] = 0.0;
+        return;
+    }
+    const LinRole &rq = a.role[0], &rk = a.role[1];
+    Walk w;
+    w.init(a, row, j, true);
+    double total = 0.0;
+    for (int64_t n = w.last; n >= w.first; --n) {
+        w.i = n;
+        w.set_piece();
+        if (w.p1 <= w.p0)
+            continue;
+        double run = 0.0;  // sum of db behind the block, and <S, dS> at the piece's end
+        if (w.pflags & kFromSlot) {
+            const f32x4 *x = reinterpret_cast<const f32x4 *>(rq.slots + (size_t)(seg * a.H + h) * kD * kD);
+            const f32x4 *y = reinterpret_cast<const f32x4 *>(rk.slots + (size_t)((seg + 1) * a.H + h) * kD * kD);
+            float d = 0.0f;
+            for (int e = tid; e < kD * kD / 4; e += 256) {
+                const f32x4 p = x[e], q = y[e];
+                d += (p[0] * q[0] + p[1] * q[1]) + (p[2] * q[2] + p[3] * q[3]);
+            }
+            run = wg_sum((double)d, red, tid);
+        } else if (rq.xfin) {
+            run = (double)rq.xfin[w.seq_index() * a.H + h];
+        }
+        for (int64_t b = w.p0 + (w.p1 - w.p0 - 1) / 256 * 256; b >= w.p0; b -= 256) {
+            const int64_t t = b + tid;
+            double x = 0.0;
+            const int64_t at = (row * a.T + t) * a.H + h;
+            if (t < w.p1)
+                x = (double)rq.dots[at] - (double)rk.dots[at];
+            double s = x;  // inclusive sum over this and the later tokens of the block
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const double u = __shfl_down(s, o);
+                if (lane + o < 64)
+                    s += u;
+            }
+            __syncthreads();
+            if (lane == 0)
+                red[wave] = s;
+            __syncthreads();
+            double later = 0.0;
+            for (int k = 3; k > wave; --k)
+                later += red[k];
+            const double all = (red[0] + red[1]) + (red[2] + red[3]);
+            if (t < w.p1) {
+                const double dg = run + later + s;
+                if (a.per_token) {
+                    const float g = a.decay[at];
+                    ddecay[at] = g > kLowest && g <= 0.0f ? (float)dg : 0.0f;
+                } else {
+                    total += dg;
+                }
+            }
+            run += all;
+        }
+    }
+    if (!a.per_token) {
+        total = wg_sum(total, red, tid);
+        if (tid == 0)
+            part[seg * a.H + h] = total;
+    }
+}
+
+__global__ __launch_bounds__(64) void lin_ddecay_sum_kernel(LinArgs a, const double *part, float *ddecay)
+{
+    const int64_t h = blockIdx.x;
+    double s = 0.0;
+    for (int64_t n = threadIdx.x; n < a.rows * a.P; n += 64)
+        s += part[n * a.H + h];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        s += __shfl_xor(s, o);
+    if (threadIdx.x == 0) {
+        const float g = a.decay[h];
+        ddecay[h] = g > kLowest && g <= 0.0f ? (float)s : 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------- token by token
+//
+// One wave per (sequence, head, 32 rows of the state); lane = row % 8 * 8 + q holds 16 channels
+// of 4 rows: 16-byte pieces, interleaved with those of the row's other 7 lanes.
+template <bool kF32>
+__global__ __launch_bounds__(256) void lin_recurrent_kernel(LinArgs a)
+{
+    constexpr int kPer = kF32 ? 4 : 8;     // channels per 16-byte piece
+    constexpr int kPieces = 16 / kPer;     // pieces per row and lane
+    const LinRole &ro = a.role[0];
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    const int64_t chain = unit >> 2;
+    if (chain >= a.N * a.H)
+        return;
+    const int v0 = (int)(unit & 3) * 32, r8 = lane >> 3, q8 = lane & 7;
+    const int64_t seq = chain / a.H, h = chain - seq * a.H;
+    float S[4][16];
+    const size_t mat = (size_t)chain * kD * kD;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const size_t at = mat + (size_t)(v0 + 8 * g + r8) * kD + (8 * p + q8) * kPer;
+            if (!ro.init) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    S[g][p * kPer + e] = 0.0f;
+            } else if constexpr (kF32) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(ro.init) + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    S[g][p * 4 + e] = x[e];
+            } else {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(ro.init) + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S[g][p * 8 + 2 * e] = lo_f(x[e]);
+                    S[g][p * 8 + 2 * e + 1] = hi_f(x[e]);
+                }
+            }
+        }
+    int64_t row = seq, t0 = 0, t1 = a.T;
+    if (a.cu) {
+        row = 0;
+        t0 = t1 = 0;
+        if (*a.status == 0) {
+            t0 = a.cu[seq];
+            t1 = a.cu[seq + 1];
+        }
+    }
+    for (int64_t t = t0; t < t1; ++t) {
+        const uint16_t *qp = ro.q.p + row * ro.q.sb + t * ro.q.st + (h / ro.q.share) * ro.q.sh;
+        const uint16_t *kp = ro.k.p + row * ro.k.sb + t * ro.k.st + (h / ro.k.share) * ro.k.sh;
+        const uint16_t *vp = ro.v.p + row * ro.v.sb + t * ro.v.st + (h / ro.v.share) * ro.v.sh;
+        const int64_t tok = row * a.T + t;
+        const float al = __builtin_amdgcn_exp2f(
+            (float)((double)clamp_decay(a.per_token ? a.decay[tok * a.H + h] : a.decay[h]) * kLog2e64));
+        float qv[16], kv[16], o[4];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const int ch = (8 * p + q8) * kPer;
+#pragma unroll
+            for (int e = 0; e < kPer; e += 4) {
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(qp + ch + e);
+                const u32x2 y = *reinterpret_cast<const u32x2 *>(kp + ch + e);
+                qv[p * kPer + e] = lo_f(x[0]);
+                qv[p * kPer + e + 1] = hi_f(x[0]);
+                qv[p * kPer + e + 2] = lo_f(x[1]);
+                qv[p * kPer + e + 3] = hi_f(x[1]);
+                kv[p * kPer + e] = lo_f(y[0]);
+                kv[p * kPer + e + 1] = hi_f(y[0]);
+                kv[p * kPer + e + 2] = lo_f(y[1]);
+                kv[p * kPer + e + 3] = hi_f(y[1]);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float vv = __uint_as_float((uint32_t)vp[v0 + 8 * g + r8] << 16);
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                S[g][e] = fmaf(vv, kv[e], S[g][e] * al);
+                s = fmaf(S[g][e], qv[e], s);
+            }
+#pragma unroll
+            for (int x = 4; x > 0; x >>= 1)
+                s += __shfl_xor(s, x);
+            o[g] = s * a.scale;
+        }
+        const float mine = q8 == 0 ? o[0] : q8 == 1 ? o[1] : q8 == 2 ? o[2] : o[3];
+        if (q8 < 4)
+            static_cast<uint16_t *>(ro.out)[(tok * a.H + h) * kD + v0 + 8 * q8 + r8] = to_bf16(mine);
+    }
+    if (!ro.fin)
+        return;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const size_t at = mat + (size_t)(v0 + 8 * g + r8) * kD + (8 * p + q8) * kPer;
+            if constexpr (kF32) {
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(ro.fin) + at) =
+                    f32x4{S[g][p * 4], S[g][p * 4 + 1], S[g][p * 4 + 2], S[g][p * 4 + 3]};
+            } else {
+                u32x4 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = pack2(S[g][p * 8 + 2 * e], S[g][p * 8 + 2 * e + 1]);
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(ro.fin) + at) = x;
+            }
+        }
+}
+
+}  // namespace
+
+hipError_t lin_launch_check(const int64_t *cu, int64_t N, int64_t T, int32_t *status, hipStream_t s)
+{
+    hipLaunchKernelGGL(lin_check_kernel, dim3(1), dim3(1024), 0, s, cu, N, T, status);
+    return hipGetLastError();
+}
+
+hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n_lead, hipStream_t s)
+{
+    const int64_t total = a.rows * a.P * a.H;
+    const unsigned grid = (unsigned)(8 * cdiv(total, 8));
+    if (a.P > 1) {
+        const int l0 = lead[0], l1 = lead[n_lead - 1];
+        hipLaunchKernelGGL(lin_states_kernel, dim3(grid, n_lead), dim3(256), 0, s, a, l0, l1);
+        hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)(kD * kD / 1024 * a.rows * a.H), n_lead), dim3(256), 0, s,
+                           a, l0, l1);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    bool dots = false;
+    for (int i = 0; i < n_roles; ++i)
+        dots = dots || a.role[i].dots;
+    const void *fn = dots ? reinterpret_cast<const void *>(&lin_walk_kernel<true>)
+                          : reinterpret_cast<const void *>(&lin_walk_kernel<false>);
+    const int bytes = (int)(dots ? sizeof(LdsWalkDots) : sizeof(LdsWalk));
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess)
+        return e;
+    if (dots)
+        hipLaunchKernelGGL(lin_walk_kernel<true>, dim3(grid, n_roles), dim3(256), bytes, s, a);
+    else
+        hipLaunchKernelGGL(lin_walk_kernel<false>, dim3(grid, n_roles), dim3(256), bytes, s, a);
+    if (a.role[0].defer)
+        hipLaunchKernelGGL(lin_final_kernel, dim3((unsigned)total), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t lin_launch_grad_tail(const LinArgs &a, const LinBwdExtra &e, hipStream_t s)
+{
+    if (e.dq_h && a.T > 0) {
+        const int64_t n = a.rows * a.T * e.Hk * (kD / 4);
+        const int64_t blocks = cdiv(n, 256) < 4096 ? cdiv(n, 256) : 4096;
+        hipLaunchKernelGGL(lin_fold_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, s, e.dq_h, e.dk_h, e.dq, e.dk,
+                           a.rows * a.T, e.Hk, a.H / e.Hk, a.cu ? a.status : nullptr);
+    }
+    if (e.ddecay) {
+        hipLaunchKernelGGL(lin_ddecay_kernel, dim3((unsigned)(a.rows * a.P * a.H)), dim3(256), 0, s, a, e.ddecay,
+                           e.part);
+        if (!a.per_token)
+            hipLaunchKernelGGL(lin_ddecay_sum_kernel, dim3((unsigned)a.H), dim3(64), 0, s, a, e.part, e.ddecay);
+    }
+    return hipGetLastError();
+}
+
+hipError_t lin_launch_recurrent(const LinArgs &a, hipStream_t s)
+{
+    const int64_t units = a.N * a.H * 4;
+    const LinRole &ro = a.role[0];
+    const bool f32 = (ro.init ? ro.init_dt : ro.fin_dt) != kBf16;
+    const int threads = units < 4096 ? 64 : 256;
+    const unsigned grid = (unsigned)cdiv(units, threads / 64);
+    if (f32)
+        hipLaunchKernelGGL(lin_recurrent_kernel<true>, dim3(grid), dim3(threads), 0, s, a);
+    else
+        hipLaunchKernelGGL(lin_recurrent_kernel<false>, dim3(grid), dim3(threads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace kda

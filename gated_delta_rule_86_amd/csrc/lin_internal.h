@@ -1,0 +1,117 @@
+// lin_internal.h -- shared by the host side (lin_api.cpp) and the gfx950 kernels
+// (lin_attn.hip) of the decayed linear attention.  Not part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+constexpr int kLC = 64;                       // tokens per chunk
+constexpr int64_t kLinGroups = 512;           // workgroups that fill the chip: two on each of 256 CUs
+constexpr int64_t kLinMinSeg = 256;           // shortest segment that a cut leaves, in tokens
+constexpr int64_t kLinGradSeg = 512;          // longest segment when the decay's gradient is wanted
+constexpr size_t kLinStateBytes = (size_t)kD * kD * sizeof(float);
+
+// Segments.  The packed tokens of a batch row (the one row of a varlen batch) are cut into P
+// segments of `len` tokens whatever the sequences in it, so workgroups get equal work and
+// no table is needed.  A sequence that crosses a segment boundary has its state there in
+// slot [segment][head] of the workspace: the states pass forms each segment's own share, the
+// scan joins them, and the output pass starts from them.
+struct LinPlan {
+    int64_t rows;      // batch rows (1 for varlen)
+    int64_t P;         // segments per row
+    int64_t len;       // tokens per segment, a multiple of kLC
+    int64_t n_seq;     // N, or B without cu_seqlens
+};
+
+inline LinPlan lin_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool varlen, int64_t groups, int64_t max_len)
+{
+    LinPlan p;
+    p.rows = varlen ? 1 : B;
+    p.n_seq = varlen ? N : B;
+    int64_t P = 1;
+    if (p.rows * H < groups)
+        P = cdiv(groups, p.rows * H);
+    const int64_t most = T / kLinMinSeg;
+    if (P > most)
+        P = most;
+    if (max_len > 0 && P < cdiv(T, max_len))
+        P = cdiv(T, max_len);
+    if (P < 1)
+        P = 1;
+    p.len = cdiv(cdiv(T, P), kLC) * kLC;
+    if (p.len < kLC)
+        p.len = kLC;
+    p.P = T > 0 ? cdiv(T, p.len) : 1;
+    return p;
+}
+
+struct LinLayout {
+    LinPlan plan;
+    size_t off_fwd, off_flam;  // slots of the state and their decay factors [rows * P][H]
+    size_t off_rev, off_rlam;  // slots of the state's gradient (backward pass)
+    size_t off_dq, off_dk;     // fp32 per value head [B, T, H, 128], when q/k heads are shared
+    size_t off_qd, off_kd;     // fp32 [B, T, H]: q.dq and k.dk, when the decay's gradient is wanted
+    size_t off_xfin;           // fp32 [n_seq][H]: <S_final, dL/dS_final>
+    size_t off_part;           // double [rows * P][H]: partial sums of a per-head decay's gradient
+    size_t total;
+};
+
+struct LinTensor {  // bf16 [B, T, heads, 128] with element strides; head h of the pass reads head h / share
+    const uint16_t *p;
+    int64_t sb, st, sh;
+    int64_t share;
+};
+
+// One walk over all tokens: out_t = sum over sources s of w(t, s) (q_t . k_s) v_s, with the
+// sources at or before t, or (rev) at or behind it.
+struct LinRole {
+    LinTensor q, k, v;
+    int rev;          // sources behind the token; the state runs from the end to the start
+    int transposed;   // the state's [V][K] matrix is held as [k of the role][v of the role]
+    const void *init; // [n_seq][H][128][128] or NULL
+    void *fin;        // state after the last step, or NULL
+    int init_dt, fin_dt;
+    float *slots;     // [rows * P][H][128][128]
+    float *lam;       // [rows * P][H]
+    int defer;        // fin is init and P > 1: see lin_final_kernel
+    void *out;        // [B, T, H, 128], bf16 or fp32 (out_f32), or NULL
+    int out_f32;
+    LinTensor x;      // dots[b, t, h] = out row . x row (x.p NULL: not wanted)
+    float *dots;
+    const float *xst; // fp32 [n_seq][H][128][128]: xfin = <final state, xst>
+    float *xfin;
+};
+
+struct LinArgs {
+    LinRole role[3];
+    const float *decay;  // natural-log decay
+    int per_token;       // decay [B, T, H], else [H]
+    float scale;
+    int64_t T, H, N;     // N = n_seq
+    int64_t rows, P, len;
+    const int64_t *cu;   // NULL: every row is one sequence
+    int32_t *status;     // device status word (NULL without cu)
+};
+
+struct LinBwdExtra {
+    int64_t Hk;
+    uint16_t *dq, *dk;        // bf16 [B, T, Hk, 128]
+    const float *dq_h, *dk_h; // fp32 per value head, or NULL when heads are not shared
+    float *ddecay;            // NULL: not wanted
+    double *part;
+};
+
+hipError_t lin_launch_check(const int64_t *cu, int64_t N, int64_t T, int32_t *status, hipStream_t s);
+// n_roles walks in one launch; with P > 1 the states pass and the scan run first, for the
+// roles that `lead` lists (roles that share slots need them once).
+hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n_lead, hipStream_t s);
+hipError_t lin_launch_grad_tail(const LinArgs &a, const LinBwdExtra &e, hipStream_t s);
+hipError_t lin_launch_recurrent(const LinArgs &a, hipStream_t s);
+
+}  // namespace kda

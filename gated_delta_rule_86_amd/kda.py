@@ -27,7 +27,7 @@ STATUS_NAMES = {
     0: "KDA_OK", 1: "KDA_ERR_NULL", 2: "KDA_ERR_SHAPE", 3: "KDA_ERR_HEAD_DIM", 4: "KDA_ERR_DTYPE",
     5: "KDA_ERR_LOWER_BOUND", 6: "KDA_ERR_SCALE", 7: "KDA_ERR_ALIGN", 8: "KDA_ERR_WORKSPACE",
     9: "KDA_ERR_CU_SEQLENS", 10: "KDA_ERR_HIP", 11: "KDA_ERR_ALIAS", 12: "KDA_ERR_FLAGS",
-    13: "KDA_ERR_SCRATCH",
+    13: "KDA_ERR_SCRATCH", 14: "KDA_ERR_HEADS", 15: "KDA_ERR_STRIDE", 16: "KDA_ERR_ROTARY",
 }
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024  # KDA_NOALLOC_SCRATCH_BYTES
 # activation switches of kda_fwd_ex (include/kda.h)
@@ -39,7 +39,9 @@ STATE_NONE, STATE_BF16, STATE_FP32 = 0, 1, 2
 EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_recurrent", "kda_fwd_recurrent_timed", "kda_fwd_timed",
            "kda_fwd_noalloc", "kda_fwd_workspace_size", "kda_bwd", "kda_bwd_workspace_size",
            "kda_status_string",
-           "kda_fwd_device_status", "kda_chunk_table", "kda_version")
+           "kda_fwd_device_status", "kda_chunk_table", "kda_version",
+           "kda_lin_fwd", "kda_lin_fwd_recurrent", "kda_lin_fwd_workspace_size", "kda_lin_bwd",
+           "kda_lin_bwd_workspace_size", "kda_qk_rope", "kda_qk_rope_bwd", "kda_qk_rope_bwd_workspace_size")
 
 
 class KDAError(RuntimeError):
@@ -90,6 +92,23 @@ def lib():
     L.kda_chunk_table.argtypes = [vp, i64, i64, i64, i64, vp, ctypes.c_size_t,
                                   ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                   ctypes.POINTER(ctypes.c_int32), vp]
+    szt, ci = ctypes.c_size_t, ctypes.c_int
+    L.kda_lin_fwd.restype = ci
+    L.kda_lin_fwd.argtypes = [vp, vp, vp, vp, ci, f32, vp, vp, ci, vp, ci, vp, vp] + [i64] * 7 + [vp, vp, szt, vp]
+    L.kda_lin_fwd_recurrent.restype = ci
+    L.kda_lin_fwd_recurrent.argtypes = L.kda_lin_fwd.argtypes
+    L.kda_lin_fwd_workspace_size.restype = szt
+    L.kda_lin_fwd_workspace_size.argtypes = [i64, i64, i64, i64, ci]
+    L.kda_lin_bwd.restype = ci
+    L.kda_lin_bwd.argtypes = [vp, vp, vp, vp, ci, f32, vp, ci] + [vp] * 9 + [i64] * 7 + [vp, vp, szt, vp]
+    L.kda_lin_bwd_workspace_size.restype = szt
+    L.kda_lin_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, ci, ci]
+    L.kda_qk_rope.restype = ci
+    L.kda_qk_rope.argtypes = [vp] * 8 + [i64] * 6 + [ci, ci, f32, ci, f32, vp, vp]
+    L.kda_qk_rope_bwd.restype = ci
+    L.kda_qk_rope_bwd.argtypes = [vp] * 12 + [i64] * 6 + [ci, ci, f32, ci, f32, vp, vp, szt, vp]
+    L.kda_qk_rope_bwd_workspace_size.restype = szt
+    L.kda_qk_rope_bwd_workspace_size.argtypes = [i64] * 5
     L.kda_version.restype = ctypes.c_int
     L.kda_version.argtypes = []
     _lib = L

@@ -58,7 +58,10 @@ typedef enum kda_status {
     KDA_ERR_HIP = 10,        /* a HIP launch or query failed */
     KDA_ERR_ALIAS = 11,      /* out overlaps an input, or final_state overlaps a non-state input */
     KDA_ERR_FLAGS = 12,      /* kda_fwd_ex: unknown bits in the activation switch mask */
-    KDA_ERR_SCRATCH = 13     /* kda_fwd_noalloc: the call needs more than KDA_NOALLOC_SCRATCH_BYTES */
+    KDA_ERR_SCRATCH = 13,    /* kda_fwd_noalloc: the call needs more than KDA_NOALLOC_SCRATCH_BYTES */
+    KDA_ERR_HEADS = 14,      /* kda_lin_*: H is not a multiple of Hk, or Hk < 1 */
+    KDA_ERR_STRIDE = 15,     /* kda_lin_*, kda_qk_rope*: a stride is negative, no multiple of 16 bytes, or too large */
+    KDA_ERR_ROTARY = 16      /* kda_qk_rope*: head size or rotary_dim not supported */
 } kda_status;
 
 typedef enum kda_state_dtype {
@@ -298,6 +301,149 @@ kda_status kda_bwd(const void *q, const void *k, const void *v, const void *g, c
  * invalid sizes.
  */
 size_t kda_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
+
+/*
+ * kda_lin_fwd -- linear attention with a decay for each head, chunked form (prompts, training).
+ * Per (sequence, head), with the state S [V][K] of kda_fwd's layout:
+ *   S <- e^g S + v k^T,   out = scale * S q.
+ *
+ *   q, k      bf16 [B, T, Hk, 128], 16-byte aligned.  H must be a multiple of Hk: value head h
+ *             reads q/k head h / (H / Hk).
+ *   v         bf16 [B, T, H, 128], 16-byte aligned.
+ *   decay     fp32 natural-log decays g <= 0: [H] (decay_per_token 0), or contiguous [B, T, H]
+ *             (decay_per_token 1; the decay of a token acts on the state before its write).
+ *             Used as min(max(g, -1000), 0); from about -104 on the factor is 0 in fp32,
+ *             -inf makes the head forget.  A NaN makes the sequence's head NaN from there on.
+ *   scale     finite output factor.
+ *   out       bf16 [B, T, H, 128], contiguous, 16-byte aligned; every token of every sequence
+ *             is written.  Must not overlap an input.
+ *   initial_state, final_state and their dtypes, cu_seqlens, cu_seqlens_host, B, T, N, K, V, workspace
+ *             (256-byte aligned, kda_lin_fwd_workspace_size bytes) and stream: as in kda_fwd,
+ *             including the in-place state carry and the handling of an invalid cu_seqlens
+ *             (kda_fwd_device_status reads the status word of this workspace too).
+ *   strides_host  NULL (q, k, v contiguous), or host int64 [9]: batch, token and head strides of
+ *             q, k, v in elements; the 128 channels of a head are contiguous.  Each a
+ *             multiple of 8, the token stride at most 2^24 (views of one fused projection).
+ * fp32 states keep fp32 accuracy (24-bit products, fp32 sums); out is rounded once.  A value that
+ * is not finite reaches its own sequence and head alone, from the first token of its chunk
+ * of 64 tokens on (of the workgroup's run of tokens, see kda_lin_fwd_workspace_size).
+ * Deterministic: fixed summation orders, no atomics.
+ */
+kda_status kda_lin_fwd(const void *q, const void *k, const void *v, const float *decay, int decay_per_token,
+                       float scale, void *out, const void *initial_state, kda_state_dtype initial_state_dtype,
+                       void *final_state, kda_state_dtype final_state_dtype, const int64_t *cu_seqlens,
+                       const int64_t *cu_seqlens_host, int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                       int64_t K, int64_t V, const int64_t *strides_host, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * kda_lin_fwd_recurrent -- the same operator token by token in fp32, for the decode step (one token
+ * per sequence, state in and out, often in place) and sequences of a few tokens.  Same
+ * arguments and results (to rounding) as kda_lin_fwd.  The workspace may be NULL without
+ * cu_seqlens; with it, 256 bytes hold the status word.
+ */
+kda_status kda_lin_fwd_recurrent(const void *q, const void *k, const void *v, const float *decay,
+                                 int decay_per_token, float scale, void *out, const void *initial_state,
+                                 kda_state_dtype initial_state_dtype, void *final_state,
+                                 kda_state_dtype final_state_dtype, const int64_t *cu_seqlens,
+                                 const int64_t *cu_seqlens_host, int64_t B, int64_t T, int64_t Hk, int64_t H,
+                                 int64_t N, int64_t K, int64_t V, const int64_t *strides_host, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * kda_lin_fwd_workspace_size -- 256 bytes, plus one fp32 128 x 128 state and one float per head and
+ * segment where the tokens of a batch row (all tokens with cu_seqlens) are cut into segments
+ * that run in parallel: when batch rows x heads leave the chip empty.  A function of
+ * (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes.
+ */
+size_t kda_lin_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
+
+/*
+ * kda_lin_bwd -- gradients of kda_lin_fwd's out and final_state.  q, k, v, decay, scale, initial_state,
+ * cu_seqlens, sizes, strides_host and stream as there.
+ *   dout          bf16 [B, T, H, 128], contiguous, 16-byte aligned: dL/dout.
+ *   dfinal_state  NULL (zero) or fp32 [N, H, 128, 128], 16-byte aligned: dL/dfinal_state.
+ *   dq, dk        bf16 [B, T, Hk, 128], dv bf16 [B, T, H, 128], contiguous, 16-byte aligned, fully
+ *                 written; heads that share a q/k head are summed in fp32 and rounded once.
+ *   ddecay        NULL (not wanted) or fp32, of decay's shape; a per-head decay's is summed over
+ *                 all tokens.  0 where decay lies outside (-1000, 0].
+ *   dinitial_state  NULL or fp32 [N, H, 128, 128], 16-byte aligned (also when initial_state is NULL).
+ *   workspace     kda_lin_bwd_workspace_size(..., ddecay != NULL) bytes, 256-byte aligned.
+ * Outputs must not overlap inputs or each other (KDA_ERR_ALIAS).  An invalid cu_seqlens found on
+ * the device leaves dq, dk, dv and a per-token ddecay unwritten, a per-head ddecay 0 and
+ * dinitial_state = dfinal_state (or 0).  Deterministic.
+ */
+kda_status kda_lin_bwd(const void *q, const void *k, const void *v, const float *decay, int decay_per_token,
+                       float scale, const void *initial_state, kda_state_dtype initial_state_dtype, const void *dout,
+                       const float *dfinal_state, void *dq, void *dk, void *dv, float *ddecay,
+                       float *dinitial_state, const int64_t *cu_seqlens, const int64_t *cu_seqlens_host, int64_t B,
+                       int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t K, int64_t V,
+                       const int64_t *strides_host, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_lin_bwd_workspace_size -- 256 bytes; per head and segment (see kda_lin_fwd_workspace_size; at
+ * most 512 tokens long when need_ddecay) two fp32 states; with Hk < H two fp32 [B, T, H, 128];
+ * with need_ddecay two fp32 [B, T, H] and small sums.  Returns 0 for invalid sizes.
+ */
+size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens,
+                                  int need_ddecay);
+
+typedef enum kda_dtype {
+    KDA_DTYPE_BF16 = 1,
+    KDA_DTYPE_FP32 = 2,
+    KDA_DTYPE_FP16 = 3
+} kda_dtype;
+
+typedef enum kda_norm {
+    KDA_NORM_NONE = 0,
+    KDA_NORM_RMS = 1, /* x / sqrt(mean(x^2) + eps) */
+    KDA_NORM_L2 = 2   /* x / sqrt(sum(x^2) + eps), the normalisation kda_fwd applies to q and k */
+} kda_norm;
+
+/*
+ * kda_qk_rope -- normalises each head of q and k and rotates pairs of its first rotary_dim channels by the
+ * token's position, in one pass over both tensors; out rounded once.
+ *   n = norm(x) * weight;   for pair i, t = position * inv_freq[i]:
+ *   (a, b) -> attention_factor * (a cos t - b sin t, a sin t + b cos t);  other channels pass as n.
+ *
+ *   q, q_out      [B, T, Hq, D], k, k_out [B, T, Hk, D], all of `dtype`, 16-byte aligned.  D a multiple
+ *                 of 16 up to 512.  An output may be its input (same pointer and strides);
+ *                 otherwise outputs overlap nothing.
+ *   q_weight, k_weight  NULL (1) or fp32 [D], 4-byte aligned, shared by the tensor's heads.
+ *   inv_freq      fp32 [rotary_dim / 2] angular frequencies (radians per position), any scaling
+ *                 for long contexts already applied; NULL when rotary_dim is 0.
+ *   positions     int64 [B, T], contiguous, or NULL: the token's index in its row.  Angles are formed in
+ *                 fp64: exact to fp32 rounding for |position * inv_freq| below 2^27.
+ *   rotary_dim    0 .. D, a multiple of 16.  interleaved: pairs (2i, 2i + 1) when 1, else
+ *                 (i, i + rotary_dim / 2).
+ *   norm, eps     eps finite and >= 0 (not used by KDA_NORM_NONE).
+ *   strides_host  NULL (contiguous) or host int64 [12]: batch, token, head strides in elements of
+ *                 q, k, q_out, k_out, each a multiple of 16 bytes.
+ * Errors: KDA_ERR_NULL, _SHAPE, _ROTARY, _DTYPE, _FLAGS (norm, interleaved), _SCALE (eps, factor), _STRIDE,
+ * _ALIGN, _ALIAS, _HIP.  T = 0 does nothing.
+ */
+kda_status kda_qk_rope(const void *q, const void *k, void *q_out, void *k_out, const float *q_weight,
+                       const float *k_weight, const float *inv_freq, const int64_t *positions, int64_t B, int64_t T,
+                       int64_t Hq, int64_t Hk, int64_t D, int64_t rotary_dim, kda_dtype dtype, kda_norm norm,
+                       float eps, int interleaved, float attention_factor, const int64_t *strides_host,
+                       void *stream);
+
+/*
+ * kda_qk_rope_bwd -- gradients of kda_qk_rope: dq, dk from dq_out, dk_out and the forward pass's inputs, and
+ * (NULL = not wanted) dq_weight, dk_weight, fp32 [D], summed over tokens and heads in a
+ * fixed order.  strides_host: int64 [18], q, k, dq_out, dk_out, dq, dk.  dq may be q or dq_out,
+ * dk k or dk_out (same pointer and strides).  The workspace (kda_qk_rope_bwd_workspace_size
+ * bytes, 256-byte aligned) is used, and may be NULL otherwise, when a weight gradient is wanted.
+ */
+kda_status kda_qk_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq, void *dk,
+                           const float *q_weight, const float *k_weight, float *dq_weight, float *dk_weight,
+                           const float *inv_freq, const int64_t *positions, int64_t B, int64_t T, int64_t Hq,
+                           int64_t Hk, int64_t D, int64_t rotary_dim, kda_dtype dtype, kda_norm norm, float eps,
+                           int interleaved, float attention_factor, const int64_t *strides_host, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Bytes of partial weight sums: 8 D for each of at most 1024 workgroups.  Returns 0 for invalid sizes. */
+size_t kda_qk_rope_bwd_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D);
 
 /* Human-readable name of a kda_status value (static string; never NULL). */
 const char *kda_status_string(int status);
