@@ -43,7 +43,7 @@ kda_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, b
         return KDA_ERR_HEADS;
     if (varlen ? (B != 1 || N < 1) : (N != 0 && N != B))
         return KDA_ERR_SHAPE;
-    if (H > ((int64_t)1 << 20) || T >= ((int64_t)1 << 35) || T > ((int64_t)1 << 40) / B ||
+    if (H > ((int64_t)1 << 16) || T >= ((int64_t)1 << 35) || T > ((int64_t)1 << 40) / B ||
         B * T > kMaxElems / (H * kD))
         return KDA_ERR_SHAPE;
     const int64_t n_seq = varlen ? N : B;

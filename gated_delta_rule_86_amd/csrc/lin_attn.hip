@@ -32,6 +32,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u2 __attribute__((vector_size(8)));   // as the buffer builtins want them
+typedef unsigned int u4 __attribute__((vector_size(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -216,6 +218,9 @@ __device__ __forceinline__ const void *matrix_of(const void *base, int64_t n, si
     return base ? static_cast<const unsigned char *>(base) + (size_t)n * bytes : nullptr;
 }
 
+// channel of register n = 16 kt + r for half 0 (half 1: 8 more)
+__device__ constexpr int first_channel(int n) { return 32 * (n >> 4) + 16 * ((n >> 3) & 1) + (n & 7); }
+
 // One 128 x 128 matrix at `base` (dt: 1 bf16, 2 fp32; NULL: zeros) into registers or back.  Buffer
 // instructions: one lane offset serves all 64 entries, the rest sits in the instruction.
 __device__ __forceinline__ void state_load(State &S, const void *base, int dt, bool tr, int wave, int lane)
@@ -224,89 +229,71 @@ __device__ __forceinline__ void state_load(State &S, const void *base, int dt, b
     const int size = dt == kBf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t r = rsrc(base, base ? (uint32_t)(kD * kD * size) : 0u);
     const int vo = (tr ? 8 * half * kD + col : col * kD + 8 * half) * size;
-    if (dt == kBf16) {
+    if (dt == kBf16 && tr) {
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int n = 0; n < 64; ++n)
+            S.t[n >> 4][n & 15] = __uint_as_float(
+                (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, vo, first_channel(n) * kD * 2, 0) << 16);
+    } else if (dt == kBf16) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int ch = 32 * kt + 16 * m;
-                if (tr) {
+        for (int n = 0; n < 64; n += 8) {
+            const u32x4 x =
+                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, first_channel(n) * 2, 0));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        S.t[kt][8 * m + e] = __uint_as_float(
-                            (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, vo, (ch + e) * kD * 2, 0) << 16);
-                } else {
-                    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, ch * 2, 0));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        S.t[kt][8 * m + 2 * e] = lo_f(x[e]);
-                        S.t[kt][8 * m + 2 * e + 1] = hi_f(x[e]);
-                    }
-                }
+            for (int e = 0; e < 4; ++e) {
+                S.t[n >> 4][(n & 15) + 2 * e] = lo_f(x[e]);
+                S.t[n >> 4][(n & 15) + 2 * e + 1] = hi_f(x[e]);
             }
+        }
+    } else if (tr) {
+#pragma unroll
+        for (int n = 0; n < 64; ++n)
+            S.t[n >> 4][n & 15] =
+                __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, vo, first_channel(n) * kD * 4, 0));
     } else {
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int n = 0; n < 64; n += 4) {
+            const u32x4 x =
+                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, first_channel(n) * 4, 0));
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int ch = 32 * kt + 16 * (n >> 1) + 4 * (n & 1);
-                if (tr) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S.t[kt][4 * n + e] =
-                            __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, vo, (ch + e) * kD * 4, 0));
-                } else {
-                    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, vo, ch * 4, 0));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S.t[kt][4 * n + e] = __uint_as_float(x[e]);
-                }
-            }
+            for (int e = 0; e < 4; ++e)
+                S.t[n >> 4][(n & 15) + e] = __uint_as_float(x[e]);
+        }
     }
 }
 
 __device__ __forceinline__ void state_store(const State &S, void *base, int dt, bool tr, int wave, int lane)
 {
-    typedef unsigned int u4 __attribute__((vector_size(16)));
     const int col = 32 * wave + (lane & 31), half = lane >> 5;
     const int size = dt == kBf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t r = rsrc(base, (uint32_t)(kD * kD * size));
     const int vo = (tr ? 8 * half * kD + col : col * kD + 8 * half) * size;
-    if (dt == kBf16) {
+    if (dt == kBf16 && tr) {
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int n = 0; n < 64; ++n)
+            __builtin_amdgcn_raw_buffer_store_b16((short)to_bf16(S.t[n >> 4][n & 15]), r, vo,
+                                                  first_channel(n) * kD * 2, 0);
+    } else if (dt == kBf16) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int ch = 32 * kt + 16 * m;
-                if (tr) {
+        for (int n = 0; n < 64; n += 8) {
+            u32x4 x;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        __builtin_amdgcn_raw_buffer_store_b16((short)to_bf16(S.t[kt][8 * m + e]), r, vo,
-                                                              (ch + e) * kD * 2, 0);
-                } else {
-                    u32x4 x;
+            for (int e = 0; e < 4; ++e)
+                x[e] = pack2(S.t[n >> 4][(n & 15) + 2 * e], S.t[n >> 4][(n & 15) + 2 * e + 1]);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), r, vo, first_channel(n) * 2, 0);
+        }
+    } else if (tr) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] = pack2(S.t[kt][8 * m + 2 * e], S.t[kt][8 * m + 2 * e + 1]);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), r, vo, ch * 2, 0);
-                }
-            }
+        for (int n = 0; n < 64; ++n)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S.t[n >> 4][n & 15]), r, vo,
+                                                  first_channel(n) * kD * 4, 0);
     } else {
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int ch = 32 * kt + 16 * (n >> 1) + 4 * (n & 1);
-                if (tr) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S.t[kt][4 * n + e]), r, vo,
-                                                              (ch + e) * kD * 4, 0);
-                } else {
-                    const f32x4 x = {S.t[kt][4 * n], S.t[kt][4 * n + 1], S.t[kt][4 * n + 2], S.t[kt][4 * n + 3]};
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), r, vo, ch * 4, 0);
-                }
-            }
+        for (int n = 0; n < 64; n += 4) {
+            const f32x4 x = {S.t[n >> 4][n & 15], S.t[n >> 4][(n & 15) + 1], S.t[n >> 4][(n & 15) + 2],
+                             S.t[n >> 4][(n & 15) + 3]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, x), r, vo, first_channel(n) * 4, 0);
+        }
     }
 }
 
@@ -318,13 +305,9 @@ __device__ __forceinline__ float state_dot(const State &S, const float *base, bo
     const int vo = (tr ? 8 * half * kD + col : col * kD + 8 * half) * 4, step = (tr ? kD : 1) * 4;
     float d = 0.0f;
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-            d = fmaf(S.t[kt][n],
-                     __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                         r, vo, (32 * kt + 16 * (n >> 3) + (n & 7)) * step, 0)),
-                     d);
+    for (int n = 0; n < 64; ++n)
+        d = fmaf(S.t[n >> 4][n & 15],
+                 __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, vo, first_channel(n) * step, 0)), d);
     return d;
 }
 
@@ -406,36 +389,83 @@ __device__ __forceinline__ float load_decay(const LinArgs &a, int64_t row, int64
     return a.decay[(row * a.T + c.t0 + t) * a.H + h];
 }
 
+// One input of the walk: this workgroup's row and head.
+struct TileSrc {
+    const uint16_t *p;
+    int64_t st;
+};
+__device__ __forceinline__ TileSrc tile_src(const LinTensor &x, int64_t row, int64_t h)
+{
+    // heads are shared by small whole numbers: 32-bit division
+    return TileSrc{x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh, x.st};
+}
 struct TileLoad {
     u32x4 r[4];
 };
 // 64 rows of 256 bytes; rows behind the chunk read as zeros (beyond the descriptor)
-__device__ __forceinline__ void tile_fetch(TileLoad &f, const LinTensor &x, int64_t row, int64_t h, const Chunk &c, int tid)
+__device__ __forceinline__ void tile_fetch(TileLoad &f, const TileSrc &x, const Chunk &c, int tid)
 {
-    const uint16_t *base = x.p + row * x.sb + c.t0 * x.st + (h / x.share) * x.sh;
     const uint32_t stride = (uint32_t)(x.st * 2);
-    const __amdgpu_buffer_rsrc_t r = rsrc(base, (uint32_t)(c.len - 1) * stride + 256u);
+    const __amdgpu_buffer_rsrc_t r = rsrc(x.p + c.t0 * x.st, (uint32_t)(c.len - 1) * stride + 256u);
+    const int tok = tid >> 4;
+    const uint32_t off = (uint32_t)tok * stride + (uint32_t)(tid & 15) * 16u;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const int at = tid + 256 * n, tok = at >> 4;
-        // a stride of 0 or less than a row would let a row behind the chunk lie inside the descriptor
-        f.r[n] = buf_b128(r, tok < c.len ? (uint32_t)tok * stride + (uint32_t)(at & 15) * 16u : 0xffffff00u);
-    }
-}
-__device__ __forceinline__ void tile_put(const TileLoad &f, unsigned char *lds, int tid)
-{
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const int at = tid + 256 * n;
-        *reinterpret_cast<u32x4 *>(lds + tile_at(at >> 4, at & 15)) = f.r[n];
-    }
+    for (int n = 0; n < 4; ++n)
+        // the token decides, not the offset alone: rows may be closer than 256 bytes (a stride of 0)
+        f.r[n] = buf_b128(r, tok + 16 * n < c.len ? off + (uint32_t)n * 16u * stride : 0xffffff00u);
 }
 
-// 8 tokens x this lane's channel of an operand whose channel group (of 4) the lane names
-__device__ __forceinline__ u32x4 tr_frag(const unsigned char *tile, int token, int channel)
+// This lane's places in the LDS tiles, as byte offsets.  The XOR of tile_at() reaches the three low bits of a
+// piece's number only, so a few bases and the instruction's own offset reach everything.
+struct Lanes {
+    int put;        // row tid / 16 (+ 16 n), piece tid % 16 of a tile
+    int row[4];     // row lane % 32 (+ 32), piece 2 v + half (+ 8)
+    int trv[2];     // transposing read of this wave's columns: token 8 half (+ 16 j) + 4 n
+    int trk[2][2];  // [kt % 2][n]: the same of channels 32 kt .. (+ 64), in the order of the state's registers
+    int w[4];       // weights of out token lane % 32 (+ 32), source piece 2 v + half
+
+    __device__ Lanes(int tid)
+    {
+        const int lane = tid & 63, wave = tid >> 6, l32 = lane & 31, half = lane >> 5, i = lane & 15, g2 = (lane >> 4) & 1;
+        const int fg = ((i & 1) << 1) | ((i >> 1) & 1);
+        put = tile_at(tid >> 4, tid & 15);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            row[v] = tile_at(l32, 2 * v + half);
+            w[v] = l32 * kPRow + (((2 * v + half) ^ (l32 & 7)) << 4);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int tok = 8 * half + 4 * n + (i >> 2);
+            trv[n] = tile_at(tok, 4 * wave + 2 * g2 + ((i & 3) >> 1)) + 8 * (i & 1);
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+                trk[kt][n] = tile_at(tok, 4 * kt + 2 * g2 + (fg >> 1)) + 8 * (fg & 1);
+        }
+    }
+};
+
+__device__ __forceinline__ void tile_put(const TileLoad &f, unsigned char *tile, const Lanes &ln)
 {
-    const u32x2 x = lds_tr(tile + tile_at(token, channel >> 3) + (channel & 7) * 2);
-    const u32x2 y = lds_tr(tile + tile_at(token + 4, channel >> 3) + (channel & 7) * 2);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        *reinterpret_cast<u32x4 *>(tile + ln.put + 4096 * n) = f.r[n];
+}
+// 16 channels, 16 jj .., of row lane % 32 of a block of 32 rows
+__device__ __forceinline__ u32x4 row_frag(const unsigned char *tile, const Lanes &ln, int block, int jj)
+{
+    return lds_b128(tile + ln.row[jj & 3] + 8192 * block + 128 * (jj >> 2));
+}
+// 8 of the 16 tokens 16 j .. of this lane's column
+__device__ __forceinline__ u32x4 col_frag(const unsigned char *tile, const Lanes &ln, int j)
+{
+    const u32x2 x = lds_tr(tile + ln.trv[0] + 4096 * j), y = lds_tr(tile + ln.trv[1] + 4096 * j);
+    return u32x4{x[0], x[1], y[0], y[1]};
+}
+__device__ __forceinline__ u32x4 key_frag(const unsigned char *tile, const Lanes &ln, int kt, int j)
+{
+    const int off = 4096 * j + 128 * (kt >> 1);
+    const u32x2 x = lds_tr(tile + ln.trk[kt & 1][0] + off), y = lds_tr(tile + ln.trk[kt & 1][1] + off);
     return u32x4{x[0], x[1], y[0], y[1]};
 }
 
@@ -443,14 +473,6 @@ __device__ __forceinline__ u32x4 tr_frag(const unsigned char *tile, int token, i
 struct Terms3 {
     u32x4 h, m, l;
 };
-__device__ __forceinline__ void cut2(const float *x, u32x4 &h, u32x4 &l)
-{
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        h[e] = pack2(x[2 * e], x[2 * e + 1]);
-        l[e] = pack2(x[2 * e] - lo_f(h[e]), x[2 * e + 1] - hi_f(h[e]));
-    }
-}
 __device__ __forceinline__ void cut3(const float *x, Terms3 &t)
 {
 #pragma unroll
@@ -467,33 +489,27 @@ __device__ __forceinline__ void cut3(const float *x, Terms3 &t)
 // in fp32, and go into the product as three bf16 terms (24 bits), so that an fp32 state keeps
 // fp32's accuracy.
 __device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const Decays &d,
-                                             int len, int lane)
+                                             const Lanes &ln, int half)
 {
-    const int half = lane >> 5, i = lane & 15, g2 = (lane >> 4) & 1;
-    const int cg = i & 3;
-    const int fg = ((cg & 1) << 1) | (cg >> 1);  // rows of the K operand in the order of the state's registers
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (16 * j < len) {
-            const int tok = 16 * j + 8 * half;
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.win[tok]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.win[tok + 4]);
-            float x[8];
+        const int tok = 16 * j + 8 * half;
+        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.win[tok]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.win[tok + 4]);
+        float x[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float w_a = e < 2 ? w0[2 * e] : w1[2 * e - 4], w_b = e < 2 ? w0[2 * e + 1] : w1[2 * e - 3];
-                x[2 * e] = lo_f(vf[j][e]) * w_a;
-                x[2 * e + 1] = hi_f(vf[j][e]) * w_b;
-            }
-            Terms3 t;
-            cut3(x, t);
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = lo_f(vf[j][e]) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
+            x[2 * e + 1] = hi_f(vf[j][e]) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
+        }
+        Terms3 t;
+        cut3(x, t);
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                const u32x4 kf = tr_frag(ktile, tok + (i >> 2), 32 * kt + 16 * g2 + 4 * fg);
-                S.t[kt] = mfma(kf, t.l, S.t[kt]);
-                S.t[kt] = mfma(kf, t.m, S.t[kt]);
-                S.t[kt] = mfma(kf, t.h, S.t[kt]);
-            }
+        for (int kt = 0; kt < 4; ++kt) {
+            const u32x4 kf = key_frag(ktile, ln, kt, j);
+            S.t[kt] = mfma(kf, t.l, S.t[kt]);
+            S.t[kt] = mfma(kf, t.m, S.t[kt]);
+            S.t[kt] = mfma(kf, t.h, S.t[kt]);
         }
     }
 }
@@ -555,32 +571,35 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
                ro.init_dt, ro.transposed != 0, wave, lane);
     double sum = 0.0;
     TileLoad fk, fv;
-    tile_fetch(fk, ro.k, row, h, c, tid);
-    tile_fetch(fv, ro.v, row, h, c, tid);
+    const TileSrc sk = tile_src(ro.k, row, h), sv = tile_src(ro.v, row, h);
+    tile_fetch(fk, sk, c, tid);
+    tile_fetch(fv, sv, c, tid);
     float g = load_decay(a, row, h, c, lane);
     int buf = 0;
-    const int half = lane >> 5, i = lane & 15, g2 = (lane >> 4) & 1;
+    const int half = lane >> 5;
+    const Lanes ln(tid);
+    if (wave == 3)
+        make_decays(lds.d[0], g, c.len, lane, rev, a.scale);
     while (c.len > 0) {
-        tile_put(fk, lds.k, tid);
-        tile_put(fv, lds.v, tid);
-        if (wave == 3)
-            make_decays(lds.d[buf], g, c.len, lane, rev, a.scale);
+        tile_put(fk, lds.k, ln);
+        tile_put(fv, lds.v, ln);
         const Chunk n = w.next();
         if (n.len > 0) {
-            tile_fetch(fk, ro.k, row, h, n, tid);
-            tile_fetch(fv, ro.v, row, h, n, tid);
             g = load_decay(a, row, h, n, lane);
+            tile_fetch(fk, sk, n, tid);
+            tile_fetch(fv, sv, n, tid);
         }
         lds_barrier();
         const Decays &d = lds.d[buf];
         u32x4 vf[4];
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
-            if (16 * jj < c.len)
-                vf[jj] = tr_frag(lds.v, 16 * jj + 8 * half + (i >> 2), 32 * wave + 16 * g2 + 4 * (i & 3));
+            vf[jj] = col_frag(lds.v, ln, jj);
         state_decay(S, d.last);
         sum += (double)d.last;
-        state_update(S, lds.k, vf, d, c.len, lane);
+        state_update(S, lds.k, vf, d, ln, half);
+        if (wave == 3 && n.len > 0)
+            make_decays(lds.d[buf ^ 1], g, n.len, lane, rev, a.scale);
         lds_barrier();
         c = n;
         buf ^= 1;
@@ -625,28 +644,20 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
 // out.  Their sums over many tokens cancel, so weights and states then go into the products
 // as three terms, and the own pairs are added to the rows outside the matrix product.
-template <bool kDots>
-__global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
+template <bool kDots, bool rev>
+__device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, unsigned char *lds_raw)
 {
-    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     LdsWalk &lds = *reinterpret_cast<LdsWalk *>(lds_raw);
     LdsWalkDots &ldx = *reinterpret_cast<LdsWalkDots *>(lds_raw);  // behind lds only with kDots
-    const int64_t total = a.rows * a.P * a.H;
-    const int64_t at = xcd_order(blockIdx.x, total);
-    if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
-        return;
-    const int64_t seg = at / a.H, h = at - seg * a.H;
     const int64_t row = seg / a.P, j = seg - row * a.P;
-    const LinRole &ro = a.role[blockIdx.y];
-    const bool rev = ro.rev != 0, tr = ro.transposed != 0;
+    const bool tr = ro.transposed != 0;
     const bool dots = kDots && ro.dots != nullptr;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int half = lane >> 5, l32 = lane & 31, i = lane & 15, g2 = (lane >> 4) & 1;
+    const int half = lane >> 5, l32 = lane & 31;
+    const Lanes ln(tid);
     const size_t init_bytes = kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1);
     const size_t fin_bytes = kLinStateBytes / (ro.fin_dt == kBf16 ? 2 : 1);
     State S;
-    if (!a.cu && a.status && at == 0 && blockIdx.y == 0 && tid == 0)
-        *a.status = 0;
 
     Walk w;
     const bool bad = device_bad(a);
@@ -672,23 +683,27 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
     if (c.len == 0)
         return;
     TileLoad fq, fk, fv;
-    tile_fetch(fq, ro.q, row, h, c, tid);
-    tile_fetch(fk, ro.k, row, h, c, tid);
-    tile_fetch(fv, ro.v, row, h, c, tid);
+    const TileSrc sq = tile_src(ro.q, row, h), sk = tile_src(ro.k, row, h), sv = tile_src(ro.v, row, h);
+    TileSrc sx = {nullptr, 0};
+    if (dots)
+        sx = tile_src(ro.x, row, h);
+    tile_fetch(fq, sq, c, tid);
+    tile_fetch(fk, sk, c, tid);
+    tile_fetch(fv, sv, c, tid);
     float g = load_decay(a, row, h, c, lane);
     if (wave == 3)
         make_decays(lds.d[0], g, c.len, lane, rev, a.scale);
     int buf = 0;
     while (c.len > 0) {
-        tile_put(fq, lds.q, tid);
-        tile_put(fk, lds.k, tid);
-        tile_put(fv, lds.v, tid);
+        tile_put(fq, lds.q, ln);
+        tile_put(fk, lds.k, ln);
+        tile_put(fv, lds.v, ln);
         const Chunk n = w.next();
         if (n.len > 0) {
-            tile_fetch(fq, ro.q, row, h, n, tid);
-            tile_fetch(fk, ro.k, row, h, n, tid);
-            tile_fetch(fv, ro.v, row, h, n, tid);
             g = load_decay(a, row, h, n, lane);
+            tile_fetch(fq, sq, n, tid);
+            tile_fetch(fk, sk, n, tid);
+            tile_fetch(fv, sv, n, tid);
         }
         if (c.flags & kPieceStart) {
             const bool slot = (c.flags & kFromSlot) != 0;
@@ -699,10 +714,9 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
         }
         lds_barrier();
         const Decays &d = lds.d[buf];
-        const int nt = c.len > 32 ? 2 : 1;
 
         // weights of one 32 x 32 block (sources sb, outputs ob) per wave 0..2, bf16 hi + lo
-        if (wave < (nt == 2 ? 3 : 1)) {
+        if (wave < 3) {
             const int sb = wave == 0 ? 0 : (wave == 2 ? 1 : (rev ? 1 : 0));
             const int ob = wave == 0 ? 0 : (wave == 2 ? 1 : (rev ? 0 : 1));
             f32x16 p;
@@ -711,9 +725,9 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
                 p[r] = 0.0f;
 #pragma unroll
             for (int jj = 0; jj < 8; ++jj)
-                p = mfma(lds_b128(lds.k + tile_at(32 * sb + l32, 2 * jj + half)),
-                         lds_b128(lds.q + tile_at(32 * ob + l32, 2 * jj + half)), p);
-            const int to = 32 * ob + l32;
+                p = mfma(row_frag(lds.k, ln, sb, jj), row_frag(lds.q, ln, ob, jj), p);
+            int to = 32 * ob + l32;
+            __asm__ volatile("" : "+v"(to));  // keep the comparisons below in the loop: 16 masks would not stay in SGPRs
             const float bho = d.bh[to], blo = d.bl[to];
 #pragma unroll
             for (int a4 = 0; a4 < 4; ++a4) {
@@ -725,7 +739,7 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
                 for (int e = 0; e < 4; ++e) {
                     float df = (bho - bhs[e]) + (blo - bls[e]);
                     df = rev ? -df : df;
-                    const bool on = rev ? s + e >= to : s + e <= to;
+                    const bool on = rev ? s + e >= to : s + e <= to;  // a token behind the row's (before it) weighs nothing
                     x[e] = on ? p[4 * a4 + e] * (a.scale * __builtin_amdgcn_exp2f(df)) : 0.0f;
                     if (dots && s + e == to) {
                         ldx.own[to] = x[e];
@@ -738,20 +752,11 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
                 const int off = to * kPRow + (((4 * sb + a4) ^ (to & 7)) << 4) + 8 * half;
                 *reinterpret_cast<u32x2 *>(lds.p[0] + off) = hi;
                 *reinterpret_cast<u32x2 *>(lds.p[1] + off) = lo;
-                if (dots)
+                if (kDots)
                     *reinterpret_cast<u32x2 *>(ldx.p3 + off) =
                         u32x2{pack2(y[0] - lo_f(lo[0]), y[1] - hi_f(lo[0])), pack2(y[2] - lo_f(lo[1]), y[3] - hi_f(lo[1]))};
             }
         }
-        if (wave == 3 && n.len > 0)
-            make_decays(lds.d[buf ^ 1], g, n.len, lane, rev, a.scale);
-
-        u32x4 vf[4];
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj)
-            if (16 * jj < c.len)
-                vf[jj] = tr_frag(lds.v, 16 * jj + 8 * half + (i >> 2), 32 * wave + 16 * g2 + 4 * (i & 3));
-
         // the state's share of the outputs: O^T[v][t], the state in bf16 hi + lo
         f32x16 O[2];
 #pragma unroll
@@ -768,14 +773,13 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
             Terms3 s;
             cut3(x, s);
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-                if (tt < nt) {
-                    const u32x4 qf = lds_b128(lds.q + tile_at(32 * tt + l32, 2 * jj + half));
-                    if (dots)
-                        O[tt] = mfma(s.l, qf, O[tt]);
-                    O[tt] = mfma(s.m, qf, O[tt]);
-                    O[tt] = mfma(s.h, qf, O[tt]);
-                }
+            for (int tt = 0; tt < 2; ++tt) {
+                const u32x4 qf = row_frag(lds.q, ln, tt, jj);
+                if (kDots)
+                    O[tt] = mfma(s.l, qf, O[tt]);
+                O[tt] = mfma(s.m, qf, O[tt]);
+                O[tt] = mfma(s.h, qf, O[tt]);
+            }
         }
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
@@ -784,40 +788,55 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
             for (int r = 0; r < 16; ++r)
                 O[tt][r] *= wo;
         }
+        u32x4 vf[4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+            vf[jj] = col_frag(lds.v, ln, jj);
         lds_barrier();  // the weights are there
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                const bool inside = rev ? (jj >> 1) >= tt : (jj >> 1) <= tt;
-                if (tt < nt && inside && 16 * jj < c.len) {
-                    const int to = 32 * tt + l32, off = to * kPRow + (((2 * jj + half) ^ (to & 7)) << 4);
-                    if (dots)
-                        O[tt] = mfma(vf[jj], lds_b128(ldx.p3 + off), O[tt]);
-                    O[tt] = mfma(vf[jj], lds_b128(lds.p[1] + off), O[tt]);
-                    O[tt] = mfma(vf[jj], lds_b128(lds.p[0] + off), O[tt]);
-                }
+        for (int jj = 0; jj < 4; ++jj) {
+            // a diagonal block of 32 tokens, and the block beside it: output block 1 forwards, 0 backwards
+            const int tt = jj >> 1;
+            auto add = [&](f32x16 &o, int block) {
+                const int off = ln.w[jj] + 32 * kPRow * block;
+                if (kDots)
+                    o = mfma(vf[jj], lds_b128(ldx.p3 + off), o);
+                o = mfma(vf[jj], lds_b128(lds.p[1] + off), o);
+                o = mfma(vf[jj], lds_b128(lds.p[0] + off), o);
+            };
+            add(O[tt], tt);
+            if (tt == 0) {
+                if (!rev)
+                    add(O[1], 1);
+            } else if (rev) {
+                add(O[0], 0);
             }
+        }
 
-        state_decay(S, d.last);
-        state_update(S, lds.k, vf, d, c.len, lane);
-
-        // rows out
+        // rows out; those behind the chunk lie beyond the descriptor
+        {
+            const uint32_t size = ro.out_f32 ? 4 : 2, stride = (uint32_t)a.H * (kD * size);
+            const __amdgpu_buffer_rsrc_t ra =
+                rsrc(static_cast<unsigned char *>(ro.out) +
+                         ((size_t)(row * a.T + c.t0) * (size_t)a.H + (size_t)h) * (kD * size),
+                     (uint32_t)(c.len - 1) * stride + kD * size);
+            const uint32_t xs = dots ? (uint32_t)sx.st * 2 : 0;
+            const __amdgpu_buffer_rsrc_t rx =
+                rsrc(sx.p + c.t0 * sx.st, dots ? (uint32_t)(c.len - 1) * xs + 256u : 0u);
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            const int t = 32 * tt + l32;
-            float dot = 0.0f;
-            if (t < c.len) {
-                const int64_t tok = row * a.T + c.t0 + t;
-                const int64_t o = (tok * a.H + h) * kD + 32 * wave + 4 * half;
+            for (int tt = 0; tt < 2; ++tt) {
+                const int t = 32 * tt + l32;
+                const uint32_t o = (uint32_t)t * stride + (32 * wave + 4 * half) * size;
                 const float own = dots ? ldx.own[t] : 0.0f;
+                float dot = 0.0f;
 #pragma unroll
                 for (int a4 = 0; a4 < 4; ++a4) {
                     f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
                     if (dots) {
-                        const u32x2 xr = *reinterpret_cast<const u32x2 *>(
-                            ro.x.p + row * ro.x.sb + (c.t0 + t) * ro.x.st + (h / ro.x.share) * ro.x.sh + 32 * wave +
-                            4 * half + 8 * a4);
+                        const u32x2 xr = __builtin_bit_cast(
+                            u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                       rx, t < c.len ? (uint32_t)t * xs + (32 * wave + 4 * half + 8 * a4) * 2 : 0xffffff00u,
+                                       0, 0));
                         dot += (lo_f(xr[0]) * y[0] + hi_f(xr[0]) * y[1]) + (lo_f(xr[1]) * y[2] + hi_f(xr[1]) * y[3]);
                         const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(t, 4 * wave + a4) + 8 * half);
                         y[0] = fmaf(own, lo_f(vr[0]), y[0]);
@@ -825,19 +844,24 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
                         y[2] = fmaf(own, lo_f(vr[1]), y[2]);
                         y[3] = fmaf(own, hi_f(vr[1]), y[3]);
                     }
-                    if (ro.out_f32)
-                        *reinterpret_cast<f32x4 *>(static_cast<float *>(ro.out) + o + 8 * a4) = y;
-                    else
-                        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(ro.out) + o + 8 * a4) =
-                            u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+                    if (ro.out_f32) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra, o + 32 * a4, 0, 0);
+                    } else {
+                        const u32x2 z = {pack2(y[0], y[1]), pack2(y[2], y[3])};
+                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, z), ra, o + 16 * a4, 0, 0);
+                    }
+                }
+                if (dots) {
+                    dot += __shfl_xor(dot, 32);
+                    if (half == 0)
+                        ldx.red[wave][t] = dot;
                 }
             }
-            if (dots) {
-                dot += __shfl_xor(dot, 32);
-                if (half == 0)
-                    ldx.red[wave][t] = dot;
-            }
         }
+        state_decay(S, d.last);
+        state_update(S, lds.k, vf, d, ln, half);
+        if (wave == 3 && n.len > 0)
+            make_decays(lds.d[buf ^ 1], g, n.len, lane, rev, a.scale);
         lds_barrier();  // every read of this chunk's tiles is done
         if (dots && tid < c.len)
             ro.dots[(row * a.T + c.t0 + tid) * a.H + h] =
@@ -866,6 +890,24 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
         c = n;
         buf ^= 1;
     }
+}
+
+template <bool kDots>
+__global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    const int64_t total = a.rows * a.P * a.H;
+    const int64_t at = xcd_order(blockIdx.x, total);
+    if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
+        return;
+    if (!a.cu && a.status && at == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *a.status = 0;
+    const LinRole &ro = a.role[blockIdx.y];
+    const int64_t seg = at / a.H, h = at - seg * a.H;
+    if (ro.rev)
+        walk<kDots, true>(a, ro, seg, h, lds_raw);
+    else
+        walk<kDots, false>(a, ro, seg, h, lds_raw);
 }
 
 // In-place state carry with cut rows: the workgroup that ends a sequence may finish before the one
