@@ -109,9 +109,11 @@ kda_status set_tensor(const void *p, const int64_t *st, const Sizes &z, int64_t 
     if (t->sb < 0 || t->st < 0 || t->sh < 0 || t->sb % 8 || t->st % 8 || t->sh % 8 || t->st > kMaxTokenStride ||
         t->sb > kMaxElems || t->sh > kMaxElems)
         return KDA_ERR_STRIDE;
+    if (z.T == 1)
+        t->st = kD;  // never a step, but the kernels take a row's end from it
     if (!aligned(p, 16))
         return KDA_ERR_ALIGN;
-    if (z.T > kMaxElems / (t->st + 1))
+    if (z.T > kMaxElems / (t->st + 1) || (z.T > 1 && t->st < kD))  // tokens' rows do not overlap
         return KDA_ERR_STRIDE;
     const size_t last = (size_t)(z.B - 1) * (size_t)t->sb + (size_t)(z.T - 1) * (size_t)t->st +
                         (size_t)(heads - 1) * (size_t)t->sh + kD;

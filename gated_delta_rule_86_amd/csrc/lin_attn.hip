@@ -119,7 +119,7 @@ struct Walk {
     int64_t first, last;   // sequences to visit
     int64_t i;             // the current one
     int64_t p0, p1;        // its piece
-    int64_t c, nc;         // chunk of it, chunks
+    int64_t t, left, nc;   // first token of the current chunk, chunks of the piece after it, chunks of it
     int pflags;
     bool rev;
 
@@ -159,7 +159,8 @@ struct Walk {
                 last = a.N - 1;
         }
         i = rev ? last + 1 : first - 1;
-        c = nc = 0;
+        p0 = p1 = t = left = nc = 0;
+        pflags = 0;
     }
     __device__ int64_t seq_index() const { return cu ? i : row; }
     __device__ void set_piece()
@@ -177,26 +178,23 @@ struct Walk {
     __device__ Chunk next()
     {
         Chunk k;
-        ++c;
-        while (c >= nc) {
+        int first_one = 0;
+        --left;
+        t += rev ? -kLC : kLC;
+        while (left < 0) {  // the next piece with tokens
             i += rev ? -1 : 1;
-            if (rev ? i < first : i > last) {
-                nc = 0;
-                c = 0;
-                k.len = 0;
-                k.t0 = 0;
-                k.seq = 0;
-                k.flags = 0;
-                return k;
-            }
+            if (rev ? i < first : i > last)
+                break;
             set_piece();
-            c = 0;
+            left = nc - 1;
+            t = rev ? p0 + left * kLC : p0;
+            first_one = kPieceStart;
         }
-        const int64_t n = rev ? nc - 1 - c : c;
-        k.t0 = p0 + n * kLC;
-        k.len = (int)(p1 - k.t0 < kLC ? p1 - k.t0 : kLC);
+        const int64_t rest = p1 - t;
+        k.len = left < 0 ? 0 : (int)(rest < kLC ? rest : kLC);
+        k.flags = pflags | first_one | (left == 0 ? kPieceEnd : 0);
+        k.t0 = t;
         k.seq = seq_index();
-        k.flags = pflags | (c == 0 ? kPieceStart : 0) | (c == nc - 1 ? kPieceEnd : 0);
         return k;
     }
 };
@@ -311,25 +309,11 @@ __device__ __forceinline__ float state_dot(const State &S, const float *base, bo
     return d;
 }
 
-// S *= 2^l2.  The factor of slow decays is close to 1 and the same rounding of it in every
-// chunk would add up over a long sequence, so it is applied as S + S (2^l2 - 1).
-__device__ __forceinline__ void state_decay(State &S, float l2)
+__device__ __forceinline__ void state_scale(State &S, float f)
 {
-    if (l2 > -0.5f) {
-        const float f = expm1f(l2 * 0.6931471805599453f);
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                S.t[kt][r] = fmaf(S.t[kt][r], f, S.t[kt][r]);
-    } else {
-        const float f = __builtin_amdgcn_exp2f(l2);
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                S.t[kt][r] *= f;
-    }
+    for (int n = 0; n < 64; ++n)
+        S.t[n >> 4][n & 15] *= f;
 }
 
 // ------------------------------------------------------------------------------- LDS
@@ -338,8 +322,16 @@ struct Decays {           // of one chunk, natural order of tokens
     float bh[kLC], bl[kLC];  // running sum of log2 decays, as a pair
     float wout[kLC];         // factor of the state's share of an output row
     float win[kLC];          // factor of a source row on its way into the state
-    float last, pad[3];      // sum over the chunk, log2
+    double last;             // sum over the chunk, log2
+    double held;             // log2 of the factor that the registers' state lacks after the chunk
+    float mul;               // factor to put into the registers' state now; 1: none
+    float pad[3];
 };
+
+// The state in registers lacks a common factor 2^held, -16 < held <= 0: decays gather there and reach the 64 registers
+// when they come to 2^-16 or less.  Slow decays would otherwise round the state in every chunk, by the same
+// factor each time, and drift.  Rows go in with 2^-held and come out with 2^held.
+constexpr double kMostHeld = -16.0;
 
 constexpr int kTile = kLC * 256;
 constexpr int kPRow = 128;  // bytes per row of the 64 x 64 weight matrix
@@ -360,59 +352,84 @@ struct LdsStates {
     Decays d[2];
 };
 
-// One wave: lane = token.
-__device__ __forceinline__ void make_decays(Decays &d, float g, int len, int lane, bool rev, float scale)
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp_f64(double x)  // 0 where the pattern has no source lane
 {
-    double b = lane < len ? (double)clamp_decay(g) * kLog2e64 : 0.0;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double u = __shfl_up(b, o);
-        if (lane >= o)
-            b += u;
-    }
-    const double last = __shfl(b, 63);
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRows, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRows, 0xf, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// One wave: lane = token.
+// `held` as it stands before the chunk, and after it
+__device__ __forceinline__ void make_decays(Decays &d, double &held, float g, const Chunk &c, int lane, bool rev, float scale)
+{
+    if (c.flags & kPieceStart)
+        held = 0.0;
+    double b = lane < c.len ? (double)clamp_decay(g) * kLog2e64 : 0.0;
+    // inclusive sum: shifts by 1, 2, 4, 8 inside each 16 lanes, then the last lane of row 0 and 2 to the next
+    // row, then lane 31 to the upper half
+    b += dpp_f64<0x111, 0xf>(b);
+    b += dpp_f64<0x112, 0xf>(b);
+    b += dpp_f64<0x114, 0xf>(b);
+    b += dpp_f64<0x118, 0xf>(b);
+    b += dpp_f64<0x142, 0xa>(b);
+    b += dpp_f64<0x143, 0xc>(b);
+    const uint64_t u = __builtin_bit_cast(uint64_t, b);
+    const double last = __builtin_bit_cast(
+        double, ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63) << 32) |
+                    (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63));
+    const double after = held + last;
+    const bool apply = !(after > kMostHeld);  // also for NaN
     const float bh = (float)b;
     d.bh[lane] = bh;
     d.bl[lane] = (float)(b - (double)bh);
-    const float head = __builtin_amdgcn_exp2f(bh), tail = __builtin_amdgcn_exp2f((float)(last - b));
-    d.wout[lane] = rev ? tail : scale * head;
-    d.win[lane] = rev ? scale * head : tail;
-    if (lane == 0)
-        d.last = (float)last;
+    const double head = b, tail = last - b, in = apply ? 0.0 : after;
+    d.wout[lane] = (rev ? 1.0f : scale) * __builtin_amdgcn_exp2f((float)((rev ? tail : head) + held));
+    d.win[lane] = (rev ? scale : 1.0f) * __builtin_amdgcn_exp2f((float)((rev ? head : tail) - in));
+    if (lane == 0) {
+        d.last = last;
+        d.held = in;
+        d.mul = apply ? __builtin_amdgcn_exp2f((float)after) : 1.0f;
+    }
+    held = in;
 }
 
-__device__ __forceinline__ float load_decay(const LinArgs &a, int64_t row, int64_t h, const Chunk &c, int lane)
+// The decay of token `lane` of the chunk; p: this workgroup's row and head
+__device__ __forceinline__ float load_decay(const LinArgs &a, const float *p, const Chunk &c, int lane)
 {
-    if (!a.per_token)
-        return a.decay[h];
     const int t = lane < c.len ? lane : c.len - 1;
-    return a.decay[(row * a.T + c.t0 + t) * a.H + h];
+    return a.per_token ? p[c.t0 * a.H + (int64_t)(uint32_t)(t * (int)a.H)] : *p;
+}
+__device__ __forceinline__ const float *decay_of(const LinArgs &a, int64_t row, int64_t h)
+{
+    return a.decay + (a.per_token ? row * a.T * a.H : 0) + h;
 }
 
 // One input of the walk: this workgroup's row and head.
 struct TileSrc {
     const uint16_t *p;
-    int64_t st;
+    uint32_t st;  // elements from token to token, below 2^24
 };
 __device__ __forceinline__ TileSrc tile_src(const LinTensor &x, int64_t row, int64_t h)
 {
     // heads are shared by small whole numbers: 32-bit division
-    return TileSrc{x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh, x.st};
+    return TileSrc{x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh, (uint32_t)x.st};
 }
 struct TileLoad {
     u32x4 r[4];
 };
-// 64 rows of 256 bytes; rows behind the chunk read as zeros (beyond the descriptor)
+// 64 rows of 256 bytes; rows behind the chunk lie beyond the descriptor (the token stride is at least
+// a row, see lin_api.cpp) and read as zeros
 __device__ __forceinline__ void tile_fetch(TileLoad &f, const TileSrc &x, const Chunk &c, int tid)
 {
-    const uint32_t stride = (uint32_t)(x.st * 2);
+    const uint32_t stride = x.st * 2;
     const __amdgpu_buffer_rsrc_t r = rsrc(x.p + c.t0 * x.st, (uint32_t)(c.len - 1) * stride + 256u);
-    const int tok = tid >> 4;
-    const uint32_t off = (uint32_t)tok * stride + (uint32_t)(tid & 15) * 16u;
+    const uint32_t off = (uint32_t)(tid >> 4) * stride + (uint32_t)(tid & 15) * 16u;
 #pragma unroll
     for (int n = 0; n < 4; ++n)
-        // the token decides, not the offset alone: rows may be closer than 256 bytes (a stride of 0)
-        f.r[n] = buf_b128(r, tok + 16 * n < c.len ? off + (uint32_t)n * 16u * stride : 0xffffff00u);
+        f.r[n] = buf_b128(r, off + (uint32_t)n * 16u * stride);
 }
 
 // This lane's places in the LDS tiles, as byte offsets.  The XOR of tile_at() reaches the three low bits of a
@@ -469,48 +486,100 @@ __device__ __forceinline__ u32x4 key_frag(const unsigned char *tile, const Lanes
     return u32x4{x[0], x[1], y[0], y[1]};
 }
 
-// cut 8 floats into bf16 terms
+// Cutting floats into bf16 terms: what a rounded pair leaves of each, x - hi(x), as one dot product
+// (hi0, hi1).(-1, 0) + x, exact.  The two constants live in registers: as an instruction's constant the compiler
+// puts both into the same half.
+struct Cutter {
+    uint32_t neg0, neg1;
+
+    __device__ Cutter() : neg0(0x0000bf80u), neg1(0xbf800000u) { __asm__ volatile("" : "+v"(neg0), "+v"(neg1)); }
+    __device__ float rest0(uint32_t pair, float x) const
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, neg0), x,
+                                               false);
+    }
+    __device__ float rest1(uint32_t pair, float x) const
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, neg1), x,
+                                               false);
+    }
+};
 struct Terms3 {
     u32x4 h, m, l;
 };
-__device__ __forceinline__ void cut3(const float *x, Terms3 &t)
+__device__ __forceinline__ void cut3(const float *x, Terms3 &t, const Cutter &cut)
 {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float a = x[2 * e], b = x[2 * e + 1];
-        t.h[e] = pack2(a, b);
-        const float a1 = a - lo_f(t.h[e]), b1 = b - hi_f(t.h[e]);
+        t.h[e] = pack2(x[2 * e], x[2 * e + 1]);
+        const float a1 = cut.rest0(t.h[e], x[2 * e]), b1 = cut.rest1(t.h[e], x[2 * e + 1]);
         t.m[e] = pack2(a1, b1);
-        t.l[e] = pack2(a1 - lo_f(t.m[e]), b1 - hi_f(t.m[e]));
+        t.l[e] = pack2(cut.rest0(t.m[e], a1), cut.rest1(t.m[e], b1));
     }
 }
 
 // S += sum over the chunk's tokens of (win v) k^T.  Source rows are weighted on the way in,
 // in fp32, and go into the product as three bf16 terms (24 bits), so that an fp32 state keeps
 // fp32's accuracy.
-__device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const Decays &d,
-                                             const Lanes &ln, int half)
+//
+// Steps of 16 tokens, in a pipeline by hand: while a step's 12 matrix instructions run, the next step's K
+// operand is on its way from LDS and its weighted rows are cut.
+__device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const Decays &d, int tok, const Cutter &cut)
+{
+    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.win[tok]);
+    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.win[tok + 4]);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = lo_f(v[e]) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
+        x[2 * e + 1] = hi_f(v[e]) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
+    }
+    cut3(x, t, cut);
+}
+
+// The scheduler keeps the order of these groups: n x { 1 matrix instruction, v vector instructions }.
+template <int kN, int kV>
+__device__ __forceinline__ void interleave()
 {
 #pragma unroll
+    for (int x = 0; x < kN; ++x) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, kV, 0);
+    }
+}
+
+__device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const Decays &d,
+                                             const Lanes &ln, int half, const Cutter &cut)
+{
+    u32x4 kf[2][4];
+    Terms3 t[2];
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+        kf[0][kt] = key_frag(ktile, ln, kt, 0);
+    weighted_terms(t[0], vf[0], d, 8 * half, cut);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int tok = 16 * j + 8 * half;
-        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.win[tok]);
-        const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.win[tok + 4]);
-        float x[8];
+        const int c = j & 1;
+        if (j < 3) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = lo_f(vf[j][e]) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
-            x[2 * e + 1] = hi_f(vf[j][e]) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
+            for (int kt = 0; kt < 4; ++kt)
+                kf[c ^ 1][kt] = key_frag(ktile, ln, kt, j + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            weighted_terms(t[c ^ 1], vf[j + 1], d, 16 * (j + 1) + 8 * half, cut);
         }
-        Terms3 t;
-        cut3(x, t);
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            const u32x4 kf = key_frag(ktile, ln, kt, j);
-            S.t[kt] = mfma(kf, t.l, S.t[kt]);
-            S.t[kt] = mfma(kf, t.m, S.t[kt]);
-            S.t[kt] = mfma(kf, t.h, S.t[kt]);
-        }
+        for (int kt = 0; kt < 4; ++kt)
+            S.t[kt] = mfma(kf[c][kt], t[c].l, S.t[kt]);
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+            S.t[kt] = mfma(kf[c][kt], t[c].m, S.t[kt]);
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+            S.t[kt] = mfma(kf[c][kt], t[c].h, S.t[kt]);
+        if (j < 3)
+            interleave<12, 5>();
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -569,23 +638,27 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
     const bool whole = !(c.flags & kFromSlot);
     state_load(S, whole ? matrix_of(ro.init, c.seq * a.H + h, kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1)) : nullptr,
                ro.init_dt, ro.transposed != 0, wave, lane);
-    double sum = 0.0;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): here, or the compiler waits in every chunk
+    double sum = 0.0, held_now = 0.0;
     TileLoad fk, fv;
     const TileSrc sk = tile_src(ro.k, row, h), sv = tile_src(ro.v, row, h);
     tile_fetch(fk, sk, c, tid);
     tile_fetch(fv, sv, c, tid);
-    float g = load_decay(a, row, h, c, lane);
+    const float *dp = decay_of(a, row, h);
+    float g = load_decay(a, dp, c, lane);
+    double held = 0.0;
     int buf = 0;
     const int half = lane >> 5;
     const Lanes ln(tid);
+    const Cutter cut;
     if (wave == 3)
-        make_decays(lds.d[0], g, c.len, lane, rev, a.scale);
+        make_decays(lds.d[0], held, g, c, lane, rev, a.scale);
     while (c.len > 0) {
         tile_put(fk, lds.k, ln);
         tile_put(fv, lds.v, ln);
         const Chunk n = w.next();
         if (n.len > 0) {
-            g = load_decay(a, row, h, n, lane);
+            g = load_decay(a, dp, n, lane);
             tile_fetch(fk, sk, n, tid);
             tile_fetch(fv, sv, n, tid);
         }
@@ -595,15 +668,18 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v, ln, jj);
-        state_decay(S, d.last);
-        sum += (double)d.last;
-        state_update(S, lds.k, vf, d, ln, half);
+        if (d.mul != 1.0f)
+            state_scale(S, d.mul);
+        sum += d.last;
+        held_now = d.held;
+        state_update(S, lds.k, vf, d, ln, half, cut);
         if (wave == 3 && n.len > 0)
-            make_decays(lds.d[buf ^ 1], g, n.len, lane, rev, a.scale);
+            make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
         lds_barrier();
         c = n;
         buf ^= 1;
     }
+    state_scale(S, __builtin_amdgcn_exp2f((float)held_now));
     state_store(S, ro.slots + (size_t)slot * kD * kD, kFp32, ro.transposed != 0, wave, lane);
     if (tid == 0)
         *lam = whole ? -1.0f : __builtin_amdgcn_exp2f((float)sum);
@@ -655,6 +731,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, l32 = lane & 31;
     const Lanes ln(tid);
+    const Cutter cut;
     const size_t init_bytes = kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1);
     const size_t fin_bytes = kLinStateBytes / (ro.fin_dt == kBf16 ? 2 : 1);
     State S;
@@ -690,9 +767,11 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
     tile_fetch(fq, sq, c, tid);
     tile_fetch(fk, sk, c, tid);
     tile_fetch(fv, sv, c, tid);
-    float g = load_decay(a, row, h, c, lane);
+    const float *dp = decay_of(a, row, h);
+    float g = load_decay(a, dp, c, lane);
+    double held = 0.0;
     if (wave == 3)
-        make_decays(lds.d[0], g, c.len, lane, rev, a.scale);
+        make_decays(lds.d[0], held, g, c, lane, rev, a.scale);
     int buf = 0;
     while (c.len > 0) {
         tile_put(fq, lds.q, ln);
@@ -700,7 +779,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         tile_put(fv, lds.v, ln);
         const Chunk n = w.next();
         if (n.len > 0) {
-            g = load_decay(a, row, h, n, lane);
+            g = load_decay(a, dp, n, lane);
             tile_fetch(fq, sq, n, tid);
             tile_fetch(fk, sk, n, tid);
             tile_fetch(fv, sv, n, tid);
@@ -711,34 +790,47 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                        slot ? matrix_of(ro.slots, (seg + (rev ? 1 : -1)) * a.H + h, kLinStateBytes)
                             : matrix_of(ro.init, c.seq * a.H + h, init_bytes),
                        slot ? (int)kFp32 : ro.init_dt, tr, wave, lane);
+            // here, or the compiler waits in every chunk, for the rows on their way too
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         }
         lds_barrier();
         const Decays &d = lds.d[buf];
 
-        // weights of one 32 x 32 block (sources sb, outputs ob) per wave 0..2, bf16 hi + lo
-        if (wave < 3) {
-            const int sb = wave == 0 ? 0 : (wave == 2 ? 1 : (rev ? 1 : 0));
-            const int ob = wave == 0 ? 0 : (wave == 2 ? 1 : (rev ? 0 : 1));
+        // The weights of one 32 x 32 block (sources sb, outputs ob) per wave, bf16 hi + lo (wave 3's block lies beyond
+        // the diagonal: zeros, never read), and the state's share of the outputs, O^T[v][t], the state in bf16
+        // hi + lo.  In steps of 16 channels: a step's products with the state run while the next 16 channels of the
+        // state are cut and every other step makes 4 of the lane's 16 weights.
+        f32x16 O[2];
+        {
+            const int sb = wave == 0 ? 0 : wave == 2 ? 1 : (wave == 1) == rev ? 1 : 0;
+            const int ob = wave == 0 ? 0 : wave == 2 ? 1 : (wave == 1) == rev ? 0 : 1;
             f32x16 p;
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                p[r] = 0.0f;
+                p[r] = O[0][r] = O[1][r] = 0.0f;
+            {
+                u32x4 kr[8], qr[8];
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj)
-                p = mfma(row_frag(lds.k, ln, sb, jj), row_frag(lds.q, ln, ob, jj), p);
+                for (int jj = 0; jj < 8; ++jj) {
+                    kr[jj] = row_frag(lds.k, ln, sb, jj);
+                    qr[jj] = row_frag(lds.q, ln, ob, jj);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj)
+                    p = mfma(kr[jj], qr[jj], p);
+            }
             int to = 32 * ob + l32;
             __asm__ volatile("" : "+v"(to));  // keep the comparisons below in the loop: 16 masks would not stay in SGPRs
             const float bho = d.bh[to], blo = d.bl[to];
-#pragma unroll
-            for (int a4 = 0; a4 < 4; ++a4) {
+            auto weights = [&](int a4) {
                 const int s = 32 * sb + 8 * a4 + 4 * half;
                 const f32x4 bhs = *reinterpret_cast<const f32x4 *>(&d.bh[s]);
                 const f32x4 bls = *reinterpret_cast<const f32x4 *>(&d.bl[s]);
                 float x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float df = (bho - bhs[e]) + (blo - bls[e]);
-                    df = rev ? -df : df;
+                    const float df = rev ? (bhs[e] - bho) + (bls[e] - blo) : (bho - bhs[e]) + (blo - bls[e]);
                     const bool on = rev ? s + e >= to : s + e <= to;  // a token behind the row's (before it) weighs nothing
                     x[e] = on ? p[4 * a4 + e] * (a.scale * __builtin_amdgcn_exp2f(df)) : 0.0f;
                     if (dots && s + e == to) {
@@ -747,38 +839,55 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                     }
                 }
                 const u32x2 hi = {pack2(x[0], x[1]), pack2(x[2], x[3])};
-                const float y[4] = {x[0] - lo_f(hi[0]), x[1] - hi_f(hi[0]), x[2] - lo_f(hi[1]), x[3] - hi_f(hi[1])};
+                const float y[4] = {cut.rest0(hi[0], x[0]), cut.rest1(hi[0], x[1]), cut.rest0(hi[1], x[2]),
+                                    cut.rest1(hi[1], x[3])};
                 const u32x2 lo = {pack2(y[0], y[1]), pack2(y[2], y[3])};
                 const int off = to * kPRow + (((4 * sb + a4) ^ (to & 7)) << 4) + 8 * half;
                 *reinterpret_cast<u32x2 *>(lds.p[0] + off) = hi;
                 *reinterpret_cast<u32x2 *>(lds.p[1] + off) = lo;
                 if (kDots)
                     *reinterpret_cast<u32x2 *>(ldx.p3 + off) =
-                        u32x2{pack2(y[0] - lo_f(lo[0]), y[1] - hi_f(lo[0])), pack2(y[2] - lo_f(lo[1]), y[3] - hi_f(lo[1]))};
-            }
-        }
-        // the state's share of the outputs: O^T[v][t], the state in bf16 hi + lo
-        f32x16 O[2];
+                        u32x2{pack2(cut.rest0(lo[0], y[0]), cut.rest1(lo[0], y[1])),
+                              pack2(cut.rest0(lo[1], y[2]), cut.rest1(lo[1], y[3]))};
+            };
+            u32x4 qf[2][2];
+            Terms3 sc[2];
+            auto cut_state = [&](int jj) {
+                float x[8];
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
+                for (int e = 0; e < 8; ++e)
+                    x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
+                cut3(x, sc[jj & 1], cut);
+            };
+            qf[0][0] = row_frag(lds.q, ln, 0, 0);
+            qf[0][1] = row_frag(lds.q, ln, 1, 0);
+            cut_state(0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                O[tt][r] = 0.0f;
+            for (int jj = 0; jj < 8; ++jj) {
+                const int b = jj & 1;
+                if (jj < 7) {
+                    qf[b ^ 1][0] = row_frag(lds.q, ln, 0, jj + 1);
+                    qf[b ^ 1][1] = row_frag(lds.q, ln, 1, jj + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    cut_state(jj + 1);
+                }
+                if (jj & 1)
+                    weights(jj >> 1);
 #pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            float x[8];
+                for (int tt = 0; tt < 2 && kDots; ++tt)
+                    O[tt] = mfma(sc[b].l, qf[b][tt], O[tt]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
-            Terms3 s;
-            cut3(x, s);
+                for (int tt = 0; tt < 2; ++tt)
+                    O[tt] = mfma(sc[b].m, qf[b][tt], O[tt]);
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const u32x4 qf = row_frag(lds.q, ln, tt, jj);
-                if (kDots)
-                    O[tt] = mfma(s.l, qf, O[tt]);
-                O[tt] = mfma(s.m, qf, O[tt]);
-                O[tt] = mfma(s.h, qf, O[tt]);
+                for (int tt = 0; tt < 2; ++tt)
+                    O[tt] = mfma(sc[b].h, qf[b][tt], O[tt]);
+                if (jj & 1)
+                    interleave<kDots ? 6 : 4, 16>();
+                else
+                    interleave<kDots ? 6 : 4, 4>();
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
@@ -793,36 +902,39 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v, ln, jj);
         lds_barrier();  // the weights are there
+        {
+            // weight operands: of each 16 sources the diagonal block's, and the block beside it for half of them
+            constexpr int kBeside = rev ? 0 : 1;  // output block that sees all sources
+            u32x4 wh[6], wl[6];
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-            // a diagonal block of 32 tokens, and the block beside it: output block 1 forwards, 0 backwards
-            const int tt = jj >> 1;
-            auto add = [&](f32x16 &o, int block) {
+            for (int x = 0; x < 6; ++x) {
+                const int jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
                 const int off = ln.w[jj] + 32 * kPRow * block;
+                wl[x] = lds_b128(lds.p[1] + off);
+                wh[x] = lds_b128(lds.p[0] + off);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < 6; ++x) {
+                const int jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
                 if (kDots)
-                    o = mfma(vf[jj], lds_b128(ldx.p3 + off), o);
-                o = mfma(vf[jj], lds_b128(lds.p[1] + off), o);
-                o = mfma(vf[jj], lds_b128(lds.p[0] + off), o);
-            };
-            add(O[tt], tt);
-            if (tt == 0) {
-                if (!rev)
-                    add(O[1], 1);
-            } else if (rev) {
-                add(O[0], 0);
+                    O[block] = mfma(vf[jj], lds_b128(ldx.p3 + ln.w[jj] + 32 * kPRow * block), O[block]);
+                O[block] = mfma(vf[jj], wl[x], O[block]);
+                O[block] = mfma(vf[jj], wh[x], O[block]);
             }
         }
 
         // rows out; those behind the chunk lie beyond the descriptor
         {
-            const uint32_t size = ro.out_f32 ? 4 : 2, stride = (uint32_t)a.H * (kD * size);
+            const bool out_f32 = ro.out_f32 != 0;
+            const uint32_t size = out_f32 ? 4 : 2, stride = (uint32_t)a.H * (kD * size);
             const __amdgpu_buffer_rsrc_t ra =
                 rsrc(static_cast<unsigned char *>(ro.out) +
                          ((size_t)(row * a.T + c.t0) * (size_t)a.H + (size_t)h) * (kD * size),
                      (uint32_t)(c.len - 1) * stride + kD * size);
-            const uint32_t xs = dots ? (uint32_t)sx.st * 2 : 0;
+            const uint32_t xs = dots ? sx.st * 2 : 0;
             const __amdgpu_buffer_rsrc_t rx =
-                rsrc(sx.p + c.t0 * sx.st, dots ? (uint32_t)(c.len - 1) * xs + 256u : 0u);
+                rsrc(dots ? sx.p + c.t0 * sx.st : nullptr, dots ? (uint32_t)(c.len - 1) * xs + 256u : 0u);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 const int t = 32 * tt + l32;
@@ -835,7 +947,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                     if (dots) {
                         const u32x2 xr = __builtin_bit_cast(
                             u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                                       rx, t < c.len ? (uint32_t)t * xs + (32 * wave + 4 * half + 8 * a4) * 2 : 0xffffff00u,
+                                       rx, (uint32_t)t * xs + (32 * wave + 4 * half + 8 * a4) * 2,
                                        0, 0));
                         dot += (lo_f(xr[0]) * y[0] + hi_f(xr[0]) * y[1]) + (lo_f(xr[1]) * y[2] + hi_f(xr[1]) * y[3]);
                         const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(t, 4 * wave + a4) + 8 * half);
@@ -844,10 +956,24 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                         y[2] = fmaf(own, lo_f(vr[1]), y[2]);
                         y[3] = fmaf(own, hi_f(vr[1]), y[3]);
                     }
-                    if (ro.out_f32) {
+                    if (dots) {
+                        O[tt][4 * a4] = y[0];
+                        O[tt][4 * a4 + 1] = y[1];
+                        O[tt][4 * a4 + 2] = y[2];
+                        O[tt][4 * a4 + 3] = y[3];
+                    }
+                }
+                if (out_f32) {
+#pragma unroll
+                    for (int a4 = 0; a4 < 4; ++a4) {
+                        const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra, o + 32 * a4, 0, 0);
-                    } else {
-                        const u32x2 z = {pack2(y[0], y[1]), pack2(y[2], y[3])};
+                    }
+                } else {
+#pragma unroll
+                    for (int a4 = 0; a4 < 4; ++a4) {
+                        const u32x2 z = {pack2(O[tt][4 * a4], O[tt][4 * a4 + 1]),
+                                         pack2(O[tt][4 * a4 + 2], O[tt][4 * a4 + 3])};
                         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, z), ra, o + 16 * a4, 0, 0);
                     }
                 }
@@ -858,15 +984,18 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 }
             }
         }
-        state_decay(S, d.last);
-        state_update(S, lds.k, vf, d, ln, half);
+        if (d.mul != 1.0f)
+            state_scale(S, d.mul);
+        state_update(S, lds.k, vf, d, ln, half, cut);
+        const double held_now = d.held;
         if (wave == 3 && n.len > 0)
-            make_decays(lds.d[buf ^ 1], g, n.len, lane, rev, a.scale);
+            make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
         lds_barrier();  // every read of this chunk's tiles is done
         if (dots && tid < c.len)
             ro.dots[(row * a.T + c.t0 + tid) * a.H + h] =
                 (ldx.red[0][tid] + ldx.red[1][tid]) + (ldx.red[2][tid] + ldx.red[3][tid]);
-        if ((c.flags & kPieceEnd) && (c.flags & kToFinal)) {
+        if ((c.flags & kPieceEnd) && (c.flags & kToFinal) && (ro.fin || (kDots && ro.xfin))) {
+            state_scale(S, __builtin_amdgcn_exp2f((float)held_now));
             if (ro.fin && ro.defer && (c.flags & kFromSlot))
                 state_store(S, ro.slots + (size_t)((seg - 1) * a.H + h) * kD * kD, kFp32, tr, wave, lane);
             else if (ro.fin)

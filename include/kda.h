@@ -323,7 +323,8 @@ size_t kda_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int ha
  *             (kda_fwd_device_status reads the status word of this workspace too).
  *   strides_host  NULL (q, k, v contiguous), or host int64 [9]: batch, token and head strides of
  *             q, k, v in elements; the 128 channels of a head are contiguous.  Each a
- *             multiple of 8, the token stride at most 2^24 (views of one fused projection).
+ *             multiple of 8, the token stride 128 .. 2^24 (views of one fused projection; batch and
+ *             head strides may be 0).
  * fp32 states keep fp32 accuracy (24-bit products, fp32 sums); out is rounded once.  A value that
  * is not finite reaches its own sequence and head alone, from the first token of its chunk
  * of 64 tokens on (of the workgroup's run of tokens, see kda_lin_fwd_workspace_size).

@@ -53,7 +53,8 @@ LIN_ERRORS = [
     (12, dict(per_token=2)),
     (14, dict(H=3)), (14, dict(Hk=0)), (14, dict(Hk=8)),
     (15, dict(strides=[8, 4, 128] * 3)), (15, dict(strides=[0, -8, 128] * 3)), (15, dict(strides=[0, 1 << 25, 128] * 3)),
-    (15, dict(strides=[0, 256, 128, 0, 256, 128, 0, 512, 100])),
+    (15, dict(strides=[0, 256, 128, 0, 256, 128, 0, 512, 100])), (15, dict(strides=[0, 0, 0] * 3)),
+    (15, dict(strides=[0, 120, 128] * 3)),
     (9, dict(B=1, cu=ptr(8), N=2, cu_host=[0, 50, 99])), (9, dict(B=1, cu=ptr(8), N=2, cu_host=[1, 50, 100])),
     (9, dict(B=1, cu=ptr(8), N=2, cu_host=[0, 101, 100])),
 ]
