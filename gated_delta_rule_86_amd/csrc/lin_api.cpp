@@ -58,7 +58,7 @@ bool make_layout(const Sizes &z, bool bwd, bool ddecay, kda::LinLayout *L)
     using kda::kAlign;
     L->plan = kda::lin_plan(z.B, z.T, z.H, z.N, z.varlen, kda::kLinGroups, ddecay ? kda::kLinGradSeg : 0);
     const kda::LinPlan &p = L->plan;
-    if (p.rows * p.P > (((int64_t)1 << 31) - 64) / (16 * z.H))  // grid sizes
+    if (p.rows * p.P > (((int64_t)1 << 31) - 64) / (64 * z.H))  // grid sizes
         return false;
     size_t off = kAlign;  // status word
     auto take = [&](size_t bytes) {

@@ -322,10 +322,9 @@ struct Decays {           // of one chunk, natural order of tokens
     float bh[kLC], bl[kLC];  // running sum of log2 decays, as a pair
     float wout[kLC];         // factor of the state's share of an output row
     float win[kLC];          // factor of a source row on its way into the state
-    double last;             // sum over the chunk, log2
     double held;             // log2 of the factor that the registers' state lacks after the chunk
     float mul;               // factor to put into the registers' state now; 1: none
-    float pad[3];
+    float pad;
 };
 
 // The state in registers lacks a common factor 2^held, -16 < held <= 0: decays gather there and reach the 64 registers
@@ -348,8 +347,9 @@ struct LdsWalkDots {
     float own[kLC];                 // weights of the tokens' own pairs
 };
 struct LdsStates {
-    unsigned char k[kTile], v[kTile];
-    Decays d[2];
+    unsigned char k[2][kTile], v[2][kTile];
+    float win[2][kLC];
+    double after[2];  // log2 of the factor between the chunk's far end and the segment's boundary
 };
 
 template <int kCtrl, int kRows>
@@ -361,13 +361,10 @@ __device__ __forceinline__ double dpp_f64(double x)  // 0 where the pattern has 
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// One wave: lane = token.
-// `held` as it stands before the chunk, and after it
-__device__ __forceinline__ void make_decays(Decays &d, double &held, float g, const Chunk &c, int lane, bool rev, float scale)
+// Running sum of the chunk's log2 decays (lane = token), and their sum.
+__device__ __forceinline__ void decay_sums(float g, int len, int lane, double &b, double &last)
 {
-    if (c.flags & kPieceStart)
-        held = 0.0;
-    double b = lane < c.len ? (double)clamp_decay(g) * kLog2e64 : 0.0;
+    b = lane < len ? (double)clamp_decay(g) * kLog2e64 : 0.0;
     // inclusive sum: shifts by 1, 2, 4, 8 inside each 16 lanes, then the last lane of row 0 and 2 to the next
     // row, then lane 31 to the upper half
     b += dpp_f64<0x111, 0xf>(b);
@@ -377,9 +374,18 @@ __device__ __forceinline__ void make_decays(Decays &d, double &held, float g, co
     b += dpp_f64<0x142, 0xa>(b);
     b += dpp_f64<0x143, 0xc>(b);
     const uint64_t u = __builtin_bit_cast(uint64_t, b);
-    const double last = __builtin_bit_cast(
+    last = __builtin_bit_cast(
         double, ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63) << 32) |
                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63));
+}
+
+// `held` as it stands before the chunk, and after it
+__device__ __forceinline__ void make_decays(Decays &d, double &held, float g, const Chunk &c, int lane, bool rev, float scale)
+{
+    if (c.flags & kPieceStart)
+        held = 0.0;
+    double b, last;
+    decay_sums(g, c.len, lane, b, last);
     const double after = held + last;
     const bool apply = !(after > kMostHeld);  // also for NaN
     const float bh = (float)b;
@@ -389,7 +395,6 @@ __device__ __forceinline__ void make_decays(Decays &d, double &held, float g, co
     d.wout[lane] = (rev ? 1.0f : scale) * __builtin_amdgcn_exp2f((float)((rev ? tail : head) + held));
     d.win[lane] = (rev ? scale : 1.0f) * __builtin_amdgcn_exp2f((float)((rev ? head : tail) - in));
     if (lane == 0) {
-        d.last = last;
         d.held = in;
         d.mul = apply ? __builtin_amdgcn_exp2f((float)after) : 1.0f;
     }
@@ -524,10 +529,10 @@ __device__ __forceinline__ void cut3(const float *x, Terms3 &t, const Cutter &cu
 //
 // Steps of 16 tokens, in a pipeline by hand: while a step's 12 matrix instructions run, the next step's K
 // operand is on its way from LDS and its weighted rows are cut.
-__device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const Decays &d, int tok, const Cutter &cut)
+__device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const float *win, int tok, const Cutter &cut)
 {
-    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.win[tok]);
-    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&d.win[tok + 4]);
+    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&win[tok]);
+    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&win[tok + 4]);
     float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -548,7 +553,7 @@ __device__ __forceinline__ void interleave()
     }
 }
 
-__device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const Decays &d,
+__device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const float *win,
                                              const Lanes &ln, int half, const Cutter &cut)
 {
     u32x4 kf[2][4];
@@ -556,7 +561,7 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
         kf[0][kt] = key_frag(ktile, ln, kt, 0);
-    weighted_terms(t[0], vf[0], d, 8 * half, cut);
+    weighted_terms(t[0], vf[0], win, 8 * half, cut);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -566,7 +571,7 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
             for (int kt = 0; kt < 4; ++kt)
                 kf[c ^ 1][kt] = key_frag(ktile, ln, kt, j + 1);
             __builtin_amdgcn_sched_barrier(0);
-            weighted_terms(t[c ^ 1], vf[j + 1], d, 16 * (j + 1) + 8 * half, cut);
+            weighted_terms(t[c ^ 1], vf[j + 1], win, 16 * (j + 1) + 8 * half, cut);
         }
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -599,9 +604,17 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 // goes on behind the segment, the first one of a reverse walk if it began before it.  lam:
 // the factor on the state at the segment's other boundary, or -1 when the share is the whole
 // state (the sequence starts inside), -2 when there is none.
+//
+// The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
+// so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
+// add nothing and are not read.  Bound by memory: 64 KiB of tiles in LDS twice, one barrier a chunk; reads
+// of 32 KiB per chunk at T = 262144, H = 8, slow decays: 4.4 TB/s.
+constexpr double kGone = -150.0;
+
 __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0, int lead1)
 {
-    __shared__ __attribute__((aligned(16))) LdsStates lds;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    LdsStates &lds = *reinterpret_cast<LdsStates *>(lds_raw);
     const int64_t total = a.rows * a.P * a.H;
     const int64_t at = xcd_order(blockIdx.x, total);
     if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
@@ -609,109 +622,138 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
     const int64_t seg = at / a.H, h = at - seg * a.H;
     const int64_t row = seg / a.P, j = seg - row * a.P;
     const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
-    const bool rev = ro.rev != 0;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool rev = ro.rev != 0, tr = ro.transposed != 0;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
     const int64_t slot = seg * a.H + h;
     float *lam = ro.lam + slot;
     const bool edge = rev ? j == 0 : j == a.P - 1;  // nothing beyond this boundary
-    if (edge || device_bad(a)) {
-        if (tid == 0)
-            *lam = -2.0f;
-        return;
-    }
     Walk w;
     w.init(a, row, j, rev);
-    // only the piece that crosses the boundary
-    if (rev)
-        w.i = w.first + 1;
-    else
-        w.i = w.last - 1;
-    w.first = rev ? w.first : w.last;
-    w.last = w.first;
-    Chunk c = w.next();
-    if (c.len == 0 || (c.flags & kToFinal)) {
+    w.i = rev ? w.first : w.last;
+    if (!edge && !device_bad(a))
+        w.set_piece();
+    const int64_t nc = w.nc;
+    if (nc == 0 || (w.pflags & kToFinal)) {
         if (tid == 0)
             *lam = -2.0f;
         return;
     }
-    State S;
-    const bool whole = !(c.flags & kFromSlot);
-    state_load(S, whole ? matrix_of(ro.init, c.seq * a.H + h, kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1)) : nullptr,
-               ro.init_dt, ro.transposed != 0, wave, lane);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): here, or the compiler waits in every chunk
-    double sum = 0.0, held_now = 0.0;
-    TileLoad fk, fv;
+    auto chunk = [&](int64_t n) {  // the n-th from the boundary
+        Chunk c;
+        const int64_t at_n = rev ? n : nc - 1 - n;
+        c.t0 = w.p0 + at_n * kLC;
+        const int64_t rest = w.p1 - c.t0;
+        c.len = (int)(rest < kLC ? rest : kLC);
+        c.seq = 0;
+        c.flags = 0;
+        return c;
+    };
     const TileSrc sk = tile_src(ro.k, row, h), sv = tile_src(ro.v, row, h);
-    tile_fetch(fk, sk, c, tid);
-    tile_fetch(fv, sv, c, tid);
     const float *dp = decay_of(a, row, h);
-    float g = load_decay(a, dp, c, lane);
-    double held = 0.0;
-    int buf = 0;
-    const int half = lane >> 5;
     const Lanes ln(tid);
     const Cutter cut;
+    State S;
+#pragma unroll
+    for (int n = 0; n < 64; ++n)
+        S.t[n >> 4][n & 15] = 0.0f;
+    TileLoad fk, fv;
+    Chunk c = chunk(0);
+    float g = load_decay(a, dp, c, lane);
+    tile_fetch(fk, sk, c, tid);
+    tile_fetch(fv, sv, c, tid);
+    double gone = 0.0;  // wave 3: log2 factor from the boundary to the next chunk's near end
+    auto sources = [&](int buf, float gn, int len) {
+        double b, last;
+        decay_sums(gn, len, lane, b, last);
+        lds.win[buf][lane] =
+            (rev ? a.scale : 1.0f) * __builtin_amdgcn_exp2f((float)((rev ? b : last - b) + gone));
+        gone += last;
+        if (lane == 0)
+            lds.after[buf] = gone;
+    };
     if (wave == 3)
-        make_decays(lds.d[0], held, g, c, lane, rev, a.scale);
-    while (c.len > 0) {
-        tile_put(fk, lds.k, ln);
-        tile_put(fv, lds.v, ln);
-        const Chunk n = w.next();
-        if (n.len > 0) {
-            g = load_decay(a, dp, n, lane);
-            tile_fetch(fk, sk, n, tid);
-            tile_fetch(fv, sv, n, tid);
-        }
+        sources(0, g, c.len);
+    if (nc > 1)
+        g = load_decay(a, dp, chunk(1), lane);
+    double after = 0.0;
+    for (int64_t n = 0;; ++n) {
+        const int buf = (int)(n & 1);
+        tile_put(fk, lds.k[buf], ln);
+        tile_put(fv, lds.v[buf], ln);
         lds_barrier();
-        const Decays &d = lds.d[buf];
+        after = lds.after[buf];
+        const bool more = n + 1 < nc && !(after < kGone);
+        Chunk next = c;
+        if (more) {
+            next = chunk(n + 1);
+            tile_fetch(fk, sk, next, tid);
+            tile_fetch(fv, sv, next, tid);
+        }
         u32x4 vf[4];
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
-            vf[jj] = col_frag(lds.v, ln, jj);
-        if (d.mul != 1.0f)
-            state_scale(S, d.mul);
-        sum += d.last;
-        held_now = d.held;
-        state_update(S, lds.k, vf, d, ln, half, cut);
-        if (wave == 3 && n.len > 0)
-            make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
-        lds_barrier();
-        c = n;
-        buf ^= 1;
+            vf[jj] = col_frag(lds.v[buf], ln, jj);
+        state_update(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
+        if (!more)
+            break;
+        if (wave == 3)
+            sources(buf ^ 1, g, next.len);
+        if (n + 2 < nc)
+            g = load_decay(a, dp, chunk(n + 2), lane);
+        c = next;
     }
-    state_scale(S, __builtin_amdgcn_exp2f((float)held_now));
-    state_store(S, ro.slots + (size_t)slot * kD * kD, kFp32, ro.transposed != 0, wave, lane);
+    const bool whole = !(w.pflags & kFromSlot);
+    const float f = after < kGone ? 0.0f : __builtin_amdgcn_exp2f((float)after);
+    if (whole && ro.init && f != 0.0f) {
+        State X;
+        state_load(X, matrix_of(ro.init, w.seq_index() * a.H + h, kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1)),
+                   ro.init_dt, tr, wave, lane);
+#pragma unroll
+        for (int n = 0; n < 64; ++n)
+            S.t[n >> 4][n & 15] = fmaf(f, X.t[n >> 4][n & 15], S.t[n >> 4][n & 15]);
+    }
+    state_store(S, ro.slots + (size_t)slot * kD * kD, kFp32, tr, wave, lane);
     if (tid == 0)
-        *lam = whole ? -1.0f : __builtin_amdgcn_exp2f((float)sum);
+        *lam = whole ? -1.0f : f;
 }
 
 // ---------------------------------------------------------------------------- scan
 //
 // slot_j <- share_j + lam_j * slot_{j-1} (forwards; backwards from the other end), so that slot
-// j is the state at the boundary behind (before) segment j.
+// j is the state at the boundary behind (before) segment j.  Two entries a thread; the loads of 8 segments are
+// on their way together.
+constexpr unsigned kScanParts = kD * kD / 512;  // workgroups per matrix
+
 __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int lead1)
 {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
     const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
-    constexpr unsigned kParts = kD * kD / 1024;  // workgroups per matrix
-    const int64_t rh = blockIdx.x / kParts, row = rh / a.H, h = rh - row * a.H;
-    const int e = ((blockIdx.x % kParts) * 256 + threadIdx.x) * 4;
-    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int64_t step = ro.rev ? -1 : 1;
-    int64_t j = ro.rev ? a.P - 1 : 0;
-    for (int64_t n = 0; n + 1 < a.P; ++n, j += step) {
-        const int64_t slot = (row * a.P + j) * a.H + h;
-        const float lam = ro.lam[slot];
-        if (lam == -2.0f)
-            continue;
-        f32x4 *p = reinterpret_cast<f32x4 *>(ro.slots + (size_t)slot * kD * kD + e);
-        f32x4 f = *p;
-        if (lam > 0.0f) {
+    const int64_t rh = blockIdx.x / kScanParts, row = rh / a.H, h = rh - row * a.H;
+    const int e = ((blockIdx.x % kScanParts) * 256 + threadIdx.x) * 2;
+    f32x2 s = {0.0f, 0.0f};
+    const int64_t last = a.P - 2;  // steps 0 .. P - 2
+    for (int64_t n = 0; n <= last; n += 8) {
+        f32x2 f[8];
+        float lam[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                f[x] = fmaf(lam, s[x], f[x]);
-            *p = f;
+        for (int x = 0; x < 8; ++x) {
+            const int64_t m = n + x <= last ? n + x : last;
+            const int64_t slot = (row * a.P + (ro.rev ? a.P - 1 - m : m)) * a.H + h;
+            lam[x] = ro.lam[slot];
+            f[x] = *reinterpret_cast<const f32x2 *>(ro.slots + (size_t)slot * kD * kD + e);
         }
-        s = f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            if (n + x > last || lam[x] == -2.0f)
+                continue;
+            if (lam[x] > 0.0f) {
+                const int64_t slot = (row * a.P + (ro.rev ? a.P - 1 - (n + x) : n + x)) * a.H + h;
+                f[x][0] = fmaf(lam[x], s[0], f[x][0]);
+                f[x][1] = fmaf(lam[x], s[1], f[x][1]);
+                *reinterpret_cast<f32x2 *>(ro.slots + (size_t)slot * kD * kD + e) = f[x];
+            }
+            s = f[x];
+        }
     }
 }
 
@@ -986,7 +1028,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         }
         if (d.mul != 1.0f)
             state_scale(S, d.mul);
-        state_update(S, lds.k, vf, d, ln, half, cut);
+        state_update(S, lds.k, vf, d.win, ln, half, cut);
         const double held_now = d.held;
         if (wave == 3 && n.len > 0)
             make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
@@ -1337,10 +1379,14 @@ hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n
     const unsigned grid = (unsigned)(8 * cdiv(total, 8));
     if (a.P > 1) {
         const int l0 = lead[0], l1 = lead[n_lead - 1];
-        hipLaunchKernelGGL(lin_states_kernel, dim3(grid, n_lead), dim3(256), 0, s, a, l0, l1);
-        hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)(kD * kD / 1024 * a.rows * a.H), n_lead), dim3(256), 0, s,
-                           a, l0, l1);
-        const hipError_t e = hipGetLastError();
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_states_kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LdsStates));
+        if (e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(lin_states_kernel, dim3(grid, n_lead), dim3(256), sizeof(LdsStates), s, a, l0, l1);
+        hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)(kScanParts * a.rows * a.H), n_lead), dim3(256), 0, s, a,
+                           l0, l1);
+        e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
