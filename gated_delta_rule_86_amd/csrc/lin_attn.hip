@@ -401,11 +401,13 @@ __device__ __forceinline__ void make_decays(Decays &d, double &held, float g, co
     held = in;
 }
 
-// The decay of token `lane` of the chunk; p: this workgroup's row and head
+// The decay of token `lane` of the chunk (0 behind it, and all 0 without a chunk); p: this workgroup's row and head
 __device__ __forceinline__ float load_decay(const LinArgs &a, const float *p, const Chunk &c, int lane)
 {
-    const int t = lane < c.len ? lane : c.len - 1;
-    return a.per_token ? p[c.t0 * a.H + (int64_t)(uint32_t)(t * (int)a.H)] : *p;
+    const uint32_t step = a.per_token ? (uint32_t)a.H * 4u : 0u;
+    const __amdgpu_buffer_rsrc_t r =
+        rsrc(p + (a.per_token ? c.t0 * a.H : 0), c.len > 0 ? (uint32_t)(c.len - 1) * step + 4u : 0u);
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (uint32_t)lane * step, 0, 0));
 }
 __device__ __forceinline__ const float *decay_of(const LinArgs &a, int64_t row, int64_t h)
 {
@@ -426,11 +428,12 @@ struct TileLoad {
     u32x4 r[4];
 };
 // 64 rows of 256 bytes; rows behind the chunk lie beyond the descriptor (the token stride is at least
-// a row, see lin_api.cpp) and read as zeros
+// a row, see lin_api.cpp) and read as zeros.  Without a chunk (len 0) nothing is read, by the same instructions: a
+// branch around them would make the compiler wait for all loads wherever older ones are used.
 __device__ __forceinline__ void tile_fetch(TileLoad &f, const TileSrc &x, const Chunk &c, int tid)
 {
     const uint32_t stride = x.st * 2;
-    const __amdgpu_buffer_rsrc_t r = rsrc(x.p + c.t0 * x.st, (uint32_t)(c.len - 1) * stride + 256u);
+    const __amdgpu_buffer_rsrc_t r = rsrc(x.p + c.t0 * x.st, c.len > 0 ? (uint32_t)(c.len - 1) * stride + 256u : 0u);
     const uint32_t off = (uint32_t)(tid >> 4) * stride + (uint32_t)(tid & 15) * 16u;
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -553,9 +556,32 @@ __device__ __forceinline__ void interleave()
     }
 }
 
+template <bool kAhead>
 __device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const float *win,
                                              const Lanes &ln, int half, const Cutter &cut)
 {
+    if constexpr (!kAhead) {  // where registers are short
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u32x4 kf[4];
+            Terms3 t;
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+                kf[kt] = key_frag(ktile, ln, kt, j);
+            weighted_terms(t, vf[j], win, 16 * j + 8 * half, cut);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+                S.t[kt] = mfma(kf[kt], t.l, S.t[kt]);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+                S.t[kt] = mfma(kf[kt], t.m, S.t[kt]);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+                S.t[kt] = mfma(kf[kt], t.h, S.t[kt]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        return;
+    }
     u32x4 kf[2][4];
     Terms3 t[2];
 #pragma unroll
@@ -693,7 +719,7 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v[buf], ln, jj);
-        state_update(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
+        state_update<true>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
         if (!more)
             break;
         if (wave == 3)
@@ -820,12 +846,22 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         tile_put(fk, lds.k, ln);
         tile_put(fv, lds.v, ln);
         const Chunk n = w.next();
-        if (n.len > 0) {
-            g = load_decay(a, dp, n, lane);
-            tile_fetch(fq, sq, n, tid);
-            tile_fetch(fk, sk, n, tid);
-            tile_fetch(fv, sv, n, tid);
+        u32x2 xr[2][4];  // x's rows of this chunk, older than the next chunk's rows: waiting for them does not wait for those
+        if (dots) {
+            const uint32_t xs = sx.st * 2;
+            const __amdgpu_buffer_rsrc_t rx = rsrc(sx.p + c.t0 * sx.st, (uint32_t)(c.len - 1) * xs + 256u);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int a4 = 0; a4 < 4; ++a4)
+                    xr[tt][a4] = __builtin_bit_cast(
+                        u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                   rx, (uint32_t)(32 * tt + l32) * xs + (32 * wave + 4 * half + 8 * a4) * 2, 0, 0));
         }
+        g = load_decay(a, dp, n, lane);
+        tile_fetch(fq, sq, n, tid);
+        tile_fetch(fk, sk, n, tid);
+        tile_fetch(fv, sv, n, tid);
         if (c.flags & kPieceStart) {
             const bool slot = (c.flags & kFromSlot) != 0;
             state_load(S,
@@ -850,16 +886,18 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 p[r] = O[0][r] = O[1][r] = 0.0f;
-            {
-                u32x4 kr[8], qr[8];
+            constexpr int kGroup = kDots ? 4 : 8;  // operands on their way together
 #pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
-                    kr[jj] = row_frag(lds.k, ln, sb, jj);
-                    qr[jj] = row_frag(lds.q, ln, ob, jj);
+            for (int j0 = 0; j0 < 8; j0 += kGroup) {
+                u32x4 kr[kGroup], qr[kGroup];
+#pragma unroll
+                for (int jj = 0; jj < kGroup; ++jj) {
+                    kr[jj] = row_frag(lds.k, ln, sb, j0 + jj);
+                    qr[jj] = row_frag(lds.q, ln, ob, j0 + jj);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int jj = 0; jj < 8; ++jj)
+                for (int jj = 0; jj < kGroup; ++jj)
                     p = mfma(kr[jj], qr[jj], p);
             }
             int to = 32 * ob + l32;
@@ -901,6 +939,30 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                     x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
                 cut3(x, sc[jj & 1], cut);
             };
+            if constexpr (kDots) {  // registers are short: no step ahead
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj) {
+                    qf[0][0] = row_frag(lds.q, ln, 0, jj);
+                    qf[0][1] = row_frag(lds.q, ln, 1, jj);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
+                    cut3(x, sc[0], cut);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+                        O[tt] = mfma(sc[0].l, qf[0][tt], O[tt]);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+                        O[tt] = mfma(sc[0].m, qf[0][tt], O[tt]);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+                        O[tt] = mfma(sc[0].h, qf[0][tt], O[tt]);
+                    if (jj & 1)
+                        weights(jj >> 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
             qf[0][0] = row_frag(lds.q, ln, 0, 0);
             qf[0][1] = row_frag(lds.q, ln, 1, 0);
             cut_state(0);
@@ -917,19 +979,17 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 if (jj & 1)
                     weights(jj >> 1);
 #pragma unroll
-                for (int tt = 0; tt < 2 && kDots; ++tt)
-                    O[tt] = mfma(sc[b].l, qf[b][tt], O[tt]);
-#pragma unroll
                 for (int tt = 0; tt < 2; ++tt)
                     O[tt] = mfma(sc[b].m, qf[b][tt], O[tt]);
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt)
                     O[tt] = mfma(sc[b].h, qf[b][tt], O[tt]);
                 if (jj & 1)
-                    interleave<kDots ? 6 : 4, 16>();
+                    interleave<4, 16>();
                 else
-                    interleave<kDots ? 6 : 4, 4>();
+                    interleave<4, 4>();
                 __builtin_amdgcn_sched_barrier(0);
+            }
             }
         }
 #pragma unroll
@@ -947,22 +1007,28 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         {
             // weight operands: of each 16 sources the diagonal block's, and the block beside it for half of them
             constexpr int kBeside = rev ? 0 : 1;  // output block that sees all sources
-            u32x4 wh[6], wl[6];
+            constexpr int kGroup = kDots ? 2 : 6;
 #pragma unroll
-            for (int x = 0; x < 6; ++x) {
-                const int jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
-                const int off = ln.w[jj] + 32 * kPRow * block;
-                wl[x] = lds_b128(lds.p[1] + off);
-                wh[x] = lds_b128(lds.p[0] + off);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            for (int x0 = 0; x0 < 6; x0 += kGroup) {
+                u32x4 w3[kGroup], wh[kGroup], wl[kGroup];
 #pragma unroll
-            for (int x = 0; x < 6; ++x) {
-                const int jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
-                if (kDots)
-                    O[block] = mfma(vf[jj], lds_b128(ldx.p3 + ln.w[jj] + 32 * kPRow * block), O[block]);
-                O[block] = mfma(vf[jj], wl[x], O[block]);
-                O[block] = mfma(vf[jj], wh[x], O[block]);
+                for (int y = 0; y < kGroup; ++y) {
+                    const int x = x0 + y, jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
+                    const int off = ln.w[jj] + 32 * kPRow * block;
+                    if (kDots)
+                        w3[y] = lds_b128(ldx.p3 + off);
+                    wl[y] = lds_b128(lds.p[1] + off);
+                    wh[y] = lds_b128(lds.p[0] + off);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int y = 0; y < kGroup; ++y) {
+                    const int x = x0 + y, jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
+                    if (kDots)
+                        O[block] = mfma(vf[jj], w3[y], O[block]);
+                    O[block] = mfma(vf[jj], wl[y], O[block]);
+                    O[block] = mfma(vf[jj], wh[y], O[block]);
+                }
             }
         }
 
@@ -974,9 +1040,6 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 rsrc(static_cast<unsigned char *>(ro.out) +
                          ((size_t)(row * a.T + c.t0) * (size_t)a.H + (size_t)h) * (kD * size),
                      (uint32_t)(c.len - 1) * stride + kD * size);
-            const uint32_t xs = dots ? sx.st * 2 : 0;
-            const __amdgpu_buffer_rsrc_t rx =
-                rsrc(dots ? sx.p + c.t0 * sx.st : nullptr, dots ? (uint32_t)(c.len - 1) * xs + 256u : 0u);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 const int t = 32 * tt + l32;
@@ -987,11 +1050,8 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 for (int a4 = 0; a4 < 4; ++a4) {
                     f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
                     if (dots) {
-                        const u32x2 xr = __builtin_bit_cast(
-                            u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                                       rx, (uint32_t)t * xs + (32 * wave + 4 * half + 8 * a4) * 2,
-                                       0, 0));
-                        dot += (lo_f(xr[0]) * y[0] + hi_f(xr[0]) * y[1]) + (lo_f(xr[1]) * y[2] + hi_f(xr[1]) * y[3]);
+                        const u32x2 xw = xr[tt][a4];
+                        dot += (lo_f(xw[0]) * y[0] + hi_f(xw[0]) * y[1]) + (lo_f(xw[1]) * y[2] + hi_f(xw[1]) * y[3]);
                         const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(t, 4 * wave + a4) + 8 * half);
                         y[0] = fmaf(own, lo_f(vr[0]), y[0]);
                         y[1] = fmaf(own, hi_f(vr[0]), y[1]);
@@ -1028,7 +1088,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         }
         if (d.mul != 1.0f)
             state_scale(S, d.mul);
-        state_update(S, lds.k, vf, d.win, ln, half, cut);
+        state_update<!kDots>(S, lds.k, vf, d.win, ln, half, cut);
         const double held_now = d.held;
         if (wave == 3 && n.len > 0)
             make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
