@@ -434,6 +434,7 @@ __device__ __forceinline__ void tile_fetch(TileLoad &f, const TileSrc &x, const 
 {
     const uint32_t stride = x.st * 2;
     const __amdgpu_buffer_rsrc_t r = rsrc(x.p + c.t0 * x.st, c.len > 0 ? (uint32_t)(c.len - 1) * stride + 256u : 0u);
+    __asm__ volatile("" : "+v"(tid));  // the offsets are formed anew: kept from chunk to chunk they would cost 12 registers
     const uint32_t off = (uint32_t)(tid >> 4) * stride + (uint32_t)(tid & 15) * 16u;
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -849,6 +850,8 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         u32x2 xr[2][4];  // x's rows of this chunk, older than the next chunk's rows: waiting for them does not wait for those
         if (dots) {
             const uint32_t xs = sx.st * 2;
+            int tx = l32;
+            __asm__ volatile("" : "+v"(tx));
             const __amdgpu_buffer_rsrc_t rx = rsrc(sx.p + c.t0 * sx.st, (uint32_t)(c.len - 1) * xs + 256u);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
@@ -856,7 +859,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 for (int a4 = 0; a4 < 4; ++a4)
                     xr[tt][a4] = __builtin_bit_cast(
                         u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                                   rx, (uint32_t)(32 * tt + l32) * xs + (32 * wave + 4 * half + 8 * a4) * 2, 0, 0));
+                                   rx, (uint32_t)(32 * tt + tx) * xs + (32 * wave + 4 * half + 8 * a4) * 2, 0, 0));
         }
         g = load_decay(a, dp, n, lane);
         tile_fetch(fq, sq, n, tid);
@@ -1007,7 +1010,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         {
             // weight operands: of each 16 sources the diagonal block's, and the block beside it for half of them
             constexpr int kBeside = rev ? 0 : 1;  // output block that sees all sources
-            constexpr int kGroup = kDots ? 2 : 6;
+            constexpr int kGroup = kDots ? 2 : 3;
 #pragma unroll
             for (int x0 = 0; x0 < 6; x0 += kGroup) {
                 u32x4 w3[kGroup], wh[kGroup], wl[kGroup];
@@ -1045,6 +1048,9 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 const int t = 32 * tt + l32;
                 const uint32_t o = (uint32_t)t * stride + (32 * wave + 4 * half) * size;
                 const float own = dots ? ldx.own[t] : 0.0f;
+                int tv = l32;
+                if (kDots)
+                    __asm__ volatile("" : "+v"(tv));  // as above: addresses formed anew
                 float dot = 0.0f;
 #pragma unroll
                 for (int a4 = 0; a4 < 4; ++a4) {
@@ -1052,7 +1058,8 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                     if (dots) {
                         const u32x2 xw = xr[tt][a4];
                         dot += (lo_f(xw[0]) * y[0] + hi_f(xw[0]) * y[1]) + (lo_f(xw[1]) * y[2] + hi_f(xw[1]) * y[3]);
-                        const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(t, 4 * wave + a4) + 8 * half);
+                        const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(tv, 4 * wave + a4) + 8 * half +
+                                                                          8192 * tt);
                         y[0] = fmaf(own, lo_f(vr[0]), y[0]);
                         y[1] = fmaf(own, hi_f(vr[0]), y[1]);
                         y[2] = fmaf(own, lo_f(vr[1]), y[2]);
