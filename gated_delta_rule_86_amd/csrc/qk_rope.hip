@@ -30,28 +30,26 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBf16 = 1, kFp32 = 2, kFp16 = 3;
 
-// 8 values from memory and back (one 16-byte piece, two in fp32); rounded once, to nearest even
+// 16 bytes of memory as values and back; values are rounded once, to nearest even
 template <int kT>
-__device__ __forceinline__ void load8(const unsigned char *p, float *x)
+struct Piece {
+    static constexpr int kSize = kT == kFp32 ? 4 : 2;
+    static constexpr int kPer = 16 / kSize;       // values
+    static constexpr int kCount = 8 / kPer;       // pieces of 8 values
+};
+template <int kT>
+__device__ __forceinline__ void widen(const u32x4 *u, float *x)
 {
-    if constexpr (kT == kFp32) {
-        const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] = a[e];
-            x[4 + e] = b[e];
-        }
-    } else {
-        const u32x4 u = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (kT == kBf16) {
-                x[2 * e] = __uint_as_float(u[e] << 16);
-                x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            } else {
-                x[2 * e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[e] & 0xffffu));
-                x[2 * e + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[e] >> 16));
-            }
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (kT == kFp32) {
+            x[e] = __uint_as_float(u[e >> 2][e & 3]);
+        } else {
+            const uint32_t w = u[0][e >> 1], half = e & 1 ? w >> 16 : w & 0xffffu;
+            if constexpr (kT == kBf16)
+                x[e] = __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+            else
+                x[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)half);
         }
     }
 }
@@ -107,6 +105,11 @@ __device__ __forceinline__ Unit unit_of(const RopeArgs &a, int u)
     Unit t;
     t.on = u < a.D / 16;
     t.pair = -1;
+    if (!t.on) {  // reads the row's first unit, counts for nothing
+        t.lo = 0;
+        t.hi = 8;
+        return t;
+    }
     if (16 * u < a.R && !a.interleaved) {
         t.lo = 8 * u;
         t.hi = a.R / 2 + 8 * u;
@@ -152,7 +155,30 @@ __device__ __forceinline__ float norm_factor(const RopeArgs &a, float ss)
     return rsqrtf((a.norm == 1 ? ss / (float)a.D : ss) + a.eps);
 }
 
-// cos/sin of the step's tokens: [token][pair][2] in LDS
+// LDS of a step: cos and sin of its tokens [token][pair][2], and where each token's row of a tensor begins, in bytes.
+constexpr int kMaxStep = 64;  // tokens
+struct Starts {
+    int64_t at[6][kMaxStep];  // q, k, their outputs (or gradients), ...
+};
+
+template <int kViews, int kSize>
+__device__ __forceinline__ void fill_starts(const RopeArgs &a, Starts &s, int64_t t0, int n, int tid)
+{
+    for (int i = tid; i < kViews * kMaxStep; i += kRopeThreads) {
+        const int view = i / kMaxStep, tt = i - view * kMaxStep;
+        if (tt < n) {
+            // the step's first token is divided once, as one value for the workgroup
+            const int64_t b0 = t0 / a.T;
+            int64_t b = b0, t = t0 - b0 * a.T + tt;
+            while (t >= a.T) {
+                t -= a.T;
+                ++b;
+            }
+            const RopeView &v = view < 2 ? a.x[view] : kViews == 4 || view >= 4 ? a.y[view & 1] : a.dy[view & 1];
+            s.at[view][tt] = (b * v.sb + t * v.st) * kSize;
+        }
+    }
+}
 __device__ __forceinline__ void fill_turns(const RopeArgs &a, float *lds, int64_t t0, int n, int tid)
 {
     const int pairs = a.R / 2;
@@ -166,11 +192,96 @@ __device__ __forceinline__ void fill_turns(const RopeArgs &a, float *lds, int64_
     }
 }
 
+// One tensor's rows (token, head) of a step, `groups` at a time.
+struct Rows {
+    int heads, count;
+    float inv;
+
+    __device__ Rows(int heads_, int n) : heads(heads_), count(n * heads_), inv(1.0f / (float)heads_) {}
+    // r below 2^18, so that (r + 1/2) / heads is far enough from whole numbers for fp32
+    __device__ int token(int r) const { return (int)(((float)r + 0.5f) * inv); }
+};
+
+template <int kT, int kRows>
+struct RowLoads {
+    u32x4 u[kRows][2 * Piece<kT>::kCount];
+};
+// kRows rows of this lane's group from row r on, `groups` apart; rows behind the last one repeat it
+template <int kT, int kRows>
+__device__ __forceinline__ void load_rows(RowLoads<kT, kRows> &f, const RopeView &v, const int64_t *starts, const Rows &ro,
+                                          const Unit &u, int r, int groups)
+{
+    constexpr int kSize = Piece<kT>::kSize;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int rr = min(r + i * groups, ro.count - 1), tt = ro.token(rr), h = rr - tt * ro.heads;
+        const unsigned char *p = v.p + starts[tt] + (int64_t)h * (v.sh * kSize);
+#pragma unroll
+        for (int c = 0; c < Piece<kT>::kCount; ++c) {
+            f.u[i][c] = *reinterpret_cast<const u32x4 *>(p + u.lo * kSize + 16 * c);
+            f.u[i][Piece<kT>::kCount + c] = *reinterpret_cast<const u32x4 *>(p + u.hi * kSize + 16 * c);
+        }
+    }
+}
+
+// A lane's 16 weights (1 without weights)
+__device__ __forceinline__ void load_weights(float *w, const float *p, const Unit &u)
+{
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        w[e] = p ? p[e < 8 ? u.lo + e : u.hi + e - 8] : 1.0f;
+}
+
+template <int kT>
+__device__ __forceinline__ void rope_side(const RopeArgs &a, int side, int n, const Starts &st, const float *turns,
+                                          const Unit &u, int group, int groups, int lanes, bool first)
+{
+    constexpr int kRows = kT == kFp32 ? 2 : 4, kSize = Piece<kT>::kSize, kC = Piece<kT>::kCount;
+    const Rows ro(a.heads[side], n);
+    float w[16];
+    load_weights(w, a.w[side], u);
+    for (int r = group; r < ro.count; r += kRows * groups) {
+        RowLoads<kT, kRows> f;
+        load_rows<kT, kRows>(f, a.x[side], st.at[side], ro, u, r, groups);
+        if (first) {  // the angles are ready; the first rows are on their way by then
+            __syncthreads();
+            first = false;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int rr = r + i * groups;
+            if (rr >= ro.count)
+                break;
+            float x[16];
+            widen<kT>(f.u[i], x);
+            widen<kT>(f.u[i] + kC, x + 8);
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                ss = fmaf(x[e], x[e], ss);
+            const float rn = norm_factor(a, row_sum(u.on ? ss : 0.0f, lanes));
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[e] *= rn * w[e];
+            const int tt = ro.token(rr), h = rr - tt * ro.heads;
+            if (u.pair >= 0)
+                rotate(x, turns + (tt * (a.R / 2) + u.pair) * 2, a.interleaved != 0, false);
+            if (u.on) {
+                unsigned char *q = a.y[side].p + st.at[2 + side][tt] + (int64_t)h * (a.y[side].sh * kSize);
+                store8<kT>(q + u.lo * kSize, x);
+                store8<kT>(q + u.hi * kSize, x + 8);
+            }
+        }
+    }
+    if (first)  // a group without rows
+        __syncthreads();
+}
+
 template <int kT>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) float turns[];
-    constexpr int kSize = kT == kFp32 ? 4 : 2;
+    __shared__ Starts st;
     const int tid = threadIdx.x;
     int lanes = 1;
     while (lanes * 16 < a.D)
@@ -180,49 +291,67 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a)
     const int64_t total = a.B * a.T;
     const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
     const int n = (int)(total - t0 < a.tokens ? total - t0 : a.tokens);
-    fill_turns(a, turns, t0, n, tid);
+    fill_starts<4, Piece<kT>::kSize>(a, st, t0, n, tid);
     __syncthreads();
-    const int heads = a.heads[0] + a.heads[1], rows = n * heads;
-    for (int r = group; r < rows; r += groups) {
-        const int tt = r / heads, hh = r - tt * heads;
-        const int side = hh >= a.heads[0] ? 1 : 0, h = side ? hh - a.heads[0] : hh;
-        const int64_t tok = t0 + tt, b = tok / a.T, t = tok - b * a.T;
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            x[e] = 0.0f;
-        const RopeView &in = a.x[side], &out = a.y[side];
-        const unsigned char *p = in.p + (b * in.sb + t * in.st + h * in.sh) * kSize;
-        if (u.on) {
-            load8<kT>(p + u.lo * kSize, x);
-            load8<kT>(p + u.hi * kSize, x + 8);
-        }
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            ss = fmaf(x[e], x[e], ss);
-        const float rn = norm_factor(a, row_sum(ss, lanes));
-        const float *w = a.w[side];
-        if (!u.on)
-            continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] *= w ? rn * w[u.lo + e] : rn;
-            x[8 + e] *= w ? rn * w[u.hi + e] : rn;
-        }
-        if (u.pair >= 0)
-            rotate(x, turns + (tt * (a.R / 2) + u.pair) * 2, a.interleaved != 0, false);
-        unsigned char *q = out.p + (b * out.sb + t * out.st + h * out.sh) * kSize;
-        store8<kT>(q + u.lo * kSize, x);
-        store8<kT>(q + u.hi * kSize, x + 8);
-    }
+    fill_turns(a, turns, t0, n, tid);
+    rope_side<kT>(a, 0, n, st, turns, u, group, groups, lanes, true);
+    rope_side<kT>(a, 1, n, st, turns, u, group, groups, lanes, false);
 }
 
 template <int kT>
-__global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(RopeArgs a)
+__device__ __forceinline__ void rope_bwd_side(const RopeArgs &a, int side, int n, const Starts &st, const float *turns,
+                                              const Unit &u, int group, int groups, int lanes, float *dw)
+{
+    constexpr int kRows = kT == kFp32 ? 1 : 2, kSize = Piece<kT>::kSize, kC = Piece<kT>::kCount;
+    const Rows ro(a.heads[side], n);
+    float w[16];
+    load_weights(w, a.w[side], u);
+    for (int r = group; r < ro.count; r += kRows * groups) {
+        RowLoads<kT, kRows> fx, fd;
+        load_rows<kT, kRows>(fx, a.x[side], st.at[side], ro, u, r, groups);
+        load_rows<kT, kRows>(fd, a.dy[side], st.at[2 + side], ro, u, r, groups);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int rr = r + i * groups;
+            if (rr >= ro.count)
+                break;
+            const int tt = ro.token(rr), h = rr - tt * ro.heads;
+            float x[16], d[16];
+            widen<kT>(fx.u[i], x);
+            widen<kT>(fx.u[i] + kC, x + 8);
+            widen<kT>(fd.u[i], d);
+            widen<kT>(fd.u[i] + kC, d + 8);
+            if (u.pair >= 0)
+                rotate(d, turns + (tt * (a.R / 2) + u.pair) * 2, a.interleaved != 0, true);
+            float ss = 0.0f, sd = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                sd = fmaf(x[e], d[e] * w[e], sd);
+            }
+            const float rn = norm_factor(a, row_sum(u.on ? ss : 0.0f, lanes));
+            sd = row_sum(u.on ? sd : 0.0f, lanes);
+            const float back = a.norm == 0 ? 0.0f : sd * rn * rn * rn / (a.norm == 1 ? (float)a.D : 1.0f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                dw[e] = fmaf(d[e], x[e] * rn, dw[e]);
+                d[e] = rn * (d[e] * w[e]) - x[e] * back;
+            }
+            if (u.on) {
+                unsigned char *q = a.y[side].p + st.at[4 + side][tt] + (int64_t)h * (a.y[side].sh * kSize);
+                store8<kT>(q + u.lo * kSize, d);
+                store8<kT>(q + u.hi * kSize, d + 8);
+            }
+        }
+    }
+}
+
+// Workgroups [0, groups_q) take q's rows, the others k's, in steps of tokens; each keeps its weight sums in registers.
+template <int kT>
+__global__ __launch_bounds__(kRopeThreads, 4) void rope_bwd_kernel(RopeArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) float turns[];
-    constexpr int kSize = kT == kFp32 ? 4 : 2;
+    __shared__ Starts st;
     const int tid = threadIdx.x;
     int lanes = 1;
     while (lanes * 16 < a.D)
@@ -230,129 +359,109 @@ __global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(RopeArgs a)
     const int group = tid / lanes, groups = kRopeThreads / lanes;
     const Unit u = unit_of(a, tid & (lanes - 1));
     const int64_t total = a.B * a.T;
-    float dw[2][16];
+    const int side = (int)blockIdx.x >= a.groups[0] ? 1 : 0, step = a.step[side];
+    float dw[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-        dw[0][e] = dw[1][e] = 0.0f;
-    for (int64_t t0 = (int64_t)blockIdx.x * a.tokens; t0 < total; t0 += (int64_t)gridDim.x * a.tokens) {
-        const int n = (int)(total - t0 < a.tokens ? total - t0 : a.tokens);
+        dw[e] = 0.0f;
+    for (int64_t t0 = (int64_t)(blockIdx.x - (side ? a.groups[0] : 0)) * step; t0 < total;
+         t0 += (int64_t)a.groups[side] * step) {
+        const int n = (int)(total - t0 < step ? total - t0 : step);
         __syncthreads();
+        fill_starts<6, Piece<kT>::kSize>(a, st, t0, n, tid);
         fill_turns(a, turns, t0, n, tid);
         __syncthreads();
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int heads = a.heads[side], rows = n * heads;
-            const RopeView &in = a.x[side], &gr = a.dy[side], &out = a.y[side];
-            const float *w = a.w[side];
-            for (int r = group; r < rows; r += groups) {
-                const int tt = r / heads, h = r - tt * heads;
-                const int64_t tok = t0 + tt, b = tok / a.T, t = tok - b * a.T;
-                float x[16], d[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[e] = d[e] = 0.0f;
-                const unsigned char *p = in.p + (b * in.sb + t * in.st + h * in.sh) * kSize;
-                const unsigned char *g = gr.p + (b * gr.sb + t * gr.st + h * gr.sh) * kSize;
-                if (u.on) {
-                    load8<kT>(p + u.lo * kSize, x);
-                    load8<kT>(p + u.hi * kSize, x + 8);
-                    load8<kT>(g + u.lo * kSize, d);
-                    load8<kT>(g + u.hi * kSize, d + 8);
-                }
-                if (u.pair >= 0)
-                    rotate(d, turns + (tt * (a.R / 2) + u.pair) * 2, a.interleaved != 0, true);
-                float ss = 0.0f, sd = 0.0f;
-                float wd[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int ch = e < 8 ? u.lo + e : u.hi + e - 8;
-                    wd[e] = w && u.on ? d[e] * w[ch] : d[e];
-                    ss = fmaf(x[e], x[e], ss);
-                    sd = fmaf(x[e], wd[e], sd);
-                }
-                const float rn = norm_factor(a, row_sum(ss, lanes));
-                sd = row_sum(sd, lanes);
-                const float back = a.norm == 0 ? 0.0f : sd * rn * rn * rn / (a.norm == 1 ? (float)a.D : 1.0f);
-                float dx[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    dw[side][e] = fmaf(d[e], x[e] * rn, dw[side][e]);
-                    dx[e] = rn * wd[e] - x[e] * back;
-                }
-                if (u.on) {
-                    unsigned char *q = out.p + (b * out.sb + t * out.st + h * out.sh) * kSize;
-                    store8<kT>(q + u.lo * kSize, dx);
-                    store8<kT>(q + u.hi * kSize, dx + 8);
-                }
-            }
-        }
+        rope_bwd_side<kT>(a, side, n, st, turns, u, group, groups, lanes, dw);
     }
+    if (!a.dw[side])
+        return;
     // this workgroup's weight sums, groups added in order
+    __syncthreads();
+    if (u.on) {
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        if (!a.dw[side])
-            continue;
-        __syncthreads();
-        if (u.on) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                turns[group * a.D + (e < 8 ? u.lo + e : u.hi + e - 8)] = dw[side][e];
-        }
-        __syncthreads();
-        for (int ch = tid; ch < a.D; ch += kRopeThreads) {
-            float s = 0.0f;
-            for (int g = 0; g < groups; ++g)
-                s += turns[g * a.D + ch];
-            a.part[((int64_t)blockIdx.x * 2 + side) * a.D + ch] = s;
-        }
+        for (int e = 0; e < 16; ++e)
+            turns[group * a.D + (e < 8 ? u.lo + e : u.hi + e - 8)] = dw[e];
+    }
+    __syncthreads();
+    for (int ch = tid; ch < a.D; ch += kRopeThreads) {
+        float s = 0.0f;
+        for (int g = 0; g < groups; ++g)
+            s += turns[g * a.D + ch];
+        a.part[(int64_t)blockIdx.x * a.D + ch] = s;
     }
 }
 
-// dw[ch] = sum of the workgroups' parts, in a fixed order; one wave per channel and side
-__global__ __launch_bounds__(256) void rope_dw_kernel(RopeArgs a, int64_t parts)
+// dw[ch] = sum of the workgroups' parts, in a fixed order: 16 channels a workgroup, 64 runs of parts side by side
+__global__ __launch_bounds__(1024) void rope_dw_kernel(RopeArgs a)
 {
-    const int side = blockIdx.y, ch = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (ch >= a.D || !a.dw[side])
+    __shared__ double sum[64][17];
+    const int side = blockIdx.y, c = threadIdx.x & 15, run = threadIdx.x >> 4, ch = blockIdx.x * 16 + c;
+    if (!a.dw[side])
         return;
+    const float *p = a.part + (side ? (int64_t)a.groups[0] * a.D : 0) + ch;
     double s = 0.0;
-    for (int64_t n = lane; n < parts; n += 64)
-        s += (double)a.part[(n * 2 + side) * a.D + ch];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        s += __shfl_xor(s, o);
-    if (lane == 0)
+#pragma unroll 4
+    for (int n = run; n < a.groups[side]; n += 64)
+        s += (double)p[(int64_t)n * a.D];
+    sum[run][c] = s;
+    __syncthreads();
+    if (run == 0) {
+        for (int i = 1; i < 64; ++i)
+            s += sum[i][c];
         a.dw[side][ch] = (float)s;
+    }
 }
 
 }  // namespace
 
-int64_t rope_groups(int64_t tokens, int heads, int D, bool backward, int *per_step)
+namespace {
+
+int lanes_of(int D)
 {
     int lanes = 1;
     while (lanes * 16 < D)
         lanes <<= 1;
-    const int groups = kRopeThreads / lanes;
-    // about four rows for each group of lanes and step, fewer where that would leave the chip empty
-    int64_t n = (4 * groups + heads - 1) / heads;
-    if (n > 16)
-        n = 16;
-    while (n > 1 && (tokens + n - 1) / n < 512)
-        n >>= 1;
-    *per_step = (int)n;
-    int64_t steps = (tokens + n - 1) / n;
-    if (steps < 1)
-        steps = 1;
-    return backward && steps > kRopeGroups ? kRopeGroups : steps;
+    return lanes;
+}
+// Tokens per step: about four rows for each group of lanes, fewer where that would leave the chip empty; cos and sin
+// of a step fit 32 KiB.
+int step_of(int64_t tokens, int heads, int D, int R, int64_t want)
+{
+    const int groups = kRopeThreads / lanes_of(D);
+    int n = (4 * groups + heads - 1) / heads;
+    const int most = R > 0 ? 8192 / R : kMaxStep;
+    n = n > most ? most : n;
+    n = n > kMaxStep ? kMaxStep : n;
+    while (n > 1 && (tokens + n - 1) / n < want)
+        n = (n + 1) / 2;
+    return n;
+}
+
+}  // namespace
+
+void rope_plan_bwd(RopeArgs *a)
+{
+    const int64_t tokens = a->B * a->T;
+    const int64_t heads = a->heads[0] + a->heads[1];
+    for (int side = 0; side < 2; ++side) {
+        // workgroups by the share of rows, all resident at once: four on each of 256 CUs
+        int64_t g = side ? kRopeGroups - kRopeGroups * a->heads[0] / heads : kRopeGroups * a->heads[0] / heads;
+        g = g < 1 ? 1 : g > kRopeGroups - 1 ? kRopeGroups - 1 : g;
+        a->step[side] = step_of(tokens, a->heads[side], a->D, a->R, g);
+        const int64_t steps = (tokens + a->step[side] - 1) / a->step[side];
+        a->groups[side] = (int)(steps < 1 ? 1 : steps < g ? steps : g);
+    }
 }
 
 hipError_t rope_launch(const RopeArgs &a0, hipStream_t s)
 {
     RopeArgs a = a0;
-    const int64_t grid = rope_groups(a.B * a.T, a.heads[0] + a.heads[1], a.D, false, &a.tokens);
-    if (a.B * a.T == 0)
+    const int64_t tokens = a.B * a.T;
+    if (tokens == 0)
         return hipSuccess;
+    a.tokens = step_of(tokens, a.heads[0] + a.heads[1], a.D, a.R, 512);
     const size_t lds = (size_t)a.tokens * a.R * sizeof(float);
-    const dim3 g((unsigned)grid), b(kRopeThreads);
+    const dim3 g((unsigned)((tokens + a.tokens - 1) / a.tokens)), b(kRopeThreads);
     if (a.dtype == kBf16)
         hipLaunchKernelGGL(rope_kernel<kBf16>, g, b, lds, s, a);
     else if (a.dtype == kFp32)
@@ -365,14 +474,11 @@ hipError_t rope_launch(const RopeArgs &a0, hipStream_t s)
 hipError_t rope_launch_bwd(const RopeArgs &a0, hipStream_t s)
 {
     RopeArgs a = a0;
-    const int64_t grid = rope_groups(a.B * a.T, a.heads[0] + a.heads[1], a.D, true, &a.tokens);
-    int lanes = 1;
-    while (lanes * 16 < a.D)
-        lanes <<= 1;
-    const size_t turns = (size_t)a.tokens * a.R * sizeof(float);
-    const size_t sums = (size_t)(kRopeThreads / lanes) * a.D * sizeof(float);
+    rope_plan_bwd(&a);
+    const size_t turns = (size_t)(a.step[0] > a.step[1] ? a.step[0] : a.step[1]) * a.R * sizeof(float);
+    const size_t sums = (size_t)(kRopeThreads / lanes_of(a.D)) * a.D * sizeof(float);
     const size_t lds = turns > sums ? turns : sums;
-    const dim3 g((unsigned)grid), b(kRopeThreads);
+    const dim3 g((unsigned)(a.groups[0] + a.groups[1])), b(kRopeThreads);
     if (a.dtype == kBf16)
         hipLaunchKernelGGL(rope_bwd_kernel<kBf16>, g, b, lds, s, a);
     else if (a.dtype == kFp32)
@@ -380,7 +486,7 @@ hipError_t rope_launch_bwd(const RopeArgs &a0, hipStream_t s)
     else
         hipLaunchKernelGGL(rope_bwd_kernel<kFp16>, g, b, lds, s, a);
     if (a.dw[0] || a.dw[1])
-        hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)((a.D + 3) / 4), 2), dim3(256), 0, s, a, grid);
+        hipLaunchKernelGGL(rope_dw_kernel, dim3((unsigned)(a.D / 16), 2), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 

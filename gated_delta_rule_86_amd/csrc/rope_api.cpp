@@ -190,8 +190,7 @@ size_t kda_qk_rope_bwd_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t 
 {
     if (check_shape(B, T, Hq, Hk, D, 0) != KDA_OK)
         return 0;
-    int step;
-    return (size_t)kda::rope_groups(B * T, (int)(Hq + Hk), (int)D, true, &step) * 2 * (size_t)D * sizeof(float);
+    return (size_t)kda::kRopeGroups * (size_t)D * sizeof(float);
 }
 
 kda_status kda_qk_rope_bwd(const void *q, const void *k, const void *dq_out, const void *dk_out, void *dq, void *dk,

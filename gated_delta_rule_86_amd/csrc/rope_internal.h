@@ -11,7 +11,7 @@ namespace kda {
 
 constexpr int kRopeMaxD = 512;          // largest head size
 constexpr int kRopeThreads = 256;
-constexpr int64_t kRopeGroups = 1024;   // workgroups of the backward pass, one row of partial weight sums each
+constexpr int64_t kRopeGroups = 1024;   // most workgroups of the backward pass, one row of partial weight sums each
 
 struct RopeView {  // [B, T, heads, D], element strides
     unsigned char *p;
@@ -32,13 +32,15 @@ struct RopeArgs {
     int norm;    // 0 none, 1 rms, 2 l2
     int interleaved;
     float eps, factor;
-    int tokens;  // per workgroup step
-    float *part;     // [groups][2][D] partial weight sums (backward pass)
+    int tokens;      // per workgroup (forward pass)
+    int step[2];     // tokens per step, and workgroups, of q and k (backward pass)
+    int groups[2];
+    float *part;     // [groups[0] + groups[1]][D] partial weight sums (backward pass)
     float *dw[2];
 };
 
-// workgroups and tokens per step for B * T tokens
-int64_t rope_groups(int64_t tokens, int heads, int D, bool backward, int *per_step);
+// sets step and groups from B, T, heads, D and R
+void rope_plan_bwd(RopeArgs *a);
 hipError_t rope_launch(const RopeArgs &a, hipStream_t s);
 hipError_t rope_launch_bwd(const RopeArgs &a, hipStream_t s);
 

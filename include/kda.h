@@ -443,7 +443,7 @@ kda_status kda_qk_rope_bwd(const void *q, const void *k, const void *dq_out, con
                            int interleaved, float attention_factor, const int64_t *strides_host, void *workspace,
                            size_t workspace_bytes, void *stream);
 
-/* Bytes of partial weight sums: 8 D for each of at most 1024 workgroups.  Returns 0 for invalid sizes. */
+/* Bytes of partial weight sums: 4 D for each of 1024 workgroups.  Returns 0 for invalid sizes. */
 size_t kda_qk_rope_bwd_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D);
 
 /* Human-readable name of a kda_status value (static string; never NULL). */
