@@ -640,8 +640,7 @@ constexpr double kGone = -150.0;
 
 __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0, int lead1)
 {
-    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-    LdsStates &lds = *reinterpret_cast<LdsStates *>(lds_raw);
+    __shared__ __attribute__((aligned(16))) LdsStates lds;
     const int64_t total = a.rows * a.P * a.H;
     const int64_t at = xcd_order(blockIdx.x, total);
     if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
@@ -1133,7 +1132,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 template <bool kDots>
 __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
 {
-    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    __shared__ __attribute__((aligned(16))) unsigned char lds_raw[kDots ? sizeof(LdsWalkDots) : sizeof(LdsWalk)];
     const int64_t total = a.rows * a.P * a.H;
     const int64_t at = xcd_order(blockIdx.x, total);
     if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
@@ -1446,30 +1445,20 @@ hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n
     const unsigned grid = (unsigned)(8 * cdiv(total, 8));
     if (a.P > 1) {
         const int l0 = lead[0], l1 = lead[n_lead - 1];
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_states_kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(LdsStates));
-        if (e != hipSuccess)
-            return e;
-        hipLaunchKernelGGL(lin_states_kernel, dim3(grid, n_lead), dim3(256), sizeof(LdsStates), s, a, l0, l1);
+        hipLaunchKernelGGL(lin_states_kernel, dim3(grid, n_lead), dim3(256), 0, s, a, l0, l1);
         hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)(kScanParts * a.rows * a.H), n_lead), dim3(256), 0, s, a,
                            l0, l1);
-        e = hipGetLastError();
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
     bool dots = false;
     for (int i = 0; i < n_roles; ++i)
         dots = dots || a.role[i].dots;
-    const void *fn = dots ? reinterpret_cast<const void *>(&lin_walk_kernel<true>)
-                          : reinterpret_cast<const void *>(&lin_walk_kernel<false>);
-    const int bytes = (int)(dots ? sizeof(LdsWalkDots) : sizeof(LdsWalk));
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess)
-        return e;
     if (dots)
-        hipLaunchKernelGGL(lin_walk_kernel<true>, dim3(grid, n_roles), dim3(256), bytes, s, a);
+        hipLaunchKernelGGL(lin_walk_kernel<true>, dim3(grid, n_roles), dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL(lin_walk_kernel<false>, dim3(grid, n_roles), dim3(256), bytes, s, a);
+        hipLaunchKernelGGL(lin_walk_kernel<false>, dim3(grid, n_roles), dim3(256), 0, s, a);
     if (a.role[0].defer)
         hipLaunchKernelGGL(lin_final_kernel, dim3((unsigned)total), dim3(256), 0, s, a);
     return hipGetLastError();

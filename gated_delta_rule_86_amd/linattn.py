@@ -10,8 +10,10 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import kda
-from .kda import KDA_OK, KDAError, _ptr, _state_code, _stream_handle, lib
+from .kda import KDA_OK, KDAError, _ptr, lib
 
 D = 128
 
@@ -28,69 +30,112 @@ def bwd_workspace_size(B: int, T: int, Hk: int, H: int, N: int = 0, varlen: bool
 def _row_strides(*tensors):
     """Batch, token and head strides in elements, or None when every tensor is contiguous.  The
     stride of a dimension of size 1 is never used and taken as 0."""
-    if all(t.is_contiguous() for t in tensors):
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
         return None
     got = []
     for t in tensors:
-        got += [0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3])]
+        s, n = t.stride(), t.shape
+        got += (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
     return (ctypes.c_int64 * len(got))(*got)
 
 
+def _gpu_index(t):
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("tensors must be on a GPU")
+    return i
+
+
+class _On:
+    """The call runs with q's device current; only a change costs anything."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, index):
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 def _check_inputs(q, k, v, decay, cu_seqlens, cu_seqlens_host):
-    import torch
-    if q.dim() != 4 or v.dim() != 4:
+    qs, vs = q.shape, v.shape
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q, k and v must be [B, T, heads, 128]")
-    B, T, Hk, K = q.shape
-    H, V = v.shape[2], v.shape[3]
-    if tuple(k.shape) != (B, T, Hk, K) or tuple(v.shape[:2]) != (B, T):
+    B, T, Hk, K = qs
+    H, V = vs[2], vs[3]
+    if k.shape != qs or vs[0] != B or vs[1] != T:
         raise ValueError("q and k must be [B, T, Hk, 128], v [B, T, H, 128]")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or (t.stride(3) != 1 and t.shape[3] != 1):
-            raise ValueError(f"{name} must be bf16 with contiguous channels")
-    if decay.dtype != torch.float32 or not decay.is_contiguous() or tuple(decay.shape) not in ((H,), (B, T, H)):
+    for t in (q, k, v):
+        if t.dtype is not torch.bfloat16 or (t.stride(3) != 1 and t.shape[3] != 1):
+            raise ValueError("q, k and v must be bf16 with contiguous channels")
+    per_token = decay.dim() == 3
+    if decay.dtype is not torch.float32 or not decay.is_contiguous() or decay.shape != ((B, T, H) if per_token else (H,)):
         raise ValueError("decay must be a contiguous fp32 [H] or [B, T, H] tensor")
     N = B
+    at = q.get_device()
+    if k.get_device() != at or v.get_device() != at or decay.get_device() != at:
+        raise ValueError("k, v and decay must be on q's device")
     if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        if cu_seqlens.dtype is not torch.int64 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be a contiguous int64 [N+1] tensor")
+        if cu_seqlens.get_device() != at:
+            raise ValueError("cu_seqlens must be on q's device")
         N = cu_seqlens.numel() - 1
-    for name, t in (("k", k), ("v", v), ("decay", decay), ("cu_seqlens", cu_seqlens)):
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} must be on q's device")
     host = None
     if cu_seqlens_host is not None:
         import numpy as np
         host = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int64))
         if cu_seqlens is None or host.shape != (N + 1,):
             raise ValueError("cu_seqlens_host must be the host copy of cu_seqlens")
-    return B, T, Hk, H, N, K, V, decay.dim() == 3, host
+    return B, T, Hk, H, N, K, V, per_token, host
 
 
-def _check_state(name, t, shape, device, dtypes):
-    if t is not None and (tuple(t.shape) != shape or not t.is_contiguous() or t.dtype not in dtypes
-                          or t.device != device):
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor of {' or '.join(map(str, dtypes))} "
+def _check_state(name, t, shape, q, bf16_too=True):
+    if t is not None and (t.shape != shape or not t.is_contiguous() or t.get_device() != q.get_device() or not (
+            t.dtype is torch.float32 or (bf16_too and t.dtype is torch.bfloat16))):
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor of fp32{' or bf16' if bf16_too else ''} "
                          "on q's device")
 
 
-def _workspace(workspace, need, device, stream):
-    import torch
+def _workspace(workspace, need, index, stream):
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
+        if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
         return workspace
     if need == 0:
         return None
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    # allocated on the current stream; the kernels run on `stream`: keep the caching
-    # allocator from reusing the block before they have finished
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        workspace.record_stream(stream)
+    workspace = torch.empty(need, dtype=torch.uint8, device=index)
+    _used_on(stream, index, workspace)
     return workspace
+
+
+def _used_on(stream, index, *tensors):
+    """Tensors allocated on the current stream whose kernels run on `stream`: keep the caching allocator from
+    reusing their blocks before those have finished."""
+    if stream is not None and stream != torch.cuda.current_stream(index):
+        for t in tensors:
+            t.record_stream(stream)
 
 
 def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def _code(t):
+    return 0 if t is None else 2 if t.dtype is torch.float32 else 1
 
 
 def fwd(q, k, v, decay, scale, out, initial_state=None, final_state=None, cu_seqlens=None, *,
@@ -104,24 +149,29 @@ def fwd(q, k, v, decay, scale, out, initial_state=None, final_state=None, cu_seq
     [N, H, 128, 128] or None, final_state may be initial_state; cu_seqlens: int64 [N+1] device
     tensor (then B is 1) or None.  cu_seqlens_host, workspace, stream: as in ``kda.fwd``.
     """
-    import torch
     B, T, Hk, H, N, K, V, per_token, host = _check_inputs(q, k, v, decay, cu_seqlens, cu_seqlens_host)
-    if out.dtype != torch.bfloat16 or out.shape != v.shape or not out.is_contiguous() or out.device != q.device:
+    if (out.dtype is not torch.bfloat16 or out.shape != v.shape or not out.is_contiguous()
+            or out.get_device() != q.get_device()):
         raise ValueError("out must be a contiguous bf16 [B, T, H, 128] tensor on q's device")
-    kinds = (torch.bfloat16, torch.float32)
-    _check_state("initial_state", initial_state, (N, H, V, K), q.device, kinds)
-    _check_state("final_state", final_state, (N, H, V, K), q.device, kinds)
-    if initial_state is not None and final_state is not None and initial_state.dtype != final_state.dtype:
+    _check_state("initial_state", initial_state, (N, H, V, K), q)
+    _check_state("final_state", final_state, (N, H, V, K), q)
+    h0_code, ht_code = _code(initial_state), _code(final_state)
+    if h0_code and ht_code and h0_code != ht_code:
         raise ValueError("initial_state and final_state dtypes must match")
+    index = _gpu_index(q)
+    L = lib()
     varlen = cu_seqlens is not None
-    need = (256 if varlen else 0) if _recurrent else workspace_size(B, T, H, N if varlen else 0, varlen)
-    call = lib().kda_lin_fwd_recurrent if _recurrent else lib().kda_lin_fwd
-    with torch.cuda.device(q.device):
-        workspace = _workspace(workspace, need, q.device, stream)
-        st = call(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), int(per_token), float(scale), _ptr(out),
-                  _ptr(initial_state), _state_code(initial_state), _ptr(final_state), _state_code(final_state),
-                  _ptr(cu_seqlens), None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
-                  _row_strides(q, k, v), _ptr(workspace), _bytes(workspace), _stream_handle(stream, q.device))
+    if _recurrent:
+        need, call = (256 if varlen else 0), L.kda_lin_fwd_recurrent
+    else:
+        need, call = L.kda_lin_fwd_workspace_size(B, T, H, N if varlen else 0, varlen), L.kda_lin_fwd
+    with _On(index):
+        if workspace is not None or need:
+            workspace = _workspace(workspace, need, index, stream)
+        st = call(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, scale, out.data_ptr(),
+                  _ptr(initial_state), h0_code, _ptr(final_state), ht_code, _ptr(cu_seqlens),
+                  None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
+                  _row_strides(q, k, v), _ptr(workspace), _bytes(workspace), _raw_stream(stream, index))
     if st != KDA_OK:
         raise KDAError(st, "kda_lin_fwd_recurrent" if _recurrent else "kda_lin_fwd")
     return workspace
@@ -143,32 +193,32 @@ def bwd(q, k, v, decay, scale, dout, initial_state=None, dfinal_state=None, cu_s
     (fp32, shape of decay; with need_ddecay), dinitial_state (fp32 [N, H, 128, 128]) and the
     workspace used.
     """
-    import torch
     B, T, Hk, H, N, K, V, per_token, host = _check_inputs(q, k, v, decay, cu_seqlens, cu_seqlens_host)
-    dev = q.device
-    if dout.dtype != torch.bfloat16 or dout.shape != v.shape or not dout.is_contiguous() or dout.device != dev:
+    if (dout.dtype is not torch.bfloat16 or dout.shape != v.shape or not dout.is_contiguous()
+            or dout.get_device() != q.get_device()):
         raise ValueError("dout must be a contiguous bf16 [B, T, H, 128] tensor on q's device")
-    _check_state("initial_state", initial_state, (N, H, V, K), dev, (torch.bfloat16, torch.float32))
-    _check_state("dfinal_state", dfinal_state, (N, H, V, K), dev, (torch.float32,))
+    _check_state("initial_state", initial_state, (N, H, V, K), q)
+    _check_state("dfinal_state", dfinal_state, (N, H, V, K), q, bf16_too=False)
+    index = _gpu_index(q)
     varlen = cu_seqlens is not None
-    need = bwd_workspace_size(B, T, Hk, H, N if varlen else 0, varlen, need_ddecay)
-    with torch.cuda.device(dev):
-        empty = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
-        r = {"dq": empty((B, T, Hk, K), torch.bfloat16), "dk": empty((B, T, Hk, K), torch.bfloat16),
-             "dv": empty((B, T, H, V), torch.bfloat16), "dinitial_state": empty((N, H, V, K), torch.float32)}
+    L = lib()
+    need = L.kda_lin_bwd_workspace_size(B, T, Hk, H, N if varlen else 0, varlen, bool(need_ddecay))
+    with _On(index):
+        bf16, fp32 = torch.bfloat16, torch.float32
+        r = {"dq": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
+             "dk": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
+             "dv": torch.empty((B, T, H, V), dtype=bf16, device=index),
+             "dinitial_state": torch.empty((N, H, V, K), dtype=fp32, device=index)}
         if need_ddecay:
-            r["ddecay"] = empty(tuple(decay.shape), torch.float32)
-        if stream is not None and stream != torch.cuda.current_stream(dev):
-            for t in r.values():
-                t.record_stream(stream)
-        workspace = _workspace(workspace, max(need, 1), dev, stream)
-        st = lib().kda_lin_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), int(per_token), float(scale),
-                               _ptr(initial_state), _state_code(initial_state), _ptr(dout), _ptr(dfinal_state),
-                               _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r.get("ddecay")),
-                               _ptr(r["dinitial_state"]), _ptr(cu_seqlens),
-                               None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
-                               _row_strides(q, k, v), _ptr(workspace), _bytes(workspace),
-                               _stream_handle(stream, dev))
+            r["ddecay"] = torch.empty(decay.shape, dtype=fp32, device=index)
+        _used_on(stream, index, *r.values())
+        workspace = _workspace(workspace, need or 1, index, stream)
+        st = L.kda_lin_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, scale,
+                           _ptr(initial_state), _code(initial_state), dout.data_ptr(), _ptr(dfinal_state),
+                           r["dq"].data_ptr(), r["dk"].data_ptr(), r["dv"].data_ptr(), _ptr(r.get("ddecay")),
+                           r["dinitial_state"].data_ptr(), _ptr(cu_seqlens),
+                           None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
+                           _row_strides(q, k, v), workspace.data_ptr(), _bytes(workspace), _raw_stream(stream, index))
     if st != KDA_OK:
         raise KDAError(st, "kda_lin_bwd")
     r["workspace"] = workspace

@@ -7,13 +7,15 @@ Argument marshalling only; there is no fallback path.
 """
 from __future__ import annotations
 
-import ctypes
 import math
 
-from .kda import KDA_OK, KDAError, _ptr, _stream_handle, lib
-from .linattn import _bytes, _workspace
+import torch
+
+from .kda import KDA_OK, KDAError, _ptr, lib
+from .linattn import _bytes, _gpu_index, _On, _raw_stream, _row_strides, _used_on, _workspace
 
 NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
+_DTYPES = {torch.bfloat16: 1, torch.float32: 2, torch.float16: 3}
 
 
 def inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_context=None, beta_fast=32.0,
@@ -29,7 +31,6 @@ def inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_con
                 that turns less than beta_slow times is divided by factor, a linear ramp over
                 the pair's index between; the attention factor is 0.1 ln(factor) + 1.
     """
-    import torch
     R = int(rotary_dim)
     if R < 0 or R % 2:
         raise ValueError("rotary_dim must be even and not negative")
@@ -60,48 +61,35 @@ def inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_con
     return f.to(device=device, dtype=torch.float32), attention_factor
 
 
-def _dtype_code(t):
-    import torch
-    code = {torch.bfloat16: 1, torch.float32: 2, torch.float16: 3}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"q and k must be bf16, fp16 or fp32, got {t.dtype}")
-    return code
-
-
-def _strides(tensors):
-    if all(t.is_contiguous() for t in tensors):
-        return None
-    got = []
-    for t in tensors:
-        got += [0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride()[:3])]
-    return (ctypes.c_int64 * len(got))(*got)
-
-
-def _check(q, k, positions, inv_freq, norm, weights, **others):
-    import torch
-    if q.dim() != 4 or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+def _check(q, k, positions, inv_freq, norm, q_weight, k_weight, like_q, like_k):
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0] or ks[1] != qs[1] or ks[3] != qs[3]:
         raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
-    code = _dtype_code(q)
-    for name, (t, like) in {"q": (q, q), "k": (k, k), **others}.items():
-        if t.shape != like.shape or t.dtype != q.dtype or t.device != q.device or (t.stride(3) != 1 and t.shape[3] != 1):
-            raise ValueError(f"{name} must be {list(like.shape)}, of q's dtype and device, with contiguous channels")
-    B, T, Hq, D = q.shape
-    if positions is not None and (positions.dtype != torch.int64 or tuple(positions.shape) != (B, T)
-                                  or not positions.is_contiguous() or positions.device != q.device):
+    dtype, at = q.dtype, q.get_device()
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"q and k must be bf16, fp16 or fp32, got {dtype}")
+    B, T, Hq, D = qs
+    for t, shape in ((q, qs), (k, ks), (like_q, qs), (like_k, ks)):
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != at or (t.stride(3) != 1 and D != 1):
+            raise ValueError("k, and the outputs or gradients of q's and k's shapes, must be of q's dtype and device, "
+                             "all with contiguous channels")
+    if positions is not None and (positions.dtype is not torch.int64 or positions.shape != (B, T)
+                                  or not positions.is_contiguous() or positions.get_device() != at):
         raise ValueError("positions must be a contiguous int64 [B, T] tensor on q's device")
     R = 0
     if inv_freq is not None:
-        if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
-                or inv_freq.device != q.device):
+        if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
+                or inv_freq.get_device() != at):
             raise ValueError("inv_freq must be a contiguous fp32 [rotary_dim / 2] tensor on q's device")
         R = 2 * inv_freq.numel()
     if norm not in NORMS:
         raise ValueError(f"norm must be one of None, 'rms', 'l2', got {norm!r}")
-    for name, w in weights.items():
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (D,) or not w.is_contiguous()
-                              or w.device != q.device):
-            raise ValueError(f"{name} must be a contiguous fp32 [D] tensor on q's device")
-    return B, T, Hq, k.shape[2], D, R, code
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not torch.float32 or w.shape != (D,) or not w.is_contiguous()
+                              or w.get_device() != at):
+            raise ValueError("q_weight and k_weight must be contiguous fp32 [D] tensors on q's device")
+    return B, T, Hq, ks[2], D, R, code
 
 
 def fwd(q, k, positions, inv_freq, q_out, k_out, *, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
@@ -114,14 +102,13 @@ def fwd(q, k, positions, inv_freq, q_out, k_out, *, q_weight=None, k_weight=None
     fp32 [D] or None.  norm: "rms", "l2" or None.  interleaved: pairs (2i, 2i + 1) instead of
     (i, i + rotary_dim / 2).
     """
-    import torch
-    B, T, Hq, Hk, D, R, code = _check(q, k, positions, inv_freq, norm, {"q_weight": q_weight, "k_weight": k_weight},
-                                      q_out=(q_out, q), k_out=(k_out, k))
-    with torch.cuda.device(q.device):
-        st = lib().kda_qk_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight),
-                               _ptr(inv_freq) if R else None, _ptr(positions), B, T, Hq, Hk, D, R, code, NORMS[norm],
-                               float(eps), int(bool(interleaved)), float(attention_factor),
-                               _strides((q, k, q_out, k_out)), _stream_handle(stream, q.device))
+    B, T, Hq, Hk, D, R, code = _check(q, k, positions, inv_freq, norm, q_weight, k_weight, q_out, k_out)
+    index = _gpu_index(q)
+    with _On(index):
+        st = lib().kda_qk_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight),
+                               _ptr(k_weight), _ptr(inv_freq) if R else None, _ptr(positions), B, T, Hq, Hk, D, R, code,
+                               NORMS[norm], eps, bool(interleaved), attention_factor,
+                               _row_strides(q, k, q_out, k_out), _raw_stream(stream, index))
     if st != KDA_OK:
         raise KDAError(st, "kda_qk_rope")
 
@@ -130,28 +117,25 @@ def bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=No
         interleaved=False, attention_factor=1.0, workspace=None, stream=None):
     """Gradients of ``fwd`` from its inputs and dq_out, dk_out (of q's and k's shape and dtype).  Returns a dict: dq, dk
     (contiguous, of q's dtype) and, for the weights given, dq_weight, dk_weight (fp32 [D])."""
-    import torch
-    B, T, Hq, Hk, D, R, code = _check(q, k, positions, inv_freq, norm, {"q_weight": q_weight, "k_weight": k_weight},
-                                      dq_out=(dq_out, q), dk_out=(dk_out, k))
-    dev = q.device
-    with torch.cuda.device(dev):
-        r = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev)}
+    B, T, Hq, Hk, D, R, code = _check(q, k, positions, inv_freq, norm, q_weight, k_weight, dq_out, dk_out)
+    index = _gpu_index(q)
+    L = lib()
+    with _On(index):
+        r = {"dq": torch.empty(q.shape, dtype=q.dtype, device=index),
+             "dk": torch.empty(k.shape, dtype=q.dtype, device=index)}
         if q_weight is not None:
-            r["dq_weight"] = torch.empty(D, dtype=torch.float32, device=dev)
+            r["dq_weight"] = torch.empty(D, dtype=torch.float32, device=index)
         if k_weight is not None:
-            r["dk_weight"] = torch.empty(D, dtype=torch.float32, device=dev)
-        if stream is not None and stream != torch.cuda.current_stream(dev):
-            for t in r.values():
-                t.record_stream(stream)
-        sums = q_weight is not None or k_weight is not None
-        need = int(lib().kda_qk_rope_bwd_workspace_size(B, T, Hq, Hk, D)) if sums else 0
-        workspace = _workspace(workspace, need, dev, stream)
-        st = lib().kda_qk_rope_bwd(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(r["dq"]), _ptr(r["dk"]),
-                                   _ptr(q_weight), _ptr(k_weight), _ptr(r.get("dq_weight")), _ptr(r.get("dk_weight")),
-                                   _ptr(inv_freq) if R else None, _ptr(positions), B, T, Hq, Hk, D, R, code,
-                                   NORMS[norm], float(eps), int(bool(interleaved)), float(attention_factor),
-                                   _strides((q, k, dq_out, dk_out, r["dq"], r["dk"])), _ptr(workspace),
-                                   _bytes(workspace), _stream_handle(stream, dev))
+            r["dk_weight"] = torch.empty(D, dtype=torch.float32, device=index)
+        _used_on(stream, index, *r.values())
+        need = L.kda_qk_rope_bwd_workspace_size(B, T, Hq, Hk, D) if len(r) > 2 else 0
+        workspace = _workspace(workspace, need, index, stream)
+        st = L.kda_qk_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), r["dq"].data_ptr(),
+                               r["dk"].data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(r.get("dq_weight")),
+                               _ptr(r.get("dk_weight")), _ptr(inv_freq) if R else None, _ptr(positions), B, T, Hq, Hk, D,
+                               R, code, NORMS[norm], eps, bool(interleaved), attention_factor,
+                               _row_strides(q, k, dq_out, dk_out, r["dq"], r["dk"]), _ptr(workspace),
+                               _bytes(workspace), _raw_stream(stream, index))
     if st != KDA_OK:
         raise KDAError(st, "kda_qk_rope_bwd")
     return r
