@@ -56,7 +56,7 @@ kda_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, b
 bool make_layout(const Sizes &z, bool bwd, bool ddecay, kda::LinLayout *L)
 {
     using kda::kAlign;
-    L->plan = kda::lin_plan(z.B, z.T, z.H, z.N, z.varlen, kda::kLinGroups, ddecay ? kda::kLinGradSeg : 0);
+    L->plan = kda::lin_plan(z.B, z.T, z.H, z.N, z.varlen, bwd ? 3 : 1, ddecay ? kda::kLinGradSeg : 0);
     const kda::LinPlan &p = L->plan;
     if (p.rows * p.P > (((int64_t)1 << 31) - 64) / (64 * z.H))  // grid sizes
         return false;

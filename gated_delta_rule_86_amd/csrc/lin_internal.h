@@ -12,9 +12,9 @@
 namespace kda {
 
 constexpr int kLC = 64;                       // tokens per chunk
-constexpr int64_t kLinGroups = 512;           // workgroups that fill the chip: two on each of 256 CUs
+constexpr int64_t kLinSlots = 512;            // workgroups that run at once: two on each of 256 CUs
 constexpr int64_t kLinMinSeg = 256;           // shortest segment that a cut leaves, in tokens
-constexpr int64_t kLinGradSeg = 512;          // longest segment when the decay's gradient is wanted
+constexpr int64_t kLinGradSeg = 1024;         // longest segment when the decay's gradient is wanted
 constexpr size_t kLinStateBytes = (size_t)kD * kD * sizeof(float);
 
 // Segments.  The packed tokens of a batch row (the one row of a varlen batch) are cut into P
@@ -29,25 +29,49 @@ struct LinPlan {
     int64_t n_seq;     // N, or B without cu_seqlens
 };
 
-inline LinPlan lin_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool varlen, int64_t groups, int64_t max_len)
+// Time of `groups` workgroups of `chunks` chunks each, in chunks of a full chip: rounds of kLinSlots, each with
+// `fixed` for its state and first loads; at most one workgroup on a CU runs its chunks in about 0.6 of the time that
+// two take side by side (T = 262144, H = 8: 815 us with 256 workgroups, 700 us with 512).
+inline double lin_rounds(int64_t groups, int64_t chunks, double fixed)
+{
+    const double round = (double)cdiv(groups, kLinSlots) * ((double)chunks + fixed);
+    return groups <= kLinSlots / 2 ? 0.6 * round : round;
+}
+
+// walks: how many share the segments (1 forward; 3 backward, two of which need states).  The cut that takes the least
+// time: the walks, the states pass (reads two of three inputs), the scan (128 KiB per slot at 5 TB/s against 9.6 us
+// for a chunk of the full chip) and two more launches.  Measured with B = 2, T = 4096, H = 16, decays per token:
+// backward 236 us with P = 16, 204 us with P = 5.
+inline LinPlan lin_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool varlen, int64_t walks, int64_t max_len)
 {
     LinPlan p;
     p.rows = varlen ? 1 : B;
     p.n_seq = varlen ? N : B;
-    int64_t P = 1;
-    if (p.rows * H < groups)
-        P = cdiv(groups, p.rows * H);
-    const int64_t most = T / kLinMinSeg;
-    if (P > most)
-        P = most;
-    if (max_len > 0 && P < cdiv(T, max_len))
-        P = cdiv(T, max_len);
-    if (P < 1)
-        P = 1;
-    p.len = cdiv(cdiv(T, P), kLC) * kLC;
-    if (p.len < kLC)
-        p.len = kLC;
-    p.P = T > 0 ? cdiv(T, p.len) : 1;
+    const int64_t chains = p.rows * H, leads = walks > 1 ? 2 : 1;
+    const int64_t least = max_len > 0 ? cdiv(T, max_len) : 1;
+    int64_t most = T / kLinMinSeg;
+    if (most > cdiv(4 * kLinSlots, chains))
+        most = cdiv(4 * kLinSlots, chains);
+    if (most < least)
+        most = least;
+    if (most < 1)
+        most = 1;
+    double best = 0.0;
+    p.P = 0;
+    for (int64_t P = least < 1 ? 1 : least; P <= most; ++P) {
+        int64_t len = cdiv(cdiv(T, P), kLC) * kLC;
+        if (len < kLC)
+            len = kLC;
+        const int64_t got = T > 0 ? cdiv(T, len) : 1, chunks = len / kLC;
+        double cost = lin_rounds(walks * chains * got, chunks, 2.5);
+        if (got > 1)
+            cost += 0.45 * lin_rounds(leads * chains * got, chunks, 1.5) + 0.0027 * (double)(leads * chains * got) + 0.4;
+        if (p.P == 0 || cost < best) {
+            best = cost;
+            p.P = got;
+            p.len = len;
+        }
+    }
     return p;
 }
 
