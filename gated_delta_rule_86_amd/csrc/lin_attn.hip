@@ -516,23 +516,27 @@ struct Cutter {
 struct Terms3 {
     u32x4 h, m, l;
 };
-__device__ __forceinline__ void cut3(const float *x, Terms3 &t, const Cutter &cut)
+// two terms (h, m) or three
+template <bool kThree>
+__device__ __forceinline__ void cut_terms(const float *x, Terms3 &t, const Cutter &cut)
 {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         t.h[e] = pack2(x[2 * e], x[2 * e + 1]);
         const float a1 = cut.rest0(t.h[e], x[2 * e]), b1 = cut.rest1(t.h[e], x[2 * e + 1]);
         t.m[e] = pack2(a1, b1);
-        t.l[e] = pack2(cut.rest0(t.m[e], a1), cut.rest1(t.m[e], b1));
+        if (kThree)
+            t.l[e] = pack2(cut.rest0(t.m[e], a1), cut.rest1(t.m[e], b1));
     }
 }
 
 // S += sum over the chunk's tokens of (win v) k^T.  Source rows are weighted on the way in,
 // in fp32, and go into the product as three bf16 terms (24 bits), so that an fp32 state keeps
-// fp32's accuracy.
+// fp32's accuracy; as two (16 bits) where the state is seen through bf16 alone.
 //
 // Steps of 16 tokens, in a pipeline by hand: while a step's 12 matrix instructions run, the next step's K
 // operand is on its way from LDS and its weighted rows are cut.
+template <bool kThree>
 __device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const float *win, int tok, const Cutter &cut)
 {
     const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&win[tok]);
@@ -543,7 +547,7 @@ __device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const 
         x[2 * e] = lo_f(v[e]) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
         x[2 * e + 1] = hi_f(v[e]) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
     }
-    cut3(x, t, cut);
+    cut_terms<kThree>(x, t, cut);
 }
 
 // The scheduler keeps the order of these groups: n x { 1 matrix instruction, v vector instructions }.
@@ -557,7 +561,7 @@ __device__ __forceinline__ void interleave()
     }
 }
 
-template <bool kAhead>
+template <bool kAhead, bool kThree>
 __device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const float *win,
                                              const Lanes &ln, int half, const Cutter &cut)
 {
@@ -569,9 +573,9 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
                 kf[kt] = key_frag(ktile, ln, kt, j);
-            weighted_terms(t, vf[j], win, 16 * j + 8 * half, cut);
+            weighted_terms<kThree>(t, vf[j], win, 16 * j + 8 * half, cut);
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
+            for (int kt = 0; kt < 4 && kThree; ++kt)
                 S.t[kt] = mfma(kf[kt], t.l, S.t[kt]);
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
@@ -588,7 +592,7 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
         kf[0][kt] = key_frag(ktile, ln, kt, 0);
-    weighted_terms(t[0], vf[0], win, 8 * half, cut);
+    weighted_terms<kThree>(t[0], vf[0], win, 8 * half, cut);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -598,10 +602,10 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
             for (int kt = 0; kt < 4; ++kt)
                 kf[c ^ 1][kt] = key_frag(ktile, ln, kt, j + 1);
             __builtin_amdgcn_sched_barrier(0);
-            weighted_terms(t[c ^ 1], vf[j + 1], win, 16 * (j + 1) + 8 * half, cut);
+            weighted_terms<kThree>(t[c ^ 1], vf[j + 1], win, 16 * (j + 1) + 8 * half, cut);
         }
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int kt = 0; kt < 4 && kThree; ++kt)
             S.t[kt] = mfma(kf[c][kt], t[c].l, S.t[kt]);
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -610,7 +614,7 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
         for (int kt = 0; kt < 4; ++kt)
             S.t[kt] = mfma(kf[c][kt], t[c].h, S.t[kt]);
         if (j < 3)
-            interleave<12, 5>();
+            interleave<kThree ? 12 : 8, 5>();
         __builtin_amdgcn_sched_barrier(0);
     }
 }
@@ -719,7 +723,7 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v[buf], ln, jj);
-        state_update<true>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
+        state_update<true, true>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
         if (!more)
             break;
         if (wave == 3)
@@ -788,7 +792,10 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
 // out.  Their sums over many tokens cancel, so weights and states then go into the products
 // as three terms, and the own pairs are added to the rows outside the matrix product.
-template <bool kDots, bool rev>
+// kThree: the state keeps fp32's accuracy (see state_update).  Not where it is seen through bf16 alone: bf16 states
+// forwards, dq and dk without dots backwards (16 of 98 matrix instructions less: T = 38000, H = 32, Hk = 8 in all
+// 484 -> 454 us).
+template <bool kDots, bool rev, bool kThree>
 __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, unsigned char *lds_raw)
 {
     LdsWalk &lds = *reinterpret_cast<LdsWalk *>(lds_raw);
@@ -939,7 +946,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
-                cut3(x, sc[jj & 1], cut);
+                cut_terms<false>(x, sc[jj & 1], cut);
             };
             if constexpr (kDots) {  // registers are short: no step ahead
 #pragma unroll
@@ -950,7 +957,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
-                    cut3(x, sc[0], cut);
+                    cut_terms<true>(x, sc[0], cut);
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt)
                         O[tt] = mfma(sc[0].l, qf[0][tt], O[tt]);
@@ -1094,7 +1101,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         }
         if (d.mul != 1.0f)
             state_scale(S, d.mul);
-        state_update<!kDots>(S, lds.k, vf, d.win, ln, half, cut);
+        state_update<!kDots, kThree>(S, lds.k, vf, d.win, ln, half, cut);
         const double held_now = d.held;
         if (wave == 3 && n.len > 0)
             make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
@@ -1141,10 +1148,27 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
         *a.status = 0;
     const LinRole &ro = a.role[blockIdx.y];
     const int64_t seg = at / a.H, h = at - seg * a.H;
-    if (ro.rev)
-        walk<kDots, true>(a, ro, seg, h, lds_raw);
-    else
-        walk<kDots, false>(a, ro, seg, h, lds_raw);
+    if constexpr (kDots) {
+        if (!ro.rev)
+            walk<true, false, true>(a, ro, seg, h, lds_raw);
+        else if (ro.dots)
+            walk<true, true, true>(a, ro, seg, h, lds_raw);
+        else
+            walk<false, true, true>(a, ro, seg, h, lds_raw);
+    } else {
+        const bool three = ro.three != 0;
+        if (ro.rev) {
+            if (three)
+                walk<false, true, true>(a, ro, seg, h, lds_raw);
+            else
+                walk<false, true, false>(a, ro, seg, h, lds_raw);
+        } else {
+            if (three)
+                walk<false, false, true>(a, ro, seg, h, lds_raw);
+            else
+                walk<false, false, false>(a, ro, seg, h, lds_raw);
+        }
+    }
 }
 
 // In-place state carry with cut rows: the workgroup that ends a sequence may finish before the one
@@ -1215,7 +1239,9 @@ __global__ __launch_bounds__(256) void lin_fold_kernel(const float *xq, const fl
     }
 }
 
-// Sum over the 256 threads of a workgroup, in a fixed order; every thread gets it.
+constexpr int kGradThreads = (int)kLinGradSeg;  // a thread for each token of a segment
+
+// Sum over the threads of a workgroup, in a fixed order; every thread gets it.
 __device__ __forceinline__ double wg_sum(double x, double *red, int tid)
 {
 #pragma unroll
@@ -1225,13 +1251,19 @@ __device__ __forceinline__ double wg_sum(double x, double *red, int tid)
     if ((tid & 63) == 0)
         red[tid >> 6] = x;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kGradThreads / 64; ++w)
+        s += red[w];
+    return s;
 }
 
-// dg of one segment and head: from the segment's end, where <S, dS> is known, back to its start
-__global__ __launch_bounds__(256) void lin_ddecay_kernel(LinArgs a, float *ddecay, double *part)
+// dg of one segment and head: from the end of each piece, where <S, dS> is known, back to its start.  Latency:
+// the tokens' dots and the states are asked for together (T = 4096, H = 16, 5 segments: 14 -> 10 us against 256
+// threads that took four turns).
+__global__ __launch_bounds__(kGradThreads) void lin_ddecay_kernel(LinArgs a, float *ddecay, double *part)
 {
-    __shared__ double red[4];
+    __shared__ double red[kGradThreads / 64];
     const int64_t seg = blockIdx.x / a.H, h = blockIdx.x - seg * a.H;
     const int64_t row = seg / a.P, j = seg - row * a.P;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -1249,50 +1281,45 @@ __global__ __launch_bounds__(256) void lin_ddecay_kernel(LinArgs a, float *ddeca
         w.set_piece();
         if (w.p1 <= w.p0)
             continue;
-        double run = 0.0;  // sum of db behind the block, and <S, dS> at the piece's end
+        // one token per thread: a piece is at most a segment long, see lin_plan
+        const int64_t t = w.p0 + tid, at = (row * a.T + t) * a.H + h;
+        const bool on = t < w.p1;
+        const double x = on ? (double)rq.dots[at] - (double)rk.dots[at] : 0.0;
+        double end = 0.0;
         if (w.pflags & kFromSlot) {
-            const f32x4 *x = reinterpret_cast<const f32x4 *>(rq.slots + (size_t)(seg * a.H + h) * kD * kD);
-            const f32x4 *y = reinterpret_cast<const f32x4 *>(rk.slots + (size_t)((seg + 1) * a.H + h) * kD * kD);
+            const f32x4 *p = reinterpret_cast<const f32x4 *>(rq.slots + (size_t)(seg * a.H + h) * kD * kD);
+            const f32x4 *q = reinterpret_cast<const f32x4 *>(rk.slots + (size_t)((seg + 1) * a.H + h) * kD * kD);
             float d = 0.0f;
-            for (int e = tid; e < kD * kD / 4; e += 256) {
-                const f32x4 p = x[e], q = y[e];
-                d += (p[0] * q[0] + p[1] * q[1]) + (p[2] * q[2] + p[3] * q[3]);
-            }
-            run = wg_sum((double)d, red, tid);
-        } else if (rq.xfin) {
-            run = (double)rq.xfin[w.seq_index() * a.H + h];
-        }
-        for (int64_t b = w.p0 + (w.p1 - w.p0 - 1) / 256 * 256; b >= w.p0; b -= 256) {
-            const int64_t t = b + tid;
-            double x = 0.0;
-            const int64_t at = (row * a.T + t) * a.H + h;
-            if (t < w.p1)
-                x = (double)rq.dots[at] - (double)rk.dots[at];
-            double s = x;  // inclusive sum over this and the later tokens of the block
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const double u = __shfl_down(s, o);
-                if (lane + o < 64)
-                    s += u;
+            for (int e = 0; e < kD * kD / 4; e += kGradThreads) {
+                const f32x4 y = p[e + tid], z = q[e + tid];
+                d += (y[0] * z[0] + y[1] * z[1]) + (y[2] * z[2] + y[3] * z[3]);
             }
-            __syncthreads();
-            if (lane == 0)
-                red[wave] = s;
-            __syncthreads();
-            double later = 0.0;
-            for (int k = 3; k > wave; --k)
-                later += red[k];
-            const double all = (red[0] + red[1]) + (red[2] + red[3]);
-            if (t < w.p1) {
-                const double dg = run + later + s;
-                if (a.per_token) {
-                    const float g = a.decay[at];
-                    ddecay[at] = g > kLowest && g <= 0.0f ? (float)dg : 0.0f;
-                } else {
-                    total += dg;
-                }
+            end = wg_sum((double)d, red, tid);
+        } else if (rq.xfin) {
+            end = (double)rq.xfin[w.seq_index() * a.H + h];
+        }
+        double s = x;  // sum over this and the later tokens
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double u = __shfl_down(s, o);
+            if (lane + o < 64)
+                s += u;
+        }
+        __syncthreads();
+        if (lane == 0)
+            red[wave] = s;
+        __syncthreads();
+        for (int k = kGradThreads / 64 - 1; k > wave; --k)
+            end += red[k];
+        if (on) {
+            const double dg = end + s;
+            if (a.per_token) {
+                const float g = a.decay[at];
+                ddecay[at] = g > kLowest && g <= 0.0f ? (float)dg : 0.0f;
+            } else {
+                total += dg;
             }
-            run += all;
         }
     }
     if (!a.per_token) {
@@ -1473,7 +1500,7 @@ hipError_t lin_launch_grad_tail(const LinArgs &a, const LinBwdExtra &e, hipStrea
                            a.rows * a.T, e.Hk, a.H / e.Hk, a.cu ? a.status : nullptr);
     }
     if (e.ddecay) {
-        hipLaunchKernelGGL(lin_ddecay_kernel, dim3((unsigned)(a.rows * a.P * a.H)), dim3(256), 0, s, a, e.ddecay,
+        hipLaunchKernelGGL(lin_ddecay_kernel, dim3((unsigned)(a.rows * a.P * a.H)), dim3(kGradThreads), 0, s, a, e.ddecay,
                            e.part);
         if (!a.per_token)
             hipLaunchKernelGGL(lin_ddecay_sum_kernel, dim3((unsigned)a.H), dim3(64), 0, s, a, e.part, e.ddecay);
