@@ -14,7 +14,9 @@ namespace kda {
 constexpr int kLC = 64;                       // tokens per chunk
 constexpr int64_t kLinSlots = 512;            // workgroups that run at once: two on each of 256 CUs
 constexpr int64_t kLinMinSeg = 256;           // shortest segment that a cut leaves, in tokens
-constexpr int64_t kLinGradSeg = 1024;         // longest segment when the decay's gradient is wanted
+// Longest segment when the decay's gradient is wanted: it sums rounding errors from the segment's end on.  B = 2,
+// T = 4096, H = 16 against 64 bits: 1.5e-6 with 832 tokens (202 us), 1.2e-6 with 512 (201 us), 0.9e-6 with 256 (231 us).
+constexpr int64_t kLinGradSeg = 512;
 constexpr size_t kLinStateBytes = (size_t)kD * kD * sizeof(float);
 
 // Segments.  The packed tokens of a batch row (the one row of a varlen batch) are cut into P
@@ -40,8 +42,8 @@ inline double lin_rounds(int64_t groups, int64_t chunks, double fixed)
 
 // walks: how many share the segments (1 forward; 3 backward, two of which need states).  The cut that takes the least
 // time: the walks, the states pass (reads two of three inputs), the scan (128 KiB per slot at 5 TB/s against 9.6 us
-// for a chunk of the full chip) and two more launches.  Measured with B = 2, T = 4096, H = 16, decays per token:
-// backward 236 us with P = 16, 204 us with P = 5.
+// for a chunk of the full chip) and two more launches.  B = 2, T = 4096, H = 16: forward 98 us with P = 16, 89 us with
+// P = 8.
 inline LinPlan lin_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool varlen, int64_t walks, int64_t max_len)
 {
     LinPlan p;

@@ -383,7 +383,7 @@ kda_status kda_lin_bwd(const void *q, const void *k, const void *v, const float 
 
 /*
  * kda_lin_bwd_workspace_size -- 256 bytes; per head and segment (see kda_lin_fwd_workspace_size; at
- * most 1024 tokens long when need_ddecay) two fp32 states; with Hk < H two fp32 [B, T, H, 128];
+ * most 512 tokens long when need_ddecay) two fp32 states; with Hk < H two fp32 [B, T, H, 128];
  * with need_ddecay two fp32 [B, T, H] and small sums.  Returns 0 for invalid sizes.
  */
 size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens,

@@ -113,14 +113,14 @@ def inputs(B, T, Hk, H, seed, decay="token", strided=False, lo=1e-3, device="cud
 
 
 def close_ddecay(got, want, q, dq, k, dk, decay, final=None, dfinal=None, what="ddecay"):
-    """dg_t = sum over the later tokens u of its segment (1024 at most) of q_u.dq_u - k_u.dk_u, plus <S, dS> at its end.
+    """dg_t = sum over the later tokens u of its segment (512 at most) of q_u.dq_u - k_u.dk_u, plus <S, dS> at its end.
 
     Rounding errors of one product q_u.dq_u against |q_u| |dq_u| / sqrt(128), the size of such a product of
     independent vectors: two exponentials (2^-23 each, one ulp), two chains of 8 to 12 matrix steps (each step rounds
     the running sum, 2^-24: 2^-21 together for each chain), the row product of 32 fused steps and a tree
     (sqrt(35) 2^-24 = 2^-21.4); in all 2^-19.6, and the same for k.dk, independent from token to token.  <S, dS> sums
     16384 products, 64 in a row (2^-21), of states with two such factors (2^-22): 2^-20.4 |S| |dS| / 128.
-    A token's error adds up over the n_u <= 1024 tokens that see it: in the norm over tokens sqrt(n_u), in a per-head
+    A token's error adds up over the n_u <= 512 tokens that see it: in the norm over tokens sqrt(n_u), in a per-head
     decay's sum n_u."""
     B, T, H = q.shape[0], q.shape[1], decay.shape[-1]
     if T == 0:
@@ -130,12 +130,12 @@ def close_ddecay(got, want, q, dq, k, dk, decay, final=None, dfinal=None, what="
     norm = lambda x: x.double().norm(dim=-1)  # noqa: E731
     a = ((norm(q) * norm(dq)) ** 2 + (norm(k) * norm(dk)) ** 2) / D * 2.0 ** -39.2
     a = a.repeat_interleave(rep, 2)                                    # [B, T, H]
-    n = torch.arange(1, T + 1, device=q.device).clamp(max=1024).double()[None, :, None]
+    n = torch.arange(1, T + 1, device=q.device).clamp(max=512).double()[None, :, None]
     x = torch.zeros(H, dtype=torch.float64, device=q.device)
     if dfinal is not None:
         x = (final.double().flatten(2).norm(dim=-1) * dfinal.double().flatten(2).norm(dim=-1) * 2.0 ** -20.4 / D).square().sum(0)
     err = (got.double() - want.double())
-    most = min(T, 1024)
+    most = min(T, 512)
     if decay.dim() == 3:
         tol = float(((a * n).sum() + (x * most).sum()).sqrt())
         assert float(err.norm()) <= tol + 2.0 ** -24 * float(want.norm()), (what, float(err.norm()), tol)
