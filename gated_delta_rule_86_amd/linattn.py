@@ -168,7 +168,7 @@ def fwd(q, k, v, decay, scale, out, initial_state=None, final_state=None, cu_seq
     with _On(index):
         if workspace is not None or need:
             workspace = _workspace(workspace, need, index, stream)
-        st = call(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, scale, out.data_ptr(),
+        st = call(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, float(scale), out.data_ptr(),
                   _ptr(initial_state), h0_code, _ptr(final_state), ht_code, _ptr(cu_seqlens),
                   None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
                   _row_strides(q, k, v), _ptr(workspace), _bytes(workspace), _raw_stream(stream, index))
@@ -213,7 +213,7 @@ def bwd(q, k, v, decay, scale, dout, initial_state=None, dfinal_state=None, cu_s
             r["ddecay"] = torch.empty(decay.shape, dtype=fp32, device=index)
         _used_on(stream, index, *r.values())
         workspace = _workspace(workspace, need or 1, index, stream)
-        st = L.kda_lin_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, scale,
+        st = L.kda_lin_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, float(scale),
                            _ptr(initial_state), _code(initial_state), dout.data_ptr(), _ptr(dfinal_state),
                            r["dq"].data_ptr(), r["dk"].data_ptr(), r["dv"].data_ptr(), _ptr(r.get("ddecay")),
                            r["dinitial_state"].data_ptr(), _ptr(cu_seqlens),

@@ -34,6 +34,8 @@ def inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_con
     R = int(rotary_dim)
     if R < 0 or R % 2:
         raise ValueError("rotary_dim must be even and not negative")
+    if not base > 1.0:
+        raise ValueError("base must be above 1")
     if not factor >= 1.0:
         raise ValueError("factor must be at least 1")
     i = torch.arange(0, R, 2, dtype=torch.float64)
@@ -107,7 +109,7 @@ def fwd(q, k, positions, inv_freq, q_out, k_out, *, q_weight=None, k_weight=None
     with _On(index):
         st = lib().kda_qk_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight),
                                _ptr(k_weight), _ptr(inv_freq) if R else None, _ptr(positions), B, T, Hq, Hk, D, R, code,
-                               NORMS[norm], eps, bool(interleaved), attention_factor,
+                               NORMS[norm], float(eps), bool(interleaved), float(attention_factor),
                                _row_strides(q, k, q_out, k_out), _raw_stream(stream, index))
     if st != KDA_OK:
         raise KDAError(st, "kda_qk_rope")
@@ -133,7 +135,7 @@ def bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=No
         st = L.kda_qk_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), r["dq"].data_ptr(),
                                r["dk"].data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(r.get("dq_weight")),
                                _ptr(r.get("dk_weight")), _ptr(inv_freq) if R else None, _ptr(positions), B, T, Hq, Hk, D,
-                               R, code, NORMS[norm], eps, bool(interleaved), attention_factor,
+                               R, code, NORMS[norm], float(eps), bool(interleaved), float(attention_factor),
                                _row_strides(q, k, dq_out, dk_out, r["dq"], r["dk"]), _ptr(workspace),
                                _bytes(workspace), _raw_stream(stream, index))
     if st != KDA_OK:

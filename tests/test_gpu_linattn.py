@@ -279,3 +279,72 @@ def test_other_stream_and_graph():
     linattn.fwd(q, k, v, d, SCALE, o3, h0, None, cu, stream=side)
     side.synchronize()
     assert torch.equal(o3, o2)
+
+
+def test_extents_of_strided_views():
+    """Memory between the rows of the views is neither read into results nor written: NaN all around q, k and v."""
+    B, T, H = 2, 130, 2
+    q, k, v, d, n = inputs(B, T, H, H, 61, "token")
+    wide = torch.full((B, T + 3, 3, H, D + 16), float("nan"), dtype=torch.bfloat16, device=dev())
+    views = [wide[:, 1:T + 1, i, :, 8:-8] for i in range(3)]
+    for x, y in zip(views, (q, k, v)):
+        x.copy_(y)
+    h0, do = states(B, H, torch.float32, n), n(B, T, H, D).bfloat16()
+    want, ws = run_fwd(q, k, v, d, h0, None)
+    out, ht = run_fwd(*views, d, h0, None)
+    assert torch.equal(out, want) and torch.equal(ht, ws)
+    o2, s2 = run_fwd(*views, d, h0, None, recurrent=True)
+    close_bf16(o2, lin_ref(q, k, v, d, SCALE, h0)[0], "out")
+    a, b = linattn.bwd(q, k, v, d, SCALE, do, h0), linattn.bwd(*views, d, SCALE, do, h0)
+    for m in ("dq", "dk", "dv", "ddecay", "dinitial_state"):
+        assert torch.equal(a[m], b[m]), m
+
+
+def test_broadcast_heads_and_batches():
+    """q and k expanded over heads and batch rows (strides 0) read as their copies."""
+    q, k, v, d, n = inputs(2, 90, 4, 4, 62, "token")
+    q1, k1 = q[:1, :, :1].expand(2, -1, 4, -1), k[:1, :, :1].expand(2, -1, 4, -1)
+    a = run_fwd(q1, k1, v, d, None, None)
+    b = run_fwd(q1.contiguous(), k1.contiguous(), v, d, None, None)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_at_once():
+    """Two calls of different sizes side by side, each with its own workspace, give what they give alone."""
+    sets = []
+    for i, (T, H) in enumerate([(3000, 2), (700, 8)]):
+        q, k, v, d, n = inputs(1, T, 1, H, 70 + i, "token")
+        do = n(1, T, H, D).bfloat16()
+        sets.append((q, k, v, d, do, run_fwd(q, k, v, d, None, None), linattn.bwd(q, k, v, d, SCALE, do)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        for s, (q, k, v, d, do, _, _) in zip(streams, sets):
+            out, ht = torch.empty_like(v), torch.empty(1, v.shape[2], D, D, device=dev())
+            s.wait_stream(torch.cuda.current_stream())
+            linattn.fwd(q, k, v, d, SCALE, out, None, ht, stream=s)
+            got.append((out, ht, linattn.bwd(q, k, v, d, SCALE, do, stream=s)))
+        torch.cuda.synchronize()
+        for (out, ht, r), (*_, f, b) in zip(got, sets):
+            assert torch.equal(out, f[0]) and torch.equal(ht, f[1])
+            assert all(torch.equal(r[m], b[m]) for m in ("dq", "dk", "dv", "ddecay"))
+
+
+def test_many_short_sequences():
+    """More sequences than segments, single tokens and empty ones among them, and sequences as long as a segment."""
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 9, (400,), generator=g).tolist() + [256, 0, 257, 1, 255]
+    cu = [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    q, k, v, d, n = inputs(1, cu[-1], 1, 1, 63, "token")
+    h0 = states(len(lens), 1, torch.float32, n)
+    ro, rs = lin_ref(q, k, v, d, SCALE, h0, cu)
+    for recurrent in (False, True):
+        out, ht = run_fwd(q, k, v, d, h0, cu, recurrent=recurrent)
+        close_bf16(out, ro, "out")
+        close_fp32(ht, rs, "final")
+    do, dht = n(1, cu[-1], 1, D).bfloat16(), n(len(lens), 1, D, D)
+    r = linattn.bwd(q, k, v, d, SCALE, do, h0, dht, torch.tensor(cu, device=dev()))
+    check_bwd(r, bwd_ref(q, k, v, d, do, h0, dht, cu, chunked=True), q, k, d)

@@ -220,7 +220,7 @@ def test_frequencies():
     assert torch.equal(g[turns > 40], f[turns > 40])                       # quick pairs stay
     assert torch.allclose(g[turns < 0.8], f[turns < 0.8] / 16, rtol=1e-6)  # slow ones are stretched whole
     assert (g <= f).all() and (g >= f / 16 * (1 - 1e-6)).all() and (g[1:] <= g[:-1]).all()
-    for bad in (dict(scaling="other"), dict(scaling="yarn"), dict(factor=0.5)):
+    for bad in (dict(scaling="other"), dict(scaling="yarn"), dict(factor=0.5), dict(base=1.0)):
         with pytest.raises(ValueError):
             qkrope.inv_freq(64, **bad)
     with pytest.raises(ValueError):
