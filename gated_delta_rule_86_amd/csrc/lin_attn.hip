@@ -639,19 +639,14 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 // The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
 // add nothing and are not read.  Bound by memory: 64 KiB of tiles in LDS twice, one barrier a chunk; reads
-// of 32 KiB per chunk at T = 262144, H = 8, slow decays: 4.4 TB/s.
+// of 32 KiB per chunk at T = 262144, H = 8, slow decays: 4.4 TB/s.  kThree as in walk(): with bf16 states a packed
+// prompt of 38000 tokens, H = 32, took 422 us in all with three terms, 406 with two.
 constexpr double kGone = -150.0;
 
-__global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0, int lead1)
+template <bool kThree>
+__device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, LdsStates &lds)
 {
-    __shared__ __attribute__((aligned(16))) LdsStates lds;
-    const int64_t total = a.rows * a.P * a.H;
-    const int64_t at = xcd_order(blockIdx.x, total);
-    if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
-        return;
-    const int64_t seg = at / a.H, h = at - seg * a.H;
     const int64_t row = seg / a.P, j = seg - row * a.P;
-    const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
     const bool rev = ro.rev != 0, tr = ro.transposed != 0;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
     const int64_t slot = seg * a.H + h;
@@ -723,7 +718,7 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v[buf], ln, jj);
-        state_update<true, true>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
+        state_update<true, kThree>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
         if (!more)
             break;
         if (wave == 3)
@@ -745,6 +740,21 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
     state_store(S, ro.slots + (size_t)slot * kD * kD, kFp32, tr, wave, lane);
     if (tid == 0)
         *lam = whole ? -1.0f : f;
+}
+
+__global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0, int lead1)
+{
+    __shared__ __attribute__((aligned(16))) LdsStates lds;
+    const int64_t total = a.rows * a.P * a.H;
+    const int64_t at = xcd_order(blockIdx.x, total);
+    if (at >= total || (int64_t)(blockIdx.x >> 3) >= ((total + 7) >> 3))
+        return;
+    const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
+    const int64_t seg = at / a.H, h = at - seg * a.H;
+    if (ro.three || ro.dots)
+        states<true>(a, ro, seg, h, lds);
+    else
+        states<false>(a, ro, seg, h, lds);
 }
 
 // ---------------------------------------------------------------------------- scan
