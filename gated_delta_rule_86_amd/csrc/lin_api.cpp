@@ -47,7 +47,7 @@ kda_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, b
         B * T > kMaxElems / (H * kD))
         return KDA_ERR_SHAPE;
     const int64_t n_seq = varlen ? N : B;
-    if (n_seq >= ((int64_t)1 << 29) || n_seq > (((int64_t)1 << 31) - 64) / (4 * H))  // grid sizes
+    if (n_seq >= ((int64_t)1 << 29) || n_seq > (((int64_t)1 << 31) - 64) / (4 * H))
         return KDA_ERR_SHAPE;
     *z = Sizes{B, T, Hk, H, N, n_seq, varlen};
     return KDA_OK;
@@ -58,7 +58,8 @@ bool make_layout(const Sizes &z, bool bwd, bool ddecay, kda::LinLayout *L)
     using kda::kAlign;
     L->plan = kda::lin_plan(z.B, z.T, z.H, z.N, z.varlen, bwd ? 3 : 1, ddecay ? kda::kLinGradSeg : 0);
     const kda::LinPlan &p = L->plan;
-    if (p.rows * p.P > (((int64_t)1 << 31) - 64) / (64 * z.H))  // grid sizes
+    // a launch holds less than 2^32 threads: 512 per segment and head at most, 8192 per row and head in the scan
+    if (p.rows * p.P > (((int64_t)1 << 23) - 8) / z.H || (p.P > 1 && p.rows >= ((int64_t)1 << 19) / z.H))
         return false;
     size_t off = kAlign;  // status word
     auto take = [&](size_t bytes) {
@@ -177,8 +178,8 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
     if (overlap(ro, ri) || overlap(ro, rf) || (h0 != ht && overlap(ri, rf)) || overlap(rw, ri) || overlap(rw, ro) ||
         overlap(rw, rf))
         return KDA_ERR_ALIAS;
-    if (!make_layout(z, false, false, lay))
-        return KDA_ERR_SHAPE;
+    if (!make_layout(z, false, false, lay) || (recurrent && z.n_seq > (((int64_t)1 << 24) - 8) / H))
+        return KDA_ERR_SHAPE;  // token by token, a launch has 256 threads per sequence and head
     // token by token, the workspace holds the status word alone
     const size_t need = recurrent ? (cu ? kda::kAlign : 0) : lay->total;
     if (need && (!ws || ws_bytes < need))

@@ -89,7 +89,8 @@ kda_status set_view(const void *p, const int64_t *st, int64_t B, int64_t T, int6
 
 kda_status check_shape(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R)
 {
-    if (B < 1 || T < 0 || Hq < 1 || Hk < 1 || Hq > 4096 || Hk > 4096 || T > ((int64_t)1 << 30) / B)
+    if (B < 1 || T < 0 || Hq < 1 || Hk < 1 || Hq > 4096 || Hk > 4096 ||
+        T > (((int64_t)1 << 30) - 64) / B)  // a launch holds less than 2^32 threads: 256 for up to 64 tokens
         return KDA_ERR_SHAPE;
     if (D < 16 || D > kda::kRopeMaxD || D % 16 || R < 0 || R > D || R % 16)
         return KDA_ERR_ROTARY;

@@ -115,6 +115,18 @@ def test_lin_workspace_sizes():
     assert linattn.bwd_workspace_size(4, 100, 4, 4) > alone
 
 
+def test_launch_limits():
+    """Sizes whose launch would hold 2^32 threads or more are refused by the checks, not by the runtime."""
+    assert linattn.workspace_size((1 << 21) - 2, 1, 4) == 256 and linattn.workspace_size(1 << 21, 1, 4) == 0
+    assert linattn.bwd_workspace_size(1 << 17, 1024, 4, 4) == 0  # the scan over two segments a row
+    assert linattn.bwd_workspace_size(1 << 17, 1024, 4, 4, need_ddecay=False) == 256
+    alone = dict(B=1, T=100, cu=ptr(8), h0=None, h0_dt=0, ht=None, ht_dt=0)
+    assert lin_call("kda_lin_fwd_recurrent", N=1 << 22, **alone) == 2
+    assert lin_call("kda_lin_fwd_recurrent", N=1 << 21, ws_bytes=255, **alone) == 8
+    rope = kda.lib().kda_qk_rope_bwd_workspace_size
+    assert rope(1, 1 << 30, 1, 1, 16) == 0 and rope(1, (1 << 30) - 64, 1, 1, 16) == 1024 * 16 * 4
+
+
 def rope_call(back=False, **ch):
     a = dict(q=ptr(0), k=ptr(1), y=[ptr(2), ptr(3)], g=[ptr(4), ptr(5)], wq=ptr(6), wk=ptr(7), f=ptr(8), pos=ptr(9),
              dwq=ptr(10), dwk=ptr(11), B=2, T=10, Hq=4, Hk=2, D=128, R=64, dtype=1, norm=1, eps=1e-6, inter=0, m=1.0,
