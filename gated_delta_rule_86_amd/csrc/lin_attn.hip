@@ -638,8 +638,8 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 //
 // The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
-// add nothing and are not read.  Bound by memory: 64 KiB of tiles in LDS twice, one barrier a chunk; reads
-// of 32 KiB per chunk at T = 262144, H = 8, slow decays: 4.4 TB/s.  kThree as in walk(): with bf16 states a packed
+// add nothing and are not read.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
+// H = 8, per-token decays: 60 us, 3.8 TB/s) where segments are short, else by a chunk's latency, 2.5 us.  kThree as in walk(): with bf16 states a packed
 // prompt of 38000 tokens, H = 32, took 422 us in all with three terms, 406 with two.
 constexpr double kGone = -150.0;
 
@@ -760,8 +760,9 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
 // ---------------------------------------------------------------------------- scan
 //
 // slot_j <- share_j + lam_j * slot_{j-1} (forwards; backwards from the other end), so that slot
-// j is the state at the boundary behind (before) segment j.  Two entries a thread; the loads of 8 segments are
-// on their way together.
+// j is the state at the boundary behind (before) segment j.  Every entry is its own chain: P steps of one fma, bound by
+// memory.  Two entries a thread, the loads of 8 segments on their way together: B = 2, T = 4096, H = 16 backwards
+// (512 slots of 64 KiB) 11 us, 4.8 TB/s.
 constexpr unsigned kScanParts = kD * kD / 512;  // workgroups per matrix
 
 __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int lead1)
@@ -798,6 +799,19 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 }
 
 // ---------------------------------------------------------------------------- output pass
+//
+// One workgroup walks the chunks of one segment and head: out^T[v][t] = S q^T scaled by wout, plus V^T times the
+// 64 x 64 weights, then the state's update.  4 waves split the 128 v channels, so each holds 128 x 32 of the state in 64
+// registers a lane from chunk to chunk and the transposed products need no exchange between waves; the weights,
+// one 32 x 32 block a wave, are the one thing they share.  66 KiB of LDS and 256 registers a lane let two workgroups
+// share a CU.  The next chunk's rows are loaded into registers while this one is worked on; three barriers a chunk.
+//
+// Per chunk a wave issues 98 matrix instructions (82 without third terms) and some 800 vector instructions, the greater part
+// of them the cuts of state and rows into bf16 terms, and the two overlap in part.  T = 262144, H = 8: 574 us, 2.2 GB at
+// 3.8 TB/s (a copy: 4.8), matrix pipes 35 % and vector pipes 35 % busy; the same loads and stores without the arithmetic
+// took 466 us.  38000 packed tokens, H = 32, Hk = 8: 280 us, 3.0 TB/s.  The three walks of a backward pass with dots
+// (75 KiB, 24-bit products), B = 2, T = 4096, H = 16: 135 us, 3.9 TB/s.  512 threads with the state's channels in halves,
+// one workgroup a CU, was slower (T = 262144: 740 us in all against 667).
 
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
 // out.  Their sums over many tokens cancel, so weights and states then go into the products
@@ -1210,6 +1224,8 @@ __global__ __launch_bounds__(256) void lin_final_kernel(LinArgs a)
 }
 
 // ------------------------------------------------------------------- cu_seqlens, checked once
+//
+// The walks trust cu_seqlens, so nothing may run on one that leads out of the tensors.  One workgroup: a launch, 4.7 us.
 
 __global__ __launch_bounds__(1024) void lin_check_kernel(const int64_t *cu, int64_t N, int64_t T, int32_t *status)
 {
@@ -1230,7 +1246,9 @@ __global__ __launch_bounds__(1024) void lin_check_kernel(const int64_t *cu, int6
 
 // ------------------------------------------------------------------- backward pass, tail
 
-// Sum of the value heads that share a q/k head, in head order, rounded once.  One thread per 4 channels.
+// Sum of the value heads that share a q/k head, in head order, rounded once.  One thread per 4 channels.  Bound by
+// memory: 13500 tokens, H = 16, Hk = 4: 45 us, 5.5 TB/s.  Folding in the walk would need the states of all
+// sharing heads in one workgroup, 64 KiB of registers each.
 __global__ __launch_bounds__(256) void lin_fold_kernel(const float *xq, const float *xk, uint16_t *yq, uint16_t *yk,
                                                        int64_t rows, int64_t Hk, int64_t G, const int32_t *status)
 {
@@ -1357,7 +1375,9 @@ __global__ __launch_bounds__(64) void lin_ddecay_sum_kernel(LinArgs a, const dou
 // ------------------------------------------------------------------- token by token
 //
 // One wave per (sequence, head, 32 rows of the state); lane = row % 8 * 8 + q holds 16 channels
-// of 4 rows: 16-byte pieces, interleaved with those of the row's other 7 lanes.
+// of 4 rows: 16-byte pieces, interleaved with those of the row's other 7 lanes.  The state is read once and written once,
+// which bounds it: 256 sequences, H = 32, fp32: 207 us, 5.2 TB/s.  Waves share nothing; few of them are
+// launched as workgroups of one wave, to reach more CUs (H = 8, one sequence: 4.5 us).
 template <bool kF32>
 __global__ __launch_bounds__(256) void lin_recurrent_kernel(LinArgs a)
 {

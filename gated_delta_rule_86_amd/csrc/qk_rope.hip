@@ -17,7 +17,8 @@
 // Bound by memory: every value is read once and written once (backward: read twice as many).  Measured: 16384
 // tokens x 40 heads of 128, bf16, forward 71 us (4.75 TB/s, what a large copy reaches); backward B = 2, T = 4096, 16 + 16
 // heads 50 us with the weights' sums (4.0 TB/s).  One row in flight per lane group ran at 2.5 TB/s; four (two
-// backwards) keep enough loads on their way.
+// backwards) keep enough loads on their way.  Small fp32 batches are bound by latency (3001 tokens, 12 + 1 heads: 26 us,
+// of which the angles, one row's loads, the sums and the second launch follow each other).
 // A lane owns 16 channels of a row as two 16-byte pieces (four in fp32) that hold both
 // halves of its pairs, D / 16 lanes (rounded up to a power of two) own the row.
 #include <hip/hip_runtime.h>

@@ -18,6 +18,10 @@
  * The library evaluates this in 16-token chunks (FlashKDA article index: "processes
  * 16-token chunks"; "Neumann-series expansion" for the intra-chunk inverse).
  *
+ * Beside it: kda_lin_*, linear attention with one decay per head (no delta rule, no gate per channel),
+ * forward, token by token and backward, on the same state layout; and kda_qk_rope*, the
+ * normalisation of q and k with the rotation by positions, which prepares the inputs of either.
+ *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers unless the name ends in _host.
  *   - The caller owns every buffer; the library allocates no device memory.  Scratch
