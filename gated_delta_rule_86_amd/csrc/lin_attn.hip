@@ -495,13 +495,17 @@ __device__ __forceinline__ u32x4 key_frag(const unsigned char *tile, const Lanes
     return u32x4{x[0], x[1], y[0], y[1]};
 }
 
-// Cutting floats into bf16 terms: what a rounded pair leaves of each, x - hi(x), as one dot product
-// (hi0, hi1).(-1, 0) + x, exact.  The two constants live in registers: as an instruction's constant the compiler
-// puts both into the same half.
+// Cutting floats into bf16 terms: what a rounded pair leaves of each, x - hi(x), exact.
 struct Cutter {
+    __device__ float rest0(uint32_t pair, float x) const { return x - lo_f(pair); }
+    __device__ float rest1(uint32_t pair, float x) const { return x - hi_f(pair); }
+};
+// The same as one dot product each, (hi0, hi1).(-1, 0) + x: fewer registers, but dot products wait for the matrix pipe.
+// The two constants live in registers: as an instruction's constant the compiler puts both into the same half.
+struct DotCutter {
     uint32_t neg0, neg1;
 
-    __device__ Cutter() : neg0(0x0000bf80u), neg1(0xbf800000u) { __asm__ volatile("" : "+v"(neg0), "+v"(neg1)); }
+    __device__ DotCutter() : neg0(0x0000bf80u), neg1(0xbf800000u) { __asm__ volatile("" : "+v"(neg0), "+v"(neg1)); }
     __device__ float rest0(uint32_t pair, float x) const
     {
         return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, neg0), x,
@@ -513,12 +517,20 @@ struct Cutter {
                                                false);
     }
 };
+template <bool kDots>
+struct CutterOf {
+    using type = Cutter;
+};
+template <>
+struct CutterOf<true> {
+    using type = DotCutter;
+};
 struct Terms3 {
     u32x4 h, m, l;
 };
 // two terms (h, m) or three
-template <bool kThree>
-__device__ __forceinline__ void cut_terms(const float *x, Terms3 &t, const Cutter &cut)
+template <bool kThree, typename Cut>
+__device__ __forceinline__ void cut_terms(const float *x, Terms3 &t, const Cut &cut)
 {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -536,8 +548,8 @@ __device__ __forceinline__ void cut_terms(const float *x, Terms3 &t, const Cutte
 //
 // Steps of 16 tokens, in a pipeline by hand: while a step's 12 matrix instructions run, the next step's K
 // operand is on its way from LDS and its weighted rows are cut.
-template <bool kThree>
-__device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const float *win, int tok, const Cutter &cut)
+template <bool kThree, typename Cut>
+__device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const float *win, int tok, const Cut &cut)
 {
     const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&win[tok]);
     const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&win[tok + 4]);
@@ -561,9 +573,9 @@ __device__ __forceinline__ void interleave()
     }
 }
 
-template <bool kAhead, bool kThree>
+template <bool kAhead, bool kThree, typename Cut>
 __device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const float *win,
-                                             const Lanes &ln, int half, const Cutter &cut)
+                                             const Lanes &ln, int half, const Cut &cut)
 {
     if constexpr (!kAhead) {  // where registers are short
 #pragma unroll
@@ -617,6 +629,23 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
             interleave<kThree ? 12 : 8, 5>();
         __builtin_amdgcn_sched_barrier(0);
     }
+}
+
+// Two workgroups share a CU, and the older one's waves go first: it would finish at nearly full speed, then the younger one
+// would run its second half alone.  Priorities that fall over 8 chunks and start again keep them close: the one behind goes
+// first.  T = 262144, H = 8: 673 -> 646 us in all.  Only where all workgroups run at once: with more, the place that one
+// leaves early goes to the next (B = 2, T = 4096, H = 16 backwards, 768 workgroups: 205 us, 213 with turns).
+__device__ __forceinline__ void take_turn(uint32_t token)
+{
+    const uint32_t p = (token / (2 * kLC)) & 3;
+    if (p == 0)
+        __builtin_amdgcn_s_setprio(3);
+    else if (p == 1)
+        __builtin_amdgcn_s_setprio(2);
+    else if (p == 2)
+        __builtin_amdgcn_s_setprio(1);
+    else
+        __builtin_amdgcn_s_setprio(0);
 }
 
 // Block -> (segment, head): the blocks of one XCD (every eighth) take neighbouring heads, so that
@@ -676,7 +705,7 @@ __device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int6
     const TileSrc sk = tile_src(ro.k, row, h), sv = tile_src(ro.v, row, h);
     const float *dp = decay_of(a, row, h);
     const Lanes ln(tid);
-    const Cutter cut;
+    const DotCutter cut;
     State S;
 #pragma unroll
     for (int n = 0; n < 64; ++n)
@@ -830,7 +859,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5, l32 = lane & 31;
     const Lanes ln(tid);
-    const Cutter cut;
+    const typename CutterOf<kDots>::type cut;
     const size_t init_bytes = kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1);
     const size_t fin_bytes = kLinStateBytes / (ro.fin_dt == kBf16 ? 2 : 1);
     State S;
@@ -873,6 +902,8 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         make_decays(lds.d[0], held, g, c, lane, rev, a.scale);
     int buf = 0;
     while (c.len > 0) {
+        if (a.turns)
+            take_turn(rev ? ~(uint32_t)c.t0 : (uint32_t)c.t0);
         tile_put(fq, lds.q, ln);
         tile_put(fk, lds.k, ln);
         tile_put(fv, lds.v, ln);
@@ -1065,7 +1096,9 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
             }
         }
 
-        // rows out; those behind the chunk lie beyond the descriptor
+        // Rows out; those behind the chunk lie beyond the descriptor.  A lane holds 4 neighbouring channels of a token:
+        // stored like that, an instruction would touch 32 rows.  They change places in this wave's part of the
+        // query tile (read for the last time before the barrier above), so that it touches 16 (8 with fp32).
         {
             const bool out_f32 = ro.out_f32 != 0;
             const uint32_t size = out_f32 ? 4 : 2, stride = (uint32_t)a.H * (kD * size);
@@ -1073,53 +1106,74 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 rsrc(static_cast<unsigned char *>(ro.out) +
                          ((size_t)(row * a.T + c.t0) * (size_t)a.H + (size_t)h) * (kD * size),
                      (uint32_t)(c.len - 1) * stride + kD * size);
+            unsigned char *stage = lds.q;
+            int to = lane;
+            if (!kDots)
+                __asm__ volatile("" : "+v"(to));
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 const int t = 32 * tt + l32;
-                const uint32_t o = (uint32_t)t * stride + (32 * wave + 4 * half) * size;
                 const float own = dots ? ldx.own[t] : 0.0f;
                 int tv = l32;
-                if (kDots)
-                    __asm__ volatile("" : "+v"(tv));  // as above: addresses formed anew
+                __asm__ volatile("" : "+v"(tv));  // as above: addresses formed anew
                 float dot = 0.0f;
+                if (dots) {
 #pragma unroll
-                for (int a4 = 0; a4 < 4; ++a4) {
-                    f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
-                    if (dots) {
+                    for (int a4 = 0; a4 < 4; ++a4) {
+                        f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
                         const u32x2 xw = xr[tt][a4];
                         dot += (lo_f(xw[0]) * y[0] + hi_f(xw[0]) * y[1]) + (lo_f(xw[1]) * y[2] + hi_f(xw[1]) * y[3]);
                         const u32x2 vr = *reinterpret_cast<const u32x2 *>(lds.v + tile_at(tv, 4 * wave + a4) + 8 * half +
                                                                           8192 * tt);
-                        y[0] = fmaf(own, lo_f(vr[0]), y[0]);
-                        y[1] = fmaf(own, hi_f(vr[0]), y[1]);
-                        y[2] = fmaf(own, lo_f(vr[1]), y[2]);
-                        y[3] = fmaf(own, hi_f(vr[1]), y[3]);
-                    }
-                    if (dots) {
-                        O[tt][4 * a4] = y[0];
-                        O[tt][4 * a4 + 1] = y[1];
-                        O[tt][4 * a4 + 2] = y[2];
-                        O[tt][4 * a4 + 3] = y[3];
+                        O[tt][4 * a4] = fmaf(own, lo_f(vr[0]), y[0]);
+                        O[tt][4 * a4 + 1] = fmaf(own, hi_f(vr[0]), y[1]);
+                        O[tt][4 * a4 + 2] = fmaf(own, lo_f(vr[1]), y[2]);
+                        O[tt][4 * a4 + 3] = fmaf(own, hi_f(vr[1]), y[3]);
                     }
                 }
-                if (out_f32) {
+                if constexpr (kDots) {  // registers are short: stored as they are
+                    const uint32_t o = (uint32_t)t * stride + (32 * wave + 4 * half) * size;
 #pragma unroll
                     for (int a4 = 0; a4 < 4; ++a4) {
                         const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra, o + 32 * a4, 0, 0);
+                        if (out_f32)
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra, o + 32 * a4, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b64(
+                                __builtin_bit_cast(u2, u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])}), ra, o + 16 * a4, 0, 0);
+                    }
+                } else if (out_f32) {  // 32 rows of 512 bytes, piece 8 wave + 2 a4 + half
+#pragma unroll
+                    for (int a4 = 0; a4 < 4; ++a4) {
+                        const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
+                        *reinterpret_cast<f32x4 *>(stage + tv * 512 + ((8 * wave + ((2 * a4 + half) ^ (tv & 7))) << 4)) = y;
+                    }
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int tr8 = 8 * n + (to >> 3), pc = to & 7;
+                        const u32x4 y = lds_b128(stage + tr8 * 512 + ((8 * wave + (pc ^ (tr8 & 7))) << 4));
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra,
+                                                               (uint32_t)(32 * tt + tr8) * stride + (8 * wave + pc) * 16, 0, 0);
                     }
                 } else {
 #pragma unroll
-                    for (int a4 = 0; a4 < 4; ++a4) {
-                        const u32x2 z = {pack2(O[tt][4 * a4], O[tt][4 * a4 + 1]),
-                                         pack2(O[tt][4 * a4 + 2], O[tt][4 * a4 + 3])};
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, z), ra, o + 16 * a4, 0, 0);
-                    }
+                    for (int a4 = 0; a4 < 4; ++a4)
+                        *reinterpret_cast<u32x2 *>(stage + tile_at(tv, 4 * wave + a4) + 8 * half + 8192 * tt) =
+                            u32x2{pack2(O[tt][4 * a4], O[tt][4 * a4 + 1]), pack2(O[tt][4 * a4 + 2], O[tt][4 * a4 + 3])};
                 }
                 if (dots) {
                     dot += __shfl_xor(dot, 32);
                     if (half == 0)
                         ldx.red[wave][t] = dot;
+                }
+            }
+            if (!kDots && !out_f32) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int tr4 = (to >> 2), pc = 4 * wave + (to & 3);
+                    const u32x4 y = lds_b128(stage + tile_at(tr4, pc) + 4096 * n);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra,
+                                                           (uint32_t)(16 * n + tr4) * stride + pc * 16, 0, 0);
                 }
             }
         }
@@ -1496,8 +1550,9 @@ hipError_t lin_launch_check(const int64_t *cu, int64_t N, int64_t T, int32_t *st
     return hipGetLastError();
 }
 
-hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n_lead, hipStream_t s)
+hipError_t lin_launch_walk(const LinArgs &a0, int n_roles, const int *lead, int n_lead, hipStream_t s)
 {
+    LinArgs a = a0;
     const int64_t total = a.rows * a.P * a.H;
     const unsigned grid = (unsigned)(8 * cdiv(total, 8));
     if (a.P > 1) {
@@ -1512,6 +1567,7 @@ hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n
     bool dots = false;
     for (int i = 0; i < n_roles; ++i)
         dots = dots || a.role[i].dots;
+    a.turns = total * n_roles <= kLinSlots;
     if (dots)
         hipLaunchKernelGGL(lin_walk_kernel<true>, dim3(grid, n_roles), dim3(256), 0, s, a);
     else

@@ -122,6 +122,7 @@ struct LinArgs {
     float scale;
     int64_t T, H, N;     // N = n_seq
     int64_t rows, P, len;
+    int turns;           // walks on one CU keep close to each other
     const int64_t *cu;   // NULL: every row is one sequence
     int32_t *status;     // device status word (NULL without cu)
 };
