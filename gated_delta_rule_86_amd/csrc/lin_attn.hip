@@ -668,7 +668,7 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 // The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
 // add nothing and are not read.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
-// H = 8, per-token decays: 60 us, 3.8 TB/s) where segments are short, else by a chunk's latency, 2.5 us.  kThree as in walk(): with bf16 states a packed
+// H = 8, per-token decays: 62 us, 3.7 TB/s) where segments are short, else by a chunk's latency, 2.5 us.  kThree as in walk(): with bf16 states a packed
 // prompt of 38000 tokens, H = 32, took 422 us in all with three terms, 406 with two.
 constexpr double kGone = -150.0;
 
@@ -836,18 +836,18 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 // share a CU.  The next chunk's rows are loaded into registers while this one is worked on; three barriers a chunk.
 //
 // Per chunk a wave issues 98 matrix instructions (82 without third terms) and some 800 vector instructions, the greater part
-// of them the cuts of state and rows into bf16 terms, and the two overlap in part.  T = 262144, H = 8: 574 us, 2.2 GB at
-// 3.8 TB/s (a copy: 4.8), matrix pipes 35 % and vector pipes 35 % busy; the same loads and stores without the arithmetic
-// took 466 us.  38000 packed tokens, H = 32, Hk = 8: 280 us, 3.0 TB/s.  The three walks of a backward pass with dots
-// (75 KiB, 24-bit products), B = 2, T = 4096, H = 16: 135 us, 3.9 TB/s.  512 threads with the state's channels in halves,
-// one workgroup a CU, was slower (T = 262144: 740 us in all against 667).
+// of them the cuts of state and rows into bf16 terms; two waves a SIMD, it is the issue of these that bounds the walk where
+// memory does not.  T = 262144, H = 8: 566 us, 2.2 GB at 3.9 TB/s (a copy: 4.8); the same loads and stores without the
+// arithmetic took 466 us.  38000 packed tokens, H = 32, Hk = 8: 284 us, 3.0 TB/s.  The three walks of a backward pass with
+// dots (75 KiB, 24-bit products), B = 2, T = 4096, H = 16: 141 us, 3.7 TB/s.  512 threads with the state's channels in
+// halves, one workgroup a CU, was slower (T = 262144: 740 us in all against 667).
 
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
 // out.  Their sums over many tokens cancel, so weights and states then go into the products
 // as three terms, and the own pairs are added to the rows outside the matrix product.
 // kThree: the state keeps fp32's accuracy (see state_update).  Not where it is seen through bf16 alone: bf16 states
-// forwards, dq and dk without dots backwards (16 of 98 matrix instructions less: T = 38000, H = 32, Hk = 8 in all
-// 484 -> 454 us).
+// forwards, dq and dk without dots backwards (16 of 98 matrix instructions less: 38000 packed tokens, H = 32, Hk = 8, in all
+// 484 -> 454 us at that time).
 template <bool kDots, bool rev, bool kThree>
 __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, unsigned char *lds_raw)
 {
