@@ -668,8 +668,8 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 // The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
 // add nothing and are not read.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
-// H = 8, per-token decays: 62 us, 3.7 TB/s) where segments are short, else by a chunk's latency, 2.5 us.  kThree as in walk(): with bf16 states a packed
-// prompt of 38000 tokens, H = 32, took 422 us in all with three terms, 406 with two.
+// H = 8, per-token decays: 62 us, 3.7 TB/s) where segments are short, else by a chunk's latency, 2.5 us.
+// kThree as in walk(): with bf16 states 38000 packed tokens, H = 32, took 422 us in all with three terms, 406 with two.
 constexpr double kGone = -150.0;
 
 template <bool kThree>
