@@ -348,3 +348,66 @@ def test_many_short_sequences():
     do, dht = n(1, cu[-1], 1, D).bfloat16(), n(len(lens), 1, D, D)
     r = linattn.bwd(q, k, v, d, SCALE, do, h0, dht, torch.tensor(cu, device=dev()))
     check_bwd(r, bwd_ref(q, k, v, d, do, h0, dht, cu, chunked=True), q, k, d)
+
+
+def test_outputs_past_32_bits():
+    """out, dout and dv of more than 2^31 elements.  A reset 100 tokens before the end makes the last tokens a small problem
+    of their own, and leaves nothing to the gradients before them."""
+    T, H, tail = 131200, 128, 100
+    q, k, _, _, n = inputs(1, T, 1, 1, 80)
+    v = n(T * (D + 8 * H)).bfloat16().as_strided((1, T, H, D), (0, D + 8 * H, 8, 1))
+    d = -0.02 * n(1, T, H).abs()
+    d[:, T - tail] = float("-inf")
+    last = lambda x: x[:, T - tail:]  # noqa: E731
+    out, ht = run_fwd(q, k, v, d, None, None)
+    assert out.numel() > 2 ** 31 and torch.isfinite(out[:, ::997]).all()
+    ro, rs = lin_ref(last(q), last(k), last(v), last(d), SCALE)
+    close_bf16(last(out), ro, "out")
+    close_fp32(ht, rs, "final")
+    do = out.zero_()
+    last(do).copy_(n(1, tail, H, D))
+    r = linattn.bwd(q, k, v, d, SCALE, do)
+    assert all((r[m][:, :T - tail] == 0).all() for m in ("dq", "dk"))
+    assert all((r["dv"][:, i:T - tail:31] == 0).all() for i in (0, 17))
+    # ddecay is a sum over the later tokens of its segment, so up to 512 tokens before the reset it is 0 to rounding only
+    wide = lambda x: x[:, T - tail - 512:]  # noqa: E731
+    assert (r["ddecay"][:, :T - tail - 512] == 0).all()
+    ref = bwd_ref(wide(q), wide(k), wide(v), wide(d), wide(do), None, None, None)
+    check_bwd({m: wide(r[m]) for m in ("dq", "dk", "dv", "ddecay")} | {"dinitial_state": r["dinitial_state"]}, ref,
+              wide(q), wide(k), wide(d))
+
+
+def test_strides_past_32_bits():
+    """Batch rows 2^31 elements apart read as their copies."""
+    T, H = 70, 2
+    base = torch.empty((1 << 31) + T * 3 * H * D, dtype=torch.bfloat16, device=dev())
+    x = base.as_strided((2, T, 3 * H, D), (1 << 31, 3 * H * D, D, 1))
+    q, k, v, d, n = inputs(2, T, 3 * H, 3 * H, 81)
+    x.copy_(q)
+    q, k, v = x.split(H, 2)
+    d, do = d[:, :, :H].contiguous(), n(2, T, H, D).bfloat16()
+    c = [y.contiguous() for y in (q, k, v)]
+    for recurrent in (False, True):
+        a, b = run_fwd(q, k, v, d, None, None, recurrent=recurrent), run_fwd(*c, d, None, None, recurrent=recurrent)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = linattn.bwd(q, k, v, d, SCALE, do), linattn.bwd(*c, d, SCALE, do)
+    assert all(torch.equal(a[m], b[m]) for m in ("dq", "dk", "dv", "ddecay", "dinitial_state"))
+
+
+def test_state_past_32_bits():
+    """Decode on states of more than 2^31 elements, in place: the first and the last sequences."""
+    N, H = 4100, 32
+    q, k, v, d, n = inputs(N, 1, 2, H, 82)
+    h = torch.zeros(N, H, D, D, dtype=torch.bfloat16, device=dev())
+    assert h.numel() > 2 ** 31
+    ends = torch.tensor([0, 1, N // 2, N - 1], device=dev())
+    h[ends] = states(4, H, torch.bfloat16, n)
+    ro, rs = lin_ref(q[ends], k[ends], v[ends], d[ends], SCALE, h[ends])
+    h1 = h[ends].clone()
+    out, _ = run_fwd(q, k, v, d, h, None, recurrent=True, in_place=True)
+    close_bf16(out[ends], ro, "out")
+    close_bf16(h[ends], rs, "final")
+    h[ends] = h1
+    out, _ = run_fwd(q, k, v, d, h, None, in_place=True)
+    close_bf16(out[ends], ro, "out")
+    close_bf16(h[ends], rs, "final")

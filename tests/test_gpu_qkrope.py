@@ -215,3 +215,23 @@ def test_stream_and_graph():
     qkrope.fwd(q, k, pos, f, qo.zero_(), ko, **kw, stream=side)
     side.synchronize()
     assert torch.equal(ko, b)
+
+
+def test_strides_past_32_bits():
+    """Batch rows 2^31 elements apart, in place, equal their copies."""
+    T, D, R = 37, 128, 64
+    base = torch.empty((1 << 31) + T * 4 * D, dtype=torch.bfloat16, device="cuda")
+    q, k, pos, f, w, n = make(2, T, 3, 1, D, R, torch.bfloat16, 9)
+    x = base.as_strided((2, T, 4, D), (1 << 31, 4 * D, D, 1))
+    x[:, :, :3].copy_(q)
+    x[:, :, 3:].copy_(k)
+    a, b = torch.empty(2, T, 3, D, dtype=torch.bfloat16, device="cuda"), torch.empty(2, T, 1, D, dtype=torch.bfloat16,
+                                                                                     device="cuda")
+    kw = dict(q_weight=w[0], k_weight=w[1])
+    qc, kc = x[:, :, :3].contiguous(), x[:, :, 3:].contiguous()
+    qkrope.fwd(qc, kc, pos, f, a, b, **kw)
+    r = qkrope.bwd(qc, kc, pos, f, a, b, **kw)
+    e = qkrope.bwd(x[:, :, :3], x[:, :, 3:], pos, f, a, b, **kw)
+    assert all(torch.equal(r[m], e[m]) for m in r)
+    qkrope.fwd(x[:, :, :3], x[:, :, 3:], pos, f, x[:, :, :3], x[:, :, 3:], **kw)
+    assert torch.equal(x[:, :, :3], a) and torch.equal(x[:, :, 3:], b)
