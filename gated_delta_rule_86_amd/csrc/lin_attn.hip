@@ -923,9 +923,9 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                                    rx, (uint32_t)(32 * tt + tx) * xs + (32 * wave + 4 * half + 8 * a4) * 2, 0, 0));
         }
         g = load_decay(a, dp, n, lane);
+        // the other rows follow further down: 12 loads at once would fill the queue and hold the wave up (packed prompts 397 ->
+        // 379 us in all)
         tile_fetch(fq, sq, n, tid);
-        tile_fetch(fk, sk, n, tid);
-        tile_fetch(fv, sv, n, tid);
         if (c.flags & kPieceStart) {
             const bool slot = (c.flags & kFromSlot) != 0;
             state_load(S,
@@ -964,6 +964,9 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 for (int jj = 0; jj < kGroup; ++jj)
                     p = mfma(kr[jj], qr[jj], p);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            tile_fetch(fk, sk, n, tid);
+            __builtin_amdgcn_sched_barrier(0);
             int to = 32 * ob + l32;
             __asm__ volatile("" : "+v"(to));  // keep the comparisons below in the loop: 16 masks would not stay in SGPRs
             const float bho = d.bh[to], blo = d.bl[to];
@@ -1067,6 +1070,9 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v, ln, jj);
+        __builtin_amdgcn_sched_barrier(0);
+        tile_fetch(fv, sv, n, tid);
+        __builtin_amdgcn_sched_barrier(0);
         lds_barrier();  // the weights are there
         {
             // weight operands: of each 16 sources the diagonal block's, and the block beside it for half of them
