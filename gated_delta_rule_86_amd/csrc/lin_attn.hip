@@ -1104,26 +1104,23 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 
         // Rows out; those behind the chunk lie beyond the descriptor.  A lane holds 4 neighbouring channels of a token:
         // stored like that, an instruction would touch 32 rows.  They change places in this wave's part of the
-        // query tile (read for the last time before the barrier above), so that it touches 16 (8 with fp32).
-        {
-            const bool out_f32 = ro.out_f32 != 0;
-            const uint32_t size = out_f32 ? 4 : 2, stride = (uint32_t)a.H * (kD * size);
-            const __amdgpu_buffer_rsrc_t ra =
-                rsrc(static_cast<unsigned char *>(ro.out) +
-                         ((size_t)(row * a.T + c.t0) * (size_t)a.H + (size_t)h) * (kD * size),
-                     (uint32_t)(c.len - 1) * stride + kD * size);
-            unsigned char *stage = lds.q;
-            int to = lane;
-            if (!kDots)
-                __asm__ volatile("" : "+v"(to));
+        // query and value tiles (read for the last time before the barrier above), so that it touches 16 (8 with fp32),
+        // and leave after the state's update.  With dots registers are short and the value rows needed: stored as they are.
+        const bool out_f32 = ro.out_f32 != 0;
+        const uint32_t size = out_f32 ? 4 : 2, stride = (uint32_t)a.H * (kD * size);
+        const __amdgpu_buffer_rsrc_t ra =
+            rsrc(static_cast<unsigned char *>(ro.out) +
+                     ((size_t)(row * a.T + c.t0) * (size_t)a.H + (size_t)h) * (kD * size),
+                 (uint32_t)(c.len - 1) * stride + kD * size);
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const int t = 32 * tt + l32;
-                const float own = dots ? ldx.own[t] : 0.0f;
-                int tv = l32;
-                __asm__ volatile("" : "+v"(tv));  // as above: addresses formed anew
-                float dot = 0.0f;
+        for (int tt = 0; tt < 2; ++tt) {
+            const int t = 32 * tt + l32;
+            int tv = l32;
+            __asm__ volatile("" : "+v"(tv));  // as above: addresses formed anew
+            if constexpr (kDots) {
                 if (dots) {
+                    const float own = ldx.own[t];
+                    float dot = 0.0f;
 #pragma unroll
                     for (int a4 = 0; a4 < 4; ++a4) {
                         f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
@@ -1136,56 +1133,59 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                         O[tt][4 * a4 + 2] = fmaf(own, lo_f(vr[1]), y[2]);
                         O[tt][4 * a4 + 3] = fmaf(own, hi_f(vr[1]), y[3]);
                     }
-                }
-                if constexpr (kDots) {  // registers are short: stored as they are
-                    const uint32_t o = (uint32_t)t * stride + (32 * wave + 4 * half) * size;
-#pragma unroll
-                    for (int a4 = 0; a4 < 4; ++a4) {
-                        const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
-                        if (out_f32)
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra, o + 32 * a4, 0, 0);
-                        else
-                            __builtin_amdgcn_raw_buffer_store_b64(
-                                __builtin_bit_cast(u2, u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])}), ra, o + 16 * a4, 0, 0);
-                    }
-                } else if (out_f32) {  // 32 rows of 512 bytes, piece 8 wave + 2 a4 + half
-#pragma unroll
-                    for (int a4 = 0; a4 < 4; ++a4) {
-                        const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
-                        *reinterpret_cast<f32x4 *>(stage + tv * 512 + ((8 * wave + ((2 * a4 + half) ^ (tv & 7))) << 4)) = y;
-                    }
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const int tr8 = 8 * n + (to >> 3), pc = to & 7;
-                        const u32x4 y = lds_b128(stage + tr8 * 512 + ((8 * wave + (pc ^ (tr8 & 7))) << 4));
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra,
-                                                               (uint32_t)(32 * tt + tr8) * stride + (8 * wave + pc) * 16, 0, 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int a4 = 0; a4 < 4; ++a4)
-                        *reinterpret_cast<u32x2 *>(stage + tile_at(tv, 4 * wave + a4) + 8 * half + 8192 * tt) =
-                            u32x2{pack2(O[tt][4 * a4], O[tt][4 * a4 + 1]), pack2(O[tt][4 * a4 + 2], O[tt][4 * a4 + 3])};
-                }
-                if (dots) {
                     dot += __shfl_xor(dot, 32);
                     if (half == 0)
                         ldx.red[wave][t] = dot;
                 }
-            }
-            if (!kDots && !out_f32) {
+                const uint32_t o = (uint32_t)t * stride + (32 * wave + 4 * half) * size;
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int tr4 = (to >> 2), pc = 4 * wave + (to & 3);
-                    const u32x4 y = lds_b128(stage + tile_at(tr4, pc) + 4096 * n);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra,
-                                                           (uint32_t)(16 * n + tr4) * stride + pc * 16, 0, 0);
+                for (int a4 = 0; a4 < 4; ++a4) {
+                    const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
+                    if (out_f32)
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra, o + 32 * a4, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            __builtin_bit_cast(u2, u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])}), ra, o + 16 * a4, 0, 0);
                 }
+            } else if (out_f32) {  // 32 rows of 512 bytes, piece 8 wave + 2 a4 + half
+                unsigned char *stage = tt ? lds.v : lds.q;
+#pragma unroll
+                for (int a4 = 0; a4 < 4; ++a4) {
+                    const f32x4 y = {O[tt][4 * a4], O[tt][4 * a4 + 1], O[tt][4 * a4 + 2], O[tt][4 * a4 + 3]};
+                    *reinterpret_cast<f32x4 *>(stage + tv * 512 + ((8 * wave + ((2 * a4 + half) ^ (tv & 7))) << 4)) = y;
+                }
+            } else {
+#pragma unroll
+                for (int a4 = 0; a4 < 4; ++a4)
+                    *reinterpret_cast<u32x2 *>(lds.q + tile_at(tv, 4 * wave + a4) + 8 * half + 8192 * tt) =
+                        u32x2{pack2(O[tt][4 * a4], O[tt][4 * a4 + 1]), pack2(O[tt][4 * a4 + 2], O[tt][4 * a4 + 3])};
             }
         }
         if (d.mul != 1.0f)
             state_scale(S, d.mul);
         state_update<!kDots, kThree>(S, lds.k, vf, d.win, ln, half, cut);
+        if constexpr (!kDots) {
+            int to = lane;
+            __asm__ volatile("" : "+v"(to));
+            if (out_f32) {
+#pragma unroll
+                for (int n8 = 0; n8 < 8; ++n8) {
+                    const int t8 = 8 * (n8 & 3) + (to >> 3), pc = to & 7;
+                    const u32x4 y = lds_b128((n8 < 4 ? lds.q : lds.v) + t8 * 512 + ((8 * wave + (pc ^ (t8 & 7))) << 4));
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra,
+                                                           (uint32_t)(32 * (n8 >> 2) + t8) * stride + (8 * wave + pc) * 16,
+                                                           0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int n4 = 0; n4 < 4; ++n4) {
+                    const int t4 = to >> 2, pc = 4 * wave + (to & 3);
+                    const u32x4 y = lds_b128(lds.q + tile_at(t4, pc) + 4096 * n4);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y), ra,
+                                                           (uint32_t)(16 * n4 + t4) * stride + pc * 16, 0, 0);
+                }
+            }
+        }
         const double held_now = d.held;
         if (wave == 3 && n.len > 0)
             make_decays(lds.d[buf ^ 1], held, g, n, lane, rev, a.scale);
