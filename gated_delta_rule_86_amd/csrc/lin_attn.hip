@@ -837,9 +837,9 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 //
 // Per chunk a wave issues 98 matrix instructions (82 without third terms) and some 800 vector instructions, the greater part
 // of them the cuts of state and rows into bf16 terms; two waves a SIMD, it is the issue of these that bounds the walk where
-// memory does not.  T = 262144, H = 8: 566 us, 2.2 GB at 3.9 TB/s (a copy: 4.8); the same loads and stores without the
-// arithmetic took 466 us.  38000 packed tokens, H = 32, Hk = 8: 284 us, 3.0 TB/s.  The three walks of a backward pass with
-// dots (75 KiB, 24-bit products), B = 2, T = 4096, H = 16: 141 us, 3.7 TB/s.  512 threads with the state's channels in
+// memory does not.  T = 262144, H = 8: 544 us, 2.2 GB at 4.0 TB/s (a copy: 4.8); the same loads and stores without the
+// arithmetic took 466 us.  38000 packed tokens, H = 32, Hk = 8: 261 us, 3.2 TB/s.  The three walks of a backward pass with
+// dots (75 KiB, 24-bit products), B = 2, T = 4096, H = 16: 137 us, 3.8 TB/s.  512 threads with the state's channels in
 // halves, one workgroup a CU, was slower (T = 262144: 740 us in all against 667).
 
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
