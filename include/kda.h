@@ -359,7 +359,8 @@ kda_status kda_lin_fwd_recurrent(const void *q, const void *k, const void *v, co
  * kda_lin_fwd_workspace_size -- 256 bytes, plus one fp32 128 x 128 state and one float per head and
  * segment where the tokens of a batch row (all tokens with cu_seqlens) are cut into segments
  * that run in parallel: when batch rows x heads leave the chip empty.  A function of
- * (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes.
+ * (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes, among them (KDA_ERR_SHAPE in the
+ * calls) batch rows x segments x heads of 2^23 or more; token by token the limit is N x heads of 2^24.
  */
 size_t kda_lin_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
 
