@@ -1030,33 +1030,33 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
-            qf[0][0] = row_frag(lds.q, ln, 0, 0);
-            qf[0][1] = row_frag(lds.q, ln, 1, 0);
-            cut_state(0);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
-                const int b = jj & 1;
-                if (jj < 7) {
-                    qf[b ^ 1][0] = row_frag(lds.q, ln, 0, jj + 1);
-                    qf[b ^ 1][1] = row_frag(lds.q, ln, 1, jj + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    cut_state(jj + 1);
-                }
-                if (jj & 1)
-                    weights(jj >> 1);
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-                    O[tt] = mfma(sc[b].m, qf[b][tt], O[tt]);
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-                    O[tt] = mfma(sc[b].h, qf[b][tt], O[tt]);
-                if (jj & 1)
-                    interleave<4, 16>();
-                else
-                    interleave<4, 4>();
+                qf[0][0] = row_frag(lds.q, ln, 0, 0);
+                qf[0][1] = row_frag(lds.q, ln, 1, 0);
+                cut_state(0);
                 __builtin_amdgcn_sched_barrier(0);
-            }
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj) {
+                    const int b = jj & 1;
+                    if (jj < 7) {
+                        qf[b ^ 1][0] = row_frag(lds.q, ln, 0, jj + 1);
+                        qf[b ^ 1][1] = row_frag(lds.q, ln, 1, jj + 1);
+                        __builtin_amdgcn_sched_barrier(0);
+                        cut_state(jj + 1);
+                    }
+                    if (jj & 1)
+                        weights(jj >> 1);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+                        O[tt] = mfma(sc[b].m, qf[b][tt], O[tt]);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+                        O[tt] = mfma(sc[b].h, qf[b][tt], O[tt]);
+                    if (jj & 1)
+                        interleave<4, 16>();
+                    else
+                        interleave<4, 4>();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
 #pragma unroll
