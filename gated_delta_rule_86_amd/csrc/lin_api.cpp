@@ -192,8 +192,6 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
     r.init_dt = (int)h0_dt;
     r.fin_dt = (int)ht_dt;
     r.out = out;
-    // whether or not a final state is asked for, so that out does not depend on that
-    r.three = h0_dt != KDA_STATE_BF16 && ht_dt != KDA_STATE_BF16;
     if (lay->plan.P > 1 && !recurrent) {
         r.slots = reinterpret_cast<float *>(w + lay->off_fwd);
         r.lam = reinterpret_cast<float *>(w + lay->off_flam);
@@ -377,7 +375,6 @@ kda_status kda_lin_bwd(const void *q, const void *k, const void *v, const float 
     rdk.init = rdv.init = dfinal_state;
     rdk.init_dt = rdv.init_dt = (int)(dfinal_state ? KDA_STATE_FP32 : KDA_STATE_NONE);
     rdv.fin = dinitial_state;
-    rdv.three = 1;
     rdv.fin_dt = (int)KDA_STATE_FP32;
     if (a.P > 1) {
         rdq.slots = f32(lay.off_fwd);

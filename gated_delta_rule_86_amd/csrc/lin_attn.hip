@@ -18,8 +18,10 @@
 // Numbers: decays are used as min(max(g, -1000), 0) (below -1000 the factor is 0 in fp32 long
 // since, so -inf means "forget").  Running sums of logarithms are fp64 and kept as pairs of
 // floats; a factor is the exponential of a difference, at most 1.  The products run on
-// bf16 MFMA with fp32 accumulation; factors that are not bf16 inputs are cut into bf16 terms
-// (hi + lo: 16 significant bits; hi + mid + lo: 24).
+// bf16 MFMA with fp32 accumulation; factors that are not bf16 inputs (the state, the weights, the weighted rows) are
+// cut into three bf16 terms, hi + mid + lo: the 24 bits of fp32, whatever type the states have in memory.  Two terms
+// (16 bits) took less time (T = 262144, H = 8: 618 us against 692; 38000 packed tokens, H = 32, Hk = 8: 385 against 472;
+// B = 2, T = 4096, H = 16: 81 against 86), but where terms cancel they lose what fp32 keeps.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -337,12 +339,11 @@ constexpr int kPRow = 128;  // bytes per row of the 64 x 64 weight matrix
 
 struct LdsWalk {
     unsigned char k[kTile], v[kTile], q[kTile];
-    unsigned char p[2][kLC * kPRow];  // weights, hi and lo terms, [out token][source token]
+    unsigned char p[3][kLC * kPRow];  // weights, hi, mid and lo terms, [out token][source token]
     Decays d[2];
 };
 struct LdsWalkDots {
     LdsWalk w;
-    unsigned char p3[kLC * kPRow];  // third term of the weights
     float red[4][kLC];
     float own[kLC];                 // weights of the tokens' own pairs
 };
@@ -528,8 +529,7 @@ struct CutterOf<true> {
 struct Terms3 {
     u32x4 h, m, l;
 };
-// two terms (h, m) or three
-template <bool kThree, typename Cut>
+template <typename Cut>
 __device__ __forceinline__ void cut_terms(const float *x, Terms3 &t, const Cut &cut)
 {
 #pragma unroll
@@ -537,18 +537,16 @@ __device__ __forceinline__ void cut_terms(const float *x, Terms3 &t, const Cut &
         t.h[e] = pack2(x[2 * e], x[2 * e + 1]);
         const float a1 = cut.rest0(t.h[e], x[2 * e]), b1 = cut.rest1(t.h[e], x[2 * e + 1]);
         t.m[e] = pack2(a1, b1);
-        if (kThree)
-            t.l[e] = pack2(cut.rest0(t.m[e], a1), cut.rest1(t.m[e], b1));
+        t.l[e] = pack2(cut.rest0(t.m[e], a1), cut.rest1(t.m[e], b1));
     }
 }
 
 // S += sum over the chunk's tokens of (win v) k^T.  Source rows are weighted on the way in,
-// in fp32, and go into the product as three bf16 terms (24 bits), so that an fp32 state keeps
-// fp32's accuracy; as two (16 bits) where the state is seen through bf16 alone.
+// in fp32, and go into the product as three bf16 terms.
 //
 // Steps of 16 tokens, in a pipeline by hand: while a step's 12 matrix instructions run, the next step's K
 // operand is on its way from LDS and its weighted rows are cut.
-template <bool kThree, typename Cut>
+template <typename Cut>
 __device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const float *win, int tok, const Cut &cut)
 {
     const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&win[tok]);
@@ -559,7 +557,7 @@ __device__ __forceinline__ void weighted_terms(Terms3 &t, const u32x4 &v, const 
         x[2 * e] = lo_f(v[e]) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
         x[2 * e + 1] = hi_f(v[e]) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
     }
-    cut_terms<kThree>(x, t, cut);
+    cut_terms(x, t, cut);
 }
 
 // The scheduler keeps the order of these groups: n x { 1 matrix instruction, v vector instructions }.
@@ -573,7 +571,7 @@ __device__ __forceinline__ void interleave()
     }
 }
 
-template <bool kAhead, bool kThree, typename Cut>
+template <bool kAhead, typename Cut>
 __device__ __forceinline__ void state_update(State &S, const unsigned char *ktile, const u32x4 *vf, const float *win,
                                              const Lanes &ln, int half, const Cut &cut)
 {
@@ -585,9 +583,9 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
                 kf[kt] = key_frag(ktile, ln, kt, j);
-            weighted_terms<kThree>(t, vf[j], win, 16 * j + 8 * half, cut);
+            weighted_terms(t, vf[j], win, 16 * j + 8 * half, cut);
 #pragma unroll
-            for (int kt = 0; kt < 4 && kThree; ++kt)
+            for (int kt = 0; kt < 4; ++kt)
                 S.t[kt] = mfma(kf[kt], t.l, S.t[kt]);
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
@@ -604,7 +602,7 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
         kf[0][kt] = key_frag(ktile, ln, kt, 0);
-    weighted_terms<kThree>(t[0], vf[0], win, 8 * half, cut);
+    weighted_terms(t[0], vf[0], win, 8 * half, cut);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -614,10 +612,10 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
             for (int kt = 0; kt < 4; ++kt)
                 kf[c ^ 1][kt] = key_frag(ktile, ln, kt, j + 1);
             __builtin_amdgcn_sched_barrier(0);
-            weighted_terms<kThree>(t[c ^ 1], vf[j + 1], win, 16 * (j + 1) + 8 * half, cut);
+            weighted_terms(t[c ^ 1], vf[j + 1], win, 16 * (j + 1) + 8 * half, cut);
         }
 #pragma unroll
-        for (int kt = 0; kt < 4 && kThree; ++kt)
+        for (int kt = 0; kt < 4; ++kt)
             S.t[kt] = mfma(kf[c][kt], t[c].l, S.t[kt]);
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -626,7 +624,7 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
         for (int kt = 0; kt < 4; ++kt)
             S.t[kt] = mfma(kf[c][kt], t[c].h, S.t[kt]);
         if (j < 3)
-            interleave<kThree ? 12 : 8, 5>();
+            interleave<12, 5>();
         __builtin_amdgcn_sched_barrier(0);
     }
 }
@@ -669,10 +667,8 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
 // add nothing and are not read.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
 // H = 8, per-token decays: 62 us, 3.7 TB/s) where segments are short, else by a chunk's latency, 2.5 us.
-// kThree as in walk(): with bf16 states 38000 packed tokens, H = 32, took 422 us in all with three terms, 406 with two.
 constexpr double kGone = -150.0;
 
-template <bool kThree>
 __device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, LdsStates &lds)
 {
     const int64_t row = seg / a.P, j = seg - row * a.P;
@@ -747,7 +743,7 @@ __device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int6
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
             vf[jj] = col_frag(lds.v[buf], ln, jj);
-        state_update<true, kThree>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
+        state_update<true>(S, lds.k[buf], vf, lds.win[buf], ln, half, cut);
         if (!more)
             break;
         if (wave == 3)
@@ -780,10 +776,7 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
         return;
     const LinRole &ro = a.role[blockIdx.y == 0 ? lead0 : lead1];
     const int64_t seg = at / a.H, h = at - seg * a.H;
-    if (ro.three || ro.dots)
-        states<true>(a, ro, seg, h, lds);
-    else
-        states<false>(a, ro, seg, h, lds);
+    states(a, ro, seg, h, lds);
 }
 
 // ---------------------------------------------------------------------------- scan
@@ -832,7 +825,7 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 // One workgroup walks the chunks of one segment and head: out^T[v][t] = S q^T scaled by wout, plus V^T times the
 // 64 x 64 weights, then the state's update.  4 waves split the 128 v channels, so each holds 128 x 32 of the state in 64
 // registers a lane from chunk to chunk and the transposed products need no exchange between waves; the weights,
-// one 32 x 32 block a wave, are the one thing they share.  66 KiB of LDS and 256 registers a lane let two workgroups
+// one 32 x 32 block a wave, are the one thing they share.  74 KiB of LDS and 256 registers a lane let two workgroups
 // share a CU.  The next chunk's rows are loaded into registers while this one is worked on; three barriers a chunk.
 //
 // Per chunk a wave issues 98 matrix instructions (82 without third terms) and some 800 vector instructions, the greater part
@@ -843,12 +836,8 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 // halves, one workgroup a CU, was slower (T = 262144: 740 us in all against 667).
 
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
-// out.  Their sums over many tokens cancel, so weights and states then go into the products
-// as three terms, and the own pairs are added to the rows outside the matrix product.
-// kThree: the state keeps fp32's accuracy (see state_update).  Not where it is seen through bf16 alone: bf16 states
-// forwards, dq and dk without dots backwards (16 of 98 matrix instructions less: 38000 packed tokens, H = 32, Hk = 8, in all
-// 484 -> 454 us at that time).
-template <bool kDots, bool rev, bool kThree>
+// out.  Their sums over many tokens cancel, so the own pairs are added to the rows outside the matrix product.
+template <bool kDots, bool rev>
 __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, unsigned char *lds_raw)
 {
     LdsWalk &lds = *reinterpret_cast<LdsWalk *>(lds_raw);
@@ -938,10 +927,10 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         lds_barrier();
         const Decays &d = lds.d[buf];
 
-        // The weights of one 32 x 32 block (sources sb, outputs ob) per wave, bf16 hi + lo (wave 3's block lies beyond
-        // the diagonal: zeros, never read), and the state's share of the outputs, O^T[v][t], the state in bf16
-        // hi + lo.  In steps of 16 channels: a step's products with the state run while the next 16 channels of the
-        // state are cut and every other step makes 4 of the lane's 16 weights.
+        // The weights of one 32 x 32 block (sources sb, outputs ob) per wave, in three terms (wave 3's block lies beyond
+        // the diagonal: zeros, never read), and the state's share of the outputs, O^T[v][t].  In steps of 16 channels: a
+        // step's products with the state run while the next 16 channels of the state are cut and every other step makes
+        // 4 of the lane's 16 weights.
         f32x16 O[2];
         {
             const int sb = wave == 0 ? 0 : wave == 2 ? 1 : (wave == 1) == rev ? 1 : 0;
@@ -988,14 +977,13 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                 const u32x2 hi = {pack2(x[0], x[1]), pack2(x[2], x[3])};
                 const float y[4] = {cut.rest0(hi[0], x[0]), cut.rest1(hi[0], x[1]), cut.rest0(hi[1], x[2]),
                                     cut.rest1(hi[1], x[3])};
-                const u32x2 lo = {pack2(y[0], y[1]), pack2(y[2], y[3])};
+                const u32x2 mid = {pack2(y[0], y[1]), pack2(y[2], y[3])};
                 const int off = to * kPRow + (((4 * sb + a4) ^ (to & 7)) << 4) + 8 * half;
                 *reinterpret_cast<u32x2 *>(lds.p[0] + off) = hi;
-                *reinterpret_cast<u32x2 *>(lds.p[1] + off) = lo;
-                if (kDots)
-                    *reinterpret_cast<u32x2 *>(ldx.p3 + off) =
-                        u32x2{pack2(cut.rest0(lo[0], y[0]), cut.rest1(lo[0], y[1])),
-                              pack2(cut.rest0(lo[1], y[2]), cut.rest1(lo[1], y[3]))};
+                *reinterpret_cast<u32x2 *>(lds.p[1] + off) = mid;
+                *reinterpret_cast<u32x2 *>(lds.p[2] + off) =
+                    u32x2{pack2(cut.rest0(mid[0], y[0]), cut.rest1(mid[0], y[1])),
+                          pack2(cut.rest0(mid[1], y[2]), cut.rest1(mid[1], y[3]))};
             };
             u32x4 qf[2][2];
             Terms3 sc[2];
@@ -1004,7 +992,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
-                cut_terms<false>(x, sc[jj & 1], cut);
+                cut_terms(x, sc[jj & 1], cut);
             };
             if constexpr (kDots) {  // registers are short: no step ahead
 #pragma unroll
@@ -1015,7 +1003,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         x[e] = S.t[jj >> 1][8 * (jj & 1) + e];
-                    cut_terms<true>(x, sc[0], cut);
+                    cut_terms(x, sc[0], cut);
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt)
                         O[tt] = mfma(sc[0].l, qf[0][tt], O[tt]);
@@ -1047,14 +1035,17 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
                         weights(jj >> 1);
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt)
+                        O[tt] = mfma(sc[b].l, qf[b][tt], O[tt]);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
                         O[tt] = mfma(sc[b].m, qf[b][tt], O[tt]);
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt)
                         O[tt] = mfma(sc[b].h, qf[b][tt], O[tt]);
                     if (jj & 1)
-                        interleave<4, 16>();
+                        interleave<6, 14>();
                     else
-                        interleave<4, 4>();
+                        interleave<6, 5>();
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -1077,26 +1068,24 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         {
             // weight operands: of each 16 sources the diagonal block's, and the block beside it for half of them
             constexpr int kBeside = rev ? 0 : 1;  // output block that sees all sources
-            constexpr int kGroup = kDots ? 2 : 3;
+            constexpr int kGroup = 2;
 #pragma unroll
             for (int x0 = 0; x0 < 6; x0 += kGroup) {
-                u32x4 w3[kGroup], wh[kGroup], wl[kGroup];
+                u32x4 wh[kGroup], wm[kGroup], wl[kGroup];
 #pragma unroll
                 for (int y = 0; y < kGroup; ++y) {
                     const int x = x0 + y, jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
                     const int off = ln.w[jj] + 32 * kPRow * block;
-                    if (kDots)
-                        w3[y] = lds_b128(ldx.p3 + off);
-                    wl[y] = lds_b128(lds.p[1] + off);
+                    wl[y] = lds_b128(lds.p[2] + off);
+                    wm[y] = lds_b128(lds.p[1] + off);
                     wh[y] = lds_b128(lds.p[0] + off);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int y = 0; y < kGroup; ++y) {
                     const int x = x0 + y, jj = x < 4 ? x : (rev ? x - 2 : x - 4), block = x < 4 ? x >> 1 : kBeside;
-                    if (kDots)
-                        O[block] = mfma(vf[jj], w3[y], O[block]);
                     O[block] = mfma(vf[jj], wl[y], O[block]);
+                    O[block] = mfma(vf[jj], wm[y], O[block]);
                     O[block] = mfma(vf[jj], wh[y], O[block]);
                 }
             }
@@ -1163,7 +1152,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         }
         if (d.mul != 1.0f)
             state_scale(S, d.mul);
-        state_update<!kDots, kThree>(S, lds.k, vf, d.win, ln, half, cut);
+        state_update<!kDots>(S, lds.k, vf, d.win, ln, half, cut);
         if constexpr (!kDots) {
             int to = lane;
             __asm__ volatile("" : "+v"(to));
@@ -1234,24 +1223,16 @@ __global__ __launch_bounds__(256, 2) void lin_walk_kernel(LinArgs a)
     const int64_t seg = at / a.H, h = at - seg * a.H;
     if constexpr (kDots) {
         if (!ro.rev)
-            walk<true, false, true>(a, ro, seg, h, lds_raw);
+            walk<true, false>(a, ro, seg, h, lds_raw);
         else if (ro.dots)
-            walk<true, true, true>(a, ro, seg, h, lds_raw);
+            walk<true, true>(a, ro, seg, h, lds_raw);
         else
-            walk<false, true, true>(a, ro, seg, h, lds_raw);
+            walk<false, true>(a, ro, seg, h, lds_raw);
     } else {
-        const bool three = ro.three != 0;
-        if (ro.rev) {
-            if (three)
-                walk<false, true, true>(a, ro, seg, h, lds_raw);
-            else
-                walk<false, true, false>(a, ro, seg, h, lds_raw);
-        } else {
-            if (three)
-                walk<false, false, true>(a, ro, seg, h, lds_raw);
-            else
-                walk<false, false, false>(a, ro, seg, h, lds_raw);
-        }
+        if (ro.rev)
+            walk<false, true>(a, ro, seg, h, lds_raw);
+        else
+            walk<false, false>(a, ro, seg, h, lds_raw);
     }
 }
 

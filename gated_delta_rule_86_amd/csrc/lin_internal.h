@@ -106,7 +106,6 @@ struct LinRole {
     int init_dt, fin_dt;
     float *slots;     // [rows * P][H][128][128]
     float *lam;       // [rows * P][H]
-    int three;        // the state keeps fp32's accuracy
     int defer;        // fin is init and P > 1: see lin_final_kernel
     void *out;        // [B, T, H, 128], bf16 or fp32 (out_f32), or NULL
     int out_f32;

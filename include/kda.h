@@ -329,7 +329,8 @@ size_t kda_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int ha
  *             q, k, v in elements; the 128 channels of a head are contiguous.  Each a
  *             multiple of 8, the token stride 128 .. 2^24 (views of one fused projection; batch and
  *             head strides may be 0).
- * fp32 states keep fp32 accuracy (24-bit products, fp32 sums); out is rounded once.  A value that
+ * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; out and bf16 final
+ * states are rounded once.  out does not depend on whether final_state is asked for.  A value that
  * is not finite reaches its own sequence and head alone, from the first token of its chunk
  * of 64 tokens on (of the workgroup's run of tokens, see kda_lin_fwd_workspace_size).
  * Deterministic: fixed summation orders, no atomics.
@@ -372,7 +373,8 @@ size_t kda_lin_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, in
  *   dq, dk        bf16 [B, T, Hk, 128], dv bf16 [B, T, H, 128], contiguous, 16-byte aligned, fully
  *                 written; heads that share a q/k head are summed in fp32 and rounded once.
  *   ddecay        NULL (not wanted) or fp32, of decay's shape; a per-head decay's is summed over
- *                 all tokens.  0 where decay lies outside (-1000, 0].
+ *                 all tokens.  0 where decay lies outside (-1000, 0].  Products as in kda_lin_fwd.  Asking for
+ *                 it changes the order of dq's and dk's fp32 sums, so single values may round differently.
  *   dinitial_state  NULL or fp32 [N, H, 128, 128], 16-byte aligned (also when initial_state is NULL).
  *   workspace     kda_lin_bwd_workspace_size(..., ddecay != NULL) bytes, 256-byte aligned.
  * Outputs must not overlap inputs or each other (KDA_ERR_ALIAS).  An invalid cu_seqlens found on
