@@ -54,7 +54,7 @@ def inv_freq(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_con
         def pair_of(turns):  # the (real) index of the pair that turns so often over the context
             return R * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(base))
         lo = max(math.floor(pair_of(beta_fast)), 0)
-        hi = min(math.ceil(pair_of(beta_slow)), R // 2 - 1)
+        hi = min(math.ceil(pair_of(beta_slow)), R - 1)  # behind the last pair where all of them turn more often
         ramp = ((torch.arange(R // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         f = f * (1 - ramp) + f / factor * ramp
         attention_factor = 0.1 * math.log(factor) + 1.0

@@ -238,3 +238,25 @@ def test_frequencies():
     with pytest.raises(ValueError):
         qkrope.inv_freq(7)
     assert qkrope.inv_freq(0)[0].numel() == 0
+
+
+@pytest.mark.parametrize("R,base", [(32, 1e4), (64, 1e4), (128, 1e4), (128, 5e5)])
+@pytest.mark.parametrize("context", [256, 4096, 32768, 65536, 131072, 1 << 20])
+def test_yarn_ramp_ends_where_its_pairs_do(R, base, context):
+    """The ramp runs between the (real) indices of the pairs that turn 32 times and once over the original context, and may end
+    behind the last pair: a pair that still turns more than once is not divided by the whole factor."""
+    factor = 4.0
+    f, _ = qkrope.inv_freq(R, base, scaling="yarn", factor=factor, original_context=context)
+    i = np.arange(R // 2, dtype=np.float64)
+    plain = base ** (-2 * i / R)
+    index = lambda turns: R * math.log(context / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+    lo, hi = max(math.floor(index(32.0)), 0), min(math.ceil(index(1.0)), R - 1)
+    keep = 1.0 - np.clip((i - lo) / (hi - lo), 0.0, 1.0)
+    want = plain * keep + plain / factor * (1.0 - keep)
+    got = f.double().numpy()
+    np.testing.assert_allclose(got, want, rtol=2.0 ** -23)
+    turns = context * plain / (2 * math.pi)
+    assert (np.abs(got / plain - 1.0)[turns >= 32.0] < 2.0 ** -22).all()
+    assert (np.abs(got / plain * factor - 1.0)[turns <= 1.0] < 2.0 ** -22).all()
+    between = (turns > 1.0) & (i > lo) & (i < hi)
+    assert (got[between] > plain[between] / factor * 1.001).all() and (got[between] < plain[between]).all()
