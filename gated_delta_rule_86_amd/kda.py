@@ -15,6 +15,7 @@ off means that input arrives already activated (kda_fwd_ex in include/kda.h).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -138,6 +139,22 @@ def _stream_handle(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _pool(stream):
+    """Context for what a call on `stream` allocates: blocks of that stream's own pool.  A block from the current stream's
+    pool may have been freed while that stream's work on it is pending, which nothing orders before kernels on `stream`."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _used_here(stream, device, *tensors):
+    """Blocks of `stream`'s pool that the caller gets: not reused before the current stream's work on them has finished
+    (the caller orders that work behind `stream`)."""
+    import torch
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(device))
 
 
 def _state_code(t) -> int:

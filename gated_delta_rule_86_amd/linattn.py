@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import kda
-from .kda import KDA_OK, KDAError, _ptr, lib
+from .kda import KDA_OK, KDAError, _pool, _ptr, _used_here, lib
 
 D = 128
 
@@ -117,17 +117,10 @@ def _workspace(workspace, need, index, stream):
         return workspace
     if need == 0:
         return None
-    workspace = torch.empty(need, dtype=torch.uint8, device=index)
-    _used_on(stream, index, workspace)
+    with _pool(stream):
+        workspace = torch.empty(need, dtype=torch.uint8, device=index)
+    _used_here(stream, index, workspace)
     return workspace
-
-
-def _used_on(stream, index, *tensors):
-    """Tensors allocated on the current stream whose kernels run on `stream`: keep the caching allocator from
-    reusing their blocks before those have finished."""
-    if stream is not None and stream != torch.cuda.current_stream(index):
-        for t in tensors:
-            t.record_stream(stream)
 
 
 def _bytes(t):
@@ -148,6 +141,9 @@ def fwd(q, k, v, decay, scale, out, initial_state=None, final_state=None, cu_seq
     decays <= 0, [H] or [B, T, H]; out: contiguous bf16 [B, T, H, 128]; states: bf16 or fp32
     [N, H, 128, 128] or None, final_state may be initial_state; cu_seqlens: int64 [N+1] device
     tensor (then B is 1) or None.  cu_seqlens_host, workspace, stream: as in ``kda.fwd``.
+
+    With ``stream`` the kernels run there and what the call allocates comes from that stream's pool; the caller orders
+    the inputs' producers before it and the results' users behind it, and keeps the tensors it passes alive until then.
     """
     B, T, Hk, H, N, K, V, per_token, host = _check_inputs(q, k, v, decay, cu_seqlens, cu_seqlens_host)
     if (out.dtype is not torch.bfloat16 or out.shape != v.shape or not out.is_contiguous()
@@ -205,13 +201,14 @@ def bwd(q, k, v, decay, scale, dout, initial_state=None, dfinal_state=None, cu_s
     need = L.kda_lin_bwd_workspace_size(B, T, Hk, H, N if varlen else 0, varlen, bool(need_ddecay))
     with _On(index):
         bf16, fp32 = torch.bfloat16, torch.float32
-        r = {"dq": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
-             "dk": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
-             "dv": torch.empty((B, T, H, V), dtype=bf16, device=index),
-             "dinitial_state": torch.empty((N, H, V, K), dtype=fp32, device=index)}
-        if need_ddecay:
-            r["ddecay"] = torch.empty(decay.shape, dtype=fp32, device=index)
-        _used_on(stream, index, *r.values())
+        with _pool(stream):
+            r = {"dq": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
+                 "dk": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
+                 "dv": torch.empty((B, T, H, V), dtype=bf16, device=index),
+                 "dinitial_state": torch.empty((N, H, V, K), dtype=fp32, device=index)}
+            if need_ddecay:
+                r["ddecay"] = torch.empty(decay.shape, dtype=fp32, device=index)
+        _used_here(stream, index, *r.values())
         workspace = _workspace(workspace, need or 1, index, stream)
         st = L.kda_lin_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, float(scale),
                            _ptr(initial_state), _code(initial_state), dout.data_ptr(), _ptr(dfinal_state),

@@ -11,8 +11,8 @@ import math
 
 import torch
 
-from .kda import KDA_OK, KDAError, _ptr, lib
-from .linattn import _bytes, _gpu_index, _On, _raw_stream, _row_strides, _used_on, _workspace
+from .kda import KDA_OK, KDAError, _pool, _ptr, _used_here, lib
+from .linattn import _bytes, _gpu_index, _On, _raw_stream, _row_strides, _workspace
 
 NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
 _DTYPES = {torch.bfloat16: 1, torch.float32: 2, torch.float16: 3}
@@ -118,18 +118,19 @@ def fwd(q, k, positions, inv_freq, q_out, k_out, *, q_weight=None, k_weight=None
 def bwd(q, k, positions, inv_freq, dq_out, dk_out, *, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
         interleaved=False, attention_factor=1.0, workspace=None, stream=None):
     """Gradients of ``fwd`` from its inputs and dq_out, dk_out (of q's and k's shape and dtype).  Returns a dict: dq, dk
-    (contiguous, of q's dtype) and, for the weights given, dq_weight, dk_weight (fp32 [D])."""
+    (contiguous, of q's dtype) and, for the weights given, dq_weight, dk_weight (fp32 [D]).  stream: as in ``linattn.fwd``."""
     B, T, Hq, Hk, D, R, code = _check(q, k, positions, inv_freq, norm, q_weight, k_weight, dq_out, dk_out)
     index = _gpu_index(q)
     L = lib()
     with _On(index):
-        r = {"dq": torch.empty(q.shape, dtype=q.dtype, device=index),
-             "dk": torch.empty(k.shape, dtype=q.dtype, device=index)}
-        if q_weight is not None:
-            r["dq_weight"] = torch.empty(D, dtype=torch.float32, device=index)
-        if k_weight is not None:
-            r["dk_weight"] = torch.empty(D, dtype=torch.float32, device=index)
-        _used_on(stream, index, *r.values())
+        with _pool(stream):
+            r = {"dq": torch.empty(q.shape, dtype=q.dtype, device=index),
+                 "dk": torch.empty(k.shape, dtype=q.dtype, device=index)}
+            if q_weight is not None:
+                r["dq_weight"] = torch.empty(D, dtype=torch.float32, device=index)
+            if k_weight is not None:
+                r["dk_weight"] = torch.empty(D, dtype=torch.float32, device=index)
+        _used_here(stream, index, *r.values())
         need = L.kda_qk_rope_bwd_workspace_size(B, T, Hq, Hk, D) if len(r) > 2 else 0
         workspace = _workspace(workspace, need, index, stream)
         st = L.kda_qk_rope_bwd(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), r["dq"].data_ptr(),
