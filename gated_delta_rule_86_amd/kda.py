@@ -202,6 +202,9 @@ def fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state
     cu_seqlens: int64 [N+1] device tensor or None (then N = B).
     cu_seqlens_host: optional host copy (sequence or CPU tensor) for a synchronous check.
     workspace: optional uint8 device tensor of at least workspace_size(...) bytes.
+    stream: optional stream for the kernels (default: the current one).  What the call allocates comes from that
+    stream's pool; the caller orders the inputs' producers before it and the results' users behind it, and
+    keeps the tensors it passes alive until then.
     stage_events: optional sequence of 5 raw hipEvent_t handles (ints); when given the call
     goes through kda_fwd_timed, which records them around each launch (see include/kda.h).
     use_*_in_kernel: activation switches.  With use_gate_in_kernel=False, g is the natural-log
@@ -258,11 +261,9 @@ def fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state
         return None
     ws_bytes = workspace_size(B, T, H, N if cu_seqlens is not None else B, cu_seqlens is not None)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
-        # allocated on the current stream; the kernels run on `stream`: keep the caching
-        # allocator from reusing the block before they have finished
-        if stream is not None and stream != torch.cuda.current_stream(q.device):
-            workspace.record_stream(stream)
+        with _pool(stream):
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
+        _used_here(stream, q.device, workspace)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(out),
             _ptr(A_log), _ptr(dt_bias), float(lower_bound), _ptr(initial_state),
             _state_code(initial_state), _ptr(final_state), _state_code(final_state),
@@ -319,20 +320,22 @@ def bwd(q, k, v, g, beta, scale, A_log, dt_bias, lower_bound, dout, initial_stat
         raise ValueError("dfinal_state must be a contiguous fp32 [N, H, V, K] tensor")
     dev = q.device
     f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
-    r = {"dq": f32(B, T, H, K), "dk": f32(B, T, H, K), "dv": f32(B, T, H, V), "dg": f32(B, T, H, K),
-         "dbeta": f32(B, T, H), "dinitial_state": f32(N, H, V, K)}
-    if use_gate_in_kernel:
-        r["dA_log"] = f32(H)
-        r["ddt_bias"] = f32(H, K)
+    with _pool(stream):
+        r = {"dq": f32(B, T, H, K), "dk": f32(B, T, H, K), "dv": f32(B, T, H, V), "dg": f32(B, T, H, K),
+             "dbeta": f32(B, T, H), "dinitial_state": f32(N, H, V, K)}
+        if use_gate_in_kernel:
+            r["dA_log"] = f32(H)
+            r["ddt_bias"] = f32(H, K)
+    _used_here(stream, dev, *r.values())
     host_cu = None
     if cu_seqlens_host is not None:
         import numpy as np
         host_cu = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int64))
     ws_bytes = bwd_workspace_size(B, T, H, N if cu_seqlens is not None else B, cu_seqlens is not None)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-        if stream is not None and stream != torch.cuda.current_stream(dev):
-            workspace.record_stream(stream)
+        with _pool(stream):
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        _used_here(stream, dev, workspace)
     st = L.kda_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(A_log), _ptr(dt_bias),
                    float(lower_bound), _ptr(initial_state), _state_code(initial_state), _ptr(dout),
                    _ptr(dfinal_state), _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dg"]),
@@ -365,9 +368,9 @@ def chunk_table(cu_seqlens, B: int, T: int, H: int, workspace=None, stream=None)
     dev = cu_seqlens.device if cu_seqlens is not None else torch.device("cuda")
     ws_bytes = workspace_size(B, T, H, N if cu_seqlens is not None else B, cu_seqlens is not None)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-        if stream is not None and stream != torch.cuda.current_stream(dev):
-            workspace.record_stream(stream)
+        with _pool(stream):
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        _used_here(stream, dev, workspace)
     seq_off = np.zeros(N + 1, dtype=np.int64)
     n_total = ctypes.c_int64(-1)
     status = ctypes.c_int32(-1)

@@ -21,6 +21,8 @@ class Block:
     def data_ptr(self):
         return 1 << 30
 
+    device = torch.device("cuda:0")
+
     def numel(self):
         return torch.Size(self.shape).numel()
 
@@ -78,6 +80,7 @@ def calls():
         "kda.fwd": lambda **k: kda.fwd(x, x, x, x, beta, 1.0, x, a, bias, -5.0, **k),
         "kda.fwd_recurrent": lambda **k: kda.fwd_recurrent(x, x, x, x, beta, 1.0, x, a, bias, -5.0, **k),
         "kda.bwd": lambda **k: kda.bwd(x, x, x, x, beta, 1.0, a, bias, -5.0, x, **k),
+        "kda.chunk_table": lambda **k: kda.chunk_table(cu, 1, 3, 2, **k),
         "linattn.fwd": lambda **k: linattn.fwd(x, x, x, d, 1.0, x, None, h, **k),
         "linattn.fwd_recurrent": lambda **k: linattn.fwd_recurrent(x, x, x, d, 1.0, x, None, h, cu, **k),
         "linattn.bwd": lambda **k: linattn.bwd(x, x, x, d, 1.0, x, **k),
@@ -86,10 +89,9 @@ def calls():
 
 
 ALLOCATING = sorted(calls())
-NEW = [n for n in ALLOCATING if not n.startswith("kda.")]
 
 
-@pytest.mark.parametrize("name", NEW)
+@pytest.mark.parametrize("name", ALLOCATING)
 def test_blocks_come_from_the_streams_own_pool(stands, name):
     calls()[name](stream=stands.side)
     assert stands.blocks and stands.current is stands.home
@@ -98,7 +100,7 @@ def test_blocks_come_from_the_streams_own_pool(stands, name):
         assert any(s is stands.home for s in b.users)  # and the caller's own use of results before their next life
 
 
-@pytest.mark.parametrize("name", NEW)
+@pytest.mark.parametrize("name", ALLOCATING)
 def test_current_stream(stands, name):
     for stream in (None, stands.home):
         calls()[name](stream=stream)
