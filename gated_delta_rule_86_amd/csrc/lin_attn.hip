@@ -351,6 +351,7 @@ struct LdsStates {
     unsigned char k[2][kTile], v[2][kTile];
     float win[2][kLC];
     double after[2];  // log2 of the factor between the chunk's far end and the segment's boundary
+    int nan[4];       // a wave's share of the rows that were not read has a decay that is NaN
 };
 
 template <int kCtrl, int kRows>
@@ -665,7 +666,7 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 //
 // The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
-// add nothing and are not read.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
+// add nothing and are not read, but for their decays: one that is NaN makes the share NaN.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
 // H = 8, per-token decays: 62 us, 3.7 TB/s) where segments are short, else by a chunk's latency, 2.5 us.
 constexpr double kGone = -150.0;
 
@@ -726,7 +727,8 @@ __device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int6
     if (nc > 1)
         g = load_decay(a, dp, chunk(1), lane);
     double after = 0.0;
-    for (int64_t n = 0;; ++n) {
+    int64_t n = 0;
+    for (;; ++n) {
         const int buf = (int)(n & 1);
         tile_put(fk, lds.k[buf], ln);
         tile_put(fv, lds.v[buf], ln);
@@ -752,9 +754,28 @@ __device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int6
             g = load_decay(a, dp, chunk(n + 2), lane);
         c = next;
     }
-    const bool whole = !(w.pflags & kFromSlot);
+    const bool starts = !(w.pflags & kFromSlot);
+    bool whole = starts;
     const float f = after < kGone ? 0.0f : __builtin_amdgcn_exp2f((float)after);
-    if (whole && ro.init && f != 0.0f) {
+    if (a.per_token && n + 1 < nc) {
+        const int64_t t0 = rev ? w.p0 + (n + 1) * kLC : w.p0, t1 = rev ? w.p1 : w.p0 + (nc - 1 - n) * kLC;
+        bool nan = false;
+        for (int64_t t = t0 + tid; t < t1; t += 256) {
+            const float d = dp[t * a.H];
+            nan = nan || d != d;
+        }
+        const bool any = __any(nan);
+        if (lane == 0)
+            lds.nan[wave] = any;
+        lds_barrier();
+        if (lds.nan[0] | lds.nan[1] | lds.nan[2] | lds.nan[3]) {
+            whole = true;
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+                S.t[e >> 4][e & 15] = __builtin_nanf("");
+        }
+    }
+    if (starts && ro.init) {  // also with a factor of 0: what is not finite lasts
         State X;
         state_load(X, matrix_of(ro.init, w.seq_index() * a.H + h, kLinStateBytes / (ro.init_dt == kBf16 ? 2 : 1)),
                    ro.init_dt, tr, wave, lane);
@@ -809,7 +830,8 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
         for (int x = 0; x < 8; ++x) {
             if (n + x > last || lam[x] == -2.0f)
                 continue;
-            if (lam[x] > 0.0f) {
+            // a factor of 0 joins what is not finite: it lasts
+            if (!(lam[x] <= 0.0f) || (lam[x] == 0.0f && !(isfinite(s[0]) && isfinite(s[1])))) {
                 const int64_t slot = (row * a.P + (ro.rev ? a.P - 1 - (n + x) : n + x)) * a.H + h;
                 f[x][0] = fmaf(lam[x], s[0], f[x][0]);
                 f[x][1] = fmaf(lam[x], s[1], f[x][1]);

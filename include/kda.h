@@ -332,7 +332,8 @@ size_t kda_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int ha
  * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; out and bf16 final
  * states are rounded once.  out does not depend on whether final_state is asked for.  A value that
  * is not finite reaches its own sequence and head alone, from the first token of its chunk
- * of 64 tokens on (of the workgroup's run of tokens, see kda_lin_fwd_workspace_size).
+ * of 64 tokens on (of the workgroup's run of tokens, see kda_lin_fwd_workspace_size), and lasts; a k or v that is not
+ * finite may be forgotten where the decays behind it come to a factor below 2^-150.
  * Deterministic: fixed summation orders, no atomics.
  */
 kda_status kda_lin_fwd(const void *q, const void *k, const void *v, const float *decay, int decay_per_token,
