@@ -156,6 +156,9 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
         return KDA_ERR_FLAGS;
     if (!isfinite(scale))
         return KDA_ERR_SCALE;
+    // token by token nothing is cut, and a launch has 256 threads per sequence and head
+    if (recurrent ? z.n_seq > (((int64_t)1 << 24) - 8) / H : !make_layout(z, false, false, lay))
+        return KDA_ERR_SHAPE;
     memset(a, 0, sizeof(*a));
     kda::LinRole &r = a->role[0];
     Range rq, rk, rv;
@@ -178,8 +181,6 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
     if (overlap(ro, ri) || overlap(ro, rf) || (h0 != ht && overlap(ri, rf)) || overlap(rw, ri) || overlap(rw, ro) ||
         overlap(rw, rf))
         return KDA_ERR_ALIAS;
-    if (!make_layout(z, false, false, lay) || (recurrent && z.n_seq > (((int64_t)1 << 24) - 8) / H))
-        return KDA_ERR_SHAPE;  // token by token, a launch has 256 threads per sequence and head
     // token by token, the workspace holds the status word alone
     const size_t need = recurrent ? (cu ? kda::kAlign : 0) : lay->total;
     if (need && (!ws || ws_bytes < need))
@@ -192,7 +193,12 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
     r.init_dt = (int)h0_dt;
     r.fin_dt = (int)ht_dt;
     r.out = out;
-    if (lay->plan.P > 1 && !recurrent) {
+    if (!recurrent) {
+        a->rows = lay->plan.rows;
+        a->P = lay->plan.P;
+        a->len = lay->plan.len;
+    }
+    if (a->P > 1) {
         r.slots = reinterpret_cast<float *>(w + lay->off_fwd);
         r.lam = reinterpret_cast<float *>(w + lay->off_flam);
         r.defer = ht && ht == h0 ? 1 : 0;
@@ -203,9 +209,6 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
     a->T = T;
     a->H = H;
     a->N = z.n_seq;
-    a->rows = lay->plan.rows;
-    a->P = lay->plan.P;
-    a->len = lay->plan.len;
     a->cu = cu;
     a->status = reinterpret_cast<int32_t *>(w);
     return KDA_OK;

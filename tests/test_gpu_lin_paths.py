@@ -100,3 +100,13 @@ def test_cu_seqlens_host():
             linattn.bwd(q, k, v, d, SCALE, do, h0, dht, c, cu_seqlens_host=bad)
     torch.cuda.synchronize()
     assert (out == 7.0).all()
+
+
+def test_token_by_token_up_to_its_limit():
+    """As many sequences x heads as a launch holds, without states: out = scale (q.k) v."""
+    B, H = (1 << 22) - 2, 4
+    q, k, v, d, _ = inputs(B, 1, 1, H, 5, "token")
+    out = torch.empty_like(v)
+    linattn.fwd_recurrent(q, k, v, d, SCALE, out)
+    for at in (slice(0, 1000), slice(B // 2, B // 2 + 1000), slice(B - 1000, B)):
+        close_bf16(out[at], SCALE * (q[at].double() * k[at].double()).sum(-1, keepdim=True) * v[at].double(), "out")

@@ -127,6 +127,16 @@ def test_launch_limits():
     assert rope(1, 1 << 30, 1, 1, 16) == 0 and rope(1, (1 << 30) - 64, 1, 1, 16) == 1024 * 16 * 4
 
 
+@pytest.mark.parametrize("B,H,code", [((1 << 21) - 2, 4, 11), (1 << 21, 4, 11), (3 << 20, 4, 11), ((1 << 22) - 2, 4, 11), (1 << 22, 4, 2),
+                                      ((1 << 24) - 8, 1, 11), (1 << 24, 1, 2), (1 << 21, 8, 2)])
+@pytest.mark.parametrize("T", [1, 9])
+def test_token_by_token_limit_without_cu_seqlens(B, H, code, T):
+    """The limit is sequences x heads of 2^24, with and without cu_seqlens.  out overlaps q in these calls, so that sizes within
+    the limit end in KDA_ERR_ALIAS, before anything could be launched."""
+    alone = dict(out=ptr(0), h0=None, h0_dt=0, ht=None, ht_dt=0, ws=None, ws_bytes=0, Hk=1)
+    assert lin_call("kda_lin_fwd_recurrent", B=B, T=T, H=H, **alone) == code
+
+
 def rope_call(back=False, **ch):
     a = dict(q=ptr(0), k=ptr(1), y=[ptr(2), ptr(3)], g=[ptr(4), ptr(5)], wq=ptr(6), wk=ptr(7), f=ptr(8), pos=ptr(9),
              dwq=ptr(10), dwk=ptr(11), B=2, T=10, Hq=4, Hk=2, D=128, R=64, dtype=1, norm=1, eps=1e-6, inter=0, m=1.0,
