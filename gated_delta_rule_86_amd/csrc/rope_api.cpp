@@ -28,36 +28,58 @@ bool plain_overlap(uintptr_t lo, uintptr_t hi, const Span &s)
     return lo < s.hi && s.lo < hi && lo != hi && s.lo != s.hi;
 }
 
-// True when two views certainly share no byte: disjoint ranges, or rows on one lattice
-// (same token stride, batches a whole number of rows apart) with disjoint places in the row.
+// What a view covers of a period of p elements: dimensions whose stride is a multiple of p repeat it.
+int64_t width(const Span &s, int64_t p)
+{
+    const int64_t n[3] = {s.B, s.T, s.heads}, st[3] = {s.sb, s.st, s.sh};
+    int64_t w = s.D;
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && st[i] % p)
+            w += (n[i] - 1) * st[i];
+    return w;
+}
+// True when two views certainly share no byte: disjoint ranges, or disjoint places in a common period (the rows of one buffer
+// with q's heads beside k's, or its batch rows with q's heads before k's), tried for every stride.
 bool disjoint(const Span &x, const Span &y)
 {
     if (!(x.lo < y.hi && y.lo < x.hi) || x.lo == x.hi || y.lo == y.hi)
         return true;
-    const int64_t rx = x.T > 1 ? x.st : x.sb, ry = y.T > 1 ? y.st : y.sb;  // from row to row
-    if (rx != ry || rx <= 0)
-        return false;
-    const int64_t row = rx * x.size;
-    if (x.T > 1 && x.B > 1 && (x.sb % rx || y.sb % ry))
-        return false;
-    const int64_t wx = ((x.heads - 1) * x.sh + x.D) * x.size, wy = ((y.heads - 1) * y.sh + y.D) * y.size;
-    const int64_t d = (int64_t)((y.lo - x.lo) % (uintptr_t)row), down = (int64_t)((x.lo - y.lo) % (uintptr_t)row);
-    const int64_t at = y.lo >= x.lo ? d : (down ? row - down : 0);  // y's place in a row that starts with x
-    return at >= wx && at + wy <= row;
+    const int64_t n[6] = {x.B, x.T, x.heads, y.B, y.T, y.heads}, st[6] = {x.sb, x.st, x.sh, y.sb, y.st, y.sh};
+    for (int i = 0; i < 6; ++i) {
+        const int64_t p = st[i];
+        if (n[i] < 2 || p <= 0)
+            continue;
+        const int64_t period = p * x.size, wx = width(x, p) * x.size, wy = width(y, p) * y.size;
+        const int64_t up = (int64_t)((y.lo - x.lo) % (uintptr_t)period), down = (int64_t)((x.lo - y.lo) % (uintptr_t)period);
+        const int64_t at = y.lo >= x.lo ? up : (down ? period - down : 0);  // y's place in a period that starts with x
+        if (at >= wx && at + wy <= period)
+            return true;
+    }
+    return false;
 }
 bool same_view(const Span &x, const Span &y)
 {
     return x.lo == y.lo && (x.B == 1 || x.sb == y.sb) && (x.T == 1 || x.st == y.st) && (x.heads == 1 || x.sh == y.sh);
 }
-// A view that is written must not hit itself.
+// A view that is written must not hit itself: from the smallest stride on, each steps over all that the smaller ones cover.
 bool injective(const Span &s)
 {
-    const int64_t head = s.heads > 1 ? s.sh : s.D, row = (s.heads - 1) * s.sh + s.D;
-    if (head < s.D)
-        return false;
-    if (s.T > 1 && s.st < row)
-        return false;
-    return s.B == 1 || s.sb >= (s.T - 1) * s.st + row;
+    int64_t n[3] = {s.B, s.T, s.heads}, st[3] = {s.sb, s.st, s.sh}, covered = s.D;
+    for (int done = 0; done < 3; ++done) {
+        int least = done;
+        for (int i = done + 1; i < 3; ++i)
+            if (st[i] < st[least])
+                least = i;
+        const int64_t many = n[least], step = st[least];
+        n[least] = n[done];
+        st[least] = st[done];
+        if (many < 2)
+            continue;
+        if (step < covered)
+            return false;
+        covered += (many - 1) * step;
+    }
+    return true;
 }
 
 kda_status set_view(const void *p, const int64_t *st, int64_t B, int64_t T, int64_t heads, int64_t D, int size,

@@ -196,6 +196,46 @@ def test_rope_allows_views_of_one_buffer():
     assert rope_call(True, **dict(one, k=ptr(0) + 512, y=[ptr(0), ptr(0) + 512])) == 11
 
 
+@pytest.mark.parametrize("B,T", [(1, 10), (2, 10), (3, 1), (1, 1)])
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (1, 1), (3, 1)])
+def test_rope_allows_any_order_of_dimensions(B, T, Hq, Hk):
+    """Outputs laid out [B, heads, T, D], [T, B, heads, D] or [heads, B, T, D] share no byte with themselves; q and k side by side in one
+    buffer of any of these may be replaced in place, and k's place must still be clear of q's."""
+    D, H = 128, Hq + Hk
+    for q_st, k_st in (([Hq * T * D, D, T * D], [Hk * T * D, D, T * D]), ([Hq * D, B * Hq * D, D], [Hk * D, B * Hk * D, D]),
+                       ([T * D, D, B * T * D], [T * D, D, B * T * D])):
+        st = [T * Hq * D, Hq * D, D, T * Hk * D, Hk * D, D] + q_st + k_st
+        assert rope_call(True, B=B, T=T, Hq=Hq, Hk=Hk, strides=st, ws=None) == 8
+    for one, at in (([H * T * D, D, T * D], Hq * T * D), ([H * D, B * H * D, D], Hq * D), ([T * D, D, B * T * D], Hq * B * T * D)):
+        ok = dict(B=B, T=T, Hq=Hq, Hk=Hk, strides=one * 4, ws=None)
+        for off, code in ((2 * at, 8), (2 * at - 2 * D, 11)):
+            p = [ptr(0), ptr(0) + off]
+            assert rope_call(True, **ok, q=p[0], k=p[1], y=p) == code
+        # the other way round: k's heads first
+        p = [ptr(0) + 2 * (at // Hq * Hk), ptr(0)]
+        assert rope_call(True, **ok, q=p[0], k=p[1], y=p) == 8
+
+
+def test_rope_views_against_brute_force():
+    """Random small layouts of two outputs: never accepted when they share a byte, with each other or with themselves."""
+    rng = np.random.default_rng(0)
+    D, accepted, clear = 16, 0, 0
+    for _ in range(3000):
+        B, T, Hq, Hk = (int(x) for x in rng.integers(1, 4, 4))
+        st = [int(x) * 8 for x in rng.integers(0, 13, 6)]
+        base = int(rng.integers(0, 24)) * 8
+        place = lambda o, s, H: [o + b * s[0] + t * s[1] + h * s[2] + c for b in range(B) for t in range(T)  # noqa: E731
+                                 for h in range(H) for c in range(D)]
+        both = place(0, st[:3], Hq) + place(base, st[3:], Hk)
+        free = len(set(both)) == len(both)
+        y = [ptr(4), ptr(4) + 2 * base]
+        full = [T * Hq * D, Hq * D, D, T * Hk * D, Hk * D, D]
+        code = rope_call(True, B=B, T=T, Hq=Hq, Hk=Hk, D=D, R=16, strides=full * 2 + st, y=y, g=[ptr(2), ptr(3)], ws=None)
+        assert code in (8, 11) and (free or code == 11)
+        accepted, clear = accepted + (code == 8), clear + free
+    assert accepted > 0.5 * clear > 20
+
+
 def test_python_refusals():
     """What the bindings refuse before the library is called."""
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
