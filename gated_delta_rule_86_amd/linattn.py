@@ -181,13 +181,13 @@ def fwd_recurrent(q, k, v, decay, scale, out, initial_state=None, final_state=No
 
 
 def bwd(q, k, v, decay, scale, dout, initial_state=None, dfinal_state=None, cu_seqlens=None, *, need_ddecay=True,
-        cu_seqlens_host=None, workspace=None, stream=None):
+        need_dinitial_state=True, cu_seqlens_host=None, workspace=None, stream=None):
     """Gradients of ``fwd``'s out and final_state (kda_lin_bwd in include/kda.h).
 
     Inputs as ``fwd``; dout: contiguous bf16 [B, T, H, 128]; dfinal_state: None or fp32
     [N, H, 128, 128].  Returns a dict of device tensors: dq, dk (bf16, shape of q), dv (bf16), ddecay
-    (fp32, shape of decay; with need_ddecay), dinitial_state (fp32 [N, H, 128, 128]) and the
-    workspace used.
+    (fp32, shape of decay; with need_ddecay), dinitial_state (fp32 [N, H, 128, 128]; also without an initial state,
+    unless need_dinitial_state is False: 64 KiB per sequence and head) and the workspace used.
     """
     B, T, Hk, H, N, K, V, per_token, host = _check_inputs(q, k, v, decay, cu_seqlens, cu_seqlens_host)
     if (dout.dtype is not torch.bfloat16 or dout.shape != v.shape or not dout.is_contiguous()
@@ -204,8 +204,9 @@ def bwd(q, k, v, decay, scale, dout, initial_state=None, dfinal_state=None, cu_s
         with _pool(stream):
             r = {"dq": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
                  "dk": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
-                 "dv": torch.empty((B, T, H, V), dtype=bf16, device=index),
-                 "dinitial_state": torch.empty((N, H, V, K), dtype=fp32, device=index)}
+                 "dv": torch.empty((B, T, H, V), dtype=bf16, device=index)}
+            if need_dinitial_state:
+                r["dinitial_state"] = torch.empty((N, H, V, K), dtype=fp32, device=index)
             if need_ddecay:
                 r["ddecay"] = torch.empty(decay.shape, dtype=fp32, device=index)
         _used_here(stream, index, *r.values())
@@ -213,7 +214,7 @@ def bwd(q, k, v, decay, scale, dout, initial_state=None, dfinal_state=None, cu_s
         st = L.kda_lin_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), per_token, float(scale),
                            _ptr(initial_state), _code(initial_state), dout.data_ptr(), _ptr(dfinal_state),
                            r["dq"].data_ptr(), r["dk"].data_ptr(), r["dv"].data_ptr(), _ptr(r.get("ddecay")),
-                           r["dinitial_state"].data_ptr(), _ptr(cu_seqlens),
+                           _ptr(r.get("dinitial_state")), _ptr(cu_seqlens),
                            None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
                            _row_strides(q, k, v), workspace.data_ptr(), _bytes(workspace), _raw_stream(stream, index))
     if st != KDA_OK:

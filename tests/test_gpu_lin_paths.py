@@ -110,3 +110,17 @@ def test_token_by_token_up_to_its_limit():
     linattn.fwd_recurrent(q, k, v, d, SCALE, out)
     for at in (slice(0, 1000), slice(B // 2, B // 2 + 1000), slice(B - 1000, B)):
         close_bf16(out[at], SCALE * (q[at].double() * k[at].double()).sum(-1, keepdim=True) * v[at].double(), "out")
+
+
+@pytest.mark.parametrize("cu", [None, [0, 64, 64, 900], [0, 1300, 2600]], ids=str)
+@pytest.mark.parametrize("need_ddecay", [False, True])
+def test_backward_without_the_initial_states_gradient(cu, need_ddecay):
+    """Not allocated, not written; everything else keeps its bits."""
+    T, N = 200 if cu is None else cu[-1], 1 if cu is None else len(cu) - 1
+    q, k, v, d, n = inputs(1, T, 1, 2, T, "token")
+    dht, do = n(N, 2, D, D), n(1, T, 2, D).bfloat16()
+    c = None if cu is None else torch.tensor(cu, device=dev())
+    a = linattn.bwd(q, k, v, d, SCALE, do, None, dht, c, need_ddecay=need_ddecay)
+    b = linattn.bwd(q, k, v, d, SCALE, do, None, dht, c, need_ddecay=need_ddecay, need_dinitial_state=False)
+    assert set(a) - set(b) == {"dinitial_state"}
+    assert all(torch.equal(a[m], b[m]) for m in set(b) - {"workspace"})
