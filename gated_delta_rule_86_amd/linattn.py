@@ -67,7 +67,11 @@ class _On:
 
 
 def _raw_stream(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream must be on the tensors' device, cuda:{index}, not on {stream.device}")
+    return stream.cuda_stream
 
 
 def _check_inputs(q, k, v, decay, cu_seqlens, cu_seqlens_host):

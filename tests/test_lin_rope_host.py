@@ -267,6 +267,14 @@ def test_python_refusals():
             qkrope.fwd(x, y, p, f, x, y, **kw)
 
 
+def test_stream_of_another_device_is_refused():
+    import types
+    there = types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=7)
+    assert linattn._raw_stream(there, 1) == qkrope._raw_stream(there, 1) == 7
+    with pytest.raises(ValueError, match="cuda:0"):
+        linattn._raw_stream(there, 0)
+
+
 def test_frequencies():
     f, m = qkrope.inv_freq(64, 10000.0)
     want = [10000.0 ** (-2 * i / 64) for i in range(32)]
