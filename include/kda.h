@@ -316,8 +316,8 @@ size_t kda_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int ha
  *   v         bf16 [B, T, H, 128], 16-byte aligned.
  *   decay     fp32 natural-log decays g <= 0: [H] (decay_per_token 0), or contiguous [B, T, H]
  *             (decay_per_token 1; the decay of a token acts on the state before its write).
- *             Used as min(max(g, -1000), 0); from about -104 on the factor is 0 in fp32,
- *             -inf makes the head forget.  A NaN makes the sequence's head NaN from there on.
+ *             Used as min(max(g, -1000), 0); from -87.34 on the factor is 0 (below 2^-126, the smallest
+ *             normal fp32 number), -inf makes the head forget.  A NaN makes the sequence's head NaN from there on.
  *   scale     finite output factor.
  *   out       bf16 [B, T, H, 128], contiguous, 16-byte aligned; every token of every sequence
  *             is written.  Must not overlap an input.

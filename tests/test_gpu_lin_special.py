@@ -105,3 +105,16 @@ def test_value_that_is_not_finite(at):
     mine = out[0, :, 0, 9].float()
     close_bf16(torch.where(torch.isnan(mine), ro[0, :, 0, 9].float(), mine), ro[0, :, 0, 9], "out")
     assert torch.isfinite(mine[:at // 64 * 64]).all()
+
+
+@pytest.mark.parametrize("f", [linattn.fwd, linattn.fwd_recurrent])
+def test_smallest_factor(f):
+    """Factors are right down to 2^-126 (e^-87.33) and 0 below it.  The exponent is rounded to fp32, 126 * 2^-24 ln 2 = 2^-17.5 of the
+    factor, and the exponential by 2^-23."""
+    z, big = torch.zeros(1, 1, 1, D, dtype=torch.bfloat16, device=dev()), 2.0 ** 100
+    for g, normal in ((-1.0, True), (-87.0, True), (-87.33, True), (-87.34, False), (-95.0, False), (-1000.0, False)):
+        d = torch.tensor([g], device=dev())
+        h0, ht = torch.full((1, 1, D, D), big, device=dev()), torch.empty(1, 1, D, D, device=dev())
+        f(z, z, z, d, SCALE, torch.empty_like(z), h0, ht)
+        want = big * d.double().exp() if normal else torch.zeros(1, dtype=torch.float64, device=dev())
+        assert ((ht.double() - want).abs() <= 2.0 ** -17 * want).all(), (g, float(ht[0, 0, 0, 0]))
