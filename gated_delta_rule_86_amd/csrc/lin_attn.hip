@@ -632,8 +632,8 @@ __device__ __forceinline__ void state_update(State &S, const unsigned char *ktil
 
 // Two workgroups share a CU, and the older one's waves go first: it would finish at nearly full speed, then the younger one
 // would run its second half alone.  Priorities that fall over 8 chunks and start again keep them close: the one behind goes
-// first.  T = 262144, H = 8: 673 -> 646 us in all.  Only where all workgroups run at once: with more, the place that one
-// leaves early goes to the next (B = 2, T = 4096, H = 16 backwards, 768 workgroups: 205 us, 213 with turns).
+// first.  T = 262144, H = 8: 673 -> 646 us in all, when it was built.  Only where all workgroups run at once: with more, the place that one
+// leaves early goes to the next (B = 2, T = 4096, H = 16 backwards, 768 workgroups, then: 205 us, 213 with turns).
 __device__ __forceinline__ void take_turn(uint32_t token)
 {
     const uint32_t p = (token / (2 * kLC)) & 3;
@@ -667,7 +667,7 @@ __device__ __forceinline__ bool device_bad(const LinArgs &a) { return a.cu && *a
 // The chunks are taken from the boundary inwards, each row weighted with its whole factor up to the boundary,
 // so the sum itself is never scaled; once that factor is below 2^-150, 0 in fp32, the chunks further in
 // add nothing and are not read, but for their decays: one that is NaN makes the share NaN.  Tiles are in LDS twice, 64 KiB, one barrier a chunk.  Bound by memory (T = 262144,
-// H = 8, per-token decays: 62 us, 3.7 TB/s) where segments are short, else by a chunk's latency, 2.5 us.
+// H = 8, per-token decays: 65 us, 3.6 TB/s) where segments are short, else by a chunk's latency, 2.5 us.
 constexpr double kGone = -150.0;
 
 __device__ __forceinline__ void states(const LinArgs &a, const LinRole &ro, int64_t seg, int64_t h, LdsStates &lds)
@@ -805,7 +805,7 @@ __global__ __launch_bounds__(256, 2) void lin_states_kernel(LinArgs a, int lead0
 // slot_j <- share_j + lam_j * slot_{j-1} (forwards; backwards from the other end), so that slot
 // j is the state at the boundary behind (before) segment j.  Every entry is its own chain: P steps of one fma, bound by
 // memory.  Two entries a thread, the loads of 8 segments on their way together: B = 2, T = 4096, H = 16 backwards
-// (512 slots of 64 KiB) 11 us, 4.8 TB/s.
+// (512 slots of 64 KiB) 11 us, 4.9 TB/s.
 constexpr unsigned kScanParts = kD * kD / 512;  // workgroups per matrix
 
 __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int lead1)
@@ -850,12 +850,13 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int lead0, int
 // one 32 x 32 block a wave, are the one thing they share.  74 KiB of LDS and 256 registers a lane let two workgroups
 // share a CU.  The next chunk's rows are loaded into registers while this one is worked on; three barriers a chunk.
 //
-// Per chunk a wave issues 98 matrix instructions (82 without third terms) and some 800 vector instructions, the greater part
-// of them the cuts of state and rows into bf16 terms; two waves a SIMD, it is the issue of these that bounds the walk where
-// memory does not.  T = 262144, H = 8: 544 us, 2.2 GB at 4.0 TB/s (a copy: 4.8); the same loads and stores without the
-// arithmetic took 466 us.  38000 packed tokens, H = 32, Hk = 8: 261 us, 3.2 TB/s.  The three walks of a backward pass with
-// dots (75 KiB, 24-bit products), B = 2, T = 4096, H = 16: 137 us, 3.8 TB/s.  512 threads with the state's channels in
-// halves, one workgroup a CU, was slower (T = 262144: 740 us in all against 667).
+// Per chunk a wave issues 122 matrix instructions (weights 8, the state's share 48, the weights' products 18, the update
+// 48) and, counted, some 1130 other vector instructions (the greater part of them the cuts of state, weights and rows into
+// bf16 terms), 150 scalar, 143 LDS and 17 memory ones; two waves a SIMD, it is the issue of these that bounds the walk.
+// T = 262144, H = 8: 616 us, 2.2 GB at 3.6 TB/s; the same loads and stores without the arithmetic took 466 us.  38000
+// packed tokens, H = 32, Hk = 8: 337 us, 2.5 TB/s.  The three walks of a backward pass with dots (75 KiB), B = 2, T = 4096,
+// H = 16: 141 us, 3.6 TB/s.  512 threads with the state's channels in halves, one workgroup a CU, was slower (T = 262144:
+// 740 us in all against 667, with two terms).
 
 // kDots: roles with dots also give the rows' products with x's rows, the tokens' own pairs left
 // out.  Their sums over many tokens cancel, so the own pairs are added to the rows outside the matrix product.
@@ -935,7 +936,7 @@ __device__ __forceinline__ void walk(const LinArgs &a, const LinRole &ro, int64_
         }
         g = load_decay(a, dp, n, lane);
         // the other rows follow further down: 12 loads at once would fill the queue and hold the wave up (packed prompts 397 ->
-        // 379 us in all)
+        // 379 us in all, with two terms)
         tile_fetch(fq, sq, n, tid);
         if (c.flags & kPieceStart) {
             const bool slot = (c.flags & kFromSlot) != 0;
@@ -1310,7 +1311,7 @@ __global__ __launch_bounds__(1024) void lin_check_kernel(const int64_t *cu, int6
 // ------------------------------------------------------------------- backward pass, tail
 
 // Sum of the value heads that share a q/k head, in head order, rounded once.  One thread per 4 channels.  Bound by
-// memory: 13500 tokens, H = 16, Hk = 4: 45 us, 5.5 TB/s.  Folding in the walk would need the states of all
+// memory: 13500 tokens, H = 16, Hk = 4: 42 us, 5.9 TB/s.  Folding in the walk would need the states of all
 // sharing heads in one workgroup, 64 KiB of registers each.
 __global__ __launch_bounds__(256) void lin_fold_kernel(const float *xq, const float *xk, uint16_t *yq, uint16_t *yk,
                                                        int64_t rows, int64_t Hk, int64_t G, const int32_t *status)

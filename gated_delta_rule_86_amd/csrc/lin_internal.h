@@ -15,8 +15,8 @@ constexpr int kLC = 64;                       // tokens per chunk
 constexpr int64_t kLinSlots = 512;            // workgroups that run at once: two on each of 256 CUs
 constexpr int64_t kLinMinSeg = 256;           // shortest segment that a cut leaves, in tokens
 // Longest segment when the decay's gradient is wanted: it sums rounding errors from the segment's end on.  B = 2,
-// T = 4096, H = 16 against 64 bits: 1.5e-6 with 832 tokens (202 us), 1.2e-6 with 512 (201 us, 189 by now), 0.9e-6 with
-// 256 (231 us).
+// T = 4096, H = 16 against 64 bits: 1.5e-6 with 832 tokens (202 us), 1.2e-6 with 512 (201 us), 0.9e-6 with 256
+// (231 us).
 constexpr int64_t kLinGradSeg = 512;
 constexpr size_t kLinStateBytes = (size_t)kD * kD * sizeof(float);
 
@@ -34,7 +34,7 @@ struct LinPlan {
 
 // Time of `groups` workgroups of `chunks` chunks each, in chunks of a full chip: rounds of kLinSlots, each with
 // `fixed` for its state and first loads; at most one workgroup on a CU runs its chunks in about 0.6 of the time that
-// two take side by side (T = 262144, H = 8: 815 us with 256 workgroups, 700 us with 512; 619 by now).
+// two take side by side (T = 262144, H = 8: 815 us with 256 workgroups, 700 us with 512, when it was chosen).
 inline double lin_rounds(int64_t groups, int64_t chunks, double fixed)
 {
     const double round = (double)cdiv(groups, kLinSlots) * ((double)chunks + fixed);
@@ -44,7 +44,7 @@ inline double lin_rounds(int64_t groups, int64_t chunks, double fixed)
 // walks: how many share the segments (1 forward; 3 backward, two of which need states).  The cut that takes the least
 // time: the walks, the states pass (reads two of three inputs), the scan (128 KiB per slot at 5 TB/s against 9.6 us
 // for a chunk of the full chip) and two more launches.  B = 2, T = 4096, H = 16: forward 98 us with P = 16, 89 us with
-// P = 8 (81 by now).
+// P = 8, when it was chosen (86 by now).
 inline LinPlan lin_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool varlen, int64_t walks, int64_t max_len)
 {
     LinPlan p;

@@ -15,8 +15,9 @@
 // per token and shared by its heads through LDS.
 //
 // Bound by memory: every value is read once and written once (backward: read twice as many).  Measured: 16384
-// tokens x 40 heads of 128, bf16, forward 71 us (4.75 TB/s, what a large copy reaches); backward B = 2, T = 4096, 16 + 16
-// heads 50 us with the weights' sums (4.0 TB/s).  One row in flight per lane group ran at 2.5 TB/s; four (two
+// tokens x 40 heads of 128, bf16, forward 72 us from pass to pass (336 MB, 4.7 TB/s; a copy of that size 5.3), 78 us from
+// its first wave to its last; backward B = 2, T = 4096, 16 + 16 heads 50 us from pass to pass with the weights' sums (201
+// MB, 4.0 TB/s), 47 us the kernel alone (219 MB by the counters, 4.7 TB/s).  One row in flight per lane group ran at 2.5 TB/s; four (two
 // backwards) keep enough loads on their way.  Small fp32 batches are bound by latency (3001 tokens, 12 + 1 heads: 26 us,
 // of which the angles, one row's loads, the sums and the second launch follow each other).
 // A lane owns 16 channels of a row as two 16-byte pieces (four in fp32) that hold both
