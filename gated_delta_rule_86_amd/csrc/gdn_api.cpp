@@ -1,0 +1,249 @@
+// gdn_api.cpp -- host side of the gated delta rule (kda_gdn_* in include/kda.h): argument checks, workspace layout,
+// launches.  The checks are plain host code that touches no HIP API, so every error path can be exercised without a GPU.
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <hip/hip_runtime.h>
+
+#include "gdn_internal.h"
+#include "kda.h"
+
+namespace {
+
+using kda::kD;
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct Range {
+    uintptr_t lo, hi;  // [lo, hi)
+};
+Range range_of(const void *p, size_t bytes)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Range{lo, p ? lo + bytes : lo};
+}
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+
+constexpr int64_t kMaxTokenStride = (int64_t)1 << 24;  // elements: 64 rows stay below 2^31 bytes
+constexpr int64_t kMaxElems = (int64_t)1 << 46;
+
+struct Sizes {
+    int64_t B, T, Hk, H, N, n_seq;
+    bool varlen;
+};
+
+kda_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, bool varlen, Sizes *z)
+{
+    if (B < 1 || T < 0 || H < 1)
+        return KDA_ERR_SHAPE;
+    if (Hk < 1 || H % Hk != 0)
+        return KDA_ERR_HEADS;
+    if (varlen ? (B != 1 || N < 1) : (N != 0 && N != B))
+        return KDA_ERR_SHAPE;
+    if (H > ((int64_t)1 << 16) || T >= ((int64_t)1 << 35) || T > ((int64_t)1 << 40) / B ||
+        B * T > kMaxElems / (H * kD))
+        return KDA_ERR_SHAPE;
+    const int64_t n_seq = varlen ? N : B;
+    if (n_seq > (((int64_t)1 << 24) - 8) / H)  // a launch holds less than 2^32 threads: 256 for each of these
+        return KDA_ERR_SHAPE;
+    *z = Sizes{B, T, Hk, H, N, n_seq, varlen};
+    return KDA_OK;
+}
+
+bool make_layout(const Sizes &z, kda::GdnLayout *L)
+{
+    using kda::kAlign;
+    L->plan = kda::gdn_plan(z.B, z.T, z.H, z.varlen);
+    const kda::GdnPlan &p = L->plan;
+    L->slots = z.B * z.T / kda::kGC + z.n_seq + 1;
+    // 256 threads for each record, 512 for each segment and head, 4096 for each row and head
+    if (L->slots > (((int64_t)1 << 24) - 8) / z.H || p.rows * p.P > (((int64_t)1 << 23) - 8) / z.H ||
+        (p.P > 1 && p.rows >= ((int64_t)1 << 20) / z.H))
+        return false;
+    size_t off = kAlign;  // status word
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = (off + bytes + kAlign - 1) / kAlign * kAlign;
+        return o;
+    };
+    L->off_rec = L->off_seg = L->off_phi = L->off_keep = 0;
+    if (z.T > 0)
+        L->off_rec = take((size_t)L->slots * (size_t)z.H * kda::kGdnRecFwd);
+    if (p.P > 1) {
+        const size_t segs = (size_t)p.rows * (size_t)p.P * (size_t)z.H * kda::kGdnStateBytes;
+        L->off_seg = take(segs);
+        L->off_phi = take(segs);
+        L->off_keep = take(segs);
+    }
+    L->total = off;
+    return true;
+}
+
+bool dtype_ok(kda_state_dtype d) { return d == KDA_STATE_NONE || d == KDA_STATE_BF16 || d == KDA_STATE_FP32; }
+
+size_t state_bytes(kda_state_dtype d) { return kda::kGdnStateBytes / (d == KDA_STATE_BF16 ? 2 : 1); }
+
+// One strided input [B, T, heads, 128]; strides in elements (batch, token, head), NULL = contiguous.
+kda_status set_tensor(const void *p, const int64_t *st, const Sizes &z, int64_t heads, kda::GdnTensor *t, Range *r)
+{
+    t->p = static_cast<const uint16_t *>(p);
+    t->share = z.H / heads;
+    t->sb = st ? st[0] : z.T * heads * kD;
+    t->st = st ? st[1] : heads * kD;
+    t->sh = st ? st[2] : kD;
+    if (t->sb < 0 || t->st < 0 || t->sh < 0 || t->sb % 8 || t->st % 8 || t->sh % 8 || t->st > kMaxTokenStride ||
+        t->sb > kMaxElems || t->sh > kMaxElems)
+        return KDA_ERR_STRIDE;
+    if (z.T == 1)
+        t->st = kD;  // never a step, but the kernels take a row's end from it
+    if (!aligned(p, 16))
+        return KDA_ERR_ALIGN;
+    if (z.T > kMaxElems / (t->st + 1) || (z.T > 1 && t->st < kD))  // tokens' rows do not overlap
+        return KDA_ERR_STRIDE;
+    const size_t last = (size_t)(z.B - 1) * (size_t)t->sb + (size_t)(z.T > 0 ? z.T - 1 : 0) * (size_t)t->st +
+                        (size_t)(heads - 1) * (size_t)t->sh + kD;
+    *r = range_of(p, z.T > 0 ? last * 2 : 0);
+    return KDA_OK;
+}
+
+kda_status check_cu(const int64_t *cu, const int64_t *host, const Sizes &z)
+{
+    if (!cu || !host)
+        return KDA_OK;
+    if (host[0] != 0 || host[z.N] != z.T)
+        return KDA_ERR_CU_SEQLENS;
+    for (int64_t i = 0; i < z.N; ++i)
+        if (host[i + 1] < host[i])
+            return KDA_ERR_CU_SEQLENS;
+    return KDA_OK;
+}
+
+// Everything that the forward entry points check; fills the kernels' arguments.
+kda_status forward_args(const void *q, const void *k, const void *v, const float *decay, const float *beta, float scale,
+                        void *out, const void *h0, kda_state_dtype h0_dt, void *ht, kda_state_dtype ht_dt,
+                        const int64_t *cu, const int64_t *cu_host, int64_t B, int64_t T, int64_t Hk, int64_t H,
+                        int64_t N, int64_t K, int64_t V, const int64_t *strides, void *ws, size_t ws_bytes,
+                        bool recurrent, kda::GdnArgs *a)
+{
+    if (T != 0 && (!q || !k || !v || !decay || !beta || !out))
+        return KDA_ERR_NULL;
+    Sizes z;
+    kda_status st = check_sizes(B, T, Hk, H, N, cu != nullptr, &z);
+    if (st != KDA_OK)
+        return st;
+    if (K != kD || V != kD)
+        return KDA_ERR_HEAD_DIM;
+    if (!dtype_ok(h0_dt) || !dtype_ok(ht_dt) || (h0 == nullptr) != (h0_dt == KDA_STATE_NONE) ||
+        (ht == nullptr) != (ht_dt == KDA_STATE_NONE) || (h0 && ht && h0_dt != ht_dt))
+        return KDA_ERR_DTYPE;
+    if (!isfinite(scale))
+        return KDA_ERR_SCALE;
+    kda::GdnLayout lay;
+    if (!recurrent && !make_layout(z, &lay))
+        return KDA_ERR_SHAPE;
+    memset(a, 0, sizeof(*a));
+    Range rq, rk, rv;
+    if ((st = set_tensor(q, strides, z, Hk, &a->q, &rq)) != KDA_OK ||
+        (st = set_tensor(k, strides ? strides + 3 : nullptr, z, Hk, &a->k, &rk)) != KDA_OK ||
+        (st = set_tensor(v, strides ? strides + 6 : nullptr, z, H, &a->v, &rv)) != KDA_OK)
+        return st;
+    if (!aligned(out, 16) || !aligned(decay, 4) || !aligned(beta, 4) || !aligned(h0, 16) || !aligned(ht, 16) ||
+        !aligned(cu, 8) || !aligned(ws, kda::kAlign))
+        return KDA_ERR_ALIGN;
+    const size_t rows = (size_t)B * (size_t)T * (size_t)H, states = (size_t)z.n_seq * (size_t)H;
+    const Range ro = range_of(out, rows * kD * 2), ri = range_of(h0, states * state_bytes(h0_dt)),
+                rf = range_of(ht, states * state_bytes(ht_dt)), rw = range_of(ws, ws_bytes);
+    const Range in[] = {rq, rk, rv, range_of(decay, rows * 4), range_of(beta, rows * 4),
+                        range_of(cu, cu ? (size_t)(N + 1) * 8 : 0)};
+    for (const Range &x : in)
+        if (overlap(ro, x) || overlap(rf, x) || overlap(rw, x))
+            return KDA_ERR_ALIAS;
+    if (overlap(ro, ri) || overlap(ro, rf) || (h0 != ht && overlap(ri, rf)) || overlap(rw, ri) || overlap(rw, ro) ||
+        overlap(rw, rf))
+        return KDA_ERR_ALIAS;
+    // token by token, the workspace holds the status word alone
+    const size_t need = recurrent ? (cu ? kda::kAlign : 0) : lay.total;
+    if (need && (!ws || ws_bytes < need))
+        return KDA_ERR_WORKSPACE;
+    if ((st = check_cu(cu, cu_host, z)) != KDA_OK)
+        return st;
+    a->decay = decay;
+    a->beta = beta;
+    a->scale = scale;
+    a->T = T;
+    a->H = H;
+    a->N = z.n_seq;
+    a->cu = cu;
+    unsigned char *w = static_cast<unsigned char *>(ws);
+    a->status = cu ? reinterpret_cast<int32_t *>(w) : nullptr;
+    a->out = static_cast<uint16_t *>(out);
+    a->init = h0;
+    a->fin = ht;
+    a->init_dt = (int)h0_dt;
+    a->fin_dt = (int)ht_dt;
+    if (!recurrent) {
+        a->rows = lay.plan.rows;
+        a->P = lay.plan.P;
+        a->len = lay.plan.len;
+        a->slots = lay.slots;
+        a->rec = w + lay.off_rec;
+        if (a->P > 1) {
+            a->seg = reinterpret_cast<float *>(w + lay.off_seg);
+            a->phi = reinterpret_cast<float *>(w + lay.off_phi);
+            if (ht && ht == h0)
+                a->keep = reinterpret_cast<float *>(w + lay.off_keep);
+        }
+    }
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_gdn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens)
+{
+    Sizes z;
+    kda::GdnLayout lay;
+    if (check_sizes(B, T, H, H, N, has_cu_seqlens != 0, &z) != KDA_OK || !make_layout(z, &lay))
+        return 0;
+    return lay.total;
+}
+
+kda_status kda_gdn_fwd(const void *q, const void *k, const void *v, const float *decay, const float *beta, float scale,
+                       void *out, const void *initial_state, kda_state_dtype initial_state_dtype, void *final_state,
+                       kda_state_dtype final_state_dtype, const int64_t *cu_seqlens, const int64_t *cu_seqlens_host,
+                       int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t K, int64_t V,
+                       const int64_t *strides_host, void *workspace, size_t workspace_bytes, void *stream)
+{
+    kda::GdnArgs a;
+    const kda_status st =
+        forward_args(q, k, v, decay, beta, scale, out, initial_state, initial_state_dtype, final_state, final_state_dtype,
+                     cu_seqlens, cu_seqlens_host, B, T, Hk, H, N, K, V, strides_host, workspace, workspace_bytes, false, &a);
+    if (st != KDA_OK)
+        return st;
+    return kda::gdn_launch_fwd(a, static_cast<int32_t *>(workspace), static_cast<hipStream_t>(stream)) == hipSuccess
+               ? KDA_OK
+               : KDA_ERR_HIP;
+}
+
+kda_status kda_gdn_fwd_recurrent(const void *q, const void *k, const void *v, const float *decay, const float *beta,
+                                 float scale, void *out, const void *initial_state, kda_state_dtype initial_state_dtype,
+                                 void *final_state, kda_state_dtype final_state_dtype, const int64_t *cu_seqlens,
+                                 const int64_t *cu_seqlens_host, int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                                 int64_t K, int64_t V, const int64_t *strides_host, void *workspace,
+                                 size_t workspace_bytes, void *stream)
+{
+    kda::GdnArgs a;
+    const kda_status st =
+        forward_args(q, k, v, decay, beta, scale, out, initial_state, initial_state_dtype, final_state, final_state_dtype,
+                     cu_seqlens, cu_seqlens_host, B, T, Hk, H, N, K, V, strides_host, workspace, workspace_bytes, true, &a);
+    if (st != KDA_OK)
+        return st;
+    return kda::gdn_launch_recurrent(a, static_cast<int32_t *>(workspace), static_cast<hipStream_t>(stream)) == hipSuccess
+               ? KDA_OK
+               : KDA_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,98 @@
+// gdn_internal.h -- shared by the host side (gdn_api.cpp) and the gfx950 kernels (gdn.hip) of the gated delta
+// rule.  Not part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+constexpr int kGC = 64;                    // tokens per chunk
+constexpr int64_t kGdnCUs = 256;           // one workgroup of a walk on each
+constexpr size_t kGdnStateBytes = (size_t)kD * kD * sizeof(float);
+constexpr int64_t kGdnMinSeg = 4 * kGC;    // shortest segment that a cut leaves, in tokens
+
+// Record of one (chunk, head) in the workspace, bytes: operands of the walks, in the order of their lanes.
+//   forward:   T' | factors | A' | 2 KiB unused
+//   backward:  T' | factors | T^T | A^T | 2 KiB unused
+// Each matrix is 6 blocks of 16 x 32 (the other two of the triangle are zero) of three bf16 terms, 1 KiB a block.
+constexpr int kGdnMat = 6 * 3 * 1024;
+constexpr int kGdnVec = 2048;
+constexpr int kGdnRecFwd = 2 * kGdnMat + kGdnVec + 2048;
+constexpr int kGdnRecBwd = 3 * kGdnMat + kGdnVec + 2048;
+
+// The tokens of a batch row (the one row of a packed batch) are cut into P segments of `len` tokens whatever the
+// sequences in it.  A chunk belongs to the segment that holds its first token.  Where a sequence's chunks go on in the
+// next segment, the state there is found before the output walk: each segment's own share F and, where it lies inside one
+// sequence, its transition Phi (S_end = S_begin Phi + F), joined by a scan.
+struct GdnPlan {
+    int64_t rows, P, len;
+};
+
+// Time of a pass in chunks of the output walk (one workgroup on a CU): the walk in rounds of kGdnCUs, and with a cut the
+// shares and transitions of all but the last segment, the scan's steps and two more launches.
+inline GdnPlan gdn_plan(int64_t B, int64_t T, int64_t H, bool varlen)
+{
+    GdnPlan p;
+    p.rows = varlen ? 1 : B;
+    p.P = 1;
+    p.len = T > 0 ? cdiv(T, kGC) * kGC : kGC;
+    const int64_t chains = p.rows * H;
+    int64_t most = T / kGdnMinSeg;
+    if (most > 2 * kGdnCUs / chains)
+        most = 2 * kGdnCUs / chains;
+    double best = (double)cdiv(chains, kGdnCUs) * ((double)(p.len / kGC) + 1.0);
+    for (int64_t P = 2; P <= most; ++P) {
+        const int64_t len = cdiv(cdiv(T, P), kGC) * kGC, got = cdiv(T, len), n = len / kGC;
+        const double cost = (double)cdiv(chains * got, kGdnCUs) * ((double)n + 1.0) +
+                            0.7 * (double)cdiv(2 * chains * (got - 1), kGdnCUs) * ((double)n + 1.0) +
+                            0.5 * (double)(got - 2) + 2.0;
+        if (got > 1 && cost < best) {
+            best = cost;
+            p.P = got;
+            p.len = len;
+        }
+    }
+    return p;
+}
+
+struct GdnTensor {  // bf16 [B, T, heads, 128] with element strides; head h of the pass reads head h / share
+    const uint16_t *p;
+    int64_t sb, st, sh;
+    int64_t share;
+};
+
+struct GdnArgs {
+    GdnTensor q, k, v, dout;
+    const float *decay, *beta;   // [B, T, H]
+    float scale;
+    int64_t T, H, N;             // N: sequences
+    int64_t rows, P, len;
+    const int64_t *cu;           // NULL: every row is one sequence
+    const int32_t *status;       // device status word (NULL without cu)
+    uint16_t *out;
+    const void *init;
+    void *fin;
+    int init_dt, fin_dt;
+    unsigned char *rec;          // [slots][H] records
+    int64_t slots;
+    float *seg;                  // [rows * P][H]: state at a segment's start, of the sequence that crosses it
+    float *phi;                  // [rows * P][H]
+    float *keep;                 // [rows * P][H]: initial state of the sequence that leaves the segment (in place), or NULL
+};
+
+struct GdnLayout {
+    GdnPlan plan;
+    int64_t slots;
+    size_t off_rec, off_seg, off_phi, off_keep;
+    size_t total;
+};
+
+hipError_t gdn_launch_fwd(const GdnArgs &a, int32_t *status, hipStream_t s);
+hipError_t gdn_launch_recurrent(const GdnArgs &a, int32_t *status, hipStream_t s);
+
+}  // namespace kda

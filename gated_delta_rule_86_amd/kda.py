@@ -42,7 +42,8 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_recurrent", "kda_fwd_recurrent_time
            "kda_status_string",
            "kda_fwd_device_status", "kda_chunk_table", "kda_version",
            "kda_lin_fwd", "kda_lin_fwd_recurrent", "kda_lin_fwd_workspace_size", "kda_lin_bwd",
-           "kda_lin_bwd_workspace_size", "kda_qk_rope", "kda_qk_rope_bwd", "kda_qk_rope_bwd_workspace_size")
+           "kda_lin_bwd_workspace_size", "kda_qk_rope", "kda_qk_rope_bwd", "kda_qk_rope_bwd_workspace_size",
+           "kda_gdn_fwd", "kda_gdn_fwd_recurrent", "kda_gdn_fwd_workspace_size")
 
 
 class KDAError(RuntimeError):
@@ -110,6 +111,12 @@ def lib():
     L.kda_qk_rope_bwd.argtypes = [vp] * 12 + [i64] * 6 + [ci, ci, f32, ci, f32, vp, vp, szt, vp]
     L.kda_qk_rope_bwd_workspace_size.restype = szt
     L.kda_qk_rope_bwd_workspace_size.argtypes = [i64] * 5
+    L.kda_gdn_fwd.restype = ci
+    L.kda_gdn_fwd.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, ci, vp, ci, vp, vp] + [i64] * 7 + [vp, vp, szt, vp]
+    L.kda_gdn_fwd_recurrent.restype = ci
+    L.kda_gdn_fwd_recurrent.argtypes = L.kda_gdn_fwd.argtypes
+    L.kda_gdn_fwd_workspace_size.restype = szt
+    L.kda_gdn_fwd_workspace_size.argtypes = [i64, i64, i64, i64, ci]
     L.kda_version.restype = ctypes.c_int
     L.kda_version.argtypes = []
     _lib = L

@@ -18,7 +18,8 @@
  * The library evaluates this in 16-token chunks (FlashKDA article index: "processes
  * 16-token chunks"; "Neumann-series expansion" for the intra-chunk inverse).
  *
- * Beside it: kda_lin_*, linear attention with one decay per head (no delta rule, no gate per channel),
+ * Beside it: kda_gdn_*, the gated delta rule with one decay per head instead of one per channel, and kda_lin_*,
+ * linear attention with one decay per head (no delta rule), each
  * forward, token by token and backward, on the same state layout; and kda_qk_rope*, the
  * normalisation of q and k with the rotation by positions, which prepares the inputs of either.
  *
@@ -63,8 +64,8 @@ typedef enum kda_status {
     KDA_ERR_ALIAS = 11,      /* out overlaps an input, or final_state overlaps a non-state input */
     KDA_ERR_FLAGS = 12,      /* kda_fwd_ex: unknown bits in the activation switch mask */
     KDA_ERR_SCRATCH = 13,    /* kda_fwd_noalloc: the call needs more than KDA_NOALLOC_SCRATCH_BYTES */
-    KDA_ERR_HEADS = 14,      /* kda_lin_*: H is not a multiple of Hk, or Hk < 1 */
-    KDA_ERR_STRIDE = 15,     /* kda_lin_*, kda_qk_rope*: a stride is negative, no multiple of 16 bytes, or too large */
+    KDA_ERR_HEADS = 14,      /* kda_lin_*, kda_gdn_*: H is not a multiple of Hk, or Hk < 1 */
+    KDA_ERR_STRIDE = 15,     /* kda_lin_*, kda_gdn_*, kda_qk_rope*: a stride is negative, no multiple of 16 bytes, or too large */
     KDA_ERR_ROTARY = 16      /* kda_qk_rope*: head size or rotary_dim not supported */
 } kda_status;
 
@@ -396,6 +397,55 @@ kda_status kda_lin_bwd(const void *q, const void *k, const void *v, const float 
  */
 size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens,
                                   int need_ddecay);
+
+/*
+ * kda_gdn_fwd -- the gated delta rule with a decay for each head, chunked form (prompts, training).  Per (sequence,
+ * head), with the state S [V][K] of kda_fwd's layout:
+ *   S~ = e^g S,   S <- S~ + beta (v - S~ k) k^T,   out = scale * S q.
+ *
+ *   q, k, v   bf16 [B, T, Hk, 128], [B, T, Hk, 128], [B, T, H, 128], strides_host: as in kda_lin_fwd (value head h reads
+ *             q/k head h / (H / Hk)).  They are used as given: kda_qk_rope with KDA_NORM_L2 makes keys of norm 1, which
+ *             keep the rule from growing for beta in [0, 2].
+ *   decay     fp32 [B, T, H], contiguous: natural-log decay of each token, used as min(max(g, -1000), 0); it acts on
+ *             the state before the token's write.  Below about -87 the factor is 0: the head forgets.
+ *   beta      fp32 [B, T, H], contiguous: write strength, used as given (0 writes nothing).
+ *   scale     finite output factor.
+ *   out       bf16 [B, T, H, 128], contiguous, 16-byte aligned; every token of every sequence is written.  Must not
+ *             overlap an input.
+ *   initial_state, final_state and their dtypes, cu_seqlens, cu_seqlens_host, B, T, N, K, V, workspace
+ *             (256-byte aligned, kda_gdn_fwd_workspace_size bytes) and stream: as in kda_fwd, including the
+ *             in-place state carry and the handling of an invalid cu_seqlens (kda_fwd_device_status reads the
+ *             status word of this workspace too).
+ * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; out and bf16 final states are
+ * rounded once.  A value that is not finite (or a NaN gate) reaches its own sequence and head alone, from the first token of its
+ * chunk of 64 tokens on, and may last.  Deterministic: fixed summation orders, no atomics.
+ * Errors: KDA_ERR_NULL, _SHAPE (also sizes whose launch would hold 2^32 threads), _HEAD_DIM, _DTYPE, _SCALE, _ALIGN,
+ * _WORKSPACE, _CU_SEQLENS, _HIP, _ALIAS, _HEADS, _STRIDE.
+ */
+kda_status kda_gdn_fwd(const void *q, const void *k, const void *v, const float *decay, const float *beta, float scale,
+                       void *out, const void *initial_state, kda_state_dtype initial_state_dtype, void *final_state,
+                       kda_state_dtype final_state_dtype, const int64_t *cu_seqlens, const int64_t *cu_seqlens_host,
+                       int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t K, int64_t V,
+                       const int64_t *strides_host, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_gdn_fwd_recurrent -- the same operator token by token in fp32, for the decode step (one token per sequence,
+ * state in and out, often in place) and sequences of a few tokens.  Same arguments and results (to rounding) as
+ * kda_gdn_fwd.  The workspace may be NULL without cu_seqlens; with it, 256 bytes hold the status word.
+ */
+kda_status kda_gdn_fwd_recurrent(const void *q, const void *k, const void *v, const float *decay, const float *beta,
+                                 float scale, void *out, const void *initial_state, kda_state_dtype initial_state_dtype,
+                                 void *final_state, kda_state_dtype final_state_dtype, const int64_t *cu_seqlens,
+                                 const int64_t *cu_seqlens_host, int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                                 int64_t K, int64_t V, const int64_t *strides_host, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * kda_gdn_fwd_workspace_size -- 256 bytes; 40 KiB per chunk of 64 tokens and head (at most T / 64 + 1 chunks for each sequence);
+ * where rows are cut into segments that run in parallel, three fp32 128 x 128 states per segment and head.  A function
+ * of (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes.
+ */
+size_t kda_gdn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
 
 typedef enum kda_dtype {
     KDA_DTYPE_BF16 = 1,
