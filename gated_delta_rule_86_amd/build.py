@@ -3,8 +3,10 @@
     python -m gated_delta_rule_86_amd.build
 
 Compiles csrc/kda_kernels.hip, csrc/kda_recurrent.hip, csrc/kda_noalloc.hip,
-csrc/kda_backward.hip, csrc/lin_attn.hip, csrc/qk_rope.hip and csrc/gdn.hip (device code) and
-csrc/kda_api.cpp, csrc/lin_api.cpp, csrc/rope_api.cpp and csrc/gdn_api.cpp (host C ABI) into
+csrc/kda_backward.hip, csrc/lin_attn.hip, csrc/qk_rope.hip, csrc/gdn.hip and
+csrc/block_norm.hip (device code) and
+csrc/kda_api.cpp, csrc/lin_api.cpp, csrc/rope_api.cpp, csrc/gdn_api.cpp and
+csrc/norm_api.cpp (host C ABI) into
 gated_delta_rule_86_amd/libkda.so.  Always rebuilds.
 """
 from __future__ import annotations
@@ -46,7 +48,8 @@ def build(verbose: bool = False) -> str:
             os.path.join(CSRC, "kda_noalloc.hip"), os.path.join(CSRC, "kda_backward.hip"),
             os.path.join(CSRC, "lin_attn.hip"), os.path.join(CSRC, "qk_rope.hip"),
             os.path.join(CSRC, "kda_api.cpp"), os.path.join(CSRC, "lin_api.cpp"),
-            os.path.join(CSRC, "rope_api.cpp"), os.path.join(CSRC, "gdn.hip"), os.path.join(CSRC, "gdn_api.cpp")]
+            os.path.join(CSRC, "rope_api.cpp"), os.path.join(CSRC, "gdn.hip"), os.path.join(CSRC, "gdn_api.cpp"),
+            os.path.join(CSRC, "block_norm.hip"), os.path.join(CSRC, "norm_api.cpp")]
     tmp = LIB + ".tmp"
     cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *srcs]
     if verbose:

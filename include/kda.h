@@ -21,7 +21,8 @@
  * Beside it: kda_gdn_*, the gated delta rule with one decay per head instead of one per channel, and kda_lin_*,
  * linear attention with one decay per head (no delta rule), each
  * forward, token by token and backward, on the same state layout; and kda_qk_rope*, the
- * normalisation of q and k with the rotation by positions, which prepares the inputs of either.
+ * normalisation of q and k with the rotation by positions, which prepares the inputs of either; and kda_gated_norm*,
+ * kda_residual_norm*, what follows a mixer: the norm of its heads with their gate, and the step to the next block.
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers unless the name ends in _host.
@@ -53,7 +54,7 @@ typedef enum kda_status {
     KDA_OK = 0,
     KDA_ERR_NULL = 1,        /* A_log or dt_bias is NULL (in-pass gate), or a token tensor is NULL while T > 0 */
     KDA_ERR_SHAPE = 2,       /* B < 1, T < 0, H < 1, N inconsistent or >= 2^29, or cu_seqlens with B != 1 */
-    KDA_ERR_HEAD_DIM = 3,    /* K or V is not 128 */
+    KDA_ERR_HEAD_DIM = 3,    /* K or V is not 128; kda_gated_norm*, kda_residual_norm*: D not supported */
     KDA_ERR_DTYPE = 4,       /* state dtype unknown, or initial/final state dtypes differ */
     KDA_ERR_LOWER_BOUND = 5, /* lower_bound not finite or outside [-5, 0] */
     KDA_ERR_SCALE = 6,       /* scale not finite */
@@ -65,7 +66,7 @@ typedef enum kda_status {
     KDA_ERR_FLAGS = 12,      /* kda_fwd_ex: unknown bits in the activation switch mask */
     KDA_ERR_SCRATCH = 13,    /* kda_fwd_noalloc: the call needs more than KDA_NOALLOC_SCRATCH_BYTES */
     KDA_ERR_HEADS = 14,      /* kda_lin_*, kda_gdn_*: H is not a multiple of Hk, or Hk < 1 */
-    KDA_ERR_STRIDE = 15,     /* kda_lin_*, kda_gdn_*, kda_qk_rope*: a stride is negative, no multiple of 16 bytes, or too large */
+    KDA_ERR_STRIDE = 15,     /* kda_lin_*, kda_gdn_*, kda_qk_rope*, norms: a stride is negative, no multiple of 16 bytes, or too large */
     KDA_ERR_ROTARY = 16      /* kda_qk_rope*: head size or rotary_dim not supported */
 } kda_status;
 
@@ -503,6 +504,77 @@ kda_status kda_qk_rope_bwd(const void *q, const void *k, const void *dq_out, con
 
 /* Bytes of partial weight sums: 4 D for each of 1024 workgroups.  Returns 0 for invalid sizes. */
 size_t kda_qk_rope_bwd_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D);
+
+typedef enum kda_gate {
+    KDA_GATE_SIGMOID = 0,
+    KDA_GATE_SILU = 1 /* z * sigmoid(z) */
+} kda_gate;
+
+/*
+ * kda_gated_norm -- the norm behind a mixer with its gate: out = x / sqrt(mean(x^2) + eps) * weight * act(gate), per token
+ * and head, in fp32, rounded once.
+ *   x, gate       [B, T, H, D] of `dtype`, 16-byte aligned.  D a multiple of 8 up to 512.
+ *   weight        NULL (1) or fp32 [D], shared by the heads.
+ *   out           [B, T, H, D], contiguous, 16-byte aligned.  May be x or gate where that is contiguous; else it overlaps
+ *                 no input.
+ *   activation    act: KDA_GATE_SIGMOID or KDA_GATE_SILU.   eps: finite and >= 0.
+ *   strides_host  NULL (contiguous) or host int64 [6]: batch, token, head strides of x and gate in elements, each a
+ *                 multiple of 16 bytes.
+ * Errors: KDA_ERR_NULL, _SHAPE (also 2^31 rows or more), _HEAD_DIM (D), _DTYPE, _FLAGS (activation), _SCALE (eps), _STRIDE,
+ * _ALIGN, _ALIAS, _HIP.  T = 0 does nothing.
+ */
+kda_status kda_gated_norm(const void *x, const void *gate, const float *weight, void *out, int64_t B, int64_t T, int64_t H,
+                          int64_t D, kda_dtype dtype, kda_gate activation, float eps, const int64_t *strides_host,
+                          void *stream);
+
+/*
+ * kda_gated_norm_bwd -- gradients of kda_gated_norm from its inputs and dout [B, T, H, D], contiguous: dx, dgate, contiguous,
+ * and dweight (NULL = not wanted), fp32 [D], summed over tokens and heads in a fixed order.  The workspace
+ * (kda_gated_norm_bwd_workspace_size bytes, 256-byte aligned) is used, and may be NULL otherwise, when dweight is wanted.
+ * Outputs overlap nothing.
+ */
+kda_status kda_gated_norm_bwd(const void *x, const void *gate, const float *weight, const void *dout, void *dx, void *dgate,
+                              float *dweight, int64_t B, int64_t T, int64_t H, int64_t D, kda_dtype dtype,
+                              kda_gate activation, float eps, const int64_t *strides_host, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Bytes of partial weight sums: 4 D for each of up to 1024 workgroups.  Returns 0 for invalid sizes. */
+size_t kda_gated_norm_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t D, kda_dtype dtype);
+
+/*
+ * kda_residual_norm -- from one block to the next: an optional norm of the block's output, its scale per channel, the
+ * residual's sum and the norm before the next block, per token, in fp32:
+ *   h = x, or x / sqrt(mean(x^2) + eps) * post_weight (post_norm KDA_NORM_RMS);   y = residual + scale * h;
+ *   residual_out = y, rounded to its type;   out = y / sqrt(mean(y^2) + eps) * weight, from the sum before it is rounded.
+ *   x, out        [B, T, D] of `dtype`; residual, residual_out [B, T, D] of `residual_dtype`: dtype or fp32.  All 16-byte
+ *                 aligned; out and residual_out contiguous.  out may be x and residual_out may be residual where that is contiguous;
+ *                 otherwise outputs overlap nothing.  D a multiple of 8 up to 8192.
+ *   weight, scale, post_weight  NULL (1) or fp32 [D]; post_weight only with KDA_NORM_RMS.
+ *   strides_host  NULL (contiguous) or host int64 [4]: batch and token strides of x and residual in elements, each a
+ *                 multiple of 16 bytes.
+ * Errors as in kda_gated_norm (_FLAGS: post_norm).
+ */
+kda_status kda_residual_norm(const void *x, const void *residual, const float *weight, const float *scale,
+                             const float *post_weight, void *out, void *residual_out, int64_t B, int64_t T, int64_t D,
+                             kda_dtype dtype, kda_dtype residual_dtype, kda_norm post_norm, float eps,
+                             const int64_t *strides_host, void *stream);
+
+/*
+ * kda_residual_norm_bwd -- gradients of kda_residual_norm: dx (of dtype) and dresidual (of residual_dtype), contiguous, from
+ * x, residual_out as the forward pass stored it (the gradients are those at the stored values), dout and
+ * dresidual_out (NULL = zero), both contiguous; and (NULL = not wanted) dweight, dscale, dpost_weight, fp32 [D], summed over
+ * tokens in a fixed order.  strides_host: int64 [4], of x and residual_out.  The workspace
+ * (kda_residual_norm_bwd_workspace_size bytes, 256-byte aligned) is used, and may be NULL otherwise, when one of the
+ * three is wanted.  Outputs overlap nothing.
+ */
+kda_status kda_residual_norm_bwd(const void *x, const void *residual_out, const void *dout, const void *dresidual_out,
+                                 const float *weight, const float *scale, const float *post_weight, void *dx,
+                                 void *dresidual, float *dweight, float *dscale, float *dpost_weight, int64_t B, int64_t T,
+                                 int64_t D, kda_dtype dtype, kda_dtype residual_dtype, kda_norm post_norm, float eps,
+                                 const int64_t *strides_host, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of partial weight sums: 12 D for each of up to 1024 workgroups.  Returns 0 for invalid sizes. */
+size_t kda_residual_norm_bwd_workspace_size(int64_t B, int64_t T, int64_t D);
 
 /* Human-readable name of a kda_status value (static string; never NULL). */
 const char *kda_status_string(int status);
