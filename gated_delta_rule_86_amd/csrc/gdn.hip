@@ -9,7 +9,17 @@
 //   out_t = scale * (e^{b_t} S q_t + sum_{s <= t} e^{b_t - b_s} (q_t.k_s) beta_s r_s),
 //   S    <- e^{L} S + sum_s e^{L - b_s} beta_s r_s k_s^T.
 // T' does not divide by beta (beta = 0 writes nothing and needs no case of its own).  It is formed as 1 - N diag(beta)
-// with N = (1 + M diag(beta))^-1 M, from which the backward pass also has (1 + diag(beta) M)^-1 = 1 - diag(beta) N.
+// with N = (1 + M diag(beta))^-1 M, from which the backward pass also has T = (1 + diag(beta) M)^-1 = 1 - diag(beta) N.
+//
+// Backward, with dS the gradient of the state after the chunk, A_ts = scale e^{b_t - b_s} q_t.k_s (s <= t), w = beta r the
+// writes and dw their gradients, dx = beta dw those of x:
+//   dw = T^T (A^T dO + tail (dS k_s)),  tail_s = e^{L - b_s},   dv = dx,   dbeta_t = dw_t.r_t,
+//   dS_before = e^{L} dS + sum_t (scale e^{b_t} dO_t) q_t^T - (e^{b_t} dx_t) k_t^T,
+//   dq_t = scale e^{b_t} S^T dO_t + sum_s P_ts k_s,           P_ts = scale e^{b_t - b_s} dO_t.w_s  (s <= t),
+//   dk_s = tail_s dS^T w_s - e^{b_s} S^T dx_s + sum_t P_ts q_t + sum_t (G_ts + G_st) k_t,
+//                                                             G_ts = -e^{b_t - b_s} dx_t.w_s     (s < t),
+//   dg_t = sum over the chunk's u >= t of (q_u.dq_u - v_u.dv_u), plus <dS, S_after>,
+// since <dS~, S~> at a token is that at the next one plus what the token's read adds and its write takes.
 //
 // Numbers: decays are used as min(max(g, -1000), 0); running sums of logarithms are fp64, a factor is the
 // exponential of a difference and at most 1.  The products run on bf16 MFMA with fp32 accumulation; q, k, v are
@@ -18,6 +28,7 @@
 #include <stdint.h>
 
 #include "gdn_internal.h"
+#include "lin_internal.h"
 
 namespace kda {
 namespace {
@@ -273,6 +284,7 @@ constexpr int kVOut = 128;    // scale e^{b_t}
 constexpr int kVBeta = 192;   // beta_s
 constexpr int kVTail = 256;   // e^{L - b_s}
 constexpr int kVLast = 320;   // [0]: e^{L}
+constexpr int kVSum = 384;    // b_t (log2), as a pair of floats: the second 64 behind the first
 
 // block of a triangular matrix with rows in row tile r and the contraction in 32-column step ks
 __device__ __forceinline__ constexpr int low_block(int r, int ks) { return r < 2 ? r : 2 + 2 * (r - 2) + ks; }  // ks <= r / 2
@@ -310,7 +322,7 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
         return;
     const int len = (int)(rest < kGC ? rest : kGC);
     const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGC;
-    unsigned char *rec = a.rec + (slot * a.H + h) * (kBwd ? kGdnRecBwd : kGdnRecFwd);
+    unsigned char *rec = a.rec + (slot * a.H + h) * a.rec_bytes;
 
     auto tile = [&](const GdnTensor &x) {
         const uint32_t stride = (uint32_t)x.st * 2;
@@ -348,6 +360,10 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
         v[kVOut + lane] = a.scale * head;
         v[kVBeta + lane] = bet;
         v[kVTail + lane] = tail;
+        if constexpr (kBwd) {
+            v[kVSum + lane] = bh;
+            v[kVSum + 64 + lane] = (float)(b - (double)bh);
+        }
         if (lane == 0)
             v[kVLast] = __builtin_amdgcn_exp2f((float)last);
     }
@@ -679,12 +695,47 @@ __device__ __forceinline__ Terms block_terms(const unsigned char *mat, int block
 constexpr int kModeOut = 0;    // out and final states
 constexpr int kModeShare = 1;  // a segment's share of the state at its end (F)
 constexpr int kModePhi = 2;    // the transition: from S = 1, without values
+constexpr int kModeStore = 3;  // backward pass: the state before each chunk and its residuals
 
 __device__ __forceinline__ void state_scale(State &S, float f)
 {
 #pragma unroll
     for (int kt = 0; kt < 8; ++kt)
         S.t[kt] *= f;
+}
+
+// Sequences without tokens that belong to segment p: the state leaves as it came.  With invalid lengths all of them.
+__device__ void empty_states(const GdnArgs &a, const Entry &e0, const Entry &e1, bool valid, int64_t p, int64_t h,
+                             const void *init, int init_dt, void *fin, int fin_dt)
+{
+    if (!a.cu && a.T != 0)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t lo = !valid ? (p == 0 ? 0 : a.N) : e0.seq, hi = !valid ? a.N : p + 1 == a.P && a.cu ? a.N : e1.seq;
+    for (int64_t b = lo; b < hi; b += 512) {
+        const int64_t i = b + tid;
+        const bool none = i < hi && (!valid || seq_begin(a, i) == seq_begin(a, i + 1));
+        if (!__syncthreads_or(none))
+            continue;
+        for (int64_t n = b; n < b + 512 && n < hi; ++n) {
+            if (valid && seq_begin(a, n) != seq_begin(a, n + 1))
+                continue;
+            State S;
+            state_zero(S);
+            const int64_t at = n * a.H + h;
+            if (init)
+                state_load(S, static_cast<const unsigned char *>(init) + at * state_size(init_dt), init_dt, wave, lane);
+            state_store(S, static_cast<unsigned char *>(fin) + at * state_size(fin_dt), fin_dt, wave, lane);
+        }
+    }
+}
+
+// rows of a D tile (tokens 16 r + 4 g ..) into column `col` of a 64 x 128 matrix
+__device__ __forceinline__ void rows_store(float *m, const f32x4 &x, int r, int g, int col)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m[(16 * r + 4 * g + i) * kD + col] = x[i];
 }
 
 template <int kMode>
@@ -698,34 +749,15 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
     Entry e0 = entry_of(a, row, p), e1 = entry_of(a, row, p + 1);
     if (!valid) {
         e0 = e1 = Entry{0, 0};
-    } else if (!kOut) {  // only the sequence that goes on in the next segment
+    } else if (kMode == kModeShare || kMode == kModePhi) {  // only the sequence that goes on in the next segment
         if (e1.chunk == 0 || (kMode == kModePhi && (e0.chunk == 0 || e0.seq != e1.seq)))
             return;
         if (e0.seq != e1.seq)
             e0 = Entry{e1.seq, 0};
     }
-    if constexpr (kOut) {  // sequences without tokens
-        if (a.fin && a.fin != a.init && (a.cu || a.T == 0)) {
-            const int64_t lo = !valid ? (p == 0 ? 0 : a.N) : e0.seq, hi = !valid ? a.N : p + 1 == a.P && a.cu ? a.N : e1.seq;
-            for (int64_t b = lo; b < hi; b += 512) {
-                const int64_t i = b + tid;
-                const bool none = i < hi && (!valid || seq_begin(a, i) == seq_begin(a, i + 1));
-                if (!__syncthreads_or(none))
-                    continue;
-                for (int64_t n = b; n < b + 512 && n < hi; ++n) {
-                    if (valid && seq_begin(a, n) != seq_begin(a, n + 1))
-                        continue;
-                    State S;
-                    state_zero(S);
-                    const int64_t at = n * a.H + h;
-                    if (a.init)
-                        state_load(S, static_cast<const unsigned char *>(a.init) + at * state_size(a.init_dt), a.init_dt, wave,
-                                   lane);
-                    state_store(S, static_cast<unsigned char *>(a.fin) + at * state_size(a.fin_dt), a.fin_dt, wave, lane);
-                }
-            }
-        }
-    }
+    if constexpr (kOut)
+        if (a.fin && a.fin != a.init)
+            empty_states(a, e0, e1, valid, p, h, a.init, a.init_dt, a.fin, a.fin_dt);
     Walk w;
     w.init(e0, e1, false);
     Chunk ch = w.next(a);
@@ -745,7 +777,7 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             tile_fetch(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
     };
     auto fetch_rec = [&](const Chunk &n) {
-        rec_fetch<kParts>(lds.rec, a.rec + ((n.len ? n.slot : 0) * a.H + h) * kGdnRecFwd, n.len != 0, wave, lane);
+        rec_fetch<kParts>(lds.rec, a.rec + ((n.len ? n.slot : 0) * a.H + h) * a.rec_bytes, n.len != 0, wave, lane);
     };
     const unsigned char *mt = lds.rec, *vec = lds.rec + kGdnMat, *ma = vec + kGdnVec;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -761,7 +793,7 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             if constexpr (kMode == kModePhi) {
                 state_one(S, wave, lane);
             } else if (ch.from_seg) {
-                if constexpr (kOut)
+                if constexpr (kOut || kMode == kModeStore)
                     state_load(S, a.seg + (segment * a.H + h) * kD * kD, 2, wave, lane);
                 else
                     state_zero(S);
@@ -778,6 +810,8 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             }
         }
         const Chunk nx = w.next(a);
+        if constexpr (kMode == kModeStore)
+            state_store(S, a.before + (ch.slot * a.H + h) * kD * kD, 2, wave, lane);
         f32x4 Z[4], O[4];
         {
             Terms c[4];
@@ -851,13 +885,17 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
                                                       (uint32_t)(16 * r + m) * (uint32_t)a.H * 256u + 32 * wave + 8 * g, 0, 0);
             }
         }
+        if constexpr (kMode == kModeStore)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                rows_store(a.res + (ch.slot * a.H + h) * kGC * kD, R[r], r, g, 16 * wave + m);
         state_scale(S, carry);
 #pragma unroll
         for (int kt = 0; kt < 8; ++kt)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
                 S.t[kt] = mfma3(col_frag(tk, ln, kt, ks), u[ks], S.t[kt]);
-        if (ch.last) {
+        if (kMode != kModeStore && ch.last) {
             if constexpr (kMode == kModeShare)
                 state_store(S, a.seg + ((segment + 1) * a.H + h) * kD * kD, 2, wave, lane);
             else if constexpr (kMode == kModePhi)
@@ -942,6 +980,485 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
         *reinterpret_cast<f32x4 *>(&st[cur][m][16 * wave + 4 * g]) = acc;
         __syncthreads();
         have = true;
+    }
+}
+
+// -------------------------------------------------------------------------- backward walk
+//
+// dL/dS from a sequence's end to its start, in the same layout; stores it after each chunk, and dw.
+
+template <bool kShare>
+__device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_t row, int64_t p, int64_t h)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int64_t segment = row * a.P + p;
+    const bool valid = !a.status || *a.status == 0;
+    Entry e0 = entry_of(a, row, p), e1 = entry_of(a, row, p + 1);
+    if (!valid) {
+        e0 = e1 = Entry{0, 0};
+    } else if (kShare) {  // only the sequence that comes from the segment before
+        if (e0.chunk == 0)
+            return;
+        if (e0.seq != e1.seq)
+            e1 = Entry{e0.seq + 1, 0};
+    }
+    if constexpr (!kShare)
+        if (a.dinit)
+            empty_states(a, e0, e1, valid, p, h, a.dfin, 2, a.dinit, 2);
+    Walk w;
+    w.init(e0, e1, true);
+    Chunk ch = w.next(a);
+    if (ch.len == 0)
+        return;
+    const Lanes ln(lane);
+    auto head_of = [&](const GdnTensor &x) {
+        return x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh;
+    };
+    const uint16_t *pk = head_of(a.k), *po = head_of(a.dout), *pq = head_of(a.q);
+    auto fetch = [&](int buf, const Chunk &n) {
+        tile_fetch(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
+        tile_fetch(lds.tile[buf][1], a.dout, po, n.t0, n.len, wave, lane);
+        tile_fetch(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
+    };
+    auto fetch_rec = [&](const Chunk &n) {
+        rec_fetch<5>(lds.rec, a.rec + ((n.len ? n.slot : 0) * a.H + h) * a.rec_bytes + kGdnMat, n.len != 0, wave, lane);
+    };
+    const unsigned char *vec = lds.rec, *mt = vec + kGdnVec, *ma = mt + kGdnMat;
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    State S;
+    state_zero(S);
+    int buf = 0;
+    fetch(0, ch);
+    fetch_rec(ch);
+    arrive();
+    for (;;) {
+        const unsigned char *tk = lds.tile[buf][0], *to = lds.tile[buf][1], *tq = lds.tile[buf][2];
+        if (ch.first) {
+            if (ch.from_seg) {
+                if constexpr (kShare)
+                    state_zero(S);
+                else
+                    state_load(S, a.dseg + (segment * a.H + h) * kD * kD, 2, wave, lane);
+            } else if (a.dfin) {
+                state_load(S, a.dfin + (ch.seq * a.H + h) * kD * kD, 2, wave, lane);
+            } else {
+                state_zero(S);
+            }
+        }
+        const Chunk nx = w.next(a);
+        if constexpr (!kShare)
+            state_store(S, a.dafter + (ch.slot * a.H + h) * kD * kD, 2, wave, lane);
+        f32x4 Y[4];
+        {
+            Terms c[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                cut8(S.t[2 * x], S.t[2 * x + 1], c[x]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                Y[r] = zero;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    Y[r] = mfma3(row_frag(tk, ln, r, x), c[x], Y[r]);
+            }
+        }
+        arrive();  // this chunk's record is there; the other buffer is read by no one
+        fetch(buf ^ 1, nx);
+        u32x4 o[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+            o[ks] = col_frag(to, ln, wave, ks);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            Y[r] *= vec4(vec, kVTail + 16 * r + 4 * g);
+#pragma unroll
+            for (int ks = r / 2; ks < 2; ++ks)
+                Y[r] = mfma3(block_terms(ma, up_block(r, ks), lane), o[ks], Y[r]);
+        }
+        Terms d[2];
+        cut8(Y[0], Y[1], d[0]);
+        cut8(Y[2], Y[3], d[1]);
+        f32x4 W[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            W[r] = zero;
+#pragma unroll
+            for (int ks = r / 2; ks < 2; ++ks)
+                W[r] = mfma6(block_terms(mt, up_block(r, ks), lane), d[ks], W[r]);
+        }
+        // what the tokens' reads and writes send to the state before the chunk
+        Terms uo[2], uw[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            f32x4 x[2], y[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int at = 32 * ks + 16 * hf + 4 * g;
+                x[hf] = widen4(u32x2{o[ks][2 * hf], o[ks][2 * hf + 1]}) * vec4(vec, kVOut + at);
+                y[hf] = -(W[2 * ks + hf] * (vec4(vec, kVBeta + at) * vec4(vec, kVHead + at)));
+            }
+            cut8(x[0], x[1], uo[ks]);
+            cut8(y[0], y[1], uw[ks]);
+        }
+        const float carry = *reinterpret_cast<const float *>(vec + 4 * kVLast);
+        arrive();  // the next chunk's tiles are there; the record is read by no one
+        fetch_rec(nx);
+        if constexpr (!kShare)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                rows_store(a.dwrite + (ch.slot * a.H + h) * kGC * kD, W[r], r, g, 16 * wave + m);
+        state_scale(S, carry);
+#pragma unroll
+        for (int kt = 0; kt < 8; ++kt)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                S.t[kt] = mfma3(col_frag(tq, ln, kt, ks), uo[ks], S.t[kt]);
+                S.t[kt] = mfma3(col_frag(tk, ln, kt, ks), uw[ks], S.t[kt]);
+            }
+        if (ch.last) {
+            if constexpr (kShare)
+                state_store(S, a.dseg + ((segment - 1) * a.H + h) * kD * kD, 2, wave, lane);
+            else if (a.dinit && !ch.to_seg)
+                state_store(S, a.dinit + (ch.seq * a.H + h) * kD * kD, 2, wave, lane);
+        }
+        if (nx.len == 0)
+            break;
+        ch = nx;
+        buf ^= 1;
+    }
+}
+
+__global__ __launch_bounds__(512, 1) void gdn_store_kernel(GdnArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) LdsWalk lds;
+    const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
+    walk<kModeStore>(a, lds, row, s - row * a.P, h);
+}
+template <bool kShare>
+__global__ __launch_bounds__(512, 1) void gdn_back_kernel(GdnArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) LdsWalk lds;
+    const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
+    walk_back<kShare>(a, lds, row, s - row * a.P, h);
+}
+
+// dL/dS at each cut, from the last to the first: dS_{p-1} = dS_p Phi_p^T + share, as gdn_scan_kernel.
+__global__ __launch_bounds__(512) void gdn_scan_back_kernel(GdnArgs a)
+{
+    __shared__ __attribute__((aligned(16))) float st[2][16][132];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+    const int64_t chain = blockIdx.x >> 3, row = chain / a.H, h = chain - row * a.H;
+    const int v0 = (int)(blockIdx.x & 7) * 16;
+    if (a.status && *a.status != 0)
+        return;
+    bool have = false;  // st[cur] holds dL/dS at segment p's end
+    int cur = 0;
+    Entry e = entry_of(a, row, a.P - 1);
+    for (int64_t p = a.P - 2; p > 0; --p) {
+        const Entry n = e;
+        e = entry_of(a, row, p);
+        if (!(e.chunk > 0 && n.chunk > 0 && e.seq == n.seq)) {
+            have = false;
+            continue;
+        }
+        const size_t at = ((size_t)(row * a.P + p) * a.H + h) * kD * kD;
+        if (!have) {
+            __syncthreads();
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(a.dseg + at + (size_t)(v0 + (tid >> 5)) * kD + (tid & 31) * 4);
+            *reinterpret_cast<f32x4 *>(&st[cur][tid >> 5][(tid & 31) * 4]) = x;
+            __syncthreads();
+        }
+        float *next = a.dseg + at - (size_t)a.H * kD * kD + (size_t)(v0 + m) * kD + 16 * wave + 4 * g;
+        f32x4 acc = *reinterpret_cast<const f32x4 *>(next);
+        const float *phi = a.phi + at + (16 * wave + m) * kD + 4 * g;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            Terms s, f;
+            cut8(*reinterpret_cast<const f32x4 *>(&st[cur][m][32 * x + 4 * g]),
+                 *reinterpret_cast<const f32x4 *>(&st[cur][m][32 * x + 16 + 4 * g]), s);
+            cut8(*reinterpret_cast<const f32x4 *>(phi + 32 * x), *reinterpret_cast<const f32x4 *>(phi + 32 * x + 16), f);
+            acc = mfma6(f, s, acc);
+        }
+        *reinterpret_cast<f32x4 *>(next) = acc;
+        cur ^= 1;
+        *reinterpret_cast<f32x4 *>(&st[cur][m][16 * wave + 4 * g]) = acc;
+        __syncthreads();
+        have = true;
+    }
+}
+
+// ------------------------------------------------------------------- gradients of a chunk
+//
+// One workgroup of 8 waves per (chunk, head).  w = beta r and dx = beta dw are cut into bf16 terms once, in LDS.  Wave w
+// forms key channels 16w .. of dq and dk for all 64 tokens (rows: channels, a lane's token is lane % 16), and one 16 x 32
+// block each of P, P^T and G + G^T, which pass through LDS to the other waves in the place of the terms.
+
+struct LdsGrad {
+    unsigned char k[kTile], q[kTile], o[kTile];
+    unsigned char w[3][kTile], x[3][kTile];  // terms of w and dx; then the blocks of P, P^T, G + G^T
+    float vec[kGdnVec / 4];
+    float sums[8][kGC];   // q.dq of each wave's channels
+    float vdv[kGC];
+    float end[8];         // <dS, S_after>, a wave's share
+};
+
+__device__ __forceinline__ Terms row_terms(const unsigned char (*t)[kTile], const Lanes &ln, int r, int p)
+{
+    return Terms{row_frag(t[0], ln, r, p), row_frag(t[1], ln, r, p), row_frag(t[2], ln, r, p)};
+}
+
+__global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) LdsGrad s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int64_t slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H;
+    if (a.status && *a.status != 0)
+        return;
+    const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(seq_begin(a, i), i); });
+    const int64_t begin = seq_begin(a, seq), c = slot - slot_of(begin, seq), rest = seq_begin(a, seq + 1) - begin - c * kGC;
+    if (rest <= 0)
+        return;
+    const int len = (int)(rest < kGC ? rest : kGC);
+    const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGC, at = slot * a.H + h;
+    const int64_t tok0 = row * a.T + t0;
+    auto head_of = [&](const GdnTensor &x) {
+        return x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh;
+    };
+    tile_fetch(s.k, a.k, head_of(a.k), t0, len, wave, lane);
+    tile_fetch(s.q, a.q, head_of(a.q), t0, len, wave, lane);
+    tile_fetch(s.o, a.dout, head_of(a.dout), t0, len, wave, lane);
+    if (wave < 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(a.rec + at * a.rec_bytes + kGdnMat, kGdnVec),
+                                                 (lds_void *)(s.vec + 256 * wave), 16, 1024 * wave + 16 * lane, 0, 0, 0);
+    // the states' columns of this wave: lane = key channel, 4 value rows 16 n + 4 g ..
+    const float *sb = a.before + at * kD * kD + 16 * wave + m, *sd = a.dafter + at * kD * kD + 16 * wave + m;
+    f32x4 S[8], dS[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            S[n][i] = sb[(16 * n + 4 * g + i) * kD];
+    // rows of r and dw: thread = token tid / 8, value channels 16 (tid % 8) ..
+    {
+        const int t = tid >> 3, v0 = 16 * (tid & 7);
+        const float *pr = a.res + at * kGC * kD + t * kD + v0, *pw = a.dwrite + at * kGC * kD + t * kD + v0;
+        const float be = t < len ? a.beta[(tok0 + t) * a.H + h] : 0.0f;
+        const uint16_t *pv = head_of(a.v) + (t0 + (t < len ? t : 0)) * a.v.st + v0;
+        const u32x4 vv[2] = {*reinterpret_cast<const u32x4 *>(pv), *reinterpret_cast<const u32x4 *>(pv + 8)};
+        float db = 0.0f, vd = 0.0f;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            f32x4 r[2], d[2], x[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                r[e] = *reinterpret_cast<const f32x4 *>(pr + 8 * hf + 4 * e);
+                d[e] = *reinterpret_cast<const f32x4 *>(pw + 8 * hf + 4 * e);
+                x[e] = d[e] * be;
+                const f32x4 v4 = widen4(u32x2{vv[hf][2 * e], vv[hf][2 * e + 1]});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    db = fmaf(d[e][i], r[e][i], db);
+                    vd = fmaf(x[e][i], v4[i], vd);
+                }
+                r[e] *= be;
+            }
+            const int piece = 2 * (tid & 7) + hf, to = t * 256 + ((piece ^ swz(t)) << 4);
+            Terms y;
+            cut8(r[0], r[1], y);
+            *reinterpret_cast<u32x4 *>(s.w[0] + to) = y.h;
+            *reinterpret_cast<u32x4 *>(s.w[1] + to) = y.m;
+            *reinterpret_cast<u32x4 *>(s.w[2] + to) = y.l;
+            cut8(x[0], x[1], y);
+            *reinterpret_cast<u32x4 *>(s.x[0] + to) = y.h;
+            *reinterpret_cast<u32x4 *>(s.x[1] + to) = y.m;
+            *reinterpret_cast<u32x4 *>(s.x[2] + to) = y.l;
+            if (t < len)
+                *reinterpret_cast<u32x4 *>(a.dv + ((tok0 + t) * a.H + h) * kD + v0 + 8 * hf) = y.h;
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            db += __shfl_xor(db, o);
+            vd += __shfl_xor(vd, o);
+        }
+        if ((tid & 7) == 0) {
+            s.vdv[t] = vd;
+            if (t < len)
+                a.dbeta[(tok0 + t) * a.H + h] = db;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dS[n][i] = sd[(16 * n + 4 * g + i) * kD];
+    arrive();
+    const Lanes ln(lane);
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    // the states' shares
+    f32x4 dq[4], dk[4];
+    float dot = 0.0f;
+    {
+        Terms cs[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            cut8(S[2 * x], S[2 * x + 1], cs[x]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            dq[r] = dk[r] = zero;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                dq[r] = mfma3(cs[x], row_frag(s.o, ln, r, x), dq[r]);
+                dk[r] = mfma6(cs[x], row_terms(s.x, ln, r, x), dk[r]);
+            }
+            dq[r] *= s.vec[kVOut + 16 * r + m];
+            dk[r] *= -s.vec[kVHead + 16 * r + m];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dot = fmaf(S[n][i], dS[n][i], dot);
+    dot *= s.vec[kVLast];
+    // channels 16 w + 4 g .. of token 16 r + m
+    auto mine = [&](const unsigned char *tile, int r) {
+        return widen4(lds_b64(tile + 4096 * r + (ln.row ^ (32 * wave))));
+    };
+    {
+        Terms cs[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            cut8(dS[2 * x], dS[2 * x + 1], cs[x]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            f32x4 y = zero;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                y = mfma6(cs[x], row_terms(s.w, ln, r, x), y);
+            y *= s.vec[kVTail + 16 * r + m];
+            const f32x4 k4 = mine(s.k, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dot = fmaf(y[i], k4[i], dot);
+            dk[r] += y;
+        }
+    }
+    // blocks of this wave: columns of tile cr, contraction 32 ck ..
+    const int cr = wave >> 1, ck = wave & 1;
+    auto within = [&](int t, int u) {  // e^{b_t - b_u} for u <= t
+        const float d = (s.vec[kVSum + t] - s.vec[kVSum + u]) + (s.vec[kVSum + 64 + t] - s.vec[kVSum + 64 + u]);
+        return u <= t ? __builtin_amdgcn_exp2f(d) : 0.0f;
+    };
+    Terms pa, pb, gs;
+    {
+        const int col = 16 * cr + m;
+        f32x4 fa[2], fb[2], fg[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int rt = 2 * ck + hf;  // row tile
+            f32x4 ya = zero, yb = zero, g1 = zero, g2 = zero;
+            if (rt <= cr) {  // rows are sources, columns out tokens
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const Terms wt = row_terms(s.w, ln, rt, x);
+                    ya = mfma3(wt, row_frag(s.o, ln, cr, x), ya);
+                    g1 = mfma6(wt, row_terms(s.x, ln, cr, x), g1);
+                }
+            }
+            if (rt >= cr) {  // rows are out tokens, columns sources
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const Terms wt = row_terms(s.w, ln, cr, x);
+                    yb = mfma3(row_frag(s.o, ln, rt, x), wt, yb);
+                    g2 = mfma6(row_terms(s.x, ln, rt, x), wt, g2);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rw = 16 * rt + 4 * g + i;
+                const float lo = within(col, rw), hi = within(rw, col);
+                fa[hf][i] = rw <= col ? a.scale * lo * ya[i] : 0.0f;
+                fb[hf][i] = rw >= col ? a.scale * hi * yb[i] : 0.0f;
+                fg[hf][i] = rw < col ? -lo * g1[i] : rw > col ? -hi * g2[i] : 0.0f;
+            }
+        }
+        cut8(fa[0], fa[1], pa);
+        cut8(fb[0], fb[1], pb);
+        cut8(fg[0], fg[1], gs);
+    }
+    __syncthreads();  // the terms of w and dx are read by no one
+    unsigned char *mp = s.w[0], *mq = mp + 8 * 3 * 1024, *mg = mq + 8 * 3 * 1024;  // 72 KiB of their 96
+    auto put = [&](unsigned char *mat, const Terms &t) {
+        u32x4 *p = reinterpret_cast<u32x4 *>(mat + wave * 3072 + lane * 16);
+        p[0] = t.h;
+        p[64] = t.m;
+        p[128] = t.l;
+    };
+    put(mp, pa);
+    put(mq, pb);
+    put(mg, gs);
+    __syncthreads();
+    auto block = [&](const unsigned char *mat, int r, int ks) {
+        const u32x4 *p = reinterpret_cast<const u32x4 *>(mat + (2 * r + ks) * 3072 + lane * 16);
+        return Terms{p[0], p[64], p[128]};
+    };
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const u32x4 kc = col_frag(s.k, ln, wave, ks), qc = col_frag(s.q, ln, wave, ks);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (ks <= r / 2)
+                dq[r] = mfma3(kc, block(mp, r, ks), dq[r]);
+            if (ks >= r / 2)
+                dk[r] = mfma3(qc, block(mq, r, ks), dk[r]);
+            dk[r] = mfma3(kc, block(mg, r, ks), dk[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const f32x4 q4 = mine(s.q, r);
+        float y = dq[r][0] * q4[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            y = fmaf(dq[r][i], q4[i], y);
+        y += __shfl_xor(y, 16);
+        y += __shfl_xor(y, 32);
+        if (g == 0)
+            s.sums[wave][16 * r + m] = y;
+        const int t = 16 * r + m;
+        if (t < len) {
+            const int64_t to = ((tok0 + t) * a.H + h) * kD + 16 * wave + 4 * g;
+            if (a.dq_h) {
+                *reinterpret_cast<f32x4 *>(a.dq_h + to) = dq[r];
+                *reinterpret_cast<f32x4 *>(a.dk_h + to) = dk[r];
+            } else {
+                *reinterpret_cast<u32x2 *>(a.dq + to) = u32x2{pack2(dq[r][0], dq[r][1]), pack2(dq[r][2], dq[r][3])};
+                *reinterpret_cast<u32x2 *>(a.dk + to) = u32x2{pack2(dk[r][0], dk[r][1]), pack2(dk[r][2], dk[r][3])};
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        dot += __shfl_xor(dot, o);
+    if (lane == 0)
+        s.end[wave] = dot;
+    __syncthreads();
+    if (wave != 0)
+        return;
+    float qd = 0.0f, end = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        qd += s.sums[n][lane];
+        end += s.end[n];
+    }
+    const double each = lane < len ? (double)qd - (double)s.vdv[lane] : 0.0;
+    const double upto = running_sum(each), total = last_lane(upto);  // by all lanes, those behind the chunk too
+    if (lane < len) {
+        const int64_t to = (tok0 + lane) * a.H + h;
+        const float gd = a.decay[to];
+        a.ddecay[to] = gd > kLowest && gd <= 0.0f ? (float)((total - upto) + each + (double)end) : 0.0f;
     }
 }
 
@@ -1114,6 +1631,33 @@ hipError_t gdn_launch_fwd(const GdnArgs &a, int32_t *status, hipStream_t s)
         return e;
     hipLaunchKernelGGL(gdn_out_kernel, dim3(grid), dim3(512), 0, s, a);
     return hipGetLastError();
+}
+
+hipError_t gdn_launch_bwd(const GdnArgs &a, int32_t *status, hipStream_t s)
+{
+    hipError_t e = launch_check(a, status, s);
+    if (e != hipSuccess)
+        return e;
+    const unsigned grid = (unsigned)(a.rows * a.P * a.H), recs = (unsigned)(a.slots * a.H);
+    if (a.T > 0) {
+        hipLaunchKernelGGL(gdn_prep_kernel<true>, dim3(recs), dim3(256), 0, s, a);
+        if (a.P > 1) {
+            hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), 0, s, a);
+            if (a.P > 2)
+                hipLaunchKernelGGL(gdn_scan_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
+            hipLaunchKernelGGL(gdn_back_kernel<true>, dim3(grid), dim3(512), 0, s, a);
+            if (a.P > 2)
+                hipLaunchKernelGGL(gdn_scan_back_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
+        }
+        hipLaunchKernelGGL(gdn_store_kernel, dim3(grid), dim3(512), 0, s, a);
+    }
+    hipLaunchKernelGGL(gdn_back_kernel<false>, dim3(grid), dim3(512), 0, s, a);
+    if (a.T > 0)
+        hipLaunchKernelGGL(gdn_grad_kernel, dim3(recs), dim3(512), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess || !a.dq_h || a.T == 0)
+        return e;
+    return lin_launch_fold(a.dq_h, a.dk_h, a.dq, a.dk, (a.cu ? 1 : a.N) * a.T, a.Hk, a.H / a.Hk, a.status, s);
 }
 
 hipError_t gdn_launch_recurrent(const GdnArgs &a, int32_t *status, hipStream_t s)

@@ -51,14 +51,14 @@ kda_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, b
     return KDA_OK;
 }
 
-bool make_layout(const Sizes &z, kda::GdnLayout *L)
+bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
 {
     using kda::kAlign;
-    L->plan = kda::gdn_plan(z.B, z.T, z.H, z.varlen);
+    L->plan = kda::gdn_plan(z.B, z.T, z.H, z.varlen, bwd);
     const kda::GdnPlan &p = L->plan;
     L->slots = z.B * z.T / kda::kGC + z.n_seq + 1;
-    // 256 threads for each record, 512 for each segment and head, 4096 for each row and head
-    if (L->slots > (((int64_t)1 << 24) - 8) / z.H || p.rows * p.P > (((int64_t)1 << 23) - 8) / z.H ||
+    // 256 threads for each record (backward 512), 512 for each segment and head, 4096 for each row and head
+    if (L->slots > (((int64_t)1 << (bwd ? 23 : 24)) - 8) / z.H || p.rows * p.P > (((int64_t)1 << 23) - 8) / z.H ||
         (p.P > 1 && p.rows >= ((int64_t)1 << 20) / z.H))
         return false;
     size_t off = kAlign;  // status word
@@ -67,14 +67,26 @@ bool make_layout(const Sizes &z, kda::GdnLayout *L)
         off = (off + bytes + kAlign - 1) / kAlign * kAlign;
         return o;
     };
-    L->off_rec = L->off_seg = L->off_phi = L->off_keep = 0;
-    if (z.T > 0)
-        L->off_rec = take((size_t)L->slots * (size_t)z.H * kda::kGdnRecFwd);
+    L->off_rec = L->off_seg = L->off_phi = L->off_keep = L->off_dseg = 0;
+    L->off_before = L->off_dafter = L->off_res = L->off_dwrite = L->off_dq = L->off_dk = 0;
+    const size_t recs = z.T > 0 ? (size_t)L->slots * (size_t)z.H : 0;
+    L->off_rec = take(recs * (bwd ? kda::kGdnRecBwd : kda::kGdnRecFwd));
     if (p.P > 1) {
         const size_t segs = (size_t)p.rows * (size_t)p.P * (size_t)z.H * kda::kGdnStateBytes;
         L->off_seg = take(segs);
         L->off_phi = take(segs);
-        L->off_keep = take(segs);
+        (bwd ? L->off_dseg : L->off_keep) = take(segs);
+    }
+    if (bwd) {
+        L->off_before = take(recs * kda::kGdnStateBytes);
+        L->off_dafter = take(recs * kda::kGdnStateBytes);
+        L->off_res = take(recs * kda::kGC * kD * sizeof(float));
+        L->off_dwrite = take(recs * kda::kGC * kD * sizeof(float));
+        if (z.Hk != z.H) {
+            const size_t rows = (size_t)z.B * (size_t)z.T * (size_t)z.H * kD * sizeof(float);
+            L->off_dq = take(rows);
+            L->off_dk = take(rows);
+        }
     }
     L->total = off;
     return true;
@@ -140,7 +152,7 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
     if (!isfinite(scale))
         return KDA_ERR_SCALE;
     kda::GdnLayout lay;
-    if (!recurrent && !make_layout(z, &lay))
+    if (!recurrent && !make_layout(z, false, &lay))
         return KDA_ERR_SHAPE;
     memset(a, 0, sizeof(*a));
     Range rq, rk, rv;
@@ -188,6 +200,7 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
         a->len = lay.plan.len;
         a->slots = lay.slots;
         a->rec = w + lay.off_rec;
+        a->rec_bytes = kda::kGdnRecFwd;
         if (a->P > 1) {
             a->seg = reinterpret_cast<float *>(w + lay.off_seg);
             a->phi = reinterpret_cast<float *>(w + lay.off_phi);
@@ -206,7 +219,7 @@ size_t kda_gdn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, in
 {
     Sizes z;
     kda::GdnLayout lay;
-    if (check_sizes(B, T, H, H, N, has_cu_seqlens != 0, &z) != KDA_OK || !make_layout(z, &lay))
+    if (check_sizes(B, T, H, H, N, has_cu_seqlens != 0, &z) != KDA_OK || !make_layout(z, false, &lay))
         return 0;
     return lay.total;
 }
@@ -242,6 +255,120 @@ kda_status kda_gdn_fwd_recurrent(const void *q, const void *k, const void *v, co
     if (st != KDA_OK)
         return st;
     return kda::gdn_launch_recurrent(a, static_cast<int32_t *>(workspace), static_cast<hipStream_t>(stream)) == hipSuccess
+               ? KDA_OK
+               : KDA_ERR_HIP;
+}
+
+size_t kda_gdn_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens)
+{
+    Sizes z;
+    kda::GdnLayout lay;
+    if (check_sizes(B, T, Hk, H, N, has_cu_seqlens != 0, &z) != KDA_OK || !make_layout(z, true, &lay))
+        return 0;
+    return lay.total;
+}
+
+kda_status kda_gdn_bwd(const void *q, const void *k, const void *v, const float *decay, const float *beta, float scale,
+                       const void *initial_state, kda_state_dtype initial_state_dtype, const void *dout,
+                       const float *dfinal_state, void *dq, void *dk, void *dv, float *ddecay, float *dbeta,
+                       float *dinitial_state, const int64_t *cu_seqlens, const int64_t *cu_seqlens_host, int64_t B,
+                       int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t K, int64_t V, const int64_t *strides_host,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (T != 0 && (!q || !k || !v || !decay || !beta || !dout || !dq || !dk || !dv || !ddecay || !dbeta))
+        return KDA_ERR_NULL;
+    Sizes z;
+    kda_status st = check_sizes(B, T, Hk, H, N, cu_seqlens != nullptr, &z);
+    if (st != KDA_OK)
+        return st;
+    if (K != kD || V != kD)
+        return KDA_ERR_HEAD_DIM;
+    if (!dtype_ok(initial_state_dtype) || (initial_state == nullptr) != (initial_state_dtype == KDA_STATE_NONE))
+        return KDA_ERR_DTYPE;
+    if (!isfinite(scale))
+        return KDA_ERR_SCALE;
+    kda::GdnLayout lay;
+    if (!make_layout(z, true, &lay))
+        return KDA_ERR_SHAPE;
+    kda::GdnArgs a;
+    memset(&a, 0, sizeof(a));
+    Range rq, rk, rv, rdo;
+    if ((st = set_tensor(q, strides_host, z, Hk, &a.q, &rq)) != KDA_OK ||
+        (st = set_tensor(k, strides_host ? strides_host + 3 : nullptr, z, Hk, &a.k, &rk)) != KDA_OK ||
+        (st = set_tensor(v, strides_host ? strides_host + 6 : nullptr, z, H, &a.v, &rv)) != KDA_OK ||
+        (st = set_tensor(dout, nullptr, z, H, &a.dout, &rdo)) != KDA_OK)
+        return st;
+    const void *p16[] = {dq, dk, dv, initial_state, dfinal_state, dinitial_state};
+    for (const void *p : p16)
+        if (!aligned(p, 16))
+            return KDA_ERR_ALIGN;
+    const void *p4[] = {decay, beta, ddecay, dbeta};
+    for (const void *p : p4)
+        if (!aligned(p, 4))
+            return KDA_ERR_ALIGN;
+    if (!aligned(cu_seqlens, 8) || !aligned(workspace, kda::kAlign))
+        return KDA_ERR_ALIGN;
+    const size_t tokens = (size_t)B * (size_t)T, states = (size_t)z.n_seq * (size_t)H, gates = tokens * (size_t)H * 4;
+    const Range in[] = {rq, rk, rv, rdo, range_of(decay, gates), range_of(beta, gates),
+                        range_of(initial_state, states * state_bytes(initial_state_dtype)),
+                        range_of(dfinal_state, states * kda::kGdnStateBytes),
+                        range_of(cu_seqlens, cu_seqlens ? (size_t)(N + 1) * 8 : 0)};
+    const Range out[] = {range_of(dq, tokens * (size_t)Hk * kD * 2), range_of(dk, tokens * (size_t)Hk * kD * 2),
+                         range_of(dv, tokens * (size_t)H * kD * 2), range_of(ddecay, gates), range_of(dbeta, gates),
+                         range_of(dinitial_state, states * kda::kGdnStateBytes), range_of(workspace, workspace_bytes)};
+    const int n_out = (int)(sizeof(out) / sizeof(out[0]));
+    for (int i = 0; i < n_out; ++i) {
+        for (const Range &x : in)
+            if (overlap(out[i], x))
+                return KDA_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return KDA_ERR_ALIAS;
+    }
+    if (!workspace || workspace_bytes < lay.total)
+        return KDA_ERR_WORKSPACE;
+    if ((st = check_cu(cu_seqlens, cu_seqlens_host, z)) != KDA_OK)
+        return st;
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    auto f32 = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
+    a.decay = decay;
+    a.beta = beta;
+    a.scale = scale;
+    a.T = T;
+    a.H = H;
+    a.Hk = Hk;
+    a.N = z.n_seq;
+    a.rows = lay.plan.rows;
+    a.P = lay.plan.P;
+    a.len = lay.plan.len;
+    a.cu = cu_seqlens;
+    a.status = cu_seqlens ? reinterpret_cast<int32_t *>(w) : nullptr;
+    a.init = initial_state;
+    a.init_dt = (int)initial_state_dtype;
+    a.rec = w + lay.off_rec;
+    a.rec_bytes = kda::kGdnRecBwd;
+    a.slots = lay.slots;
+    if (a.P > 1) {
+        a.seg = f32(lay.off_seg);
+        a.phi = f32(lay.off_phi);
+        a.dseg = f32(lay.off_dseg);
+    }
+    a.dfin = dfinal_state;
+    a.dinit = dinitial_state;
+    a.before = f32(lay.off_before);
+    a.dafter = f32(lay.off_dafter);
+    a.res = f32(lay.off_res);
+    a.dwrite = f32(lay.off_dwrite);
+    a.dq = static_cast<uint16_t *>(dq);
+    a.dk = static_cast<uint16_t *>(dk);
+    a.dv = static_cast<uint16_t *>(dv);
+    if (Hk != H) {
+        a.dq_h = f32(lay.off_dq);
+        a.dk_h = f32(lay.off_dk);
+    }
+    a.ddecay = ddecay;
+    a.dbeta = dbeta;
+    return kda::gdn_launch_bwd(a, static_cast<int32_t *>(workspace), static_cast<hipStream_t>(stream)) == hipSuccess
                ? KDA_OK
                : KDA_ERR_HIP;
 }

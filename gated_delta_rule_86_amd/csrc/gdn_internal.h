@@ -18,7 +18,7 @@ constexpr int64_t kGdnMinSeg = 4 * kGC;    // shortest segment that a cut leaves
 
 // Record of one (chunk, head) in the workspace, bytes: operands of the walks, in the order of their lanes.
 //   forward:   T' | factors | A' | 2 KiB unused
-//   backward:  T' | factors | T^T | A^T | 2 KiB unused
+//   backward:  T' | factors | T^T | A^T | 2 KiB unused   (A without beta)
 // Each matrix is 6 blocks of 16 x 32 (the other two of the triangle are zero) of three bf16 terms, 1 KiB a block.
 constexpr int kGdnMat = 6 * 3 * 1024;
 constexpr int kGdnVec = 2048;
@@ -33,9 +33,9 @@ struct GdnPlan {
     int64_t rows, P, len;
 };
 
-// Time of a pass in chunks of the output walk (one workgroup on a CU): the walk in rounds of kGdnCUs, and with a cut the
-// shares and transitions of all but the last segment, the scan's steps and two more launches.
-inline GdnPlan gdn_plan(int64_t B, int64_t T, int64_t H, bool varlen)
+// Time of a pass in chunks of the forward pass's output walk (one workgroup on a CU): the walks in rounds of kGdnCUs, and
+// with a cut the shares and transitions of all but the last segment, the scans' steps and more launches.
+inline GdnPlan gdn_plan(int64_t B, int64_t T, int64_t H, bool varlen, bool bwd)
 {
     GdnPlan p;
     p.rows = varlen ? 1 : B;
@@ -45,12 +45,14 @@ inline GdnPlan gdn_plan(int64_t B, int64_t T, int64_t H, bool varlen)
     int64_t most = T / kGdnMinSeg;
     if (most > 2 * kGdnCUs / chains)
         most = 2 * kGdnCUs / chains;
-    double best = (double)cdiv(chains, kGdnCUs) * ((double)(p.len / kGC) + 1.0);
+    const double walks = bwd ? 1.6 : 1.0;
+    double best = walks * (double)cdiv(chains, kGdnCUs) * ((double)(p.len / kGC) + 1.0);
     for (int64_t P = 2; P <= most; ++P) {
         const int64_t len = cdiv(cdiv(T, P), kGC) * kGC, got = cdiv(T, len), n = len / kGC;
-        const double cost = (double)cdiv(chains * got, kGdnCUs) * ((double)n + 1.0) +
-                            0.7 * (double)cdiv(2 * chains * (got - 1), kGdnCUs) * ((double)n + 1.0) +
-                            0.5 * (double)(got - 2) + 2.0;
+        double cost = walks * (double)cdiv(chains * got, kGdnCUs) + 0.7 * (double)cdiv(2 * chains * (got - 1), kGdnCUs);
+        if (bwd)
+            cost += 0.9 * (double)cdiv(chains * (got - 1), kGdnCUs);
+        cost = cost * ((double)n + 1.0) + (bwd ? 2.0 : 1.0) * (0.5 * (double)(got - 2) + 2.0);
         if (got > 1 && cost < best) {
             best = cost;
             p.P = got;
@@ -79,20 +81,32 @@ struct GdnArgs {
     void *fin;
     int init_dt, fin_dt;
     unsigned char *rec;          // [slots][H] records
-    int64_t slots;
+    int64_t slots, rec_bytes;
     float *seg;                  // [rows * P][H]: state at a segment's start, of the sequence that crosses it
     float *phi;                  // [rows * P][H]
     float *keep;                 // [rows * P][H]: initial state of the sequence that leaves the segment (in place), or NULL
+    // backward pass
+    int64_t Hk;
+    const float *dfin;           // dL/dfinal_state or NULL
+    float *dinit;                // dL/dinitial_state or NULL
+    float *dseg;                 // [rows * P][H]: dL/dS at a segment's end, of the sequence that goes on behind it
+    float *before, *dafter;      // [slots][H] states before each chunk, dL/dS after it
+    float *res, *dwrite;         // [slots][H][64][128]: residuals r_t, and dL/d(beta r)_t
+    uint16_t *dq, *dk, *dv;
+    float *dq_h, *dk_h;          // fp32 [B, T, H, 128] when q/k heads are shared, else NULL
+    float *ddecay, *dbeta;
 };
 
 struct GdnLayout {
     GdnPlan plan;
     int64_t slots;
     size_t off_rec, off_seg, off_phi, off_keep;
+    size_t off_dseg, off_before, off_dafter, off_res, off_dwrite, off_dq, off_dk;
     size_t total;
 };
 
 hipError_t gdn_launch_fwd(const GdnArgs &a, int32_t *status, hipStream_t s);
+hipError_t gdn_launch_bwd(const GdnArgs &a, int32_t *status, hipStream_t s);
 hipError_t gdn_launch_recurrent(const GdnArgs &a, int32_t *status, hipStream_t s);
 
 }  // namespace kda

@@ -1587,13 +1587,22 @@ hipError_t lin_launch_walk(const LinArgs &a0, int n_roles, const int *lead, int 
     return hipGetLastError();
 }
 
+hipError_t lin_launch_fold(const float *xq, const float *xk, uint16_t *yq, uint16_t *yk, int64_t rows, int64_t Hk, int64_t G,
+                           const int32_t *status, hipStream_t s)
+{
+    const int64_t n = rows * Hk * (kD / 4);
+    const int64_t blocks = cdiv(n, 256) < 4096 ? cdiv(n, 256) : 4096;
+    hipLaunchKernelGGL(lin_fold_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, s, xq, xk, yq, yk, rows, Hk, G, status);
+    return hipGetLastError();
+}
+
 hipError_t lin_launch_grad_tail(const LinArgs &a, const LinBwdExtra &e, hipStream_t s)
 {
     if (e.dq_h && a.T > 0) {
-        const int64_t n = a.rows * a.T * e.Hk * (kD / 4);
-        const int64_t blocks = cdiv(n, 256) < 4096 ? cdiv(n, 256) : 4096;
-        hipLaunchKernelGGL(lin_fold_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, s, e.dq_h, e.dk_h, e.dq, e.dk,
-                           a.rows * a.T, e.Hk, a.H / e.Hk, a.cu ? a.status : nullptr);
+        const hipError_t err = lin_launch_fold(e.dq_h, e.dk_h, e.dq, e.dk, a.rows * a.T, e.Hk, a.H / e.Hk,
+                                               a.cu ? a.status : nullptr, s);
+        if (err != hipSuccess)
+            return err;
     }
     if (e.ddecay) {
         hipLaunchKernelGGL(lin_ddecay_kernel, dim3((unsigned)(a.rows * a.P * a.H)), dim3(kGradThreads), 0, s, a, e.ddecay,

@@ -139,6 +139,10 @@ hipError_t lin_launch_check(const int64_t *cu, int64_t N, int64_t T, int32_t *st
 // n_roles walks in one launch; with P > 1 the states pass and the scan run first, for the
 // roles that `lead` lists (roles that share slots need them once).
 hipError_t lin_launch_walk(const LinArgs &a, int n_roles, const int *lead, int n_lead, hipStream_t s);
+// dq, dk [rows][Hk][128] in bf16 from fp32 [rows][Hk * G][128]: the heads that share a q/k head added in order.  Nothing
+// where *status is set.
+hipError_t lin_launch_fold(const float *xq, const float *xk, uint16_t *yq, uint16_t *yk, int64_t rows, int64_t Hk, int64_t G,
+                           const int32_t *status, hipStream_t s);
 hipError_t lin_launch_grad_tail(const LinArgs &a, const LinBwdExtra &e, hipStream_t s);
 hipError_t lin_launch_recurrent(const LinArgs &a, hipStream_t s);
 

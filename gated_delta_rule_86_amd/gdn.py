@@ -1,4 +1,5 @@
-"""The gated delta rule with a decay for each head: kda_gdn_fwd and kda_gdn_fwd_recurrent of libkda.so (include/kda.h).
+"""The gated delta rule with a decay for each head: kda_gdn_fwd, kda_gdn_fwd_recurrent and
+kda_gdn_bwd of libkda.so (include/kda.h).
 
     S~ = e^{g_t} S_{t-1},   S_t = S~ + beta_t (v_t - S~ k_t) k_t^T,   out_t = scale * S_t q_t
 
@@ -11,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import kda
-from .kda import KDA_OK, KDAError, _ptr, lib
+from .kda import KDA_OK, KDAError, _pool, _ptr, _used_here, lib
 from .linattn import _bytes, _check_inputs, _check_state, _code, _gpu_index, _On, _raw_stream, _row_strides, _workspace
 
 D = 128
@@ -19,6 +20,10 @@ D = 128
 
 def workspace_size(B: int, T: int, H: int, N: int = 0, varlen: bool = False) -> int:
     return int(lib().kda_gdn_fwd_workspace_size(B, T, H, N, 1 if varlen else 0))
+
+
+def bwd_workspace_size(B: int, T: int, Hk: int, H: int, N: int = 0, varlen: bool = False) -> int:
+    return int(lib().kda_gdn_bwd_workspace_size(B, T, Hk, H, N, 1 if varlen else 0))
 
 
 def _check(q, k, v, decay, beta, cu_seqlens, cu_seqlens_host):
@@ -75,6 +80,49 @@ def fwd_recurrent(q, k, v, decay, beta, scale, out, initial_state=None, final_st
     out) and other short sequences.  Same arguments and keywords as ``fwd``; without cu_seqlens
     it needs no workspace and returns None."""
     return fwd(q, k, v, decay, beta, scale, out, initial_state, final_state, cu_seqlens, _recurrent=True, **kw)
+
+
+def bwd(q, k, v, decay, beta, scale, dout, initial_state=None, dfinal_state=None, cu_seqlens=None, *,
+        need_dinitial_state=True, cu_seqlens_host=None, workspace=None, stream=None):
+    """Gradients of ``fwd``'s out and final_state (kda_gdn_bwd in include/kda.h).
+
+    Inputs as ``fwd``; dout: contiguous bf16 [B, T, H, 128]; dfinal_state: None or fp32
+    [N, H, 128, 128].  Returns a dict of device tensors: dq, dk (bf16, shape of q), dv (bf16), ddecay, dbeta
+    (fp32 [B, T, H]), dinitial_state (fp32 [N, H, 128, 128]; also without an initial state,
+    unless need_dinitial_state is False) and the workspace used.
+    """
+    B, T, Hk, H, N, K, V, _, host = _check(q, k, v, decay, beta, cu_seqlens, cu_seqlens_host)
+    if (dout.dtype is not torch.bfloat16 or dout.shape != v.shape or not dout.is_contiguous()
+            or dout.get_device() != q.get_device()):
+        raise ValueError("dout must be a contiguous bf16 [B, T, H, 128] tensor on q's device")
+    _check_state("initial_state", initial_state, (N, H, V, K), q)
+    _check_state("dfinal_state", dfinal_state, (N, H, V, K), q, bf16_too=False)
+    index = _gpu_index(q)
+    varlen = cu_seqlens is not None
+    L = lib()
+    need = L.kda_gdn_bwd_workspace_size(B, T, Hk, H, N if varlen else 0, varlen)
+    with _On(index):
+        bf16, fp32 = torch.bfloat16, torch.float32
+        with _pool(stream):
+            r = {"dq": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
+                 "dk": torch.empty((B, T, Hk, K), dtype=bf16, device=index),
+                 "dv": torch.empty((B, T, H, V), dtype=bf16, device=index),
+                 "ddecay": torch.empty((B, T, H), dtype=fp32, device=index),
+                 "dbeta": torch.empty((B, T, H), dtype=fp32, device=index)}
+            if need_dinitial_state:
+                r["dinitial_state"] = torch.empty((N, H, V, K), dtype=fp32, device=index)
+        _used_here(stream, index, *r.values())
+        workspace = _workspace(workspace, need or 1, index, stream)
+        st = L.kda_gdn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), beta.data_ptr(), float(scale),
+                           _ptr(initial_state), _code(initial_state), dout.data_ptr(), _ptr(dfinal_state),
+                           r["dq"].data_ptr(), r["dk"].data_ptr(), r["dv"].data_ptr(), r["ddecay"].data_ptr(),
+                           r["dbeta"].data_ptr(), _ptr(r.get("dinitial_state")), _ptr(cu_seqlens),
+                           None if host is None else host.ctypes.data, B, T, Hk, H, N if varlen else B, K, V,
+                           _row_strides(q, k, v), workspace.data_ptr(), _bytes(workspace), _raw_stream(stream, index))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_gdn_bwd")
+    r["workspace"] = workspace
+    return r
 
 
 device_status = kda.device_status

@@ -43,7 +43,7 @@ EXPORTS = ("kda_fwd", "kda_fwd_ex", "kda_fwd_recurrent", "kda_fwd_recurrent_time
            "kda_fwd_device_status", "kda_chunk_table", "kda_version",
            "kda_lin_fwd", "kda_lin_fwd_recurrent", "kda_lin_fwd_workspace_size", "kda_lin_bwd",
            "kda_lin_bwd_workspace_size", "kda_qk_rope", "kda_qk_rope_bwd", "kda_qk_rope_bwd_workspace_size",
-           "kda_gdn_fwd", "kda_gdn_fwd_recurrent", "kda_gdn_fwd_workspace_size",
+           "kda_gdn_fwd", "kda_gdn_fwd_recurrent", "kda_gdn_fwd_workspace_size", "kda_gdn_bwd", "kda_gdn_bwd_workspace_size",
            "kda_gated_norm", "kda_gated_norm_bwd", "kda_gated_norm_bwd_workspace_size", "kda_residual_norm",
            "kda_residual_norm_bwd", "kda_residual_norm_bwd_workspace_size")
 
@@ -119,6 +119,10 @@ def lib():
     L.kda_gdn_fwd_recurrent.argtypes = L.kda_gdn_fwd.argtypes
     L.kda_gdn_fwd_workspace_size.restype = szt
     L.kda_gdn_fwd_workspace_size.argtypes = [i64, i64, i64, i64, ci]
+    L.kda_gdn_bwd.restype = ci
+    L.kda_gdn_bwd.argtypes = [vp, vp, vp, vp, vp, f32, vp, ci] + [vp] * 10 + [i64] * 7 + [vp, vp, szt, vp]
+    L.kda_gdn_bwd_workspace_size.restype = szt
+    L.kda_gdn_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, ci]
     L.kda_gated_norm.restype = ci
     L.kda_gated_norm.argtypes = [vp] * 4 + [i64] * 4 + [ci, ci, f32, vp, vp]
     L.kda_gated_norm_bwd.restype = ci

@@ -448,6 +448,34 @@ kda_status kda_gdn_fwd_recurrent(const void *q, const void *k, const void *v, co
  */
 size_t kda_gdn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
 
+/*
+ * kda_gdn_bwd -- gradients of kda_gdn_fwd's out and final_state.  q, k, v, decay, beta, scale, initial_state,
+ * cu_seqlens, sizes, strides_host and stream as there.
+ *   dout          bf16 [B, T, H, 128], contiguous, 16-byte aligned: dL/dout.
+ *   dfinal_state  NULL (zero) or fp32 [N, H, 128, 128], 16-byte aligned: dL/dfinal_state.
+ *   dq, dk        bf16 [B, T, Hk, 128], dv bf16 [B, T, H, 128], contiguous, 16-byte aligned, fully
+ *                 written; heads that share a q/k head are summed in fp32 and rounded once.
+ *   ddecay, dbeta fp32 [B, T, H], fully written.  ddecay is 0 where decay lies outside (-1000, 0].
+ *   dinitial_state  NULL or fp32 [N, H, 128, 128], 16-byte aligned (also when initial_state is NULL).
+ *   workspace     kda_gdn_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * Products as in kda_gdn_fwd.  Outputs must not overlap inputs or each other (KDA_ERR_ALIAS).  An invalid cu_seqlens
+ * found on the device leaves dq, dk, dv, ddecay and dbeta unwritten and makes dinitial_state = dfinal_state (or 0).
+ * Deterministic.
+ */
+kda_status kda_gdn_bwd(const void *q, const void *k, const void *v, const float *decay, const float *beta, float scale,
+                       const void *initial_state, kda_state_dtype initial_state_dtype, const void *dout,
+                       const float *dfinal_state, void *dq, void *dk, void *dv, float *ddecay, float *dbeta,
+                       float *dinitial_state, const int64_t *cu_seqlens, const int64_t *cu_seqlens_host, int64_t B,
+                       int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t K, int64_t V, const int64_t *strides_host,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_gdn_bwd_workspace_size -- 256 bytes; 250 KiB per chunk of 64 tokens and head (at most T / 64 + 1 chunks for each
+ * sequence); where rows are cut, three fp32 128 x 128 states per segment and head; with Hk < H two fp32 [B, T, H, 128].
+ * Returns 0 for invalid sizes.
+ */
+size_t kda_gdn_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens);
+
 typedef enum kda_dtype {
     KDA_DTYPE_BF16 = 1,
     KDA_DTYPE_FP32 = 2,

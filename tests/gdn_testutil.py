@@ -36,6 +36,74 @@ def gdn_ref(q, k, v, decay, beta, scale, h0=None, cu=None):
     return out, torch.stack(final)
 
 
+def gdn_ref_bwd(q, k, v, decay, beta, scale, dout, h0=None, dht=None, cu=None):
+    """Gradients by the recurrence run backwards in fp64.  Returns a dict with dq, dk, dv, ddecay, dbeta, dinitial_state and the
+    sizes of what ddecay and dbeta are sums of: sum_size [B, T, H] (products of q.dq and v.dv), state_size (<S, dS> after the
+    token) and beta_size, each for independent vectors (norms multiplied, over the root of the count)."""
+    B, T, Hk, _ = q.shape
+    H = v.shape[2]
+    rep = H // Hk
+    q, k, v = q.double().repeat_interleave(rep, 2), k.double().repeat_interleave(rep, 2), v.double()
+    g, beta, do = decay.double(), beta.double(), dout.double() * scale
+    a = g.clamp(-1000.0, 0.0).exp()
+    bounds = [(b, 0, T) for b in range(B)] if cu is None else [(0, cu[i], cu[i + 1]) for i in range(len(cu) - 1)]
+    dq, dk, dv = torch.zeros_like(v), torch.zeros_like(v), torch.zeros_like(v)
+    dg, db, state_size, beta_size = (torch.zeros_like(a) for _ in range(4))
+    dh0 = torch.zeros(len(bounds), H, D, D, dtype=torch.float64, device=q.device)
+    for n, (b, lo, hi) in enumerate(bounds):
+        S = torch.zeros(H, D, D, dtype=torch.float64, device=q.device) if h0 is None else h0[n].double()
+        steps = []
+        for t in range(lo, hi):
+            decayed = S * a[b, t][:, None, None]
+            r = v[b, t] - (decayed * k[b, t][:, None, :]).sum(-1)
+            S = decayed + (r * beta[b, t][:, None])[:, :, None] * k[b, t][:, None, :]
+            steps.append((t, S, decayed, r))
+        dS = torch.zeros_like(S) if dht is None else dht[n].double()
+        for t, S, decayed, r in reversed(steps):
+            state_size[b, t] = S.flatten(1).norm(dim=1) * dS.flatten(1).norm(dim=1) / D
+            dq[b, t] = (S * do[b, t][:, :, None]).sum(1)
+            dS = dS + do[b, t][:, :, None] * q[b, t][:, None, :]
+            w = (dS * k[b, t][:, None, :]).sum(-1)
+            db[b, t] = (w * r).sum(-1)
+            beta_size[b, t] = w.norm(dim=1) * r.norm(dim=1) / D ** 0.5
+            dr = w * beta[b, t][:, None]
+            dv[b, t] = dr
+            dk[b, t] = (dS * (r * beta[b, t][:, None])[:, :, None]).sum(1) - (decayed * dr[:, :, None]).sum(1)
+            dS = dS - dr[:, :, None] * k[b, t][:, None, :]
+            dg[b, t] = (dS * decayed).sum((-1, -2))
+            dS = dS * a[b, t][:, None, None]
+        dh0[n] = dS
+    dg = torch.where((g > -1000.0) & (g <= 0.0), dg, 0.0)
+    sum_size = (q.norm(dim=-1) * dq.norm(dim=-1) + v.norm(dim=-1) * dv.norm(dim=-1)) / D ** 0.5
+    share = lambda x: x.unflatten(2, (Hk, rep)).sum(3)  # noqa: E731
+    return {"dq": share(dq), "dk": share(dk), "dv": dv, "ddecay": dg, "dbeta": db, "dinitial_state": dh0,
+            "sum_size": sum_size, "state_size": state_size, "beta_size": beta_size}
+
+
+def close_grads(r, want, what="", grow=1.0):
+    """dq, dk, dv, dinitial_state as outputs above.  dbeta: a dot product of 128 values that are each off by FP32_REL_L2 of
+    their size.  ddecay: such dot products added over the up to 64 later tokens of a chunk (independent errors: 8 times one's),
+    and <S, dS> at its end."""
+    for n in ("dq", "dk", "dv"):
+        close_bf16(r[n], want[n], (what, n), grow)
+    if "dinitial_state" in r:
+        close_fp32(r["dinitial_state"], want["dinitial_state"], (what, "dinitial_state"), grow * FP32_REL_L2, grow * FP32_MAX)
+    if not want["dbeta"].numel():
+        return
+    biggest = lambda x: x.amax(1, keepdim=True).expand_as(x)  # noqa: E731
+    tol = {"dbeta": want["beta_size"].square().mean(1, keepdim=True).sqrt() + want["beta_size"],
+           "ddecay": 8 * biggest(want["sum_size"]) + biggest(want["state_size"])}
+    for n, size in tol.items():
+        got = r[n].double()
+        assert got.shape == want[n].shape and torch.isfinite(got).all(), (what, n)
+        if not got.numel():
+            continue
+        err, size = (got - want[n]).abs(), grow * FP32_REL_L2 * size
+        bad = err > 4 * size + 2.0 ** -23 * want[n].abs()
+        assert not bad.any(), (what, n, int(bad.sum()), float(err.max()), float((err / size).max()))
+        assert float(err.norm()) <= float(size.norm()) + 2.0 ** -24 * float(want[n].norm()), (what, n, float(err.norm()), float(size.norm()))
+
+
 def inputs(B, T, Hk, H, seed, strided=False, keys="normal", lo=1e-3, device="cuda"):
     """q, k of norm 1, v, decays spread over their logarithm between lo and 1, betas in (0, 1), and a generator."""
     g = torch.Generator(device=device)
