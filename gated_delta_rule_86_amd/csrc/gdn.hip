@@ -83,9 +83,13 @@ struct Terms {  // three bf16 terms of 8 floats
 // two floats into word e of each term
 __device__ __forceinline__ void cut2(float x, float y, Terms &t, int e)
 {
-    t.h[e] = pack2(x, y);
+    uint32_t h = pack2(x, y);
+    __asm__("" : "+v"(h));  // one conversion for both: else each value is converted again to get its rest
+    t.h[e] = h;
     const float x1 = x - lo_f(t.h[e]), y1 = y - hi_f(t.h[e]);
-    t.m[e] = pack2(x1, y1);
+    uint32_t m = pack2(x1, y1);
+    __asm__("" : "+v"(m));
+    t.m[e] = m;
     t.l[e] = pack2(x1 - lo_f(t.m[e]), y1 - hi_f(t.m[e]));
 }
 __device__ __forceinline__ void cut8(f32x4 a, f32x4 b, Terms &t)
@@ -138,7 +142,19 @@ __device__ __forceinline__ void arrive()
 
 // ------------------------------------------------------------------ sequences and chunks
 
+// A value that is the same in all lanes, said so: descriptors and branches on it stay scalar.
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 __device__ __forceinline__ int64_t seq_begin(const GdnArgs &a, int64_t i) { return a.cu ? a.cu[i] : i * a.T; }
+
+// First element of a tensor's row and head (heads are shared by small whole numbers: 32-bit division)
+__device__ __forceinline__ const uint16_t *head_base(const GdnTensor &x, int64_t row, int64_t h)
+{
+    return x.p + uniform(row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh);
+}
 
 // Records: chunk c of sequence i has slot floor(begin / 64) + i + c; the slots of different sequences differ.
 __device__ __forceinline__ int64_t slot_of(int64_t begin, int64_t i) { return begin / kGC + i; }
@@ -172,11 +188,11 @@ __device__ __forceinline__ Entry entry_of(const GdnArgs &a, int64_t row, int64_t
     if (p == 0)
         return Entry{0, 0};
     // the first sequence that begins at `at` or behind, or the one before it if it has a chunk there
-    const int64_t m = a.cu[0] >= at ? 0 : last_at_most(a.N + 1, at - 1, [&](int64_t n) { return a.cu[n]; });
+    const int64_t m = uniform(a.cu[0]) >= at ? 0 : last_at_most(a.N + 1, at - 1, [&](int64_t n) { return uniform(a.cu[n]); });
     if (m >= a.N)
         return Entry{a.N, 0};
-    const int64_t c = (at - a.cu[m] + kGC - 1) / kGC;
-    return c * kGC < a.cu[m + 1] - a.cu[m] ? Entry{m, c} : Entry{m + 1, 0};
+    const int64_t begin = uniform(a.cu[m]), c = (at - begin + kGC - 1) / kGC;
+    return c * kGC < uniform(a.cu[m + 1]) - begin ? Entry{m, c} : Entry{m + 1, 0};
 }
 
 struct Chunk {
@@ -196,22 +212,30 @@ struct Walk {
 
     __device__ void init(const Entry &a0, const Entry &a1, bool rev_)
     {
-        e0 = a0;
-        e1 = a1;
+        e0 = Entry{uniform(a0.seq), uniform(a0.chunk)};
+        e1 = Entry{uniform(a1.seq), uniform(a1.chunk)};
         rev = rev_;
         i = rev ? e1.seq + 1 : e0.seq - 1;
         c = c_lo = c_hi = 0;
         begin = len = 0;
     }
+    // The 64-bit comparisons run on the vector unit; said to be uniform once more, the results stay scalar.
     __device__ Chunk next(const GdnArgs &a)
     {
-        Chunk k;
-        k.first = false;
+        Chunk k = advance(a);
+        k.len = __builtin_amdgcn_readfirstlane(k.len);
+        k.seq = uniform(k.seq);
+        k.slot = uniform(k.slot);
+        k.t0 = uniform(k.t0);
+        return k;
+    }
+    __device__ Chunk advance(const GdnArgs &a)
+    {
+        Chunk k = {0, 0, 0, 0, false, false, false, false};
         c += rev ? -1 : 1;
         while (rev ? c < c_lo : c >= c_hi) {
             i += rev ? -1 : 1;
             if (rev ? i < e0.seq : (i > e1.seq || (i == e1.seq && e1.chunk == 0))) {
-                k.len = 0;
                 c_lo = 0, c_hi = 0;  // from now on every call ends here
                 c = rev ? -1 : 0;
                 i = rev ? e0.seq : e1.seq;
@@ -222,8 +246,8 @@ struct Walk {
                 c = -1;
                 continue;
             }
-            begin = seq_begin(a, i);
-            len = seq_begin(a, i + 1) - begin;
+            begin = uniform(seq_begin(a, i));
+            len = uniform(seq_begin(a, i + 1)) - begin;
             const int64_t n = (len + kGC - 1) / kGC;
             c_lo = i == e0.seq ? e0.chunk : 0;
             c_hi = i == e1.seq ? e1.chunk : n;
@@ -316,8 +340,9 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
     const int64_t slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H;
     if (a.status && *a.status != 0)
         return;
-    const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(seq_begin(a, i), i); });
-    const int64_t begin = seq_begin(a, seq), c = slot - slot_of(begin, seq), rest = seq_begin(a, seq + 1) - begin - c * kGC;
+    const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(uniform(seq_begin(a, i)), i); });
+    const int64_t begin = uniform(seq_begin(a, seq)), c = slot - slot_of(begin, seq),
+                  rest = uniform(seq_begin(a, seq + 1)) - begin - c * kGC;
     if (rest <= 0)
         return;
     const int len = (int)(rest < kGC ? rest : kGC);
@@ -326,8 +351,7 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
 
     auto tile = [&](const GdnTensor &x) {
         const uint32_t stride = (uint32_t)x.st * 2;
-        return rsrc(x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh + t0 * x.st,
-                    (uint32_t)(len - 1) * stride + 256u);
+        return rsrc(head_base(x, row, h) + t0 * x.st, (uint32_t)(len - 1) * stride + 256u);
     };
     const __amdgpu_buffer_rsrc_t rk = tile(a.k), rq = tile(a.q);
     const uint32_t sk = (uint32_t)a.k.st * 2, sq = (uint32_t)a.q.st * 2;
@@ -624,7 +648,8 @@ __device__ __forceinline__ void tile_fetch(unsigned char *lds, const GdnTensor &
                                            int wave, int lane)
 {
     const uint32_t stride = (uint32_t)x.st * 2;
-    const __amdgpu_buffer_rsrc_t r = rsrc(base + t0 * x.st, len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u);
+    const uint32_t bytes = __builtin_amdgcn_readfirstlane((int)(len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u));
+    const __amdgpu_buffer_rsrc_t r = rsrc(base + t0 * x.st, bytes);
     const int row = 4 * wave + (lane >> 4);
     const uint32_t off = (uint32_t)row * stride + (uint32_t)(((lane & 15) ^ swz(row)) << 4);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + 1024 * wave), 16, off, 0, 0, 0);
@@ -649,6 +674,46 @@ __device__ __forceinline__ u32x2 lds_tr(const unsigned char *p)
     typedef __attribute__((address_space(3))) s16x4 lds_s4;
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p));
 }
+
+// The same for four row tiles of one channel block, and of two.  While loads to LDS are on their way, the compiler waits for all of
+// them before the builtin; these blocks wait for their own reads alone.
+struct Col4 {
+    u32x2 r[4];  // 4 tokens 16 r + 4 g .. each
+};
+__device__ __forceinline__ uint32_t lds_address(const unsigned char *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)p;
+}
+__device__ __forceinline__ Col4 lds_tr4(uint32_t at)
+{
+    Col4 x;
+    __asm__ volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                     "ds_read_b64_tr_b16 %1, %4 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %2, %4 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %3, %4 offset:12288\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(x.r[0]), "=&v"(x.r[1]), "=&v"(x.r[2]), "=&v"(x.r[3])
+                     : "v"(at)
+                     : "memory");
+    return x;
+}
+__device__ __forceinline__ void lds_tr8(uint32_t at, uint32_t bt, Col4 &x, Col4 &y)
+{
+    __asm__ volatile("ds_read_b64_tr_b16 %0, %8\n\t"
+                     "ds_read_b64_tr_b16 %1, %8 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %2, %8 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %3, %8 offset:12288\n\t"
+                     "ds_read_b64_tr_b16 %4, %9\n\t"
+                     "ds_read_b64_tr_b16 %5, %9 offset:4096\n\t"
+                     "ds_read_b64_tr_b16 %6, %9 offset:8192\n\t"
+                     "ds_read_b64_tr_b16 %7, %9 offset:12288\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(x.r[0]), "=&v"(x.r[1]), "=&v"(x.r[2]), "=&v"(x.r[3]), "=&v"(y.r[0]), "=&v"(y.r[1]),
+                       "=&v"(y.r[2]), "=&v"(y.r[3])
+                     : "v"(at), "v"(bt)
+                     : "memory");
+}
+__device__ __forceinline__ u32x4 join(u32x2 x, u32x2 y) { return u32x4{x[0], x[1], y[0], y[1]}; }
 
 // This lane's places in a tile; the channel block is XORed in.
 struct Lanes {
@@ -678,6 +743,25 @@ __device__ __forceinline__ u32x4 col_frag(const unsigned char *tile, const Lanes
 {
     const u32x2 x = col_frag4(tile, ln, kt, 2 * ks), y = col_frag4(tile, ln, kt, 2 * ks + 1);
     return u32x4{x[0], x[1], y[0], y[1]};
+}
+// S += sum over the chunk's tokens of channel rows (tile) times value columns (u), the reads a step ahead of the products
+__device__ __forceinline__ void state_add(State &S, const unsigned char *tile, const Lanes &ln, const Terms *u)
+{
+    const uint32_t at = lds_address(tile);
+    Col4 x[2], y[2];
+    lds_tr8(at + ln.tr, at + (ln.tr ^ 32), x[0], x[1]);
+#pragma unroll
+    for (int kt = 0; kt < 8; kt += 2) {
+        if (kt < 6)
+            lds_tr8(at + (ln.tr ^ (32 * kt + 64)), at + (ln.tr ^ (32 * kt + 96)), y[0], y[1]);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                S.t[kt + n] = mfma3(join(x[n].r[2 * ks], x[n].r[2 * ks + 1]), u[ks], S.t[kt + n]);
+        x[0] = y[0];
+        x[1] = y[1];
+    }
 }
 __device__ __forceinline__ f32x4 widen4(u32x2 x) { return f32x4{lo_f(x[0]), hi_f(x[0]), lo_f(x[1]), hi_f(x[1])}; }
 __device__ __forceinline__ f32x4 vec4(const unsigned char *vec, int at)
@@ -764,9 +848,7 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
     if (ch.len == 0)
         return;
     const Lanes ln(lane);
-    auto head_of = [&](const GdnTensor &x) {
-        return x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh;
-    };
+    auto head_of = [&](const GdnTensor &x) { return head_base(x, row, h); };
     const uint16_t *pk = head_of(a.k), *pv = head_of(a.v), *pq = head_of(a.q);
     constexpr int kParts = kOut ? 5 : 3;
     auto fetch = [&](int buf, const Chunk &n) {
@@ -808,10 +890,15 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             } else {
                 state_zero(S);
             }
+            // here, or the compiler waits behind the branch in every chunk, and for the loads to LDS with it
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         }
         const Chunk nx = w.next(a);
         if constexpr (kMode == kModeStore)
             state_store(S, a.before + (ch.slot * a.H + h) * kD * kD, 2, wave, lane);
+        Col4 cv;
+        if constexpr (kMode != kModePhi)
+            cv = lds_tr4(lds_address(tv) + (ln.tr ^ (32 * wave)));
         f32x4 Z[4], O[4];
         {
             Terms c[4];
@@ -841,7 +928,7 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
                 const int r = 2 * ks + hf;
                 x[hf] = -vec4(vec, kVHead + 16 * r + 4 * g) * Z[r];
                 if constexpr (kMode != kModePhi)
-                    x[hf] += widen4(col_frag4(tv, ln, wave, r));
+                    x[hf] += widen4(cv.r[r]);
             }
             cut8(x[0], x[1], xr[ks]);
         }
@@ -890,11 +977,7 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             for (int r = 0; r < 4; ++r)
                 rows_store(a.res + (ch.slot * a.H + h) * kGC * kD, R[r], r, g, 16 * wave + m);
         state_scale(S, carry);
-#pragma unroll
-        for (int kt = 0; kt < 8; ++kt)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                S.t[kt] = mfma3(col_frag(tk, ln, kt, ks), u[ks], S.t[kt]);
+        state_add(S, tk, ln, u);
         if (kMode != kModeStore && ch.last) {
             if constexpr (kMode == kModeShare)
                 state_store(S, a.seg + ((segment + 1) * a.H + h) * kD * kD, 2, wave, lane);
@@ -913,14 +996,16 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
 
 __global__ __launch_bounds__(512, 1) void gdn_out_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) LdsWalk lds;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
+    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
     const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
     walk<kModeOut>(a, lds, row, s - row * a.P, h);
 }
 // y = 0: shares, y = 1: transitions
 __global__ __launch_bounds__(512, 1) void gdn_cut_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) LdsWalk lds;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
+    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
     const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
     if (blockIdx.y == 0)
         walk<kModeShare>(a, lds, row, s - row * a.P, h);
@@ -1012,9 +1097,7 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
     if (ch.len == 0)
         return;
     const Lanes ln(lane);
-    auto head_of = [&](const GdnTensor &x) {
-        return x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh;
-    };
+    auto head_of = [&](const GdnTensor &x) { return head_base(x, row, h); };
     const uint16_t *pk = head_of(a.k), *po = head_of(a.dout), *pq = head_of(a.q);
     auto fetch = [&](int buf, const Chunk &n) {
         tile_fetch(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
@@ -1045,10 +1128,13 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
             } else {
                 state_zero(S);
             }
+            // here, or the compiler waits behind the branch in every chunk, and for the loads to LDS with it
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         }
         const Chunk nx = w.next(a);
         if constexpr (!kShare)
             state_store(S, a.dafter + (ch.slot * a.H + h) * kD * kD, 2, wave, lane);
+        const Col4 co = lds_tr4(lds_address(to) + (ln.tr ^ (32 * wave)));
         f32x4 Y[4];
         {
             Terms c[4];
@@ -1065,10 +1151,7 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
         }
         arrive();  // this chunk's record is there; the other buffer is read by no one
         fetch(buf ^ 1, nx);
-        u32x4 o[2];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-            o[ks] = col_frag(to, ln, wave, ks);
+        const u32x4 o[2] = {join(co.r[0], co.r[1]), join(co.r[2], co.r[3])};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             Y[r] *= vec4(vec, kVTail + 16 * r + 4 * g);
@@ -1109,13 +1192,8 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
             for (int r = 0; r < 4; ++r)
                 rows_store(a.dwrite + (ch.slot * a.H + h) * kGC * kD, W[r], r, g, 16 * wave + m);
         state_scale(S, carry);
-#pragma unroll
-        for (int kt = 0; kt < 8; ++kt)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                S.t[kt] = mfma3(col_frag(tq, ln, kt, ks), uo[ks], S.t[kt]);
-                S.t[kt] = mfma3(col_frag(tk, ln, kt, ks), uw[ks], S.t[kt]);
-            }
+        state_add(S, tq, ln, uo);
+        state_add(S, tk, ln, uw);
         if (ch.last) {
             if constexpr (kShare)
                 state_store(S, a.dseg + ((segment - 1) * a.H + h) * kD * kD, 2, wave, lane);
@@ -1131,14 +1209,16 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
 
 __global__ __launch_bounds__(512, 1) void gdn_store_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) LdsWalk lds;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
+    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
     const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
     walk<kModeStore>(a, lds, row, s - row * a.P, h);
 }
 template <bool kShare>
 __global__ __launch_bounds__(512, 1) void gdn_back_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) LdsWalk lds;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
+    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
     const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
     walk_back<kShare>(a, lds, row, s - row * a.P, h);
 }
@@ -1216,16 +1296,15 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
     const int64_t slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H;
     if (a.status && *a.status != 0)
         return;
-    const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(seq_begin(a, i), i); });
-    const int64_t begin = seq_begin(a, seq), c = slot - slot_of(begin, seq), rest = seq_begin(a, seq + 1) - begin - c * kGC;
+    const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(uniform(seq_begin(a, i)), i); });
+    const int64_t begin = uniform(seq_begin(a, seq)), c = slot - slot_of(begin, seq),
+                  rest = uniform(seq_begin(a, seq + 1)) - begin - c * kGC;
     if (rest <= 0)
         return;
     const int len = (int)(rest < kGC ? rest : kGC);
     const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGC, at = slot * a.H + h;
     const int64_t tok0 = row * a.T + t0;
-    auto head_of = [&](const GdnTensor &x) {
-        return x.p + row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh;
-    };
+    auto head_of = [&](const GdnTensor &x) { return head_base(x, row, h); };
     tile_fetch(s.k, a.k, head_of(a.k), t0, len, wave, lane);
     tile_fetch(s.q, a.q, head_of(a.q), t0, len, wave, lane);
     tile_fetch(s.o, a.dout, head_of(a.dout), t0, len, wave, lane);
@@ -1620,7 +1699,7 @@ hipError_t gdn_launch_fwd(const GdnArgs &a, int32_t *status, hipStream_t s)
     }
     const unsigned grid = (unsigned)(a.rows * a.P * a.H);
     if (e == hipSuccess && a.P > 1) {
-        hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), 0, s, a);
+        hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), sizeof(LdsWalk), s, a);
         e = hipGetLastError();
         if (e == hipSuccess && a.P > 2) {
             hipLaunchKernelGGL(gdn_scan_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
@@ -1629,7 +1708,7 @@ hipError_t gdn_launch_fwd(const GdnArgs &a, int32_t *status, hipStream_t s)
     }
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(gdn_out_kernel, dim3(grid), dim3(512), 0, s, a);
+    hipLaunchKernelGGL(gdn_out_kernel, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
     return hipGetLastError();
 }
 
@@ -1642,16 +1721,16 @@ hipError_t gdn_launch_bwd(const GdnArgs &a, int32_t *status, hipStream_t s)
     if (a.T > 0) {
         hipLaunchKernelGGL(gdn_prep_kernel<true>, dim3(recs), dim3(256), 0, s, a);
         if (a.P > 1) {
-            hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), 0, s, a);
+            hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), sizeof(LdsWalk), s, a);
             if (a.P > 2)
                 hipLaunchKernelGGL(gdn_scan_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
-            hipLaunchKernelGGL(gdn_back_kernel<true>, dim3(grid), dim3(512), 0, s, a);
+            hipLaunchKernelGGL(gdn_back_kernel<true>, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
             if (a.P > 2)
                 hipLaunchKernelGGL(gdn_scan_back_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
         }
-        hipLaunchKernelGGL(gdn_store_kernel, dim3(grid), dim3(512), 0, s, a);
+        hipLaunchKernelGGL(gdn_store_kernel, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
     }
-    hipLaunchKernelGGL(gdn_back_kernel<false>, dim3(grid), dim3(512), 0, s, a);
+    hipLaunchKernelGGL(gdn_back_kernel<false>, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
     if (a.T > 0)
         hipLaunchKernelGGL(gdn_grad_kernel, dim3(recs), dim3(512), 0, s, a);
     e = hipGetLastError();
