@@ -2,7 +2,7 @@
 //
 // Per (sequence, head), state S [V = 128][K = 128], natural-log decay g_t <= 0, write strength beta_t:
 //   S~ = e^{g_t} S_{t-1},   r_t = v_t - S~ k_t,   S_t = S~ + beta_t r_t k_t^T,   out_t = scale * S_t q_t.
-// In chunks of C = 64 tokens, with b the inclusive running sum of g inside the chunk, L its last entry and
+// In chunks of C = 32 tokens, with b the inclusive running sum of g inside the chunk, L its last entry and
 // S the state before the chunk, the residuals R (rows r_t) solve a unit triangular system:
 //   r_t = x_t - sum_{s < t} e^{b_t - b_s} (k_t.k_s) beta_s r_s,   x_t = v_t - e^{b_t} S k_t,
 //   so R = T' X with T' = (1 + M diag(beta))^-1, M_ts = e^{b_t - b_s} k_t.k_s for s < t;
@@ -34,13 +34,12 @@ namespace kda {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u4 __attribute__((vector_size(16)));   // as the buffer builtins want them
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kBf16 = 1;  // kda_state_dtype
 constexpr float kLowest = -1000.0f;
@@ -60,9 +59,19 @@ __device__ __forceinline__ float clamp_decay(float g)
     return g < kLowest ? kLowest : (g > 0.0f ? 0.0f : g);  // NaN stays NaN
 }
 
-// v_mfma_f32_16x16x32_bf16: A[m][k] in lane m + 16*(k/8), element k%8; B[k][n] in lane n + 16*(k/8), element
-// k%8; D[m][n] in lane n + 16*(m/4), element m%4.  The order of k is free as long as A and B agree: everywhere here
-// element j of lane group g stands for k = 4g + j (j < 4) or 16 + 4g + j - 4, so two D tiles are one B (or A) operand.
+
+// The order of a product's contraction is free as long as both operands agree.
+//
+// v_mfma_f32_32x32x16_bf16: A[m][k] in lane m + 32*(k/8), element k%8; B[k][n] in lane n + 32*(k/8), element k%8;
+// D[m][n] in lane n + 32*((m/4)%2), element 4*(m/8) + m%4.  Elements 8s .. 8s+7 of a D tile are the operand of a
+// contraction over its rows 16s .. 16s+15 in the order 4h + j (j < 4), 8 + 4h + j - 4, with h = lane / 32.
+__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+// v_mfma_f32_16x16x32_bf16: lanes as above with 16 for 32; D[m][n] in lane n + 16*(m/4), element m%4: two tiles are the
+// operand of a contraction over their 32 rows.
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
@@ -92,27 +101,40 @@ __device__ __forceinline__ void cut2(float x, float y, Terms &t, int e)
     t.m[e] = m;
     t.l[e] = pack2(x1 - lo_f(t.m[e]), y1 - hi_f(t.m[e]));
 }
-__device__ __forceinline__ void cut8(f32x4 a, f32x4 b, Terms &t)
+__device__ __forceinline__ Terms cut8(f32x4 a, f32x4 b)
 {
+    Terms t;
     cut2(a[0], a[1], t, 0);
     cut2(a[2], a[3], t, 1);
     cut2(b[0], b[1], t, 2);
     cut2(b[2], b[3], t, 3);
+    return t;
+}
+__device__ __forceinline__ Terms cut8(const f32x16 &x, int s)
+{
+    Terms t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        cut2(x[8 * s + 2 * e], x[8 * s + 2 * e + 1], t, e);
+    return t;
 }
 // products with an exact factor, and of two cut factors (the terms left out are below 2^-24 of the product)
-__device__ __forceinline__ f32x4 mfma3(u32x4 a, const Terms &b, f32x4 c)
+template <typename D>
+__device__ __forceinline__ D mfma3(u32x4 a, const Terms &b, D c)
 {
     c = mfma(a, b.l, c);
     c = mfma(a, b.m, c);
     return mfma(a, b.h, c);
 }
-__device__ __forceinline__ f32x4 mfma3(const Terms &a, u32x4 b, f32x4 c)
+template <typename D>
+__device__ __forceinline__ D mfma3(const Terms &a, u32x4 b, D c)
 {
     c = mfma(a.l, b, c);
     c = mfma(a.m, b, c);
     return mfma(a.h, b, c);
 }
-__device__ __forceinline__ f32x4 mfma6(const Terms &a, const Terms &b, f32x4 c)
+template <typename D>
+__device__ __forceinline__ D mfma6(const Terms &a, const Terms &b, D c)
 {
     c = mfma(a.l, b.h, c);
     c = mfma(a.h, b.l, c);
@@ -131,6 +153,23 @@ __device__ __forceinline__ u32x4 buf_b128(__amdgpu_buffer_rsrc_t r, uint32_t off
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
+// 16 bytes a lane straight into LDS, 1 KiB from `lds` on in the order of the lanes.  In assembly, because the compiler would
+// wait for all such loads before each transposing read of LDS; arrive() waits for them.  No register is written.
+__device__ __forceinline__ void load_lds(const void *base, uint32_t bytes, uint32_t off, uint32_t lds)
+{
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    const u32x4 r = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu,
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :
+                     : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(r)
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)p;
+}
 // Everything that this wave has in flight has arrived, and then the other waves' too.
 __device__ __forceinline__ void arrive()
 {
@@ -156,8 +195,10 @@ __device__ __forceinline__ const uint16_t *head_base(const GdnTensor &x, int64_t
     return x.p + uniform(row * x.sb + (int64_t)((uint32_t)h / (uint32_t)x.share) * x.sh);
 }
 
-// Records: chunk c of sequence i has slot floor(begin / 64) + i + c; the slots of different sequences differ.
+// Records: chunk c of sequence i has slot floor(begin / 32) + i + c, its block c / 2 of 64 tokens slot floor(begin / 64) +
+// i + c / 2; the slots of different sequences differ.
 __device__ __forceinline__ int64_t slot_of(int64_t begin, int64_t i) { return begin / kGC + i; }
+__device__ __forceinline__ int64_t block_of(int64_t begin, int64_t i) { return begin / kGB + i; }
 
 // Largest i in [0, N) with key(i) <= x, for a key that does not decrease; key(0) <= x.
 template <typename F>
@@ -196,11 +237,12 @@ __device__ __forceinline__ Entry entry_of(const GdnArgs &a, int64_t row, int64_t
 }
 
 struct Chunk {
-    int64_t seq, slot;
+    int64_t seq, slot, block;
     int64_t t0;     // first token, in its row
     int len;        // 0: no chunk
-    bool first, last;  // of the workgroup's piece of the sequence
+    bool first, last;       // of the workgroup's piece of the sequence
     bool from_seg, to_seg;  // the piece begins (ends) at a cut
+    bool opens, closes;     // the first (last) chunk of a block of 64 tokens
 };
 
 // The chunks from one entry to another, in order (or from the last to the first).
@@ -226,12 +268,13 @@ struct Walk {
         k.len = __builtin_amdgcn_readfirstlane(k.len);
         k.seq = uniform(k.seq);
         k.slot = uniform(k.slot);
+        k.block = uniform(k.block);
         k.t0 = uniform(k.t0);
         return k;
     }
     __device__ Chunk advance(const GdnArgs &a)
     {
-        Chunk k = {0, 0, 0, 0, false, false, false, false};
+        Chunk k = {0, 0, 0, 0, 0, false, false, false, false, false, false};
         c += rev ? -1 : 1;
         while (rev ? c < c_lo : c >= c_hi) {
             i += rev ? -1 : 1;
@@ -266,7 +309,10 @@ struct Walk {
         k.len = (int)(rest < kGC ? rest : kGC);
         k.seq = i;
         k.slot = slot_of(begin, i) + c;
+        k.block = block_of(begin, i) + (c >> 1);
         k.t0 = (a.cu ? begin : 0) + c * kGC;
+        k.opens = (c & 1) == 0;
+        k.closes = (c & 1) == 1 || rest <= kGC;
         return k;
     }
 };
@@ -279,66 +325,77 @@ __device__ __forceinline__ double dpp_f64(double x)  // 0 where the pattern has 
     const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRows, 0xf, false);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-// Inclusive sum over the lanes: shifts by 1, 2, 4, 8 inside each 16, then the last lane of row 0 and 2 to the next
-// row, then lane 31 to the upper half.
-__device__ __forceinline__ double running_sum(double b)
+// Inclusive sum over the lanes of each half of the wave: shifts by 1, 2, 4, 8 inside each 16, then the last lane of row 0
+// and 2 to the next row.
+__device__ __forceinline__ double running_sum32(double b)
 {
     b += dpp_f64<0x111, 0xf>(b);
     b += dpp_f64<0x112, 0xf>(b);
     b += dpp_f64<0x114, 0xf>(b);
     b += dpp_f64<0x118, 0xf>(b);
     b += dpp_f64<0x142, 0xa>(b);
+    return b;
+}
+// The same over all 64: lane 31 to the upper half
+__device__ __forceinline__ double running_sum64(double b)
+{
+    b = running_sum32(b);
     b += dpp_f64<0x143, 0xc>(b);
     return b;
 }
-__device__ __forceinline__ double last_lane(double b)
+__device__ __forceinline__ double of_lane(double b, int lane)
 {
     const uint64_t u = __builtin_bit_cast(uint64_t, b);
     return __builtin_bit_cast(double,
-                              ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63) << 32) |
-                                  (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63));
+                              ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane) << 32) |
+                                  (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane));
 }
 
 // ------------------------------------------------------------------------------- records
 //
-// Factors of a record, 64 floats each (token of the chunk):
-constexpr int kVHead = 0;     // e^{b_t}
-constexpr int kVWrite = 64;   // beta_s e^{L - b_s}
-constexpr int kVOut = 128;    // scale e^{b_t}
-constexpr int kVBeta = 192;   // beta_s
-constexpr int kVTail = 256;   // e^{L - b_s}
-constexpr int kVLast = 320;   // [0]: e^{L}
-constexpr int kVSum = 384;    // b_t (log2), as a pair of floats: the second 64 behind the first
+// Factors of a record, 32 floats each (token of the chunk):
+constexpr int kVHead = 0;    // e^{b_t}
+constexpr int kVWrite = 32;  // beta_s e^{L - b_s}
+constexpr int kVOut = 64;    // scale e^{b_t}
+constexpr int kVBeta = 96;   // beta_s
+constexpr int kVTail = 128;  // e^{L - b_s}
+constexpr int kVLast = 160;  // [0]: e^{L}
 
-// block of a triangular matrix with rows in row tile r and the contraction in 32-column step ks
-__device__ __forceinline__ constexpr int low_block(int r, int ks) { return r < 2 ? r : 2 + 2 * (r - 2) + ks; }  // ks <= r / 2
-__device__ __forceinline__ constexpr int up_block(int r, int ks) { return r < 2 ? 2 * r + ks : 4 + (r - 2); }  // ks >= r / 2
-
-__device__ __forceinline__ void store_terms(unsigned char *mat, int block, int lane, const Terms &t)
+// The terms of one step (16 of the contraction) of a 32 x 32 matrix, in the order of the lanes
+__device__ __forceinline__ void store_terms(unsigned char *mat, int step, int lane, const Terms &t)
 {
-    u32x4 *p = reinterpret_cast<u32x4 *>(mat + block * 1024 + lane * 16);
+    u32x4 *p = reinterpret_cast<u32x4 *>(mat + step * 3072 + lane * 16);
     p[0] = t.h;
-    p[6 * 64] = t.m;
-    p[12 * 64] = t.l;
+    p[64] = t.m;
+    p[128] = t.l;
+}
+__device__ __forceinline__ Terms load_terms(const unsigned char *mat, int step, int lane)
+{
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(mat + step * 3072 + lane * 16);
+    return Terms{p[0], p[64], p[128]};
 }
 
-constexpr int kNRow = 68;  // floats per row of the triangular matrix in LDS
+constexpr int kNRow = 36;      // floats per row of the triangular matrix in LDS
+constexpr int kPrepWaves = 4;
 
 struct LdsPrep {
     float n[kGC * kNRow];
     float bh[kGC], bl[kGC], beta[kGC];
 };
 
-// One workgroup of 4 waves per (chunk, head).  Wave w forms row tile w of M = e^{b_t - b_s} k_t.k_s; the four
-// 16 x 16 blocks on the diagonal of N are solved column by column, the blocks below them with fp32 matrix
-// instructions, a wave per block column: N_IJ = (1 - N_II beta)(M_IJ - sum_{J <= K < I} M_IK beta N_KJ).
+// One wave per (chunk, head), nothing shared between waves.  M = e^{b_t - b_s} k_t.k_s; N's two 16 x 16 blocks on the diagonal
+// are solved column by column, the block below them with fp32 matrix instructions:
+// N_10 = (1 - N_11 beta)(M_10 - M_10 beta N_00).
 template <bool kBwd>
-__global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
+__global__ __launch_bounds__(64 * kPrepWaves) void gdn_prep_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(16))) LdsPrep s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-    const int64_t slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H;
-    if (a.status && *a.status != 0)
+    __shared__ __attribute__((aligned(16))) LdsPrep lds[kPrepWaves];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l32 = lane & 31,
+              h = lane >> 5;
+    LdsPrep &s = lds[wave];
+    const uint32_t unit = blockIdx.x * kPrepWaves + wave;  // below 2^26
+    const int64_t slot = unit / (uint32_t)a.H, head = unit - (uint32_t)slot * (uint32_t)a.H;
+    if (slot >= a.slots || (a.status && *a.status != 0))
         return;
     const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(uniform(seq_begin(a, i)), i); });
     const int64_t begin = uniform(seq_begin(a, seq)), c = slot - slot_of(begin, seq),
@@ -347,154 +404,102 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
         return;
     const int len = (int)(rest < kGC ? rest : kGC);
     const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGC;
-    unsigned char *rec = a.rec + (slot * a.H + h) * a.rec_bytes;
+    unsigned char *rec = a.rec + (slot * a.H + head) * a.rec_bytes;
 
     auto tile = [&](const GdnTensor &x) {
         const uint32_t stride = (uint32_t)x.st * 2;
-        return rsrc(head_base(x, row, h) + t0 * x.st, (uint32_t)(len - 1) * stride + 256u);
+        return rsrc(head_base(x, row, head) + t0 * x.st, __builtin_amdgcn_readfirstlane((int)((uint32_t)(len - 1) * stride + 256u)));
     };
     const __amdgpu_buffer_rsrc_t rk = tile(a.k), rq = tile(a.q);
-    const uint32_t sk = (uint32_t)a.k.st * 2, sq = (uint32_t)a.q.st * 2;
-    u32x4 kf[4][4], qf[4][4];  // row tiles, 32 channels each step; behind the chunk zeros
+    const uint32_t ok = (uint32_t)l32 * (uint32_t)a.k.st * 2 + 16u * h, oq = (uint32_t)l32 * (uint32_t)a.q.st * 2 + 16u * h;
+    u32x4 kf[8], qf[8];  // row lane % 32, 16 channels each step; behind the chunk zeros
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int x = 0; x < 8; ++x)
+        kf[x] = buf_b128(rk, ok + 32u * x);
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
-            kf[r][p] = buf_b128(rk, (uint32_t)(16 * r + m) * sk + (uint32_t)(64 * p + 16 * g));
-    // forward: A' of out rows 16 w ..; backward: A^T of source rows 16 w ..
-#pragma unroll
-    for (int r = 0; r < (kBwd ? 4 : 1); ++r)
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-            qf[r][p] = buf_b128(rq, (uint32_t)(16 * (kBwd ? r : wave) + m) * sq + (uint32_t)(64 * p + 16 * g));
-
-    const int64_t gate = ((row * a.T + t0) * a.H + h);
-    const float dec = lane < len ? a.decay[gate + (int64_t)lane * a.H] : 0.0f;
-    const float bet = lane < len ? a.beta[gate + (int64_t)lane * a.H] : 0.0f;
-    const double b = running_sum((double)clamp_decay(dec) * kLog2e64), last = last_lane(b);
-    if (wave == 0) {
-        const float bh = (float)b;
-        s.bh[lane] = bh;
-        s.bl[lane] = (float)(b - (double)bh);
-        s.beta[lane] = bet;
-        float *v = reinterpret_cast<float *>(rec + kGdnMat);
-        const float head = __builtin_amdgcn_exp2f((float)b), tail = __builtin_amdgcn_exp2f((float)(last - b));
-        v[kVHead + lane] = head;
-        v[kVWrite + lane] = bet * tail;
-        v[kVOut + lane] = a.scale * head;
-        v[kVBeta + lane] = bet;
-        v[kVTail + lane] = tail;
-        if constexpr (kBwd) {
-            v[kVSum + lane] = bh;
-            v[kVSum + 64 + lane] = (float)(b - (double)bh);
-        }
-        if (lane == 0)
+    for (int x = 0; x < 8; ++x)
+        qf[x] = buf_b128(rq, oq + 32u * x);
+    const int64_t gate = (row * a.T + t0) * a.H + head;
+    const float dec = l32 < len ? a.decay[gate + (int64_t)l32 * a.H] : 0.0f;
+    const float bet = l32 < len ? a.beta[gate + (int64_t)l32 * a.H] : 0.0f;
+    const double b = running_sum32((double)clamp_decay(dec) * kLog2e64), last = of_lane(b, 31);
+    const float bh = (float)b, bl = (float)(b - (double)bh);
+    if (h == 0) {
+        s.bh[l32] = bh;
+        s.bl[l32] = bl;
+        s.beta[l32] = bet;
+        float *v = reinterpret_cast<float *>(rec + kGdnMat) + l32;
+        const float from = __builtin_amdgcn_exp2f((float)b), tail = __builtin_amdgcn_exp2f((float)(last - b));
+        v[kVHead] = from;
+        v[kVWrite] = bet * tail;
+        v[kVOut] = a.scale * from;
+        v[kVBeta] = bet;
+        v[kVTail] = tail;
+        if (l32 == 0)
             v[kVLast] = __builtin_amdgcn_exp2f((float)last);
     }
-    __syncthreads();
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    // e^{b_t - b_s} for s <= t, else 0
-    auto within = [&](int t, int u) {
-        const float d = (s.bh[t] - s.bh[u]) + (s.bl[t] - s.bl[u]);
-        return u <= t ? __builtin_amdgcn_exp2f(d) : 0.0f;
-    };
-    // row tile `wave` of M, strictly below the diagonal
-    u32x4 kw[4];
+    __builtin_amdgcn_wave_barrier();
+    f32x16 kk, qk;
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-        kw[p] = wave == 0 ? kf[0][p] : wave == 1 ? kf[1][p] : wave == 2 ? kf[2][p] : kf[3][p];
+    for (int i = 0; i < 16; ++i)
+        kk[i] = qk[i] = 0.0f;
+    // rows: sources 8 n + 4 h .., columns: tokens, a lane's is lane % 32
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j > wave)
-            continue;
-        f32x4 d = zero;
+    for (int x = 0; x < 8; ++x)
+        kk = mfma(kf[x], kf[x], kk);
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
-            d = mfma(kw[p], kf[j][p], d);
+    for (int x = 0; x < 8; ++x)
+        qk = kBwd ? mfma(qf[x], kf[x], qk) : mfma(kf[x], qf[x], qk);
+    auto vec4 = [&](const float *p, int n) { return *reinterpret_cast<const f32x4 *>(p + 8 * n + 4 * h); };
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const f32x4 uh = vec4(s.bh, n), ul = vec4(s.bl, n), ub = vec4(s.beta, n);
+        f32x4 m4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = 16 * wave + 4 * g + i, u = 16 * j + m;
-            s.n[t * kNRow + u] = u < t ? d[i] * within(t, u) : 0.0f;
-        }
-    }
-    // A: products of q and k
-    if constexpr (!kBwd) {
-        f32x4 t4[4] = {zero, zero, zero, zero};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j > wave)
-                continue;
-            f32x4 d = zero;  // rows: sources 16 j .., columns: out tokens 16 w ..
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                d = mfma(kf[j][p], qf[0][p], d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * wave + m, u = 16 * j + 4 * g + i;
-                t4[j][i] = u <= t ? d[i] * (a.scale * within(t, u)) * s.beta[u] : 0.0f;
+            const int u = 8 * n + 4 * h + i;
+            // e^{b_t - b_u}, t = lane % 32
+            const float w = u <= l32 ? __builtin_amdgcn_exp2f((bh - uh[i]) + (bl - ul[i])) : 0.0f;
+            m4[i] = u < l32 ? kk[4 * n + i] * w : 0.0f;
+            if constexpr (!kBwd) {  // A'
+                qk[4 * n + i] = u <= l32 ? qk[4 * n + i] * (a.scale * w) * ub[i] : 0.0f;
+            } else {  // A, rows: tokens u, columns: sources, a lane's is lane % 32
+                const float z = u >= l32 ? __builtin_amdgcn_exp2f((uh[i] - bh) + (ul[i] - bl)) : 0.0f;
+                qk[4 * n + i] = u >= l32 ? qk[4 * n + i] * (a.scale * z) : 0.0f;
             }
         }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (2 * ks > wave)
-                continue;
-            Terms t;
-            cut8(t4[2 * ks], t4[2 * ks + 1], t);
-            store_terms(rec + kGdnMat + kGdnVec, low_block(wave, ks), lane, t);
-        }
-    } else {
-        f32x4 t4[4] = {zero, zero, zero, zero};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j < wave)
-                continue;
-            f32x4 d = zero;  // rows: out tokens 16 j .., columns: sources 16 w ..
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                d = mfma(qf[j][p], kw[p], d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * j + 4 * g + i, u = 16 * wave + m;
-                t4[j][i] = u <= t ? d[i] * (a.scale * within(t, u)) : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (2 * ks + 1 < wave)
-                continue;
-            Terms t;
-            cut8(t4[2 * ks], t4[2 * ks + 1], t);
-            store_terms(rec + 2 * kGdnMat + kGdnVec, up_block(wave, ks), lane, t);
-        }
+        *reinterpret_cast<f32x4 *>(&s.n[l32 * kNRow + 8 * n + 4 * h]) = m4;
     }
-    // N's diagonal block: lane m its column m.  Rows of the wave's own block only; the four lane groups do the same.
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+        store_terms(rec + (kBwd ? 2 : 1) * kGdnMat + kGdnVec, st, lane, cut8(qk, st));
+    __builtin_amdgcn_wave_barrier();
+    // N's diagonal blocks: lanes of block lane / 16 % 2, column lane % 16; both halves of the wave do the same
     {
-        float y[16];  // beta times the column so far
-        float x[16];
-        const float *blk = s.n + 16 * wave * (kNRow + 1);
-        const float *bb = s.beta + 16 * wave;
-        y[0] = x[0] = 0.0f;
+        const int blk = l32 >> 4, m = l32 & 15;
+        const float *p = s.n + 16 * blk * (kNRow + 1), *bb = s.beta + 16 * blk;
+        float x[16], y[16];  // the column so far, and beta times it
+        x[0] = y[0] = 0.0f;
 #pragma unroll
         for (int i = 1; i < 16; ++i) {
-            float z = blk[i * kNRow + m];
+            float z = p[i * kNRow + m];
 #pragma unroll
             for (int k = 1; k < i; ++k)
-                z = fmaf(-blk[i * kNRow + k], y[k], z);
+                z = fmaf(-p[i * kNRow + k], y[k], z);
             x[i] = i > m ? z : 0.0f;
             y[i] = bb[i] * x[i];
         }
         __builtin_amdgcn_wave_barrier();
-        if (g == 0) {
-            float *w = s.n + 16 * wave * (kNRow + 1) + m;
+        if (h == 0) {
+            float *w = s.n + 16 * blk * (kNRow + 1) + m;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 w[i * kNRow] = x[i];
         }
     }
-    __syncthreads();
-    // the blocks below it
-    f32x4 n[3], y[4];
+    __builtin_amdgcn_wave_barrier();
     {
+        const int m = lane & 15, g = lane >> 4;
         auto rows = [&](int bi, int bj) {  // D layout of a block
             f32x4 r;
 #pragma unroll
@@ -502,171 +507,148 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs a)
                 r[i] = s.n[(16 * bi + 4 * g + i) * kNRow + 16 * bj + m];
             return r;
         };
-        auto left = [&](int bi, int bk) {  // minus a block, as A operand
+        auto minus = [&](int bi, int bk) {  // minus a block, as A operand
             return -*reinterpret_cast<const f32x4 *>(&s.n[(16 * bi + m) * kNRow + 16 * bk + 4 * g]);
         };
         auto beta4 = [&](int bi) { return *reinterpret_cast<const f32x4 *>(&s.beta[16 * bi + 4 * g]); };
-        y[0] = rows(wave, wave) * beta4(wave);
+        const f32x4 p = mfma_f32(minus(1, 0), rows(0, 0) * beta4(0), rows(1, 0));
+        const f32x4 n = mfma_f32(minus(1, 1), p * beta4(1), p);
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int d = 1; d < 4; ++d) {
-            if (wave + d > 3)
-                break;
-            const int bi = wave + d;
-            f32x4 p = rows(bi, wave);
-#pragma unroll
-            for (int e = 0; e < d; ++e)
-                p = mfma_f32(left(bi, wave + e), y[e], p);
-            n[d - 1] = mfma_f32(left(bi, bi), p * beta4(bi), p);
-            y[d] = n[d - 1] * beta4(bi);
-        }
+        for (int i = 0; i < 4; ++i)
+            s.n[(16 + 4 * g + i) * kNRow + m] = n[i];
     }
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();
+    // T' = 1 - N beta, and for the backward pass T = 1 - beta N, transposed
 #pragma unroll
-    for (int d = 1; d < 4; ++d)
-        if (wave + d < 4)
+    for (int st = 0; st < 2; ++st) {
+        f32x4 x[2], y[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s.n[(16 * (wave + d) + 4 * g + i) * kNRow + 16 * wave + m] = n[d - 1][i];
-    __syncthreads();
-    // T' = 1 - N beta, rows 16 w ..
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        if (2 * ks > wave)
-            continue;
-        const int t = 16 * wave + m;
-        f32x4 x[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int u0 = 32 * ks + 16 * hf + 4 * g;
-            const f32x4 nn = *reinterpret_cast<const f32x4 *>(&s.n[t * kNRow + u0]);
+        for (int e = 0; e < 2; ++e) {
+            const int u0 = 16 * st + 8 * e + 4 * h;
+            const f32x4 nn = *reinterpret_cast<const f32x4 *>(&s.n[l32 * kNRow + u0]);
             const f32x4 bb = *reinterpret_cast<const f32x4 *>(&s.beta[u0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[hf][i] = u0 + i < t ? -nn[i] * bb[i] : u0 + i == t ? 1.0f : 0.0f;
+            for (int i = 0; i < 4; ++i) {
+                x[e][i] = u0 + i < l32 ? -nn[i] * bb[i] : u0 + i == l32 ? 1.0f : 0.0f;
+                if constexpr (kBwd)
+                    y[e][i] = u0 + i > l32 ? -s.n[(u0 + i) * kNRow + l32] * bb[i] : u0 + i == l32 ? 1.0f : 0.0f;
+            }
         }
-        Terms tt;
-        cut8(x[0], x[1], tt);
-        store_terms(rec, low_block(wave, ks), lane, tt);
-    }
-    // T = 1 - beta N, transposed: rows are sources 16 w ..
-    if constexpr (kBwd) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (2 * ks + 1 < wave)
-                continue;
-            const int u = 16 * wave + m;
-            f32x4 x[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 32 * ks + 16 * hf + 4 * g + i;
-                    x[hf][i] = u < t ? -s.n[t * kNRow + u] * s.beta[t] : u == t ? 1.0f : 0.0f;
-                }
-            Terms tt;
-            cut8(x[0], x[1], tt);
-            store_terms(rec + kGdnMat + kGdnVec, up_block(wave, ks), lane, tt);
-        }
+        store_terms(rec, st, lane, cut8(x[0], x[1]));
+        if constexpr (kBwd)
+            store_terms(rec + kGdnMat + kGdnVec, st, lane, cut8(y[0], y[1]));
     }
 }
 
 // ------------------------------------------------------------------------- state in registers
 //
-// Wave w of 8 holds value columns 16w .. 16w+15 of the state, all 128 key channels: S[kt][i], lane = column + 16 g:
-// channel 16 kt + 4 g + i, the D layout of S^T.  Nothing of it ever crosses waves.
+// Wave w of 4 holds 32 value columns of the state, all 128 key channels: S.t[kt][r], lane = column + 32 h: channel
+// 32 kt + 16 (r / 8) + 8 h + r % 8, so that elements 8s .. 8s+7 are 8 neighbouring channels, as an operand wants them.
+// Nothing of it ever crosses waves.  Lane n % 32 holds column n, or (where rows of out are stored) column
+// 16 (n/4 % 2) + 4 (n/8) + n%4: a lane of an out tile then has 16 neighbouring channels.
 
 struct State {
-    f32x4 t[8];
+    f32x16 t[4];
 };
-
-__device__ __forceinline__ void state_load(State &S, const void *base, int dt, int wave, int lane)
+template <bool kOut>
+__device__ __forceinline__ int column_of(int n)
 {
-    const int v = 16 * wave + (lane & 15), g = lane >> 4;
-    if (dt == kBf16) {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + v * kD + 4 * g;
-#pragma unroll
-        for (int kt = 0; kt < 8; ++kt) {
-            const u32x2 x = *reinterpret_cast<const u32x2 *>(p + 16 * kt);
-            S.t[kt] = f32x4{lo_f(x[0]), hi_f(x[0]), lo_f(x[1]), hi_f(x[1])};
-        }
-    } else {
-        const float *p = static_cast<const float *>(base) + v * kD + 4 * g;
-#pragma unroll
-        for (int kt = 0; kt < 8; ++kt)
-            S.t[kt] = *reinterpret_cast<const f32x4 *>(p + 16 * kt);
-    }
+    return kOut ? 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3) : n;
 }
-__device__ __forceinline__ void state_store(const State &S, void *base, int dt, int wave, int lane)
+
+// v: the lane's value column
+__device__ __forceinline__ void state_load(State &S, const void *base, int dt, int v, int lane)
 {
-    const int v = 16 * wave + (lane & 15), g = lane >> 4;
-    if (dt == kBf16) {
-        uint16_t *p = static_cast<uint16_t *>(base) + v * kD + 4 * g;
+    const int at = v * kD + 8 * (lane >> 5);
 #pragma unroll
-        for (int kt = 0; kt < 8; ++kt)
-            *reinterpret_cast<u32x2 *>(p + 16 * kt) =
-                u32x2{pack2(S.t[kt][0], S.t[kt][1]), pack2(S.t[kt][2], S.t[kt][3])};
-    } else {
-        float *p = static_cast<float *>(base) + v * kD + 4 * g;
+    for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-        for (int kt = 0; kt < 8; ++kt)
-            *reinterpret_cast<f32x4 *>(p + 16 * kt) = S.t[kt];
-    }
+        for (int st = 0; st < 2; ++st) {
+            if (dt == kBf16) {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(base) + at + 32 * kt + 16 * st);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S.t[kt][8 * st + 2 * e] = lo_f(x[e]);
+                    S.t[kt][8 * st + 2 * e + 1] = hi_f(x[e]);
+                }
+            } else {
+                const f32x4 *p = reinterpret_cast<const f32x4 *>(static_cast<const float *>(base) + at + 32 * kt + 16 * st);
+                const f32x4 x = p[0], y = p[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S.t[kt][8 * st + e] = x[e];
+                    S.t[kt][8 * st + 4 + e] = y[e];
+                }
+            }
+        }
+}
+__device__ __forceinline__ void state_store(const State &S, void *base, int dt, int v, int lane)
+{
+    const int at = v * kD + 8 * (lane >> 5);
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            if (dt == kBf16) {
+                u32x4 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = pack2(S.t[kt][8 * st + 2 * e], S.t[kt][8 * st + 2 * e + 1]);
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(base) + at + 32 * kt + 16 * st) = x;
+            } else {
+                f32x4 *p = reinterpret_cast<f32x4 *>(static_cast<float *>(base) + at + 32 * kt + 16 * st);
+                p[0] = f32x4{S.t[kt][8 * st], S.t[kt][8 * st + 1], S.t[kt][8 * st + 2], S.t[kt][8 * st + 3]};
+                p[1] = f32x4{S.t[kt][8 * st + 4], S.t[kt][8 * st + 5], S.t[kt][8 * st + 6], S.t[kt][8 * st + 7]};
+            }
+        }
 }
 __device__ __forceinline__ void state_zero(State &S)
 {
 #pragma unroll
-    for (int kt = 0; kt < 8; ++kt)
-        S.t[kt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            S.t[kt][r] = 0.0f;
 }
-__device__ __forceinline__ void state_one(State &S, int wave, int lane)
+__device__ __forceinline__ void state_one(State &S, int v, int lane)
 {
-    const int v = 16 * wave + (lane & 15), g = lane >> 4;
 #pragma unroll
-    for (int kt = 0; kt < 8; ++kt)
+    for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            S.t[kt][i] = 16 * kt + 4 * g + i == v ? 1.0f : 0.0f;
+        for (int r = 0; r < 16; ++r)
+            S.t[kt][r] = 32 * kt + 16 * (r >> 3) + 8 * (lane >> 5) + (r & 7) == v ? 1.0f : 0.0f;
 }
 __device__ __forceinline__ size_t state_size(int dt) { return kGdnStateBytes / (dt == kBf16 ? 2 : 1); }
 
 // ------------------------------------------------------------------------------- LDS
 //
-// Tiles of 64 tokens x 128 channels are rows of 256 bytes; the 16-byte pieces of a row are XORed with its number, so that
-// 16 rows of one piece lie in different banks, whether read along the row or transposed.
+// Tiles are rows (tokens) of 256 bytes (128 channels); the 16-byte pieces of a row are XORed with a function of its
+// number modulo 8, so that 8 rows of one piece and 4 rows of two neighbouring pieces lie in different banks.
+
+__device__ __forceinline__ int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
 
 constexpr int kTile = kGC * 256;
-__device__ __forceinline__ int swz(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
 
 struct LdsWalk {
     unsigned char tile[2][3][kTile];  // k, v, q of two chunks
-    unsigned char rec[kGdnMat * 2 + kGdnVec + 2048];
+    unsigned char rec[2][2 * kGdnMat + kGdnVec];
 };
 
-// A tile's 16 KiB straight into LDS: instruction n of 16 covers rows 4n .. 4n+3, wave w takes n = w and w + 8.
-// Rows behind the chunk lie beyond the descriptor and arrive as zeros.
-__device__ __forceinline__ void tile_fetch(unsigned char *lds, const GdnTensor &x, const uint16_t *base, int64_t t0, int len,
+// A tile straight into LDS: 4 rows an instruction, wave w of kWaves takes rows 4w .. and every 4 kWaves behind them.  Rows
+// behind the chunk lie beyond the descriptor and arrive as zeros.
+template <int kWaves, int kRows>
+__device__ __forceinline__ void tile_fetch(const unsigned char *lds, const GdnTensor &x, const uint16_t *base, int64_t t0, int len,
                                            int wave, int lane)
 {
-    const uint32_t stride = (uint32_t)x.st * 2;
-    const uint32_t bytes = __builtin_amdgcn_readfirstlane((int)(len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u));
-    const __amdgpu_buffer_rsrc_t r = rsrc(base + t0 * x.st, bytes);
+    const uint32_t stride = (uint32_t)x.st * 2, bytes = len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u;
     const int row = 4 * wave + (lane >> 4);
-    const uint32_t off = (uint32_t)row * stride + (uint32_t)(((lane & 15) ^ swz(row)) << 4);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + 1024 * wave), 16, off, 0, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + 1024 * (wave + 8)), 16, off + 32 * stride, 0, 0, 0);
-}
-// kParts x 8 KiB of a record
-template <int kParts>
-__device__ __forceinline__ void rec_fetch(unsigned char *lds, const unsigned char *src, bool on, int wave, int lane)
-{
-    const __amdgpu_buffer_rsrc_t r = rsrc(src, on ? kParts * 8192u : 0u);
+    const uint32_t off = (uint32_t)row * stride + (uint32_t)(((lane & 15) ^ swz(row)) << 4), to = lds_address(lds);
 #pragma unroll
-    for (int n = 0; n < kParts; ++n)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + 8192 * n + 1024 * wave), 16,
-                                                 (uint32_t)(8192 * n + 1024 * wave + 16 * lane), 0, 0, 0);
+    for (int n = 0; n < kRows / (4 * kWaves); ++n)
+        load_lds(base + t0 * x.st, bytes, off + (uint32_t)(4 * kWaves * n) * stride, to + 1024 * (wave + kWaves * n));
 }
 
-__device__ __forceinline__ u32x2 lds_b64(const unsigned char *p) { return *reinterpret_cast<const u32x2 *>(p); }
 // Transposing read: lane i of each 16 lanes gives the address of 4 channels of token i / 4 and gets channel i of
 // the 16 for the 4 tokens.
 __device__ __forceinline__ u32x2 lds_tr(const unsigned char *p)
@@ -675,103 +657,72 @@ __device__ __forceinline__ u32x2 lds_tr(const unsigned char *p)
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p));
 }
 
-// The same for four row tiles of one channel block, and of two.  While loads to LDS are on their way, the compiler waits for all of
-// them before the builtin; these blocks wait for their own reads alone.
-struct Col4 {
-    u32x2 r[4];  // 4 tokens 16 r + 4 g .. each
-};
-__device__ __forceinline__ uint32_t lds_address(const unsigned char *p)
-{
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)p;
-}
-__device__ __forceinline__ Col4 lds_tr4(uint32_t at)
-{
-    Col4 x;
-    __asm__ volatile("ds_read_b64_tr_b16 %0, %4\n\t"
-                     "ds_read_b64_tr_b16 %1, %4 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %2, %4 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %3, %4 offset:12288\n\t"
-                     "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(x.r[0]), "=&v"(x.r[1]), "=&v"(x.r[2]), "=&v"(x.r[3])
-                     : "v"(at)
-                     : "memory");
-    return x;
-}
-__device__ __forceinline__ void lds_tr8(uint32_t at, uint32_t bt, Col4 &x, Col4 &y)
-{
-    __asm__ volatile("ds_read_b64_tr_b16 %0, %8\n\t"
-                     "ds_read_b64_tr_b16 %1, %8 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %2, %8 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %3, %8 offset:12288\n\t"
-                     "ds_read_b64_tr_b16 %4, %9\n\t"
-                     "ds_read_b64_tr_b16 %5, %9 offset:4096\n\t"
-                     "ds_read_b64_tr_b16 %6, %9 offset:8192\n\t"
-                     "ds_read_b64_tr_b16 %7, %9 offset:12288\n\t"
-                     "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(x.r[0]), "=&v"(x.r[1]), "=&v"(x.r[2]), "=&v"(x.r[3]), "=&v"(y.r[0]), "=&v"(y.r[1]),
-                       "=&v"(y.r[2]), "=&v"(y.r[3])
-                     : "v"(at), "v"(bt)
-                     : "memory");
-}
-__device__ __forceinline__ u32x4 join(u32x2 x, u32x2 y) { return u32x4{x[0], x[1], y[0], y[1]}; }
-
 // This lane's places in a tile; the channel block is XORed in.
 struct Lanes {
-    int row;  // token lane % 16 of a row tile, channels 4 g .. of 16
-    int tr;   // transposing read: tokens 4 g .. of a row tile
+    int row;  // row lane % 32, 8 channels 8 h .. of 16
+    int key;  // transposing: tokens 4 h .. of 8, the 32 channels of a state's tile in the order of its registers
+    int col;  // the same, 32 channels in the order of lanes
+    int out;  // the same, in the order of column_of<true>
 
     __device__ explicit Lanes(int lane)
     {
-        const int m = lane & 15, g = lane >> 4, u = 4 * g + (m >> 2);
-        row = m * 256 + (((g >> 1) ^ swz(m)) << 4) + 8 * (g & 1);
-        tr = u * 256 + ((((m >> 1) & 1) ^ swz(u)) << 4) + 8 * (m & 1);
+        const int l32 = lane & 31, h = lane >> 5, g2 = (lane >> 4) & 1, i = lane & 15, t = 4 * h + (i >> 2), q = i & 3;
+        auto at = [&](int channel) { return t * 256 + (((channel >> 3) ^ swz(t)) << 4) + 2 * (channel & 4); };
+        row = l32 * 256 + ((h ^ swz(l32)) << 4);
+        key = at(16 * g2 + 8 * (q & 1) + 4 * (q >> 1));
+        col = at(16 * g2 + 4 * q);
+        out = at(16 * (q & 1) + 8 * g2 + 4 * (q >> 1));
     }
 };
-// 32 channels 32 p .. of the tokens of row tile r: a lane's token is lane % 16
-__device__ __forceinline__ u32x4 row_frag(const unsigned char *tile, const Lanes &ln, int r, int p)
+// 16 channels 16 x .. of row lane % 32 of a block of 32 rows
+__device__ __forceinline__ u32x4 row_frag(const unsigned char *tile, const Lanes &ln, int x, int block = 0)
 {
-    const u32x2 x = lds_b64(tile + 4096 * r + (ln.row ^ (64 * p))), y = lds_b64(tile + 4096 * r + (ln.row ^ (64 * p + 32)));
+    return *reinterpret_cast<const u32x4 *>(tile + 8192 * block + (ln.row ^ (32 * x)));
+}
+// tokens 8 n + 4 h .. of 32 channels 32 kt ..
+__device__ __forceinline__ u32x2 col_frag4(const unsigned char *tile, int at, int kt, int n)
+{
+    return lds_tr(tile + 2048 * n + (at ^ (64 * kt)));
+}
+// 16 tokens 16 st .., as an operand of a contraction over tokens
+__device__ __forceinline__ u32x4 col_frag(const unsigned char *tile, int at, int kt, int st)
+{
+    const u32x2 x = col_frag4(tile, at, kt, 2 * st), y = col_frag4(tile, at, kt, 2 * st + 1);
     return u32x4{x[0], x[1], y[0], y[1]};
-}
-// 4 tokens 16 r + 4 g .. of channel 16 kt + lane % 16
-__device__ __forceinline__ u32x2 col_frag4(const unsigned char *tile, const Lanes &ln, int kt, int r)
-{
-    return lds_tr(tile + 4096 * r + (ln.tr ^ (32 * kt)));
-}
-// 32 tokens 32 ks .. of channel 16 kt + lane % 16
-__device__ __forceinline__ u32x4 col_frag(const unsigned char *tile, const Lanes &ln, int kt, int ks)
-{
-    const u32x2 x = col_frag4(tile, ln, kt, 2 * ks), y = col_frag4(tile, ln, kt, 2 * ks + 1);
-    return u32x4{x[0], x[1], y[0], y[1]};
-}
-// S += sum over the chunk's tokens of channel rows (tile) times value columns (u), the reads a step ahead of the products
-__device__ __forceinline__ void state_add(State &S, const unsigned char *tile, const Lanes &ln, const Terms *u)
-{
-    const uint32_t at = lds_address(tile);
-    Col4 x[2], y[2];
-    lds_tr8(at + ln.tr, at + (ln.tr ^ 32), x[0], x[1]);
-#pragma unroll
-    for (int kt = 0; kt < 8; kt += 2) {
-        if (kt < 6)
-            lds_tr8(at + (ln.tr ^ (32 * kt + 64)), at + (ln.tr ^ (32 * kt + 96)), y[0], y[1]);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-                S.t[kt + n] = mfma3(join(x[n].r[2 * ks], x[n].r[2 * ks + 1]), u[ks], S.t[kt + n]);
-        x[0] = y[0];
-        x[1] = y[1];
-    }
 }
 __device__ __forceinline__ f32x4 widen4(u32x2 x) { return f32x4{lo_f(x[0]), hi_f(x[0]), lo_f(x[1]), hi_f(x[1])}; }
-__device__ __forceinline__ f32x4 vec4(const unsigned char *vec, int at)
+// factors of tokens 8 n + 4 h ..
+__device__ __forceinline__ f32x4 vec4(const unsigned char *vec, int which, int n, int lane)
 {
-    return *reinterpret_cast<const f32x4 *>(vec + 4 * at);
+    return *reinterpret_cast<const f32x4 *>(vec + 4 * (which + 8 * n + 4 * (lane >> 5)));
 }
-__device__ __forceinline__ Terms block_terms(const unsigned char *mat, int block, int lane)
+__device__ __forceinline__ float vec1(const unsigned char *vec, int at)
 {
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(mat + block * 1024 + lane * 16);
-    return Terms{p[0], p[6 * 64], p[12 * 64]};
+    return *reinterpret_cast<const float *>(vec + 4 * at);
+}
+__device__ __forceinline__ f32x16 zero16()
+{
+    f32x16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        z[i] = 0.0f;
+    return z;
+}
+
+// S <- f S + sum over the chunk's tokens of key channels (tile) times value columns (u)
+__device__ __forceinline__ void state_add(State &S, const unsigned char *tile, const Lanes &ln, const Terms *u)
+{
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+            S.t[kt] = mfma3(col_frag(tile, ln.key, kt, st), u[st], S.t[kt]);
+}
+__device__ __forceinline__ void state_scale(State &S, float f)
+{
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+        S.t[kt] *= f;
 }
 
 // --------------------------------------------------------------------------- forward walk
@@ -779,14 +730,9 @@ __device__ __forceinline__ Terms block_terms(const unsigned char *mat, int block
 constexpr int kModeOut = 0;    // out and final states
 constexpr int kModeShare = 1;  // a segment's share of the state at its end (F)
 constexpr int kModePhi = 2;    // the transition: from S = 1, without values
-constexpr int kModeStore = 3;  // backward pass: the state before each chunk and its residuals
-
-__device__ __forceinline__ void state_scale(State &S, float f)
-{
-#pragma unroll
-    for (int kt = 0; kt < 8; ++kt)
-        S.t[kt] *= f;
-}
+constexpr int kModeStore = 3;  // backward pass: the state before each block and the residuals
+constexpr int kWalkWaves = 4;
+constexpr int kWalkThreads = 64 * kWalkWaves;
 
 // Sequences without tokens that belong to segment p: the state leaves as it came.  With invalid lengths all of them.
 __device__ void empty_states(const GdnArgs &a, const Entry &e0, const Entry &e1, bool valid, int64_t p, int64_t h,
@@ -794,40 +740,40 @@ __device__ void empty_states(const GdnArgs &a, const Entry &e0, const Entry &e1,
 {
     if (!a.cu && a.T != 0)
         return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, v = 32 * (tid >> 6) + (lane & 31);
     const int64_t lo = !valid ? (p == 0 ? 0 : a.N) : e0.seq, hi = !valid ? a.N : p + 1 == a.P && a.cu ? a.N : e1.seq;
-    for (int64_t b = lo; b < hi; b += 512) {
+    for (int64_t b = lo; b < hi; b += kWalkThreads) {
         const int64_t i = b + tid;
         const bool none = i < hi && (!valid || seq_begin(a, i) == seq_begin(a, i + 1));
         if (!__syncthreads_or(none))
             continue;
-        for (int64_t n = b; n < b + 512 && n < hi; ++n) {
+        for (int64_t n = b; n < b + kWalkThreads && n < hi; ++n) {
             if (valid && seq_begin(a, n) != seq_begin(a, n + 1))
                 continue;
             State S;
             state_zero(S);
             const int64_t at = n * a.H + h;
             if (init)
-                state_load(S, static_cast<const unsigned char *>(init) + at * state_size(init_dt), init_dt, wave, lane);
-            state_store(S, static_cast<unsigned char *>(fin) + at * state_size(fin_dt), fin_dt, wave, lane);
+                state_load(S, static_cast<const unsigned char *>(init) + at * state_size(init_dt), init_dt, v, lane);
+            state_store(S, static_cast<unsigned char *>(fin) + at * state_size(fin_dt), fin_dt, v, lane);
         }
     }
 }
 
-// rows of a D tile (tokens 16 r + 4 g ..) into column `col` of a 64 x 128 matrix
-__device__ __forceinline__ void rows_store(float *m, const f32x4 &x, int r, int g, int col)
+// A D tile (rows: tokens, columns: lane % 32) into a 32 x 128 matrix, from its column on
+__device__ __forceinline__ void rows_store(float *m, const f32x16 &x, int lane)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m[(16 * r + 4 * g + i) * kD + col] = x[i];
+    for (int i = 0; i < 16; ++i)
+        m[(8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)) * kD + (lane & 31)] = x[i];
 }
 
 template <int kMode>
 __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row, int64_t p, int64_t h)
 {
-    constexpr bool kOut = kMode == kModeOut;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m = lane & 15, g = lane >> 4;
+    constexpr bool kOut = kMode == kModeOut, kValues = kMode != kModePhi;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31;
+    const int v = 32 * wave + column_of<kOut>(l32);
     const int64_t segment = row * a.P + p;
     const bool valid = !a.status || *a.status == 0;
     Entry e0 = entry_of(a, row, p), e1 = entry_of(a, row, p + 1);
@@ -848,235 +794,273 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
     if (ch.len == 0)
         return;
     const Lanes ln(lane);
-    auto head_of = [&](const GdnTensor &x) { return head_base(x, row, h); };
-    const uint16_t *pk = head_of(a.k), *pv = head_of(a.v), *pq = head_of(a.q);
-    constexpr int kParts = kOut ? 5 : 3;
+    const uint16_t *pk = head_base(a.k, row, h), *pv = head_base(a.v, row, h), *pq = head_base(a.q, row, h);
     auto fetch = [&](int buf, const Chunk &n) {
-        tile_fetch(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
-        if constexpr (kMode != kModePhi)
-            tile_fetch(lds.tile[buf][1], a.v, pv, n.t0, n.len, wave, lane);
+        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
+        if constexpr (kValues)
+            tile_fetch<kWalkWaves, kGC>(lds.tile[buf][1], a.v, pv, n.t0, n.len, wave, lane);
         if constexpr (kOut)
-            tile_fetch(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
+            tile_fetch<kWalkWaves, kGC>(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
+        constexpr int kBytes = kOut ? 2 * kGdnMat + kGdnVec : kGdnMat + kGdnVec;
+        const unsigned char *rec = a.rec + (n.slot * a.H + h) * a.rec_bytes;
+        for (int i = wave; i < kBytes / 1024; i += kWalkWaves)
+            load_lds(rec, kBytes, (uint32_t)(1024 * i + 16 * lane), lds_address(lds.rec[buf]) + 1024 * i);
     };
-    auto fetch_rec = [&](const Chunk &n) {
-        rec_fetch<kParts>(lds.rec, a.rec + ((n.len ? n.slot : 0) * a.H + h) * a.rec_bytes, n.len != 0, wave, lane);
-    };
-    const unsigned char *mt = lds.rec, *vec = lds.rec + kGdnMat, *ma = vec + kGdnVec;
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
     State S;
     state_zero(S);
     int buf = 0;
     fetch(0, ch);
-    fetch_rec(ch);
-    arrive();
+    // stored a chunk later, behind the wait for the loads: a store is then waited for a whole chunk after it
+    u32x4 held[2];     // rows of out
+    f32x16 held_r;     // residuals
+    Chunk before = ch;
+    before.len = 0;
+    auto store_held = [&]() {
+        if (before.len == 0)
+            return;
+        if constexpr (kOut) {
+            if (l32 < before.len) {
+                uint16_t *o = a.out + ((row * a.T + before.t0 + l32) * a.H + h) * kD + 32 * wave + 16 * (lane >> 5);
+                reinterpret_cast<u32x4 *>(o)[0] = held[0];
+                reinterpret_cast<u32x4 *>(o)[1] = held[1];
+            }
+        }
+        if constexpr (kMode == kModeStore)
+            rows_store(a.res + (before.slot * a.H + h) * kGC * kD + 32 * wave, held_r, lane);
+    };
     for (;;) {
-        const unsigned char *tk = lds.tile[buf][0], *tv = lds.tile[buf][1], *tq = lds.tile[buf][2];
+        const unsigned char *tk = lds.tile[buf][0], *tv = lds.tile[buf][1], *tq = lds.tile[buf][2], *mt = lds.rec[buf],
+                            *vec = mt + kGdnMat, *ma = vec + kGdnVec;
+        const Chunk nx = w.next(a);
+        arrive();  // this chunk's tiles and record are there; the other buffer is read by no one
+        if (nx.len)
+            fetch(buf ^ 1, nx);
+        store_held();
         if (ch.first) {
             if constexpr (kMode == kModePhi) {
-                state_one(S, wave, lane);
+                state_one(S, v, lane);
             } else if (ch.from_seg) {
                 if constexpr (kOut || kMode == kModeStore)
-                    state_load(S, a.seg + (segment * a.H + h) * kD * kD, 2, wave, lane);
+                    state_load(S, a.seg + (segment * a.H + h) * kD * kD, 2, v, lane);
                 else
                     state_zero(S);
             } else if (kOut && a.keep && ch.to_seg) {
-                state_load(S, a.keep + (segment * a.H + h) * kD * kD, 2, wave, lane);
+                state_load(S, a.keep + (segment * a.H + h) * kD * kD, 2, v, lane);
             } else if (a.init) {
                 state_load(S, static_cast<const unsigned char *>(a.init) + (ch.seq * a.H + h) * state_size(a.init_dt),
-                           a.init_dt, wave, lane);
+                           a.init_dt, v, lane);
                 if constexpr (kMode == kModeShare)
                     if (a.keep)
-                        state_store(S, a.keep + (segment * a.H + h) * kD * kD, 2, wave, lane);
+                        state_store(S, a.keep + (segment * a.H + h) * kD * kD, 2, v, lane);
             } else {
                 state_zero(S);
             }
-            // here, or the compiler waits behind the branch in every chunk, and for the loads to LDS with it
+            // here, or the compiler waits behind the branch in every chunk
             __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         }
-        const Chunk nx = w.next(a);
         if constexpr (kMode == kModeStore)
-            state_store(S, a.before + (ch.slot * a.H + h) * kD * kD, 2, wave, lane);
-        Col4 cv;
-        if constexpr (kMode != kModePhi)
-            cv = lds_tr4(lds_address(tv) + (ln.tr ^ (32 * wave)));
-        f32x4 Z[4], O[4];
-        {
-            Terms c[4];
+            if (ch.opens)
+                state_store(S, a.before + (ch.block * a.H + h) * kD * kD, 2, v, lane);
+        f32x16 Z = zero16(), O = zero16();
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                cut8(S.t[2 * x], S.t[2 * x + 1], c[x]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                Z[r] = O[r] = zero;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    Z[r] = mfma3(row_frag(tk, ln, r, x), c[x], Z[r]);
-                if constexpr (kOut)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)  // transposed: rows are value columns, a lane's token is lane % 16
-                        O[r] = mfma3(c[x], row_frag(tq, ln, r, x), O[r]);
-            }
+        for (int x = 0; x < 8; ++x) {
+            const Terms c = cut8(S.t[x >> 1], x & 1);
+            Z = mfma3(row_frag(tk, ln, x), c, Z);
+            if constexpr (kOut)  // transposed: rows are value columns, a lane's token is lane % 32
+                O = mfma3(c, row_frag(tq, ln, x), O);
         }
-        arrive();  // this chunk's record is there; the other buffer is read by no one
-        fetch(buf ^ 1, nx);
-        Terms xr[2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            f32x4 x[2];
+        for (int n = 0; n < 4; ++n) {
+            const f32x4 f = vec4(vec, kVHead, n, lane);
+            f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (kValues)
+                x = widen4(col_frag4(tv, kOut ? ln.out : ln.col, wave, n));
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int r = 2 * ks + hf;
-                x[hf] = -vec4(vec, kVHead + 16 * r + 4 * g) * Z[r];
-                if constexpr (kMode != kModePhi)
-                    x[hf] += widen4(cv.r[r]);
-            }
-            cut8(x[0], x[1], xr[ks]);
+            for (int i = 0; i < 4; ++i)
+                Z[4 * n + i] = fmaf(-f[i], Z[4 * n + i], x[i]);
         }
-        f32x4 R[4];
+        f32x16 R = zero16();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            R[r] = zero;
-#pragma unroll
-            for (int ks = 0; ks <= r / 2; ++ks)
-                R[r] = mfma6(block_terms(mt, low_block(r, ks), lane), xr[ks], R[r]);
-        }
+        for (int st = 0; st < 2; ++st)
+            R = mfma6(load_terms(mt, st, lane), cut8(Z, st), R);
         if constexpr (kOut) {
-            const float *vo = reinterpret_cast<const float *>(vec) + kVOut;
-            Terms rr[2];
-            cut8(R[0], R[1], rr[0]);
-            cut8(R[2], R[3], rr[1]);
+            O *= vec1(vec, kVOut + l32);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                O[r] *= vo[16 * r + m];
-#pragma unroll
-                for (int ks = 0; ks <= r / 2; ++ks)
-                    O[r] = mfma6(rr[ks], block_terms(ma, low_block(r, ks), lane), O[r]);
-            }
-        }
-        Terms u[2];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-            cut8(R[2 * ks] * vec4(vec, kVWrite + 32 * ks + 4 * g), R[2 * ks + 1] * vec4(vec, kVWrite + 32 * ks + 16 + 4 * g),
-                 u[ks]);
-        const float carry = *reinterpret_cast<const float *>(vec + 4 * kVLast);
-        arrive();  // the next chunk's tiles are there; the record is read by no one
-        fetch_rec(nx);
-        if constexpr (kOut) {
-            const __amdgpu_buffer_rsrc_t ro = rsrc(a.out + ((row * a.T + ch.t0) * a.H + h) * kD,
-                                                   (uint32_t)(ch.len - 1) * (uint32_t)a.H * 256u + 256u);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const u32x2 y = {pack2(O[r][0], O[r][1]), pack2(O[r][2], O[r][3])};
-                typedef unsigned int u2 __attribute__((vector_size(8)));
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, y), ro,
-                                                      (uint32_t)(16 * r + m) * (uint32_t)a.H * 256u + 32 * wave + 8 * g, 0, 0);
-            }
+            for (int st = 0; st < 2; ++st)
+                O = mfma6(cut8(R, st), load_terms(ma, st, lane), O);
         }
         if constexpr (kMode == kModeStore)
+            held_r = R;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                rows_store(a.res + (ch.slot * a.H + h) * kGC * kD, R[r], r, g, 16 * wave + m);
-        state_scale(S, carry);
+        for (int n = 0; n < 4; ++n) {
+            const f32x4 f = vec4(vec, kVWrite, n, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                R[4 * n + i] *= f[i];
+        }
+        const Terms u[2] = {cut8(R, 0), cut8(R, 1)};
+        state_scale(S, vec1(vec, kVLast));
         state_add(S, tk, ln, u);
+        if constexpr (kOut)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                held[e >> 2][e & 3] = pack2(O[2 * e], O[2 * e + 1]);
+        before = ch;
         if (kMode != kModeStore && ch.last) {
             if constexpr (kMode == kModeShare)
-                state_store(S, a.seg + ((segment + 1) * a.H + h) * kD * kD, 2, wave, lane);
+                state_store(S, a.seg + ((segment + 1) * a.H + h) * kD * kD, 2, v, lane);
             else if constexpr (kMode == kModePhi)
-                state_store(S, a.phi + (segment * a.H + h) * kD * kD, 2, wave, lane);
+                state_store(S, a.phi + (segment * a.H + h) * kD * kD, 2, v, lane);
             else if (a.fin && !ch.to_seg)
                 state_store(S, static_cast<unsigned char *>(a.fin) + (ch.seq * a.H + h) * state_size(a.fin_dt), a.fin_dt,
-                            wave, lane);
+                            v, lane);
         }
         if (nx.len == 0)
             break;
         ch = nx;
         buf ^= 1;
     }
+    store_held();
 }
 
-__global__ __launch_bounds__(512, 1) void gdn_out_kernel(GdnArgs a)
+// Workgroup b of a walk: head b % H of segment b / H
+struct Place {
+    int64_t row, p, h;
+
+    __device__ explicit Place(const GdnArgs &a)
+    {
+        const uint32_t b = blockIdx.x, s = b / (uint32_t)a.H;
+        h = b - s * (uint32_t)a.H;
+        row = s / (uint32_t)a.P;
+        p = s - (uint32_t)row * (uint32_t)a.P;
+    }
+};
+
+__global__ __launch_bounds__(kWalkThreads, 2) void gdn_out_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
-    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
-    const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
-    walk<kModeOut>(a, lds, row, s - row * a.P, h);
+    const Place at(a);
+    walk<kModeOut>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
 }
 // y = 0: shares, y = 1: transitions
-__global__ __launch_bounds__(512, 1) void gdn_cut_kernel(GdnArgs a)
+__global__ __launch_bounds__(kWalkThreads, 2) void gdn_cut_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
-    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
-    const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
+    const Place at(a);
     if (blockIdx.y == 0)
-        walk<kModeShare>(a, lds, row, s - row * a.P, h);
+        walk<kModeShare>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
     else
-        walk<kModePhi>(a, lds, row, s - row * a.P, h);
+        walk<kModePhi>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
+}
+__global__ __launch_bounds__(kWalkThreads, 2) void gdn_store_kernel(GdnArgs a)
+{
+    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
+    const Place at(a);
+    walk<kModeStore>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
 }
 
 // ----------------------------------------------------------------------------------- scan
 //
-// State at each cut: S_{p+1} = S_p Phi_p + F_p where segment p lies inside one sequence (else F_p is the state).  A
-// workgroup of 8 waves takes 16 value columns of one row and head; wave w forms key channels 16w ..
+// State at each cut: S_{p+1} = S_p Phi_p + F_p where segment p lies inside one sequence (else F_p is the state); backwards
+// (kRev) the gradients of the states at the cuts, dS_{p-1} = dS_p Phi_p^T + F_p.  A workgroup of 8 waves takes 16 value
+// columns of one row and head; wave w forms key channels 16w .. of each state and hands its terms to the others
+// through LDS.  The next step's Phi and F are on their way meanwhile.
+template <bool kRev>
 __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(16))) float st[2][16][132];
+    __shared__ __attribute__((aligned(16))) uint32_t terms[2][3][4][64][4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-    const int64_t chain = blockIdx.x >> 3, row = chain / a.H, h = chain - row * a.H;
-    const int v0 = (int)(blockIdx.x & 7) * 16;
+    const uint32_t chain = blockIdx.x >> 3, row = chain / (uint32_t)a.H, h = chain - row * (uint32_t)a.H;
+    const int v = (int)(blockIdx.x & 7) * 16 + m;
     if (a.status && *a.status != 0)
         return;
-    bool have = false;  // st[cur] holds the state at segment p's start
-    int cur = 0;
-    Entry e = entry_of(a, row, 1);
-    for (int64_t p = 1; p + 1 < a.P; ++p) {
-        const Entry n = entry_of(a, row, p + 1);
-        const bool inside = e.chunk > 0 && n.chunk > 0 && e.seq == n.seq;
-        e = n;
-        if (!inside) {
-            have = false;
-            continue;
-        }
-        const size_t at = ((size_t)(row * a.P + p) * a.H + h) * kD * kD;
-        if (!have) {
-            __syncthreads();
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(a.seg + at + (size_t)(v0 + (tid >> 5)) * kD + (tid & 31) * 4);
-            *reinterpret_cast<f32x4 *>(&st[cur][tid >> 5][(tid & 31) * 4]) = x;
-            __syncthreads();
-        }
-        float *next = a.seg + at + (size_t)a.H * kD * kD + (size_t)(v0 + m) * kD + 16 * wave + 4 * g;
-        f32x4 acc = *reinterpret_cast<const f32x4 *>(next);
-        const float *phi = a.phi + at + 16 * wave + m;
+    float *base = (kRev ? a.dseg : a.seg) + ((size_t)row * a.P * a.H + h) * kD * kD;
+    const float *phis = a.phi + ((size_t)row * a.P * a.H + h) * kD * kD;
+    const size_t step = (size_t)a.H * kD * kD;
+    const int64_t first = kRev ? a.P - 2 : 1, dir = kRev ? -1 : 1;
+    auto inside = [&](int64_t p) {
+        if (p < 1 || p > a.P - 2)
+            return false;
+        const Entry e = entry_of(a, row, p), n = entry_of(a, row, p + 1);
+        return e.chunk > 0 && n.chunk > 0 && e.seq == n.seq;
+    };
+    f32x4 f[8], acc, own;
+    auto fetch = [&](int64_t p) {
+        acc = *reinterpret_cast<const f32x4 *>(base + (size_t)(p + dir) * step + (size_t)v * kD + 16 * wave + 4 * g);
+        const float *phi = phis + (size_t)p * step;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            Terms s, f;
-            cut8(*reinterpret_cast<const f32x4 *>(&st[cur][m][32 * x + 4 * g]),
-                 *reinterpret_cast<const f32x4 *>(&st[cur][m][32 * x + 16 + 4 * g]), s);
-            f32x4 y[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+        for (int x = 0; x < 8; ++x) {
+            if constexpr (kRev) {
+                f[x] = *reinterpret_cast<const f32x4 *>(phi + (16 * wave + m) * kD + 16 * x + 4 * g);
+            } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    y[hf][i] = phi[(32 * x + 16 * hf + 4 * g + i) * kD];
-            cut8(y[0], y[1], f);
-            acc = mfma6(f, s, acc);  // rows: key channels, columns: value columns
+                    f[x][i] = phi[(16 * x + 4 * g + i) * kD + 16 * wave + m];
+            }
         }
-        *reinterpret_cast<f32x4 *>(next) = acc;
-        cur ^= 1;
-        *reinterpret_cast<f32x4 *>(&st[cur][m][16 * wave + 4 * g]) = acc;
+    };
+    int cur = 0;
+    bool have = false;  // terms[cur] are those of the state that segment p begins (ends) with
+    bool in = inside(first);
+    if (in)
+        fetch(first);
+    for (int64_t p = first; kRev ? p >= 1 : p + 1 < a.P; p += dir) {
+        const bool next = inside(p + dir);
+        if (!in) {
+            have = false;
+            in = next;
+            if (in)
+                fetch(p + dir);
+            continue;
+        }
+        if (!have) {
+            own = *reinterpret_cast<const f32x4 *>(base + (size_t)p * step + (size_t)v * kD + 16 * wave + 4 * g);
+            Terms t;
+            cut2(own[0], own[1], t, 0);
+            cut2(own[2], own[3], t, 1);
+            const int x = wave >> 1, e = 2 * (wave & 1);
+            *reinterpret_cast<u32x2 *>(&terms[cur][0][x][lane][e]) = u32x2{t.h[0], t.h[1]};
+            *reinterpret_cast<u32x2 *>(&terms[cur][1][x][lane][e]) = u32x2{t.m[0], t.m[1]};
+            *reinterpret_cast<u32x2 *>(&terms[cur][2][x][lane][e]) = u32x2{t.l[0], t.l[1]};
+        }
+        Terms ft[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            ft[x] = cut8(f[2 * x], f[2 * x + 1]);
+        f32x4 sum = acc;
+        if (next)
+            fetch(p + dir);
         __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const Terms s = {*reinterpret_cast<const u32x4 *>(terms[cur][0][x][lane]),
+                             *reinterpret_cast<const u32x4 *>(terms[cur][1][x][lane]),
+                             *reinterpret_cast<const u32x4 *>(terms[cur][2][x][lane])};
+            sum = mfma6(ft[x], s, sum);  // rows: key channels, columns: value columns
+        }
+        *reinterpret_cast<f32x4 *>(base + (size_t)(p + dir) * step + (size_t)v * kD + 16 * wave + 4 * g) = sum;
+        cur ^= 1;  // the next barrier keeps the writes two steps on behind these reads
+        Terms t;
+        cut2(sum[0], sum[1], t, 0);
+        cut2(sum[2], sum[3], t, 1);
+        const int x = wave >> 1, e = 2 * (wave & 1);
+        *reinterpret_cast<u32x2 *>(&terms[cur][0][x][lane][e]) = u32x2{t.h[0], t.h[1]};
+        *reinterpret_cast<u32x2 *>(&terms[cur][1][x][lane][e]) = u32x2{t.m[0], t.m[1]};
+        *reinterpret_cast<u32x2 *>(&terms[cur][2][x][lane][e]) = u32x2{t.l[0], t.l[1]};
         have = true;
+        in = next;
     }
 }
 
 // -------------------------------------------------------------------------- backward walk
 //
-// dL/dS from a sequence's end to its start, in the same layout; stores it after each chunk, and dw.
+// dL/dS from a sequence's end to its start, in the same layout; stores it after each block, and dw.
 
 template <bool kShare>
 __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_t row, int64_t p, int64_t h)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m = lane & 15, g = lane >> 4;
+    const int v = 32 * wave + (lane & 31);
     const int64_t segment = row * a.P + p;
     const bool valid = !a.status || *a.status == 0;
     Entry e0 = entry_of(a, row, p), e1 = entry_of(a, row, p + 1);
@@ -1097,234 +1081,194 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
     if (ch.len == 0)
         return;
     const Lanes ln(lane);
-    auto head_of = [&](const GdnTensor &x) { return head_base(x, row, h); };
-    const uint16_t *pk = head_of(a.k), *po = head_of(a.dout), *pq = head_of(a.q);
+    const uint16_t *pk = head_base(a.k, row, h), *po = head_base(a.dout, row, h), *pq = head_base(a.q, row, h);
     auto fetch = [&](int buf, const Chunk &n) {
-        tile_fetch(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
-        tile_fetch(lds.tile[buf][1], a.dout, po, n.t0, n.len, wave, lane);
-        tile_fetch(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
+        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
+        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][1], a.dout, po, n.t0, n.len, wave, lane);
+        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
+        constexpr int kBytes = 2 * kGdnMat + kGdnVec;
+        const unsigned char *rec = a.rec + (n.slot * a.H + h) * a.rec_bytes + kGdnMat;
+        for (int i = wave; i < kBytes / 1024; i += kWalkWaves)
+            load_lds(rec, kBytes, (uint32_t)(1024 * i + 16 * lane), lds_address(lds.rec[buf]) + 1024 * i);
     };
-    auto fetch_rec = [&](const Chunk &n) {
-        rec_fetch<5>(lds.rec, a.rec + ((n.len ? n.slot : 0) * a.H + h) * a.rec_bytes + kGdnMat, n.len != 0, wave, lane);
-    };
-    const unsigned char *vec = lds.rec, *mt = vec + kGdnVec, *ma = mt + kGdnMat;
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
     State S;
     state_zero(S);
     int buf = 0;
     fetch(0, ch);
-    fetch_rec(ch);
-    arrive();
+    f32x16 held;  // dw, stored a chunk later as in the forward walk
+    Chunk before = ch;
+    before.len = 0;
+    auto store_held = [&]() {
+        if (!kShare && before.len)
+            rows_store(a.dwrite + (before.slot * a.H + h) * kGC * kD + 32 * wave, held, lane);
+    };
     for (;;) {
-        const unsigned char *tk = lds.tile[buf][0], *to = lds.tile[buf][1], *tq = lds.tile[buf][2];
+        const unsigned char *tk = lds.tile[buf][0], *to = lds.tile[buf][1], *tq = lds.tile[buf][2], *vec = lds.rec[buf],
+                            *mt = vec + kGdnVec, *ma = mt + kGdnMat;
+        const Chunk nx = w.next(a);
+        arrive();  // this chunk's tiles and record are there; the other buffer is read by no one
+        if (nx.len)
+            fetch(buf ^ 1, nx);
+        store_held();
         if (ch.first) {
             if (ch.from_seg) {
                 if constexpr (kShare)
                     state_zero(S);
                 else
-                    state_load(S, a.dseg + (segment * a.H + h) * kD * kD, 2, wave, lane);
+                    state_load(S, a.dseg + (segment * a.H + h) * kD * kD, 2, v, lane);
             } else if (a.dfin) {
-                state_load(S, a.dfin + (ch.seq * a.H + h) * kD * kD, 2, wave, lane);
+                state_load(S, a.dfin + (ch.seq * a.H + h) * kD * kD, 2, v, lane);
             } else {
                 state_zero(S);
             }
-            // here, or the compiler waits behind the branch in every chunk, and for the loads to LDS with it
+            // here, or the compiler waits behind the branch in every chunk
             __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
         }
-        const Chunk nx = w.next(a);
-        if constexpr (!kShare)
-            state_store(S, a.dafter + (ch.slot * a.H + h) * kD * kD, 2, wave, lane);
-        const Col4 co = lds_tr4(lds_address(to) + (ln.tr ^ (32 * wave)));
-        f32x4 Y[4];
-        {
-            Terms c[4];
+        if (!kShare && ch.closes)
+            state_store(S, a.dafter + (ch.block * a.H + h) * kD * kD, 2, v, lane);
+        f32x16 Y = zero16();
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                cut8(S.t[2 * x], S.t[2 * x + 1], c[x]);
+        for (int x = 0; x < 8; ++x)
+            Y = mfma3(row_frag(tk, ln, x), cut8(S.t[x >> 1], x & 1), Y);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                Y[r] = zero;
+        for (int n = 0; n < 4; ++n) {
+            const f32x4 f = vec4(vec, kVTail, n, lane);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    Y[r] = mfma3(row_frag(tk, ln, r, x), c[x], Y[r]);
-            }
+            for (int i = 0; i < 4; ++i)
+                Y[4 * n + i] *= f[i];
         }
-        arrive();  // this chunk's record is there; the other buffer is read by no one
-        fetch(buf ^ 1, nx);
-        const u32x4 o[2] = {join(co.r[0], co.r[1]), join(co.r[2], co.r[3])};
+        u32x4 o[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            Y[r] *= vec4(vec, kVTail + 16 * r + 4 * g);
-#pragma unroll
-            for (int ks = r / 2; ks < 2; ++ks)
-                Y[r] = mfma3(block_terms(ma, up_block(r, ks), lane), o[ks], Y[r]);
+        for (int st = 0; st < 2; ++st) {
+            o[st] = col_frag(to, ln.col, wave, st);
+            Y = mfma3(load_terms(ma, st, lane), o[st], Y);
         }
-        Terms d[2];
-        cut8(Y[0], Y[1], d[0]);
-        cut8(Y[2], Y[3], d[1]);
-        f32x4 W[4];
+        f32x16 W = zero16();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            W[r] = zero;
-#pragma unroll
-            for (int ks = r / 2; ks < 2; ++ks)
-                W[r] = mfma6(block_terms(mt, up_block(r, ks), lane), d[ks], W[r]);
-        }
+        for (int st = 0; st < 2; ++st)
+            W = mfma6(load_terms(mt, st, lane), cut8(Y, st), W);
+        held = W;
         // what the tokens' reads and writes send to the state before the chunk
-        Terms uo[2], uw[2];
+        f32x16 x;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            f32x4 x[2], y[2];
+        for (int n = 0; n < 4; ++n) {
+            const f32x4 f = vec4(vec, kVOut, n, lane), be = vec4(vec, kVBeta, n, lane), hd = vec4(vec, kVHead, n, lane);
+            const f32x4 o4 = widen4(u32x2{o[n >> 1][2 * (n & 1)], o[n >> 1][2 * (n & 1) + 1]});
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int at = 32 * ks + 16 * hf + 4 * g;
-                x[hf] = widen4(u32x2{o[ks][2 * hf], o[ks][2 * hf + 1]}) * vec4(vec, kVOut + at);
-                y[hf] = -(W[2 * ks + hf] * (vec4(vec, kVBeta + at) * vec4(vec, kVHead + at)));
+            for (int i = 0; i < 4; ++i) {
+                x[4 * n + i] = o4[i] * f[i];
+                W[4 * n + i] *= -(be[i] * hd[i]);
             }
-            cut8(x[0], x[1], uo[ks]);
-            cut8(y[0], y[1], uw[ks]);
         }
-        const float carry = *reinterpret_cast<const float *>(vec + 4 * kVLast);
-        arrive();  // the next chunk's tiles are there; the record is read by no one
-        fetch_rec(nx);
-        if constexpr (!kShare)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                rows_store(a.dwrite + (ch.slot * a.H + h) * kGC * kD, W[r], r, g, 16 * wave + m);
-        state_scale(S, carry);
+        const Terms uo[2] = {cut8(x, 0), cut8(x, 1)}, uw[2] = {cut8(W, 0), cut8(W, 1)};
+        state_scale(S, vec1(vec, kVLast));
         state_add(S, tq, ln, uo);
         state_add(S, tk, ln, uw);
+        before = ch;
         if (ch.last) {
             if constexpr (kShare)
-                state_store(S, a.dseg + ((segment - 1) * a.H + h) * kD * kD, 2, wave, lane);
+                state_store(S, a.dseg + ((segment - 1) * a.H + h) * kD * kD, 2, v, lane);
             else if (a.dinit && !ch.to_seg)
-                state_store(S, a.dinit + (ch.seq * a.H + h) * kD * kD, 2, wave, lane);
+                state_store(S, a.dinit + (ch.seq * a.H + h) * kD * kD, 2, v, lane);
         }
         if (nx.len == 0)
             break;
         ch = nx;
         buf ^= 1;
     }
+    store_held();
 }
 
-__global__ __launch_bounds__(512, 1) void gdn_store_kernel(GdnArgs a)
-{
-    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
-    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
-    const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
-    walk<kModeStore>(a, lds, row, s - row * a.P, h);
-}
 template <bool kShare>
-__global__ __launch_bounds__(512, 1) void gdn_back_kernel(GdnArgs a)
+__global__ __launch_bounds__(kWalkThreads, 2) void gdn_back_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
-    LdsWalk &lds = *reinterpret_cast<LdsWalk *>(raw);
-    const int64_t h = blockIdx.x % a.H, s = blockIdx.x / a.H, row = s / a.P;
-    walk_back<kShare>(a, lds, row, s - row * a.P, h);
+    const Place at(a);
+    walk_back<kShare>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
 }
 
-// dL/dS at each cut, from the last to the first: dS_{p-1} = dS_p Phi_p^T + share, as gdn_scan_kernel.
-__global__ __launch_bounds__(512) void gdn_scan_back_kernel(GdnArgs a)
-{
-    __shared__ __attribute__((aligned(16))) float st[2][16][132];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-    const int64_t chain = blockIdx.x >> 3, row = chain / a.H, h = chain - row * a.H;
-    const int v0 = (int)(blockIdx.x & 7) * 16;
-    if (a.status && *a.status != 0)
-        return;
-    bool have = false;  // st[cur] holds dL/dS at segment p's end
-    int cur = 0;
-    Entry e = entry_of(a, row, a.P - 1);
-    for (int64_t p = a.P - 2; p > 0; --p) {
-        const Entry n = e;
-        e = entry_of(a, row, p);
-        if (!(e.chunk > 0 && n.chunk > 0 && e.seq == n.seq)) {
-            have = false;
-            continue;
-        }
-        const size_t at = ((size_t)(row * a.P + p) * a.H + h) * kD * kD;
-        if (!have) {
-            __syncthreads();
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(a.dseg + at + (size_t)(v0 + (tid >> 5)) * kD + (tid & 31) * 4);
-            *reinterpret_cast<f32x4 *>(&st[cur][tid >> 5][(tid & 31) * 4]) = x;
-            __syncthreads();
-        }
-        float *next = a.dseg + at - (size_t)a.H * kD * kD + (size_t)(v0 + m) * kD + 16 * wave + 4 * g;
-        f32x4 acc = *reinterpret_cast<const f32x4 *>(next);
-        const float *phi = a.phi + at + (16 * wave + m) * kD + 4 * g;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            Terms s, f;
-            cut8(*reinterpret_cast<const f32x4 *>(&st[cur][m][32 * x + 4 * g]),
-                 *reinterpret_cast<const f32x4 *>(&st[cur][m][32 * x + 16 + 4 * g]), s);
-            cut8(*reinterpret_cast<const f32x4 *>(phi + 32 * x), *reinterpret_cast<const f32x4 *>(phi + 32 * x + 16), f);
-            acc = mfma6(f, s, acc);
-        }
-        *reinterpret_cast<f32x4 *>(next) = acc;
-        cur ^= 1;
-        *reinterpret_cast<f32x4 *>(&st[cur][m][16 * wave + 4 * g]) = acc;
-        __syncthreads();
-        have = true;
-    }
-}
-
-// ------------------------------------------------------------------- gradients of a chunk
+// ------------------------------------------------------------------- gradients of a block
 //
-// One workgroup of 8 waves per (chunk, head).  w = beta r and dx = beta dw are cut into bf16 terms once, in LDS.  Wave w
-// forms key channels 16w .. of dq and dk for all 64 tokens (rows: channels, a lane's token is lane % 16), and one 16 x 32
-// block each of P, P^T and G + G^T, which pass through LDS to the other waves in the place of the terms.
+// One workgroup of 8 waves per (block of 64 tokens, head); the formulas hold for blocks of any length, r_t and dw_t are the
+// tokens' own.  w = beta r and dx = beta dw are cut into bf16 terms once, in LDS.  Waves 0 .. 3 form what the state before
+// the block gives to dq and dk, 32 key channels each (rows: channels, a lane's token is lane % 32); waves 4 .. 7 what its
+// gradient behind the block gives to dk, and the 32 x 32 tiles of P, P^T and G + G^T, which all reach the first four through
+// LDS in the place of the terms.
 
 struct LdsGrad {
-    unsigned char k[kTile], q[kTile], o[kTile];
-    unsigned char w[3][kTile], x[3][kTile];  // terms of w and dx; then the blocks of P, P^T, G + G^T
-    float vec[kGdnVec / 4];
-    float sums[8][kGC];   // q.dq of each wave's channels
-    float vdv[kGC];
-    float end[8];         // <dS, S_after>, a wave's share
+    unsigned char k[kGB * 256], q[kGB * 256], o[kGB * 256];
+    unsigned char w[3][kGB * 256], x[3][kGB * 256];  // terms of w and dx; then the matrices and dk's share
+    float bh[kGB], bl[kGB], from[kGB], tail[kGB];    // running sums of log2 decays as pairs, and their factors
+    float last;
+    float sums[4][kGB];   // q.dq of each wave's channels
+    float vdv[kGB];
+    float end[4];         // <dS, S_after>, a wave's share
 };
+// Steps of the matrices in LDS (3 KiB each).  P: columns tokens t, contraction sources, steps 0 .. 1 + 2 t; P^T: columns sources s,
+// contraction tokens, steps 2 s .. 3; G + G^T all.
+constexpr int kGradP = 0, kGradPT = 6, kGradG = 12, kGradMats = 20;
 
-__device__ __forceinline__ Terms row_terms(const unsigned char (*t)[kTile], const Lanes &ln, int r, int p)
+__device__ __forceinline__ Terms row_terms(const unsigned char (*t)[kGB * 256], const Lanes &ln, int x, int block)
 {
-    return Terms{row_frag(t[0], ln, r, p), row_frag(t[1], ln, r, p), row_frag(t[2], ln, r, p)};
+    return Terms{row_frag(t[0], ln, x, block), row_frag(t[1], ln, x, block), row_frag(t[2], ln, x, block)};
 }
 
 __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) LdsGrad s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m = lane & 15, g = lane >> 4;
-    const int64_t slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
+    LdsGrad &s = *reinterpret_cast<LdsGrad *>(raw);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, h = lane >> 5;
+    const int64_t block = blockIdx.x / (uint32_t)a.H, head = blockIdx.x - (uint32_t)block * (uint32_t)a.H;
     if (a.status && *a.status != 0)
         return;
-    const int64_t seq = last_at_most(a.N, slot, [&](int64_t i) { return slot_of(uniform(seq_begin(a, i)), i); });
-    const int64_t begin = uniform(seq_begin(a, seq)), c = slot - slot_of(begin, seq),
-                  rest = uniform(seq_begin(a, seq + 1)) - begin - c * kGC;
+    const int64_t seq = last_at_most(a.N, block, [&](int64_t i) { return block_of(uniform(seq_begin(a, i)), i); });
+    const int64_t begin = uniform(seq_begin(a, seq)), c = block - block_of(begin, seq),
+                  rest = uniform(seq_begin(a, seq + 1)) - begin - c * kGB;
     if (rest <= 0)
         return;
-    const int len = (int)(rest < kGC ? rest : kGC);
-    const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGC, at = slot * a.H + h;
-    const int64_t tok0 = row * a.T + t0;
-    auto head_of = [&](const GdnTensor &x) { return head_base(x, row, h); };
-    tile_fetch(s.k, a.k, head_of(a.k), t0, len, wave, lane);
-    tile_fetch(s.q, a.q, head_of(a.q), t0, len, wave, lane);
-    tile_fetch(s.o, a.dout, head_of(a.dout), t0, len, wave, lane);
-    if (wave < 2)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(a.rec + at * a.rec_bytes + kGdnMat, kGdnVec),
-                                                 (lds_void *)(s.vec + 256 * wave), 16, 1024 * wave + 16 * lane, 0, 0, 0);
-    // the states' columns of this wave: lane = key channel, 4 value rows 16 n + 4 g ..
-    const float *sb = a.before + at * kD * kD + 16 * wave + m, *sd = a.dafter + at * kD * kD + 16 * wave + m;
-    f32x4 S[8], dS[8];
+    const int len = (int)(rest < kGB ? rest : kGB);
+    const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGB, tok0 = row * a.T + t0;
+    const int64_t slot = slot_of(begin, seq) + 2 * c;
+    tile_fetch<8, kGB>(s.k, a.k, head_base(a.k, row, head), t0, len, wave, lane);
+    tile_fetch<8, kGB>(s.q, a.q, head_base(a.q, row, head), t0, len, wave, lane);
+    tile_fetch<8, kGB>(s.o, a.dout, head_base(a.dout, row, head), t0, len, wave, lane);
+    // the state's columns of this wave: lane = key channel, elements 8 x + j: value row 16 x + 8 h + j
+    const int kg = wave & 3, kc = 32 * kg + column_of<true>(l32);
+    const int64_t at = (block * a.H + head) * kD * kD;
+    // one lane offset for all of them, the rest sits in the instruction
+    const __amdgpu_buffer_rsrc_t rs = rsrc(a.before + at, kGdnStateBytes), rd = rsrc(a.dafter + at, kGdnStateBytes);
+    const int lane_at = 4 * (8 * h * kD + kc);
+    auto element = [&](__amdgpu_buffer_rsrc_t r, int i) {
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, 4 * kD * (16 * (i >> 3) + (i & 7)), 0));
+    };
+    float S[64];
+    if (wave < 4) {
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+        for (int i = 0; i < 64; ++i)
+            S[i] = element(rs, i);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            S[n][i] = sb[(16 * n + 4 * g + i) * kD];
+        for (int i = 0; i < 64; ++i)
+            S[i] = element(rd, i);
+    }
+    if (wave == 7) {
+        const float dec = lane < len ? a.decay[(tok0 + lane) * a.H + head] : 0.0f;
+        const double b = running_sum64((double)clamp_decay(dec) * kLog2e64), last = of_lane(b, 63);
+        s.bh[lane] = (float)b;
+        s.bl[lane] = (float)(b - (double)(float)b);
+        s.from[lane] = __builtin_amdgcn_exp2f((float)b);
+        s.tail[lane] = __builtin_amdgcn_exp2f((float)(last - b));
+        if (lane == 0)
+            s.last = __builtin_amdgcn_exp2f((float)last);
+    }
     // rows of r and dw: thread = token tid / 8, value channels 16 (tid % 8) ..
     {
         const int t = tid >> 3, v0 = 16 * (tid & 7);
-        const float *pr = a.res + at * kGC * kD + t * kD + v0, *pw = a.dwrite + at * kGC * kD + t * kD + v0;
-        const float be = t < len ? a.beta[(tok0 + t) * a.H + h] : 0.0f;
-        const uint16_t *pv = head_of(a.v) + (t0 + (t < len ? t : 0)) * a.v.st + v0;
+        const bool on = t < len;
+        const int64_t from = ((slot + (t >> 5)) * a.H + head) * kGC * kD + (t & 31) * kD + v0;  // a chunk without tokens has no rows
+        const float *pr = a.res + (on ? from : (slot * a.H + head) * kGC * kD), *pw = a.dwrite + (pr - a.res);
+        const float be = on ? a.beta[(tok0 + t) * a.H + head] : 0.0f;
+        const uint16_t *pv = head_base(a.v, row, head) + (t0 + (on ? t : 0)) * a.v.st + v0;
         const u32x4 vv[2] = {*reinterpret_cast<const u32x4 *>(pv), *reinterpret_cast<const u32x4 *>(pv + 8)};
         float db = 0.0f, vd = 0.0f;
 #pragma unroll
@@ -1334,6 +1278,8 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
             for (int e = 0; e < 2; ++e) {
                 r[e] = *reinterpret_cast<const f32x4 *>(pr + 8 * hf + 4 * e);
                 d[e] = *reinterpret_cast<const f32x4 *>(pw + 8 * hf + 4 * e);
+                if (!on)
+                    r[e] = d[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 x[e] = d[e] * be;
                 const f32x4 v4 = widen4(u32x2{vv[hf][2 * e], vv[hf][2 * e + 1]});
 #pragma unroll
@@ -1343,18 +1289,17 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
                 }
                 r[e] *= be;
             }
-            const int piece = 2 * (tid & 7) + hf, to = t * 256 + ((piece ^ swz(t)) << 4);
-            Terms y;
-            cut8(r[0], r[1], y);
+            const int to = t * 256 + (((2 * (tid & 7) + hf) ^ swz(t)) << 4);
+            Terms y = cut8(r[0], r[1]);
             *reinterpret_cast<u32x4 *>(s.w[0] + to) = y.h;
             *reinterpret_cast<u32x4 *>(s.w[1] + to) = y.m;
             *reinterpret_cast<u32x4 *>(s.w[2] + to) = y.l;
-            cut8(x[0], x[1], y);
+            y = cut8(x[0], x[1]);
             *reinterpret_cast<u32x4 *>(s.x[0] + to) = y.h;
             *reinterpret_cast<u32x4 *>(s.x[1] + to) = y.m;
             *reinterpret_cast<u32x4 *>(s.x[2] + to) = y.l;
-            if (t < len)
-                *reinterpret_cast<u32x4 *>(a.dv + ((tok0 + t) * a.H + h) * kD + v0 + 8 * hf) = y.h;
+            if (on)
+                *reinterpret_cast<u32x4 *>(a.dv + ((tok0 + t) * a.H + head) * kD + v0 + 8 * hf) = y.h;
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
@@ -1362,180 +1307,245 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
             vd += __shfl_xor(vd, o);
         }
         if ((tid & 7) == 0) {
-            s.vdv[t] = vd;
-            if (t < len)
-                a.dbeta[(tok0 + t) * a.H + h] = db;
+            s.vdv[t] = on ? vd : 0.0f;
+            if (on)
+                a.dbeta[(tok0 + t) * a.H + head] = db;
         }
     }
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            dS[n][i] = sd[(16 * n + 4 * g + i) * kD];
     arrive();
     const Lanes ln(lane);
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    // the states' shares
-    f32x4 dq[4], dk[4];
-    float dot = 0.0f;
-    {
-        Terms cs[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            cut8(S[2 * x], S[2 * x + 1], cs[x]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            dq[r] = dk[r] = zero;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                dq[r] = mfma3(cs[x], row_frag(s.o, ln, r, x), dq[r]);
-                dk[r] = mfma6(cs[x], row_terms(s.x, ln, r, x), dk[r]);
-            }
-            dq[r] *= s.vec[kVOut + 16 * r + m];
-            dk[r] *= -s.vec[kVHead + 16 * r + m];
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            dot = fmaf(S[n][i], dS[n][i], dot);
-    dot *= s.vec[kVLast];
-    // channels 16 w + 4 g .. of token 16 r + m
-    auto mine = [&](const unsigned char *tile, int r) {
-        return widen4(lds_b64(tile + 4096 * r + (ln.row ^ (32 * wave))));
+    auto terms_of = [&](int x) {
+        return cut8(f32x4{S[8 * x], S[8 * x + 1], S[8 * x + 2], S[8 * x + 3]},
+                    f32x4{S[8 * x + 4], S[8 * x + 5], S[8 * x + 6], S[8 * x + 7]});
     };
-    {
-        Terms cs[4];
+    // 16 channels 32 kg + 16 h .. of token 32 th + lane % 32
+    auto mine = [&](const unsigned char *tile, int th, float *y) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            cut8(dS[2 * x], dS[2 * x + 1], cs[x]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            f32x4 y = zero;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                y = mfma6(cs[x], row_terms(s.w, ln, r, x), y);
-            y *= s.vec[kVTail + 16 * r + m];
-            const f32x4 k4 = mine(s.k, r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dot = fmaf(y[i], k4[i], dot);
-            dk[r] += y;
-        }
-    }
-    // blocks of this wave: columns of tile cr, contraction 32 ck ..
-    const int cr = wave >> 1, ck = wave & 1;
-    auto within = [&](int t, int u) {  // e^{b_t - b_u} for u <= t
-        const float d = (s.vec[kVSum + t] - s.vec[kVSum + u]) + (s.vec[kVSum + 64 + t] - s.vec[kVSum + 64 + u]);
-        return u <= t ? __builtin_amdgcn_exp2f(d) : 0.0f;
-    };
-    Terms pa, pb, gs;
-    {
-        const int col = 16 * cr + m;
-        f32x4 fa[2], fb[2], fg[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int rt = 2 * ck + hf;  // row tile
-            f32x4 ya = zero, yb = zero, g1 = zero, g2 = zero;
-            if (rt <= cr) {  // rows are sources, columns out tokens
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const Terms wt = row_terms(s.w, ln, rt, x);
-                    ya = mfma3(wt, row_frag(s.o, ln, cr, x), ya);
-                    g1 = mfma6(wt, row_terms(s.x, ln, cr, x), g1);
-                }
-            }
-            if (rt >= cr) {  // rows are out tokens, columns sources
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const Terms wt = row_terms(s.w, ln, cr, x);
-                    yb = mfma3(row_frag(s.o, ln, rt, x), wt, yb);
-                    g2 = mfma6(row_terms(s.x, ln, rt, x), wt, g2);
-                }
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int t = 32 * th + l32, piece = 4 * kg + 2 * h + e;
+            const u32x4 u = *reinterpret_cast<const u32x4 *>(tile + t * 256 + ((piece ^ swz(t)) << 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int rw = 16 * rt + 4 * g + i;
-                const float lo = within(col, rw), hi = within(rw, col);
-                fa[hf][i] = rw <= col ? a.scale * lo * ya[i] : 0.0f;
-                fb[hf][i] = rw >= col ? a.scale * hi * yb[i] : 0.0f;
-                fg[hf][i] = rw < col ? -lo * g1[i] : rw > col ? -hi * g2[i] : 0.0f;
+                y[8 * e + 2 * i] = lo_f(u[i]);
+                y[8 * e + 2 * i + 1] = hi_f(u[i]);
             }
         }
-        cut8(fa[0], fa[1], pa);
-        cut8(fb[0], fb[1], pb);
-        cut8(fg[0], fg[1], gs);
-    }
-    __syncthreads();  // the terms of w and dx are read by no one
-    unsigned char *mp = s.w[0], *mq = mp + 8 * 3 * 1024, *mg = mq + 8 * 3 * 1024;  // 72 KiB of their 96
-    auto put = [&](unsigned char *mat, const Terms &t) {
-        u32x4 *p = reinterpret_cast<u32x4 *>(mat + wave * 3072 + lane * 16);
-        p[0] = t.h;
-        p[64] = t.m;
-        p[128] = t.l;
     };
-    put(mp, pa);
-    put(mq, pb);
-    put(mg, gs);
+    unsigned char *mats = s.w[0], *share = mats + kGradMats * 3072;
+    f32x16 dq[2], dk[2];
+    if (wave < 4) {
+        dq[0] = dq[1] = dk[0] = dk[1] = zero16();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const Terms c8 = terms_of(x);
+#pragma unroll
+            for (int th = 0; th < 2; ++th) {
+                dq[th] = mfma3(c8, row_frag(s.o, ln, x, th), dq[th]);
+                dk[th] = mfma6(c8, row_terms(s.x, ln, x, th), dk[th]);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one step at a time: more of them in flight do not fit the registers
+        }
+#pragma unroll
+        for (int th = 0; th < 2; ++th) {
+            dq[th] *= a.scale * s.from[32 * th + l32];
+            dk[th] *= -s.from[32 * th + l32];
+        }
+        __syncthreads();
+    } else {
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            dot = fmaf(S[i], element(rs, i), dot);
+        dot *= s.last;
+        dk[0] = dk[1] = zero16();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const Terms c8 = terms_of(x);
+#pragma unroll
+            for (int th = 0; th < 2; ++th)
+                dk[th] = mfma6(c8, row_terms(s.w, ln, x, th), dk[th]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int th = 0; th < 2; ++th) {
+            dk[th] *= s.tail[32 * th + l32];
+            float k16[16];
+            mine(s.k, th, k16);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                dot = fmaf(dk[th][i], k16[i], dot);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1)
+            dot += __shfl_xor(dot, o);
+        if (lane == 0)
+            s.end[kg] = dot;
+        // The tiles: rows of row tile rt (a lane's 16 in the order of a D tile), columns of column tile ct.  e^{b_t - b_u} for u <= t
+        // is formed where it is used.
+        auto tile = [&](int rt, int ct, const f32x16 &d, float f, bool low, f32x16 y) {  // low: rows are the sources
+            const float ch = s.bh[32 * ct + l32], cl = s.bl[32 * ct + l32];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const f32x4 rh = *reinterpret_cast<const f32x4 *>(&s.bh[32 * rt + 8 * n + 4 * h]);
+                const f32x4 rl = *reinterpret_cast<const f32x4 *>(&s.bl[32 * rt + 8 * n + 4 * h]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rw = 32 * rt + 8 * n + 4 * h + i, cl_ = 32 * ct + l32;
+                    const float b = low ? (ch - rh[i]) + (cl - rl[i]) : (rh[i] - ch) + (rl[i] - cl);
+                    const bool on = low ? rw <= cl_ : rw >= cl_;
+                    const float z = d[4 * n + i] * (f * __builtin_amdgcn_exp2f(on ? b : 0.0f));
+                    // P with its diagonal; G without, one triangle at a time
+                    y[4 * n + i] = (f < 0.0f ? on && rw != cl_ : on) ? z : y[4 * n + i];
+                }
+            }
+            return y;
+        };
+        f32x16 put[3];
+        int where[3] = {-1, -1, -1};
+        auto keep = [&](int n, int step, const f32x16 &y) {  // 2 steps each, written when the terms in LDS are done with
+            put[n] = y;
+            where[n] = step;
+        };
+        // P and P^T are scaled by a factor above 0 and G by -1; with a scale of 0 or below the sign is taken apart
+        auto p_low = [&](int rt, int ct) {
+            f32x16 d = zero16();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                d = mfma3(row_terms(s.w, ln, x, rt), row_frag(s.o, ln, x, ct), d);
+                if (x & 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+            return tile(rt, ct, d * a.scale, 1.0f, true, zero16());
+        };
+        auto p_high = [&](int rt, int ct) {
+            f32x16 d = zero16();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                d = mfma3(row_frag(s.o, ln, x, rt), row_terms(s.w, ln, x, ct), d);
+                if (x & 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+            return tile(rt, ct, d * a.scale, 1.0f, false, zero16());
+        };
+        auto g_low = [&](int rt, int ct, const f32x16 &y) {
+            f32x16 d = zero16();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                d = mfma6(row_terms(s.w, ln, x, rt), row_terms(s.x, ln, x, ct), d);
+                if (x & 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+            return tile(rt, ct, d, -1.0f, true, y);
+        };
+        auto g_high = [&](int rt, int ct, const f32x16 &y) {
+            f32x16 d = zero16();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                d = mfma6(row_terms(s.x, ln, x, rt), row_terms(s.w, ln, x, ct), d);
+                if (x & 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+            return tile(rt, ct, d, -1.0f, false, y);
+        };
+        if (kg < 2) {  // the diagonal tiles of G + G^T and of P
+            keep(0, kGradG + 4 * kg + 2 * kg, g_high(kg, kg, g_low(kg, kg, zero16())));
+            keep(1, kGradP + (kg ? 4 : 0), p_low(kg, kg));
+        } else if (kg == 2) {
+            keep(0, kGradG + 4, g_low(0, 1, zero16()));
+            keep(1, kGradG + 2, g_high(1, 0, zero16()));
+            keep(2, kGradP + 2, p_low(0, 1));
+        } else {
+            keep(0, kGradPT, p_high(0, 0));
+            keep(1, kGradPT + 2, p_high(1, 0));
+            keep(2, kGradPT + 4, p_high(1, 1));
+        }
+        __syncthreads();  // the terms of w and dx are read by no one
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+            if (where[n] >= 0) {
+                store_terms(mats, where[n], lane, cut8(put[n], 0));
+                store_terms(mats, where[n] + 1, lane, cut8(put[n], 1));
+            }
+        f32x4 *y = reinterpret_cast<f32x4 *>(share + kg * 8192) + lane;
+#pragma unroll
+        for (int th = 0; th < 2; ++th)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                y[64 * (4 * th + n)] = f32x4{dk[th][4 * n], dk[th][4 * n + 1], dk[th][4 * n + 2], dk[th][4 * n + 3]};
+    }
     __syncthreads();
-    auto block = [&](const unsigned char *mat, int r, int ks) {
-        const u32x4 *p = reinterpret_cast<const u32x4 *>(mat + (2 * r + ks) * 3072 + lane * 16);
-        return Terms{p[0], p[64], p[128]};
-    };
+    if (wave < 4) {
+        const f32x4 *y = reinterpret_cast<const f32x4 *>(share + kg * 8192) + lane;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        const u32x4 kc = col_frag(s.k, ln, wave, ks), qc = col_frag(s.q, ln, wave, ks);
+        for (int th = 0; th < 2; ++th)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (ks <= r / 2)
-                dq[r] = mfma3(kc, block(mp, r, ks), dq[r]);
-            if (ks >= r / 2)
-                dk[r] = mfma3(qc, block(mq, r, ks), dk[r]);
-            dk[r] = mfma3(kc, block(mg, r, ks), dk[r]);
+            for (int n = 0; n < 4; ++n) {
+                const f32x4 z = y[64 * (4 * th + n)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dk[th][4 * n + i] += z[i];
+            }
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {  // 16 tokens each of the contraction
+            const u32x4 kc4 = col_frag(s.k + 8192 * (st >> 1), ln.out, kg, st & 1);
+            const u32x4 qc4 = col_frag(s.q + 8192 * (st >> 1), ln.out, kg, st & 1);
+#pragma unroll
+            for (int th = 0; th < 2; ++th) {
+                if (st < 2 + 2 * th)
+                    dq[th] = mfma3(kc4, load_terms(mats, kGradP + 2 * th + st, lane), dq[th]);
+                if (st >= 2 * th)
+                    dk[th] = mfma3(qc4, load_terms(mats, kGradPT + 2 * th + st, lane), dk[th]);
+                dk[th] = mfma3(kc4, load_terms(mats, kGradG + 4 * th + st, lane), dk[th]);
+            }
         }
-    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const f32x4 q4 = mine(s.q, r);
-        float y = dq[r][0] * q4[0];
+        for (int th = 0; th < 2; ++th) {
+            float q16[16], y1 = 0.0f;
+            mine(s.q, th, q16);
 #pragma unroll
-        for (int i = 1; i < 4; ++i)
-            y = fmaf(dq[r][i], q4[i], y);
-        y += __shfl_xor(y, 16);
-        y += __shfl_xor(y, 32);
-        if (g == 0)
-            s.sums[wave][16 * r + m] = y;
-        const int t = 16 * r + m;
-        if (t < len) {
-            const int64_t to = ((tok0 + t) * a.H + h) * kD + 16 * wave + 4 * g;
+            for (int i = 0; i < 16; ++i)
+                y1 = fmaf(dq[th][i], q16[i], y1);
+            y1 += __shfl_xor(y1, 32);
+            const int t = 32 * th + l32;
+            if (h == 0)
+                s.sums[kg][t] = y1;
+            if (t >= len)
+                continue;
+            const int64_t to = ((tok0 + t) * a.H + head) * kD + 32 * kg + 16 * h;
             if (a.dq_h) {
-                *reinterpret_cast<f32x4 *>(a.dq_h + to) = dq[r];
-                *reinterpret_cast<f32x4 *>(a.dk_h + to) = dk[r];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    reinterpret_cast<f32x4 *>(a.dq_h + to)[n] = f32x4{dq[th][4 * n], dq[th][4 * n + 1], dq[th][4 * n + 2], dq[th][4 * n + 3]};
+                    reinterpret_cast<f32x4 *>(a.dk_h + to)[n] = f32x4{dk[th][4 * n], dk[th][4 * n + 1], dk[th][4 * n + 2], dk[th][4 * n + 3]};
+                }
             } else {
-                *reinterpret_cast<u32x2 *>(a.dq + to) = u32x2{pack2(dq[r][0], dq[r][1]), pack2(dq[r][2], dq[r][3])};
-                *reinterpret_cast<u32x2 *>(a.dk + to) = u32x2{pack2(dk[r][0], dk[r][1]), pack2(dk[r][2], dk[r][3])};
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    u32x4 x, z;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = pack2(dq[th][8 * n + 2 * e], dq[th][8 * n + 2 * e + 1]);
+                        z[e] = pack2(dk[th][8 * n + 2 * e], dk[th][8 * n + 2 * e + 1]);
+                    }
+                    reinterpret_cast<u32x4 *>(a.dq + to)[n] = x;
+                    reinterpret_cast<u32x4 *>(a.dk + to)[n] = z;
+                }
             }
         }
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        dot += __shfl_xor(dot, o);
-    if (lane == 0)
-        s.end[wave] = dot;
     __syncthreads();
     if (wave != 0)
         return;
     float qd = 0.0f, end = 0.0f;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
+    for (int n = 0; n < 4; ++n) {
         qd += s.sums[n][lane];
         end += s.end[n];
     }
     const double each = lane < len ? (double)qd - (double)s.vdv[lane] : 0.0;
-    const double upto = running_sum(each), total = last_lane(upto);  // by all lanes, those behind the chunk too
+    const double upto = running_sum64(each), total = of_lane(upto, 63);  // by all lanes, those behind the block too
     if (lane < len) {
-        const int64_t to = (tok0 + lane) * a.H + h;
+        const int64_t to = (tok0 + lane) * a.H + head;
         const float gd = a.decay[to];
         a.ddecay[to] = gd > kLowest && gd <= 0.0f ? (float)((total - upto) + each + (double)end) : 0.0f;
     }
@@ -1692,23 +1702,18 @@ hipError_t launch_check(const GdnArgs &a, int32_t *status, hipStream_t s)
 
 hipError_t gdn_launch_fwd(const GdnArgs &a, int32_t *status, hipStream_t s)
 {
-    hipError_t e = launch_check(a, status, s);
-    if (e == hipSuccess && a.T > 0) {
-        hipLaunchKernelGGL(gdn_prep_kernel<false>, dim3((unsigned)(a.slots * a.H)), dim3(256), 0, s, a);
-        e = hipGetLastError();
-    }
-    const unsigned grid = (unsigned)(a.rows * a.P * a.H);
-    if (e == hipSuccess && a.P > 1) {
-        hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), sizeof(LdsWalk), s, a);
-        e = hipGetLastError();
-        if (e == hipSuccess && a.P > 2) {
-            hipLaunchKernelGGL(gdn_scan_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
-            e = hipGetLastError();
-        }
-    }
+    const hipError_t e = launch_check(a, status, s);
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(gdn_out_kernel, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
+    const unsigned grid = (unsigned)(a.rows * a.P * a.H);
+    if (a.T > 0) {
+        hipLaunchKernelGGL(gdn_prep_kernel<false>, dim3((unsigned)cdiv(a.slots * a.H, kPrepWaves)), dim3(64 * kPrepWaves), 0, s, a);
+        if (a.P > 1)
+            hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
+        if (a.P > 2)
+            hipLaunchKernelGGL(gdn_scan_kernel<false>, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
+    }
+    hipLaunchKernelGGL(gdn_out_kernel, dim3(grid), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
     return hipGetLastError();
 }
 
@@ -1717,22 +1722,22 @@ hipError_t gdn_launch_bwd(const GdnArgs &a, int32_t *status, hipStream_t s)
     hipError_t e = launch_check(a, status, s);
     if (e != hipSuccess)
         return e;
-    const unsigned grid = (unsigned)(a.rows * a.P * a.H), recs = (unsigned)(a.slots * a.H);
+    const unsigned grid = (unsigned)(a.rows * a.P * a.H), scan = (unsigned)(8 * a.rows * a.H);
     if (a.T > 0) {
-        hipLaunchKernelGGL(gdn_prep_kernel<true>, dim3(recs), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(gdn_prep_kernel<true>, dim3((unsigned)cdiv(a.slots * a.H, kPrepWaves)), dim3(64 * kPrepWaves), 0, s, a);
         if (a.P > 1) {
-            hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(512), sizeof(LdsWalk), s, a);
+            hipLaunchKernelGGL(gdn_cut_kernel, dim3(grid, 2), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
             if (a.P > 2)
-                hipLaunchKernelGGL(gdn_scan_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
-            hipLaunchKernelGGL(gdn_back_kernel<true>, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
+                hipLaunchKernelGGL(gdn_scan_kernel<false>, dim3(scan), dim3(512), 0, s, a);
+            hipLaunchKernelGGL(gdn_back_kernel<true>, dim3(grid), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
             if (a.P > 2)
-                hipLaunchKernelGGL(gdn_scan_back_kernel, dim3((unsigned)(8 * a.rows * a.H)), dim3(512), 0, s, a);
+                hipLaunchKernelGGL(gdn_scan_kernel<true>, dim3(scan), dim3(512), 0, s, a);
         }
-        hipLaunchKernelGGL(gdn_store_kernel, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
+        hipLaunchKernelGGL(gdn_store_kernel, dim3(grid), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
     }
-    hipLaunchKernelGGL(gdn_back_kernel<false>, dim3(grid), dim3(512), sizeof(LdsWalk), s, a);
+    hipLaunchKernelGGL(gdn_back_kernel<false>, dim3(grid), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
     if (a.T > 0)
-        hipLaunchKernelGGL(gdn_grad_kernel, dim3(recs), dim3(512), 0, s, a);
+        hipLaunchKernelGGL(gdn_grad_kernel, dim3((unsigned)(a.blocks * a.H)), dim3(512), sizeof(LdsGrad), s, a);
     e = hipGetLastError();
     if (e != hipSuccess || !a.dq_h || a.T == 0)
         return e;

@@ -57,9 +57,10 @@ bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
     L->plan = kda::gdn_plan(z.B, z.T, z.H, z.varlen, bwd);
     const kda::GdnPlan &p = L->plan;
     L->slots = z.B * z.T / kda::kGC + z.n_seq + 1;
-    // 256 threads for each record (backward 512), 512 for each segment and head, 4096 for each row and head
-    if (L->slots > (((int64_t)1 << (bwd ? 23 : 24)) - 8) / z.H || p.rows * p.P > (((int64_t)1 << 23) - 8) / z.H ||
-        (p.P > 1 && p.rows >= ((int64_t)1 << 20) / z.H))
+    L->blocks = z.B * z.T / kda::kGB + z.n_seq + 1;
+    // 64 threads for each record, 512 for each block, 256 for each segment and head, 4096 for each row and head
+    if (L->slots > (((int64_t)1 << 26) - 8) / z.H || (bwd && L->blocks > (((int64_t)1 << 23) - 8) / z.H) ||
+        p.rows * p.P > (((int64_t)1 << 24) - 8) / z.H || (p.P > 1 && p.rows >= ((int64_t)1 << 20) / z.H))
         return false;
     size_t off = kAlign;  // status word
     auto take = [&](size_t bytes) {
@@ -69,7 +70,7 @@ bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
     };
     L->off_rec = L->off_seg = L->off_phi = L->off_keep = L->off_dseg = 0;
     L->off_before = L->off_dafter = L->off_res = L->off_dwrite = L->off_dq = L->off_dk = 0;
-    const size_t recs = z.T > 0 ? (size_t)L->slots * (size_t)z.H : 0;
+    const size_t recs = z.T > 0 ? (size_t)L->slots * (size_t)z.H : 0, blocks = z.T > 0 ? (size_t)L->blocks * (size_t)z.H : 0;
     L->off_rec = take(recs * (bwd ? kda::kGdnRecBwd : kda::kGdnRecFwd));
     if (p.P > 1) {
         const size_t segs = (size_t)p.rows * (size_t)p.P * (size_t)z.H * kda::kGdnStateBytes;
@@ -78,8 +79,8 @@ bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
         (bwd ? L->off_dseg : L->off_keep) = take(segs);
     }
     if (bwd) {
-        L->off_before = take(recs * kda::kGdnStateBytes);
-        L->off_dafter = take(recs * kda::kGdnStateBytes);
+        L->off_before = take(blocks * kda::kGdnStateBytes);
+        L->off_dafter = take(blocks * kda::kGdnStateBytes);
         L->off_res = take(recs * kda::kGC * kD * sizeof(float));
         L->off_dwrite = take(recs * kda::kGC * kD * sizeof(float));
         if (z.Hk != z.H) {
@@ -199,6 +200,7 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
         a->P = lay.plan.P;
         a->len = lay.plan.len;
         a->slots = lay.slots;
+        a->blocks = lay.blocks;
         a->rec = w + lay.off_rec;
         a->rec_bytes = kda::kGdnRecFwd;
         if (a->P > 1) {
@@ -348,6 +350,7 @@ kda_status kda_gdn_bwd(const void *q, const void *k, const void *v, const float 
     a.rec = w + lay.off_rec;
     a.rec_bytes = kda::kGdnRecBwd;
     a.slots = lay.slots;
+    a.blocks = lay.blocks;
     if (a.P > 1) {
         a.seg = f32(lay.off_seg);
         a.phi = f32(lay.off_phi);

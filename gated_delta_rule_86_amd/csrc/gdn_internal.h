@@ -11,19 +11,20 @@
 
 namespace kda {
 
-constexpr int kGC = 64;                    // tokens per chunk
-constexpr int64_t kGdnCUs = 256;           // one workgroup of a walk on each
+constexpr int kGC = 32;                    // tokens per chunk
+constexpr int kGB = 64;                    // tokens per block of the backward pass: one state is kept for two chunks
+constexpr int64_t kGdnSlots = 512;         // workgroups of a walk that run at once: two on each of 256 CUs
 constexpr size_t kGdnStateBytes = (size_t)kD * kD * sizeof(float);
-constexpr int64_t kGdnMinSeg = 4 * kGC;    // shortest segment that a cut leaves, in tokens
+constexpr int64_t kGdnMinSeg = 256;        // shortest segment that a cut leaves, in tokens
 
 // Record of one (chunk, head) in the workspace, bytes: operands of the walks, in the order of their lanes.
-//   forward:   T' | factors | A' | 2 KiB unused
-//   backward:  T' | factors | T^T | A^T | 2 KiB unused   (A without beta)
-// Each matrix is 6 blocks of 16 x 32 (the other two of the triangle are zero) of three bf16 terms, 1 KiB a block.
-constexpr int kGdnMat = 6 * 3 * 1024;
-constexpr int kGdnVec = 2048;
-constexpr int kGdnRecFwd = 2 * kGdnMat + kGdnVec + 2048;
-constexpr int kGdnRecBwd = 3 * kGdnMat + kGdnVec + 2048;
+//   forward:   T' | factors | A'
+//   backward:  T' | factors | T^T | A^T   (A without beta)
+// Each matrix is 32 x 32 in three bf16 terms.
+constexpr int kGdnMat = 2 * 3 * 1024;
+constexpr int kGdnVec = 1024;
+constexpr int kGdnRecFwd = 2 * kGdnMat + kGdnVec;
+constexpr int kGdnRecBwd = 3 * kGdnMat + kGdnVec;
 
 // The tokens of a batch row (the one row of a packed batch) are cut into P segments of `len` tokens whatever the
 // sequences in it.  A chunk belongs to the segment that holds its first token.  Where a sequence's chunks go on in the
@@ -33,27 +34,35 @@ struct GdnPlan {
     int64_t rows, P, len;
 };
 
-// Time of a pass in chunks of the forward pass's output walk (one workgroup on a CU): the walks in rounds of kGdnCUs, and
-// with a cut the shares and transitions of all but the last segment, the scans' steps and more launches.
+// Time of `groups` workgroups of `chunks` chunks each, in chunks of a full chip: rounds of kGdnSlots; a workgroup alone on
+// its CU takes about 0.6 of the time that two take side by side.
+inline double gdn_rounds(int64_t groups, double chunks)
+{
+    const double round = (double)cdiv(groups, kGdnSlots) * chunks;
+    return groups <= kGdnSlots / 2 ? 0.6 * round : round;
+}
+
+// The cut that takes the least time: the walks, and with a cut the shares and transitions of all but the last segment, the
+// scans' steps and more launches.
 inline GdnPlan gdn_plan(int64_t B, int64_t T, int64_t H, bool varlen, bool bwd)
 {
     GdnPlan p;
     p.rows = varlen ? 1 : B;
     p.P = 1;
-    p.len = T > 0 ? cdiv(T, kGC) * kGC : kGC;
+    p.len = T > 0 ? cdiv(T, kGB) * kGB : kGB;
     const int64_t chains = p.rows * H;
     int64_t most = T / kGdnMinSeg;
-    if (most > 2 * kGdnCUs / chains)
-        most = 2 * kGdnCUs / chains;
-    const double walks = bwd ? 1.6 : 1.0;
-    double best = walks * (double)cdiv(chains, kGdnCUs) * ((double)(p.len / kGC) + 1.0);
-    for (int64_t P = 2; P <= most; ++P) {
-        const int64_t len = cdiv(cdiv(T, P), kGC) * kGC, got = cdiv(T, len), n = len / kGC;
-        double cost = walks * (double)cdiv(chains * got, kGdnCUs) + 0.7 * (double)cdiv(2 * chains * (got - 1), kGdnCUs);
-        if (bwd)
-            cost += 0.9 * (double)cdiv(chains * (got - 1), kGdnCUs);
-        cost = cost * ((double)n + 1.0) + (bwd ? 2.0 : 1.0) * (0.5 * (double)(got - 2) + 2.0);
-        if (got > 1 && cost < best) {
+    if (most > 2 * kGdnSlots / chains)
+        most = 2 * kGdnSlots / chains;
+    double best = 0.0;
+    for (int64_t P = 1; P <= (most > 1 ? most : 1); ++P) {
+        const int64_t len = T > 0 ? cdiv(cdiv(T, P), kGB) * kGB : kGB, got = T > 0 ? cdiv(T, len) : 1;
+        const double n = (double)(len / kGC) + 2.0;
+        double cost = gdn_rounds(chains * got, bwd ? 1.7 * n : n);
+        if (got > 1)
+            cost += gdn_rounds(2 * chains * (got - 1), 0.65 * n) + (bwd ? gdn_rounds(chains * (got - 1), 1.0 * n) : 0.0) +
+                    (bwd ? 2.0 : 1.0) * (0.3 * (double)got + 2.0);
+        if (P == 1 || cost < best) {
             best = cost;
             p.P = got;
             p.len = len;
@@ -81,7 +90,7 @@ struct GdnArgs {
     void *fin;
     int init_dt, fin_dt;
     unsigned char *rec;          // [slots][H] records
-    int64_t slots, rec_bytes;
+    int64_t slots, blocks, rec_bytes;
     float *seg;                  // [rows * P][H]: state at a segment's start, of the sequence that crosses it
     float *phi;                  // [rows * P][H]
     float *keep;                 // [rows * P][H]: initial state of the sequence that leaves the segment (in place), or NULL
@@ -90,8 +99,8 @@ struct GdnArgs {
     const float *dfin;           // dL/dfinal_state or NULL
     float *dinit;                // dL/dinitial_state or NULL
     float *dseg;                 // [rows * P][H]: dL/dS at a segment's end, of the sequence that goes on behind it
-    float *before, *dafter;      // [slots][H] states before each chunk, dL/dS after it
-    float *res, *dwrite;         // [slots][H][64][128]: residuals r_t, and dL/d(beta r)_t
+    float *before, *dafter;      // [blocks][H] states before each block, dL/dS after it
+    float *res, *dwrite;         // [slots][H][32][128]: residuals r_t, and dL/d(beta r)_t
     uint16_t *dq, *dk, *dv;
     float *dq_h, *dk_h;          // fp32 [B, T, H, 128] when q/k heads are shared, else NULL
     float *ddecay, *dbeta;
@@ -99,7 +108,7 @@ struct GdnArgs {
 
 struct GdnLayout {
     GdnPlan plan;
-    int64_t slots;
+    int64_t slots, blocks;
     size_t off_rec, off_seg, off_phi, off_keep;
     size_t off_dseg, off_before, off_dafter, off_res, off_dwrite, off_dq, off_dk;
     size_t total;

@@ -419,7 +419,7 @@ size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, i
  *             status word of this workspace too).
  * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; out and bf16 final states are
  * rounded once.  A value that is not finite (or a NaN gate) reaches its own sequence and head alone, from the first token of its
- * chunk of 64 tokens on, and may last.  Deterministic: fixed summation orders, no atomics.
+ * chunk of 32 tokens on, and may last.  Deterministic: fixed summation orders, no atomics.
  * Errors: KDA_ERR_NULL, _SHAPE (also sizes whose launch would hold 2^32 threads), _HEAD_DIM, _DTYPE, _SCALE, _ALIGN,
  * _WORKSPACE, _CU_SEQLENS, _HIP, _ALIAS, _HEADS, _STRIDE.
  */
@@ -442,7 +442,7 @@ kda_status kda_gdn_fwd_recurrent(const void *q, const void *k, const void *v, co
                                  size_t workspace_bytes, void *stream);
 
 /*
- * kda_gdn_fwd_workspace_size -- 256 bytes; 40 KiB per chunk of 64 tokens and head (at most T / 64 + 1 chunks for each sequence);
+ * kda_gdn_fwd_workspace_size -- 256 bytes; 13 KiB per chunk of 32 tokens and head (T / 32 chunks in all, and one for each sequence);
  * where rows are cut into segments that run in parallel, three fp32 128 x 128 states per segment and head.  A function
  * of (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes.
  */
@@ -470,8 +470,8 @@ kda_status kda_gdn_bwd(const void *q, const void *k, const void *v, const float 
                        void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * kda_gdn_bwd_workspace_size -- 256 bytes; 250 KiB per chunk of 64 tokens and head (at most T / 64 + 1 chunks for each
- * sequence); where rows are cut, three fp32 128 x 128 states per segment and head; with Hk < H two fp32 [B, T, H, 128].
+ * kda_gdn_bwd_workspace_size -- 256 bytes; 51 KiB per chunk of 32 tokens and head (T / 32 chunks in all, and one for each sequence) and
+ * 128 KiB per block of 64; where rows are cut, three fp32 128 x 128 states per segment and head; with Hk < H two fp32 [B, T, H, 128].
  * Returns 0 for invalid sizes.
  */
 size_t kda_gdn_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens);

@@ -96,22 +96,22 @@ def test_workspaces():
     assert gdn.workspace_size(2, 10, 1, 3, True) == 0 and gdn.bwd_workspace_size(1, 64, 2, 3) == 0
     shared, alone = gdn.bwd_workspace_size(4, 100, 2, 4), gdn.bwd_workspace_size(4, 100, 4, 4)
     assert shared - alone == 2 * 4 * 100 * 4 * 512
-    # a chunk's place is floor(begin / 64) + sequence + chunk: enough for any lengths
+    # a chunk's place is floor(begin / 32) + sequence + chunk, a block's the same with 64: enough for any lengths
     rng = np.random.default_rng(1)
-    for _ in range(200):
-        lens = rng.integers(0, 200, rng.integers(1, 20))
+    for n in range(400):
+        lens, C = rng.integers(0, 200, rng.integers(1, 20)), 32 << (n & 1)
         begin = np.concatenate([[0], lens.cumsum()])
-        seen = [begin[i] // 64 + i + c for i in range(len(lens)) for c in range(-(-lens[i] // 64))]
-        assert len(set(seen)) == len(seen) and (not seen or max(seen) < begin[-1] // 64 + len(lens) + 1)
+        seen = [begin[i] // C + i + c for i in range(len(lens)) for c in range(-(-lens[i] // C))]
+        assert len(set(seen)) == len(seen) and (not seen or max(seen) < begin[-1] // C + len(lens) + 1)
 
 
 @pytest.mark.parametrize("name", ["kda_gdn_fwd", "kda_gdn_bwd"])
 def test_launch_limits(name):
     """Sizes whose launch would hold 2^32 threads or more are refused by the checks, not by the runtime."""
     small = dict(h0=None, h0_dt=0, ht=None, ht_dt=0, ws=None, dht=None, dh0=None)
-    per = 1 << (24 if name == "kda_gdn_fwd" else 23)   # records times heads
-    assert gdn_call(name, B=1, T=(per // 4 - 16) * 64, H=4, Hk=1, **small) == 8
-    assert gdn_call(name, B=1, T=per // 4 * 64, H=4, Hk=1, **small) == 2
+    most = (1 << 26) // 4 * 32 if name == "kda_gdn_fwd" else (1 << 23) // 4 * 64   # chunks, blocks times heads
+    assert gdn_call(name, B=1, T=most - 1024, H=4, Hk=1, **small) == 8
+    assert gdn_call(name, B=1, T=most, H=4, Hk=1, **small) == 2
     assert gdn_call("kda_gdn_fwd_recurrent", B=1, cu=ptr(8), N=1 << 22, **small) == 2
     assert gdn_call("kda_gdn_fwd_recurrent", B=1, cu=ptr(8), N=(1 << 22) - 2, **small) == 8
 
