@@ -89,17 +89,17 @@ __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c)
 struct Terms {  // three bf16 terms of 8 floats
     u32x4 h, m, l;
 };
-// two floats into word e of each term
+// Two floats into word e of each term: the upper 16 bits, those of what they leave, and the rest, which has 8 bits: exact.
 __device__ __forceinline__ void cut2(float x, float y, Terms &t, int e)
 {
-    uint32_t h = pack2(x, y);
-    __asm__("" : "+v"(h));  // one conversion for both: else each value is converted again to get its rest
-    t.h[e] = h;
-    const float x1 = x - lo_f(t.h[e]), y1 = y - hi_f(t.h[e]);
-    uint32_t m = pack2(x1, y1);
-    __asm__("" : "+v"(m));
-    t.m[e] = m;
-    t.l[e] = pack2(x1 - lo_f(t.m[e]), y1 - hi_f(t.m[e]));
+    constexpr uint32_t kUpper = 0x07060302u;  // the upper halves of two words
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    t.h[e] = __builtin_amdgcn_perm(b, a, kUpper);
+    const float x1 = x - __uint_as_float(a & 0xffff0000u), y1 = y - __uint_as_float(b & 0xffff0000u);
+    const uint32_t a1 = __float_as_uint(x1), b1 = __float_as_uint(y1);
+    t.m[e] = __builtin_amdgcn_perm(b1, a1, kUpper);
+    const float x2 = x1 - __uint_as_float(a1 & 0xffff0000u), y2 = y1 - __uint_as_float(b1 & 0xffff0000u);
+    t.l[e] = __builtin_amdgcn_perm(__float_as_uint(y2), __float_as_uint(x2), kUpper);
 }
 __device__ __forceinline__ Terms cut8(f32x4 a, f32x4 b)
 {
@@ -219,8 +219,10 @@ __device__ __forceinline__ int64_t last_at_most(int64_t N, int64_t x, F key)
 struct Entry {
     int64_t seq, chunk;  // chunk > 0: the sequence comes from the segment before
 };
+template <bool kUniform = true>  // the same segment for all lanes
 __device__ __forceinline__ Entry entry_of(const GdnArgs &a, int64_t row, int64_t p)
 {
+    auto cu = [&](int64_t n) { return kUniform ? uniform(a.cu[n]) : a.cu[n]; };
     const int64_t at = p * a.len;
     if (!a.cu)
         return p >= a.P ? Entry{row + 1, 0} : Entry{row, at / kGC};  // len is a multiple of a chunk
@@ -229,11 +231,11 @@ __device__ __forceinline__ Entry entry_of(const GdnArgs &a, int64_t row, int64_t
     if (p == 0)
         return Entry{0, 0};
     // the first sequence that begins at `at` or behind, or the one before it if it has a chunk there
-    const int64_t m = uniform(a.cu[0]) >= at ? 0 : last_at_most(a.N + 1, at - 1, [&](int64_t n) { return uniform(a.cu[n]); });
+    const int64_t m = cu(0) >= at ? 0 : last_at_most(a.N + 1, at - 1, cu);
     if (m >= a.N)
         return Entry{a.N, 0};
-    const int64_t begin = uniform(a.cu[m]), c = (at - begin + kGC - 1) / kGC;
-    return c * kGC < uniform(a.cu[m + 1]) - begin ? Entry{m, c} : Entry{m + 1, 0};
+    const int64_t begin = cu(m), c = (at - begin + kGC - 1) / kGC;
+    return c * kGC < cu(m + 1) - begin ? Entry{m, c} : Entry{m + 1, 0};
 }
 
 struct Chunk {
@@ -351,6 +353,27 @@ __device__ __forceinline__ double of_lane(double b, int lane)
                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane));
 }
 
+// A state that has passed transitions of a norm below 2^-150 counts as 0 (a finite one; others make their rows NaN).
+constexpr float kDead = -150.0f;
+
+// How many of the chunks [c_lo, c_hi) of a sequence, counted from the end (or from the start), a state has to pass until it counts
+// as 0; one more than all of them if it never does.  By a wave, 64 chunks at a time.
+template <bool kFromEnd>
+__device__ __forceinline__ int64_t live_chunks(const GdnArgs &a, int64_t slot0, int64_t c_lo, int64_t c_hi, int64_t h, int lane)
+{
+    double sum = 0.0;
+    for (int64_t n = 0; n < c_hi - c_lo; n += 64) {
+        const int64_t i = n + lane, c = kFromEnd ? c_hi - 1 - i : c_lo + i;
+        const float x = i < c_hi - c_lo ? a.norm[(slot0 + c) * a.H + h] : 0.0f;
+        const double upto = sum + running_sum64((double)x);
+        const uint64_t hit = __ballot(i < c_hi - c_lo && upto < (double)kDead);
+        if (hit)
+            return uniform(n + __builtin_ctzll(hit) + 1);
+        sum = of_lane(upto, 63);
+    }
+    return c_hi - c_lo + 1;
+}
+
 // ------------------------------------------------------------------------------- records
 //
 // Factors of a record, 32 floats each (token of the chunk):
@@ -451,6 +474,17 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gdn_prep_kernel(GdnArgs a)
     for (int x = 0; x < 8; ++x)
         qk = kBwd ? mfma(qf[x], kf[x], qk) : mfma(kf[x], qf[x], qk);
     auto vec4 = [&](const float *p, int n) { return *reinterpret_cast<const f32x4 *>(p + 8 * n + 4 * h); };
+    if (a.norm) {  // log2 of a bound of the transition's norm: |e^g (1 - beta k k^T)| = e^g max(1, |1 - beta k.k|) for each token
+        float own = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            own = 8 * (i >> 2) + 4 * h + (i & 3) == l32 ? kk[i] : own;
+        own += __shfl_xor(own, 32);
+        const float f = fabsf(1.0f - bet * own), grow = f > 1.0f ? __builtin_amdgcn_logf(f) : f != f ? f : 0.0f;
+        const double bound = last + of_lane(running_sum32((double)grow), 31);
+        if (lane == 0)
+            a.norm[slot * a.H + head] = (float)bound;
+    }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
         const f32x4 uh = vec4(s.bh, n), ul = vec4(s.bl, n), ub = vec4(s.beta, n);
@@ -619,6 +653,23 @@ __device__ __forceinline__ void state_one(State &S, int v, int lane)
         for (int r = 0; r < 16; ++r)
             S.t[kt][r] = 32 * kt + 16 * (r >> 3) + 8 * (lane >> 5) + (r & 7) == v ? 1.0f : 0.0f;
 }
+// 0, or NaN where a value of the lane's column is not finite
+__device__ __forceinline__ float state_lost(const State &S)
+{
+    float x = 0.0f;
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            x = fmaf(S.t[kt][r], 0.0f, x);
+    return x + __shfl_xor(x, 32);
+}
+__device__ __forceinline__ void state_add1(State &S, float x)
+{
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+        S.t[kt] += x;
+}
 __device__ __forceinline__ size_t state_size(int dt) { return kGdnStateBytes / (dt == kBf16 ? 2 : 1); }
 
 // ------------------------------------------------------------------------------- LDS
@@ -635,18 +686,16 @@ struct LdsWalk {
     unsigned char rec[2][2 * kGdnMat + kGdnVec];
 };
 
-// A tile straight into LDS: 4 rows an instruction, wave w of kWaves takes rows 4w .. and every 4 kWaves behind them.  Rows
-// behind the chunk lie beyond the descriptor and arrive as zeros.
-template <int kWaves, int kRows>
-__device__ __forceinline__ void tile_fetch(const unsigned char *lds, const GdnTensor &x, const uint16_t *base, int64_t t0, int len,
-                                           int wave, int lane)
+// Half n of a tile straight into LDS: 4 rows an instruction, wave w of kWaves takes rows 4w .. and those 4 kWaves behind
+// them.  Rows behind the chunk lie beyond the descriptor and arrive as zeros.
+template <int kWaves>
+__device__ __forceinline__ void tile_half(const unsigned char *lds, const GdnTensor &x, const uint16_t *base, int64_t t0, int len,
+                                          int n, int wave, int lane)
 {
-    const uint32_t stride = (uint32_t)x.st * 2, bytes = len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u;
+    const uint32_t stride = (uint32_t)x.st * 2;
     const int row = 4 * wave + (lane >> 4);
-    const uint32_t off = (uint32_t)row * stride + (uint32_t)(((lane & 15) ^ swz(row)) << 4), to = lds_address(lds);
-#pragma unroll
-    for (int n = 0; n < kRows / (4 * kWaves); ++n)
-        load_lds(base + t0 * x.st, bytes, off + (uint32_t)(4 * kWaves * n) * stride, to + 1024 * (wave + kWaves * n));
+    const uint32_t off = (uint32_t)(row + 4 * kWaves * n) * stride + (uint32_t)(((lane & 15) ^ swz(row)) << 4);
+    load_lds(base + t0 * x.st, len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u, off, lds_address(lds) + 1024 * (wave + kWaves * n));
 }
 
 // Transposing read: lane i of each 16 lanes gives the address of 4 channels of token i / 4 and gets channel i of
@@ -709,14 +758,38 @@ __device__ __forceinline__ f32x16 zero16()
     return z;
 }
 
-// S <- f S + sum over the chunk's tokens of key channels (tile) times value columns (u)
-__device__ __forceinline__ void state_add(State &S, const unsigned char *tile, const Lanes &ln, const Terms *u)
+// Order of what stands since the last call: kN matrix instructions with kV vector instructions behind each, and no others
+// across.  A matrix instruction takes 32 cycles, in which one wave can issue six others; left alone the compiler puts
+// products and cuts behind each other, and neither the wave's own nor the other wave's overlap.
+template <int kN, int kV>
+__device__ __forceinline__ void mixed()
+{
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, kV, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Key channels (rows: the state's registers) of tokens 16 st .. of a tile
+struct KeyFrags {
+    u32x4 t[4];
+};
+__device__ __forceinline__ KeyFrags key_frags(const unsigned char *tile, const Lanes &ln, int st)
+{
+    KeyFrags k;
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt)
+        k.t[kt] = col_frag(tile, ln.key, kt, st);
+    return k;
+}
+// S += keys times value columns, 12 products
+__device__ __forceinline__ void state_add(State &S, const KeyFrags &k, const Terms &u)
 {
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-            S.t[kt] = mfma3(col_frag(tile, ln.key, kt, st), u[st], S.t[kt]);
+        S.t[kt] = mfma3(k.t[kt], u, S.t[kt]);
 }
 __device__ __forceinline__ void state_scale(State &S, float f)
 {
@@ -788,6 +861,31 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
     if constexpr (kOut)
         if (a.fin && a.fin != a.init)
             empty_states(a, e0, e1, valid, p, h, a.init, a.init_dt, a.fin, a.fin_dt);
+    float lost = 0.0f;    // NaN where a state that is not finite was left out
+    bool skipped = false;  // chunks whose share of the state at the cut counts as 0
+    if constexpr (kMode == kModeShare || kMode == kModePhi) {
+        const int64_t begin = uniform(seq_begin(a, e1.seq)), n = e1.chunk - e0.chunk;
+        const int64_t live = live_chunks<true>(a, slot_of(begin, e1.seq), e0.chunk, e1.chunk, h, lane);
+        if constexpr (kMode == kModePhi) {
+            if (tid == 0)
+                a.dead[segment * a.H + h] = live <= n;
+            if (live <= n)
+                return;
+        } else {
+            if (e0.chunk == 0 && a.init && (a.keep || live <= n)) {
+                State S;
+                state_load(S, static_cast<const unsigned char *>(a.init) + (e0.seq * a.H + h) * state_size(a.init_dt),
+                           a.init_dt, v, lane);
+                if (a.keep)
+                    state_store(S, a.keep + (segment * a.H + h) * kD * kD, 2, v, lane);
+                lost = state_lost(S);
+            }
+            if (live <= n) {
+                skipped = true;
+                e0.chunk = e1.chunk - live;
+            }
+        }
+    }
     Walk w;
     w.init(e0, e1, false);
     Chunk ch = w.next(a);
@@ -795,21 +893,30 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
         return;
     const Lanes ln(lane);
     const uint16_t *pk = head_base(a.k, row, h), *pv = head_base(a.v, row, h), *pq = head_base(a.q, row, h);
-    auto fetch = [&](int buf, const Chunk &n) {
-        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
-        if constexpr (kValues)
-            tile_fetch<kWalkWaves, kGC>(lds.tile[buf][1], a.v, pv, n.t0, n.len, wave, lane);
-        if constexpr (kOut)
-            tile_fetch<kWalkWaves, kGC>(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
-        constexpr int kBytes = kOut ? 2 * kGdnMat + kGdnVec : kGdnMat + kGdnVec;
-        const unsigned char *rec = a.rec + (n.slot * a.H + h) * a.rec_bytes;
-        for (int i = wave; i < kBytes / 1024; i += kWalkWaves)
-            load_lds(rec, kBytes, (uint32_t)(1024 * i + 16 * lane), lds_address(lds.rec[buf]) + 1024 * i);
+    // A chunk's loads in kLoads parts: asked for all at once they fill the load queue and hold the wave up for some 2000 cycles.
+    constexpr int kTiles = kOut ? 3 : kValues ? 2 : 1, kBytes = kOut ? 2 * kGdnMat + kGdnVec : kGdnMat + kGdnVec;
+    constexpr int kLoads = 2 * kTiles + (kBytes / 1024 + kWalkWaves - 1) / kWalkWaves;
+    auto fetch = [&](int buf, const Chunk &n, int part) {
+        if (part >= kLoads)
+            return;
+        if (part < 2 * kTiles) {
+            const int t = part >> 1;
+            tile_half<kWalkWaves>(lds.tile[buf][t], t == 0 ? a.k : t == 1 ? a.v : a.q, t == 0 ? pk : t == 1 ? pv : pq, n.t0, n.len,
+                                  part & 1, wave, lane);
+        } else {
+            int i = wave + kWalkWaves * (part - 2 * kTiles);  // the last KiB by several waves, rather than a branch
+            i = i < kBytes / 1024 ? i : kBytes / 1024 - 1;
+            load_lds(a.rec + (n.slot * a.H + h) * a.rec_bytes, n.len ? kBytes : 0, (uint32_t)(1024 * i + 16 * lane),
+                     lds_address(lds.rec[buf]) + 1024 * i);
+        }
     };
     State S;
     state_zero(S);
     int buf = 0;
-    fetch(0, ch);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        fetch(0, ch, i);
+    Terms c = cut8(S.t[0], 0);  // of the state's first 16 channels
     // stored a chunk later, behind the wait for the loads: a store is then waited for a whole chunk after it
     u32x4 held[2];     // rows of out
     f32x16 held_r;     // residuals
@@ -833,13 +940,11 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
                             *vec = mt + kGdnMat, *ma = vec + kGdnVec;
         const Chunk nx = w.next(a);
         arrive();  // this chunk's tiles and record are there; the other buffer is read by no one
-        if (nx.len)
-            fetch(buf ^ 1, nx);
         store_held();
         if (ch.first) {
             if constexpr (kMode == kModePhi) {
                 state_one(S, v, lane);
-            } else if (ch.from_seg) {
+            } else if (ch.from_seg || skipped) {
                 if constexpr (kOut || kMode == kModeStore)
                     state_load(S, a.seg + (segment * a.H + h) * kD * kD, 2, v, lane);
                 else
@@ -849,67 +954,129 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             } else if (a.init) {
                 state_load(S, static_cast<const unsigned char *>(a.init) + (ch.seq * a.H + h) * state_size(a.init_dt),
                            a.init_dt, v, lane);
-                if constexpr (kMode == kModeShare)
-                    if (a.keep)
-                        state_store(S, a.keep + (segment * a.H + h) * kD * kD, 2, v, lane);
             } else {
                 state_zero(S);
             }
             // here, or the compiler waits behind the branch in every chunk
             __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+            c = cut8(S.t[0], 0);
         }
         if constexpr (kMode == kModeStore)
             if (ch.opens)
                 state_store(S, a.before + (ch.block * a.H + h) * kD * kD, 2, v, lane);
-        f32x16 Z = zero16(), O = zero16();
+        f32x16 Z = zero16(), O = zero16(), R = zero16();
+        u32x4 kf = row_frag(tk, ln, 0), qf = kf;
+        if constexpr (kOut)
+            qf = row_frag(tq, ln, 0);
+        Terms t0, t1, a0, a1;
+        u32x2 v4[4];
+        f32x4 f4[4];
+        __builtin_amdgcn_sched_barrier(0);
+        // what is read for a step, and the cut for it, stand in the step before
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const Terms c = cut8(S.t[x >> 1], x & 1);
-            Z = mfma3(row_frag(tk, ln, x), c, Z);
+            Terms cn = c;
+            u32x4 kn = kf, qn = qf;
+            if (x < 7) {
+                kn = row_frag(tk, ln, x + 1);
+                if constexpr (kOut)
+                    qn = row_frag(tq, ln, x + 1);
+                cn = cut8(S.t[(x + 1) >> 1], (x + 1) & 1);
+            }
+            if (x == 6) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    f4[n] = vec4(vec, kVHead, n, lane);
+                    if constexpr (kValues)
+                        v4[n] = col_frag4(tv, kOut ? ln.out : ln.col, wave, n);
+                }
+            }
+            if (x == 7)
+                t0 = load_terms(mt, 0, lane);
+            Z = mfma(kf, c.l, Z);
             if constexpr (kOut)  // transposed: rows are value columns, a lane's token is lane % 32
-                O = mfma3(c, row_frag(tq, ln, x), O);
+                O = mfma(c.l, qf, O);
+            Z = mfma(kf, c.m, Z);
+            if constexpr (kOut)
+                O = mfma(c.m, qf, O);
+            Z = mfma(kf, c.h, Z);
+            if constexpr (kOut)
+                O = mfma(c.h, qf, O);
+            fetch(buf ^ 1, nx, x);
+            mixed<kOut ? 6 : 3, kOut ? 8 : 15>();
+            c = cn;
+            kf = kn;
+            qf = qn;
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const f32x4 f = vec4(vec, kVHead, n, lane);
-            f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (kValues)
-                x = widen4(col_frag4(tv, kOut ? ln.out : ln.col, wave, n));
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                Z[4 * n + i] = fmaf(-f[i], Z[4 * n + i], x[i]);
-        }
-        f32x16 R = zero16();
+                Z[4 * n + i] = kValues ? fmaf(-f4[n][i], Z[4 * n + i], i == 0   ? lo_f(v4[n][0])
+                                                                       : i == 1 ? hi_f(v4[n][0])
+                                                                       : i == 2 ? lo_f(v4[n][1])
+                                                                                : hi_f(v4[n][1]))
+                                       : -f4[n][i] * Z[4 * n + i];
+        Terms x0 = cut8(Z, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
-            R = mfma6(load_terms(mt, st, lane), cut8(Z, st), R);
+        for (int i = 8; i < kLoads; ++i)
+            fetch(buf ^ 1, nx, i);
+        t1 = load_terms(mt, 1, lane);
+        R = mfma6(t0, x0, R);
+        const Terms x1 = cut8(Z, 1);
+        mixed<6, 8>();
+        const float carry = vec1(vec, kVLast), vo = vec1(vec, kVOut + l32);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            f4[n] = vec4(vec, kVWrite, n, lane);
+        if constexpr (kOut)
+            a0 = load_terms(ma, 0, lane);
+        KeyFrags k0 = key_frags(tk, ln, 0);
+        R = mfma6(t1, x1, R);
+        state_scale(S, carry);
+        if constexpr (kOut)
+            O *= vo;
+        mixed<6, kOut ? 14 : 11>();
         if constexpr (kOut) {
-            O *= vec1(vec, kVOut + l32);
-#pragma unroll
-            for (int st = 0; st < 2; ++st)
-                O = mfma6(cut8(R, st), load_terms(ma, st, lane), O);
+            const Terms r0 = cut8(R, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            a1 = load_terms(ma, 1, lane);
+            O = mfma6(r0, a0, O);
+            const Terms r1 = cut8(R, 1);
+            mixed<6, 8>();
+            O = mfma6(r1, a1, O);
         }
         if constexpr (kMode == kModeStore)
             held_r = R;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const f32x4 f = vec4(vec, kVWrite, n, lane);
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                R[4 * n + i] *= f[i];
-        }
-        const Terms u[2] = {cut8(R, 0), cut8(R, 1)};
-        state_scale(S, vec1(vec, kVLast));
-        state_add(S, tk, ln, u);
+                R[4 * n + i] *= f4[n][i];
+        const Terms u0 = cut8(R, 0);
+        if constexpr (kOut)
+            mixed<6, 10>();
+        else
+            __builtin_amdgcn_sched_barrier(0);
+        const KeyFrags k1 = key_frags(tk, ln, 1);
+        state_add(S, k0, u0);
+        const Terms u1 = cut8(R, 1);
+        mixed<12, 4>();
+        state_add(S, k1, u1);
+        c = cut8(S.t[0], 0);
         if constexpr (kOut)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 held[e >> 2][e & 3] = pack2(O[2 * e], O[2 * e + 1]);
+        mixed<12, 5>();
         before = ch;
         if (kMode != kModeStore && ch.last) {
-            if constexpr (kMode == kModeShare)
+            if constexpr (kMode == kModeShare) {
+                if (skipped)
+                    state_add1(S, lost);
                 state_store(S, a.seg + ((segment + 1) * a.H + h) * kD * kD, 2, v, lane);
-            else if constexpr (kMode == kModePhi)
+            } else if constexpr (kMode == kModePhi)
                 state_store(S, a.phi + (segment * a.H + h) * kD * kD, 2, v, lane);
             else if (a.fin && !ch.to_seg)
                 state_store(S, static_cast<unsigned char *>(a.fin) + (ch.seq * a.H + h) * state_size(a.fin_dt), a.fin_dt,
@@ -969,6 +1136,8 @@ template <bool kRev>
 __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint32_t terms[2][3][4][64][4];
+    __shared__ float lost[2][8][16];
+    __shared__ uint8_t kinds[kGdnMaxCuts];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
     const uint32_t chain = blockIdx.x >> 3, row = chain / (uint32_t)a.H, h = chain - row * (uint32_t)a.H;
     const int v = (int)(blockIdx.x & 7) * 16 + m;
@@ -977,16 +1146,23 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
     float *base = (kRev ? a.dseg : a.seg) + ((size_t)row * a.P * a.H + h) * kD * kD;
     const float *phis = a.phi + ((size_t)row * a.P * a.H + h) * kD * kD;
     const size_t step = (size_t)a.H * kD * kD;
-    const int64_t first = kRev ? a.P - 2 : 1, dir = kRev ? -1 : 1;
-    auto inside = [&](int64_t p) {
-        if (p < 1 || p > a.P - 2)
-            return false;
-        const Entry e = entry_of(a, row, p), n = entry_of(a, row, p + 1);
-        return e.chunk > 0 && n.chunk > 0 && e.seq == n.seq;
-    };
+    const int first = kRev ? (int)a.P - 2 : 1, dir = kRev ? -1 : 1;
+    // what each segment is: 0 not inside one sequence, 1 inside, 2 inside and its transition counts as 0
+    for (int p = tid; p < a.P; p += 512) {
+        int kind = 0;
+        if (p >= 1 && p <= a.P - 2) {
+            const Entry e = entry_of<false>(a, row, p), n = entry_of<false>(a, row, p + 1);
+            if (e.chunk > 0 && n.chunk > 0 && e.seq == n.seq)
+                kind = a.dead[((int64_t)row * a.P + p) * a.H + h] ? 2 : 1;
+        }
+        kinds[p] = (uint8_t)kind;
+    }
+    __syncthreads();
+    auto kind_of = [&](int p) { return p < 1 || p > a.P - 2 ? 0 : __builtin_amdgcn_readfirstlane((int)kinds[p]); };
     f32x4 f[8], acc, own;
-    auto fetch = [&](int64_t p) {
-        acc = *reinterpret_cast<const f32x4 *>(base + (size_t)(p + dir) * step + (size_t)v * kD + 16 * wave + 4 * g);
+    auto at = [&](int p) { return reinterpret_cast<f32x4 *>(base + (size_t)p * step + (size_t)v * kD + 16 * wave + 4 * g); };
+    auto fetch = [&](int p) {
+        acc = *at(p + dir);
         const float *phi = phis + (size_t)p * step;
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -1000,55 +1176,68 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
         }
     };
     int cur = 0;
-    bool have = false;  // terms[cur] are those of the state that segment p begins (ends) with
-    bool in = inside(first);
-    if (in)
-        fetch(first);
-    for (int64_t p = first; kRev ? p >= 1 : p + 1 < a.P; p += dir) {
-        const bool next = inside(p + dir);
-        if (!in) {
-            have = false;
-            in = next;
-            if (in)
-                fetch(p + dir);
-            continue;
-        }
-        if (!have) {
-            own = *reinterpret_cast<const f32x4 *>(base + (size_t)p * step + (size_t)v * kD + 16 * wave + 4 * g);
-            Terms t;
-            cut2(own[0], own[1], t, 0);
-            cut2(own[2], own[3], t, 1);
-            const int x = wave >> 1, e = 2 * (wave & 1);
-            *reinterpret_cast<u32x2 *>(&terms[cur][0][x][lane][e]) = u32x2{t.h[0], t.h[1]};
-            *reinterpret_cast<u32x2 *>(&terms[cur][1][x][lane][e]) = u32x2{t.m[0], t.m[1]};
-            *reinterpret_cast<u32x2 *>(&terms[cur][2][x][lane][e]) = u32x2{t.l[0], t.l[1]};
-        }
-        Terms ft[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            ft[x] = cut8(f[2 * x], f[2 * x + 1]);
-        f32x4 sum = acc;
-        if (next)
-            fetch(p + dir);
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const Terms s = {*reinterpret_cast<const u32x4 *>(terms[cur][0][x][lane]),
-                             *reinterpret_cast<const u32x4 *>(terms[cur][1][x][lane]),
-                             *reinterpret_cast<const u32x4 *>(terms[cur][2][x][lane])};
-            sum = mfma6(ft[x], s, sum);  // rows: key channels, columns: value columns
-        }
-        *reinterpret_cast<f32x4 *>(base + (size_t)(p + dir) * step + (size_t)v * kD + 16 * wave + 4 * g) = sum;
-        cur ^= 1;  // the next barrier keeps the writes two steps on behind these reads
+    bool have = false;  // `own` is the state that segment p begins (ends) with
+    auto share_terms = [&]() {
         Terms t;
-        cut2(sum[0], sum[1], t, 0);
-        cut2(sum[2], sum[3], t, 1);
+        cut2(own[0], own[1], t, 0);
+        cut2(own[2], own[3], t, 1);
         const int x = wave >> 1, e = 2 * (wave & 1);
         *reinterpret_cast<u32x2 *>(&terms[cur][0][x][lane][e]) = u32x2{t.h[0], t.h[1]};
         *reinterpret_cast<u32x2 *>(&terms[cur][1][x][lane][e]) = u32x2{t.m[0], t.m[1]};
         *reinterpret_cast<u32x2 *>(&terms[cur][2][x][lane][e]) = u32x2{t.l[0], t.l[1]};
-        have = true;
-        in = next;
+    };
+    int kind = kind_of(first);
+    if (kind == 1)
+        fetch(first);
+    for (int p = first; p >= 1 && p <= a.P - 2; p += dir) {
+        const int next = kind_of(p + dir);
+        if (kind == 0) {
+            have = false;
+        } else {
+            if (!have)
+                own = *at(p);
+            if (kind == 2) {
+                // nothing of the state is left, unless a row of it is not finite: that makes the row NaN
+                float x = own[0] * 0.0f + own[1] * 0.0f + own[2] * 0.0f + own[3] * 0.0f;
+                x += __shfl_xor(x, 16);
+                x += __shfl_xor(x, 32);
+                if (g == 0)
+                    lost[cur][wave][m] = x;
+                __syncthreads();
+                x = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                    x += lost[cur][w][m];
+                own = *at(p + dir);
+                if (x != x) {
+                    own += x;
+                    *at(p + dir) = own;
+                }
+            } else {
+                share_terms();
+                Terms ft[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    ft[x] = cut8(f[2 * x], f[2 * x + 1]);
+                own = acc;
+                if (next == 1)
+                    fetch(p + dir);
+                __syncthreads();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const Terms s = {*reinterpret_cast<const u32x4 *>(terms[cur][0][x][lane]),
+                                     *reinterpret_cast<const u32x4 *>(terms[cur][1][x][lane]),
+                                     *reinterpret_cast<const u32x4 *>(terms[cur][2][x][lane])};
+                    own = mfma6(ft[x], s, own);  // rows: key channels, columns: value columns
+                }
+                *at(p + dir) = own;
+            }
+            cur ^= 1;  // the next step's barrier keeps the writes two steps on behind these reads
+            have = true;
+        }
+        if (kind != 1 && next == 1)
+            fetch(p + dir);
+        kind = next;
     }
 }
 
@@ -1075,6 +1264,22 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
     if constexpr (!kShare)
         if (a.dinit)
             empty_states(a, e0, e1, valid, p, h, a.dfin, 2, a.dinit, 2);
+    float lost = 0.0f;
+    bool skipped = false;  // as in the forward walk, from the segment's start on
+    if (kShare && valid) {
+        const int64_t begin = uniform(seq_begin(a, e0.seq)), len = uniform(seq_begin(a, e0.seq + 1)) - begin;
+        const int64_t end = e1.seq == e0.seq ? e1.chunk : (len + kGC - 1) / kGC, n = end - e0.chunk;
+        const int64_t live = live_chunks<false>(a, slot_of(begin, e0.seq), e0.chunk, end, h, lane);
+        if (live <= n) {
+            if (e1.seq != e0.seq && a.dfin) {
+                State S;
+                state_load(S, a.dfin + (e0.seq * a.H + h) * kD * kD, 2, v, lane);
+                lost = state_lost(S);
+            }
+            skipped = true;
+            e1 = Entry{e0.seq, e0.chunk + live};
+        }
+    }
     Walk w;
     w.init(e0, e1, true);
     Chunk ch = w.next(a);
@@ -1082,19 +1287,28 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
         return;
     const Lanes ln(lane);
     const uint16_t *pk = head_base(a.k, row, h), *po = head_base(a.dout, row, h), *pq = head_base(a.q, row, h);
-    auto fetch = [&](int buf, const Chunk &n) {
-        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][0], a.k, pk, n.t0, n.len, wave, lane);
-        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][1], a.dout, po, n.t0, n.len, wave, lane);
-        tile_fetch<kWalkWaves, kGC>(lds.tile[buf][2], a.q, pq, n.t0, n.len, wave, lane);
-        constexpr int kBytes = 2 * kGdnMat + kGdnVec;
-        const unsigned char *rec = a.rec + (n.slot * a.H + h) * a.rec_bytes + kGdnMat;
-        for (int i = wave; i < kBytes / 1024; i += kWalkWaves)
-            load_lds(rec, kBytes, (uint32_t)(1024 * i + 16 * lane), lds_address(lds.rec[buf]) + 1024 * i);
+    constexpr int kBytes = 2 * kGdnMat + kGdnVec, kLoads = 6 + (kBytes / 1024 + kWalkWaves - 1) / kWalkWaves;
+    auto fetch = [&](int buf, const Chunk &n, int part) {  // in parts, as in the forward walk
+        if (part >= kLoads)
+            return;
+        if (part < 6) {
+            const int t = part >> 1;
+            tile_half<kWalkWaves>(lds.tile[buf][t], t == 0 ? a.k : t == 1 ? a.dout : a.q, t == 0 ? pk : t == 1 ? po : pq, n.t0, n.len,
+                                  part & 1, wave, lane);
+        } else {
+            int i = wave + kWalkWaves * (part - 6);
+            i = i < kBytes / 1024 ? i : kBytes / 1024 - 1;
+            load_lds(a.rec + (n.slot * a.H + h) * a.rec_bytes + kGdnMat, n.len ? kBytes : 0, (uint32_t)(1024 * i + 16 * lane),
+                     lds_address(lds.rec[buf]) + 1024 * i);
+        }
     };
     State S;
     state_zero(S);
     int buf = 0;
-    fetch(0, ch);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        fetch(0, ch, i);
+    Terms c = cut8(S.t[0], 0);  // of the state's first 16 channels
     f32x16 held;  // dw, stored a chunk later as in the forward walk
     Chunk before = ch;
     before.len = 0;
@@ -1107,11 +1321,9 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
                             *mt = vec + kGdnVec, *ma = mt + kGdnMat;
         const Chunk nx = w.next(a);
         arrive();  // this chunk's tiles and record are there; the other buffer is read by no one
-        if (nx.len)
-            fetch(buf ^ 1, nx);
         store_held();
         if (ch.first) {
-            if (ch.from_seg) {
+            if (ch.from_seg) {  // also where chunks were left out
                 if constexpr (kShare)
                     state_zero(S);
                 else
@@ -1123,52 +1335,110 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
             }
             // here, or the compiler waits behind the branch in every chunk
             __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+            c = cut8(S.t[0], 0);
         }
         if (!kShare && ch.closes)
             state_store(S, a.dafter + (ch.block * a.H + h) * kD * kD, 2, v, lane);
-        f32x16 Y = zero16();
+        f32x16 Y = zero16(), W = zero16();
+        u32x4 kf = row_frag(tk, ln, 0), o[2];
+        Terms a0, a1, t0, t1;
+        f32x4 f4[4], fo[4], fb[4], fh[4];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-            Y = mfma3(row_frag(tk, ln, x), cut8(S.t[x >> 1], x & 1), Y);
+        for (int x = 0; x < 8; ++x) {
+            Terms cn = c;
+            u32x4 kn = kf;
+            if (x < 7) {
+                kn = row_frag(tk, ln, x + 1);
+                cn = cut8(S.t[(x + 1) >> 1], (x + 1) & 1);
+            }
+            if (x == 6) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const f32x4 f = vec4(vec, kVTail, n, lane);
+                for (int n = 0; n < 4; ++n) {
+                    f4[n] = vec4(vec, kVTail, n, lane);
+                    fo[n] = vec4(vec, kVOut, n, lane);
+                }
+#pragma unroll
+                for (int st = 0; st < 2; ++st)
+                    o[st] = col_frag(to, ln.col, wave, st);
+            }
+            if (x == 7) {
+                a0 = load_terms(ma, 0, lane);
+                a1 = load_terms(ma, 1, lane);
+            }
+            Y = mfma3(kf, c, Y);
+            fetch(buf ^ 1, nx, x);
+            mixed<3, 15>();
+            c = cn;
+            kf = kn;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                Y[4 * n + i] *= f[i];
-        }
-        u32x4 o[2];
+                Y[4 * n + i] *= f4[n][i];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            o[st] = col_frag(to, ln.col, wave, st);
-            Y = mfma3(load_terms(ma, st, lane), o[st], Y);
-        }
-        f32x16 W = zero16();
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-            W = mfma6(load_terms(mt, st, lane), cut8(Y, st), W);
-        held = W;
-        // what the tokens' reads and writes send to the state before the chunk
-        f32x16 x;
+        for (int i = 8; i < kLoads; ++i)
+            fetch(buf ^ 1, nx, i);
+        t0 = load_terms(mt, 0, lane);
+        Y = mfma3(a0, o[0], Y);
+        Y = mfma3(a1, o[1], Y);
+        // what the tokens' reads and writes send to the state before the chunk: first the reads
+        f32x16 g;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const f32x4 f = vec4(vec, kVOut, n, lane), be = vec4(vec, kVBeta, n, lane), hd = vec4(vec, kVHead, n, lane);
             const f32x4 o4 = widen4(u32x2{o[n >> 1][2 * (n & 1)], o[n >> 1][2 * (n & 1) + 1]});
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[4 * n + i] = o4[i] * f[i];
-                W[4 * n + i] *= -(be[i] * hd[i]);
-            }
+            for (int i = 0; i < 4; ++i)
+                g[4 * n + i] = o4[i] * fo[n][i];
         }
-        const Terms uo[2] = {cut8(x, 0), cut8(x, 1)}, uw[2] = {cut8(W, 0), cut8(W, 1)};
-        state_scale(S, vec1(vec, kVLast));
-        state_add(S, tq, ln, uo);
-        state_add(S, tk, ln, uw);
+        const Terms g0 = cut8(g, 0);
+        mixed<6, 12>();
+        const float carry = vec1(vec, kVLast);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            fb[n] = vec4(vec, kVBeta, n, lane);
+            fh[n] = vec4(vec, kVHead, n, lane);
+        }
+        t1 = load_terms(mt, 1, lane);
+        const Terms y0 = cut8(Y, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        KeyFrags k0 = key_frags(tq, ln, 0);
+        W = mfma6(t0, y0, W);
+        const Terms y1 = cut8(Y, 1);
+        mixed<6, 8>();
+        W = mfma6(t1, y1, W);
+        state_scale(S, carry);
+        const Terms g1 = cut8(g, 1);
+        mixed<6, 18>();
+        KeyFrags k1 = key_frags(tq, ln, 1);
+        state_add(S, k0, g0);
+        held = W;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                W[4 * n + i] *= -(fb[n][i] * fh[n][i]);
+        const Terms w0 = cut8(W, 0);
+        mixed<12, 7>();
+        k0 = key_frags(tk, ln, 0);
+        state_add(S, k1, g1);
+        const Terms w1 = cut8(W, 1);
+        mixed<12, 4>();
+        k1 = key_frags(tk, ln, 1);
+        state_add(S, k0, w0);
+        __builtin_amdgcn_sched_barrier(0);
+        state_add(S, k1, w1);
+        c = cut8(S.t[0], 0);
+        mixed<12, 4>();
         before = ch;
         if (ch.last) {
-            if constexpr (kShare)
+            if constexpr (kShare) {
+                if (skipped)
+                    state_add1(S, lost);
                 state_store(S, a.dseg + ((segment - 1) * a.H + h) * kD * kD, 2, v, lane);
-            else if (a.dinit && !ch.to_seg)
+            } else if (a.dinit && !ch.to_seg)
                 state_store(S, a.dinit + (ch.seq * a.H + h) * kD * kD, 2, v, lane);
         }
         if (nx.len == 0)
@@ -1229,9 +1499,12 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
     const int len = (int)(rest < kGB ? rest : kGB);
     const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGB, tok0 = row * a.T + t0;
     const int64_t slot = slot_of(begin, seq) + 2 * c;
-    tile_fetch<8, kGB>(s.k, a.k, head_base(a.k, row, head), t0, len, wave, lane);
-    tile_fetch<8, kGB>(s.q, a.q, head_base(a.q, row, head), t0, len, wave, lane);
-    tile_fetch<8, kGB>(s.o, a.dout, head_base(a.dout, row, head), t0, len, wave, lane);
+    tile_half<8>(s.k, a.k, head_base(a.k, row, head), t0, len, 0, wave, lane);
+    tile_half<8>(s.k, a.k, head_base(a.k, row, head), t0, len, 1, wave, lane);
+    tile_half<8>(s.q, a.q, head_base(a.q, row, head), t0, len, 0, wave, lane);
+    tile_half<8>(s.q, a.q, head_base(a.q, row, head), t0, len, 1, wave, lane);
+    tile_half<8>(s.o, a.dout, head_base(a.dout, row, head), t0, len, 0, wave, lane);
+    tile_half<8>(s.o, a.dout, head_base(a.dout, row, head), t0, len, 1, wave, lane);
     // the state's columns of this wave: lane = key channel, elements 8 x + j: value row 16 x + 8 h + j
     const int kg = wave & 3, kc = 32 * kg + column_of<true>(l32);
     const int64_t at = (block * a.H + head) * kD * kD;
@@ -1299,7 +1572,8 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
             *reinterpret_cast<u32x4 *>(s.x[1] + to) = y.m;
             *reinterpret_cast<u32x4 *>(s.x[2] + to) = y.l;
             if (on)
-                *reinterpret_cast<u32x4 *>(a.dv + ((tok0 + t) * a.H + head) * kD + v0 + 8 * hf) = y.h;
+                *reinterpret_cast<u32x4 *>(a.dv + ((tok0 + t) * a.H + head) * kD + v0 + 8 * hf) =
+                    u32x4{pack2(x[0][0], x[0][1]), pack2(x[0][2], x[0][3]), pack2(x[1][0], x[1][1]), pack2(x[1][2], x[1][3])};
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {

@@ -68,7 +68,7 @@ bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
         off = (off + bytes + kAlign - 1) / kAlign * kAlign;
         return o;
     };
-    L->off_rec = L->off_seg = L->off_phi = L->off_keep = L->off_dseg = 0;
+    L->off_rec = L->off_seg = L->off_phi = L->off_keep = L->off_dseg = L->off_dead = L->off_norm = 0;
     L->off_before = L->off_dafter = L->off_res = L->off_dwrite = L->off_dq = L->off_dk = 0;
     const size_t recs = z.T > 0 ? (size_t)L->slots * (size_t)z.H : 0, blocks = z.T > 0 ? (size_t)L->blocks * (size_t)z.H : 0;
     L->off_rec = take(recs * (bwd ? kda::kGdnRecBwd : kda::kGdnRecFwd));
@@ -77,6 +77,8 @@ bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
         L->off_seg = take(segs);
         L->off_phi = take(segs);
         (bwd ? L->off_dseg : L->off_keep) = take(segs);
+        L->off_dead = take((size_t)p.rows * (size_t)p.P * (size_t)z.H * sizeof(int32_t));
+        L->off_norm = take(recs * sizeof(float));
     }
     if (bwd) {
         L->off_before = take(blocks * kda::kGdnStateBytes);
@@ -206,6 +208,8 @@ kda_status forward_args(const void *q, const void *k, const void *v, const float
         if (a->P > 1) {
             a->seg = reinterpret_cast<float *>(w + lay.off_seg);
             a->phi = reinterpret_cast<float *>(w + lay.off_phi);
+            a->dead = reinterpret_cast<int32_t *>(w + lay.off_dead);
+            a->norm = reinterpret_cast<float *>(w + lay.off_norm);
             if (ht && ht == h0)
                 a->keep = reinterpret_cast<float *>(w + lay.off_keep);
         }
@@ -354,6 +358,8 @@ kda_status kda_gdn_bwd(const void *q, const void *k, const void *v, const float 
     if (a.P > 1) {
         a.seg = f32(lay.off_seg);
         a.phi = f32(lay.off_phi);
+        a.dead = reinterpret_cast<int32_t *>(w + lay.off_dead);
+        a.norm = f32(lay.off_norm);
         a.dseg = f32(lay.off_dseg);
     }
     a.dfin = dfinal_state;

@@ -15,6 +15,7 @@ constexpr int kGC = 32;                    // tokens per chunk
 constexpr int kGB = 64;                    // tokens per block of the backward pass: one state is kept for two chunks
 constexpr int64_t kGdnSlots = 512;         // workgroups of a walk that run at once: two on each of 256 CUs
 constexpr size_t kGdnStateBytes = (size_t)kD * kD * sizeof(float);
+constexpr int64_t kGdnMaxCuts = 1024;      // segments of a row, at most
 constexpr int64_t kGdnMinSeg = 256;        // shortest segment that a cut leaves, in tokens
 
 // Record of one (chunk, head) in the workspace, bytes: operands of the walks, in the order of their lanes.
@@ -53,7 +54,7 @@ inline GdnPlan gdn_plan(int64_t B, int64_t T, int64_t H, bool varlen, bool bwd)
     const int64_t chains = p.rows * H;
     int64_t most = T / kGdnMinSeg;
     if (most > 2 * kGdnSlots / chains)
-        most = 2 * kGdnSlots / chains;
+        most = 2 * kGdnSlots / chains;  // at most kGdnMaxCuts
     double best = 0.0;
     for (int64_t P = 1; P <= (most > 1 ? most : 1); ++P) {
         const int64_t len = T > 0 ? cdiv(cdiv(T, P), kGB) * kGB : kGB, got = T > 0 ? cdiv(T, len) : 1;
@@ -93,6 +94,8 @@ struct GdnArgs {
     int64_t slots, blocks, rec_bytes;
     float *seg;                  // [rows * P][H]: state at a segment's start, of the sequence that crosses it
     float *phi;                  // [rows * P][H]
+    int32_t *dead;               // [rows * P][H]: the transition counts as 0 (and is not formed)
+    float *norm;                 // [slots][H]: log2 of a bound of each chunk's transition; NULL without cuts
     float *keep;                 // [rows * P][H]: initial state of the sequence that leaves the segment (in place), or NULL
     // backward pass
     int64_t Hk;
@@ -109,7 +112,7 @@ struct GdnArgs {
 struct GdnLayout {
     GdnPlan plan;
     int64_t slots, blocks;
-    size_t off_rec, off_seg, off_phi, off_keep;
+    size_t off_rec, off_seg, off_phi, off_keep, off_dead, off_norm;
     size_t off_dseg, off_before, off_dafter, off_res, off_dwrite, off_dq, off_dk;
     size_t total;
 };

@@ -179,3 +179,37 @@ def test_not_finite_stays_in_its_head():
         assert torch.equal(out[0, :64, 0], ref[0, :64, 0]) and torch.equal(out[1, :128, 1], ref[1, :128, 1])
         assert torch.equal(out[0, :192, 2], ref[0, :192, 2])
         assert out[0, 100, 0].isnan().any() and out[1, 130, 1].isnan().any() and out[0, 200:, 2].isnan().all()
+
+
+@pytest.mark.parametrize("lo,hi", [(0.05, 0.5), (1.0, 20.0), (0.0, 3.0)], ids=str)
+@pytest.mark.parametrize("beta", [0.9, 2.5])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_cut_rows_that_forget(lo, hi, beta, in_place):
+    """Decays that leave nothing of a state behind a few hundred tokens, a few, or in one head only: what the cuts leave out counts
+    as 0.  beta 2.5 makes single transitions grow."""
+    q, k, v, d, b, n = inputs(1, 3000, 1, 3, 31)
+    d = -(lo + (hi - lo) * torch.rand(d.shape, device=d.device))
+    d[:, :, 2] *= 1e-3
+    b = b * beta
+    if beta > 2:  # no running away in the head that keeps its state
+        b[:, :, 2] *= 0.3
+    check((q, k, v, d, b), n(1, 3, D, D), in_place=in_place)
+    cu = [0, 1300, 1301, 3000]
+    check((q, k, v, d, b), n(3, 3, D, D), cu, in_place=in_place)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("decay", [-0.001, -5.0])
+def test_state_that_is_not_finite_lasts(bad, decay):
+    """A row of the initial state that is not finite stays NaN to the end, over cuts of its sequence too, and reaches nothing else."""
+    q, k, v, d, b, n = inputs(1, 2500, 1, 2, 33)
+    d = torch.full_like(d, decay)
+    h0 = n(1, 2, D, D)
+    clean, cfin = run(q, k, v, d, b, h0)
+    h0[0, 1, 7, 9] = bad
+    out, fin = run(q, k, v, d, b, h0)
+    keep = torch.ones(D, dtype=torch.bool, device=q.device)
+    keep[7] = False
+    assert torch.equal(out[:, :, 0], clean[:, :, 0]) and torch.equal(out[:, :, 1, keep], clean[:, :, 1, keep])
+    assert torch.equal(fin[:, 0], cfin[:, 0]) and torch.equal(fin[:, 1, keep], cfin[:, 1, keep])
+    assert fin[0, 1, 7].isnan().all() and not torch.isfinite(out[:, :, 1, 7]).any()

@@ -141,3 +141,27 @@ def test_repeats():
     dout, h0 = n(*v.shape).bfloat16(), n(1, 2, D, D)
     x, y = (gdn.bwd(q, k, v, d, b, SCALE, dout, h0, h0) for _ in range(2))
     assert all(torch.equal(x[m], y[m]) for m in x if m != "workspace")
+
+
+@pytest.mark.parametrize("lo,hi", [(0.05, 0.5), (1.0, 20.0), (0.0, 3.0)], ids=str)
+def test_cut_rows_that_forget(lo, hi):
+    q, k, v, d, b, n = inputs(1, 2000, 1, 3, 31)
+    d = -(lo + (hi - lo) * torch.rand(d.shape, device=d.device))
+    d[:, :, 2] *= 1e-3
+    check((q, k, v, d, b, n), n(1, 3, D, D), n(1, 3, D, D))
+    check((q, k, v, d, b, n), n(3, 3, D, D), n(3, 3, D, D), [0, 900, 901, 2000])
+
+
+def test_gradient_that_is_not_finite_lasts():
+    """A row of dfinal_state that is not finite reaches the start of its sequence, over cuts and strong decays, and no other row."""
+    q, k, v, d, b, n = inputs(1, 2500, 1, 2, 33)
+    d = torch.full_like(d, -5.0)
+    dout, h0, dht = n(*v.shape).bfloat16(), n(1, 2, D, D), n(1, 2, D, D)
+    clean = gdn.bwd(q, k, v, d, b, SCALE, dout, h0, dht)
+    dht[0, 1, 7, 9] = float("nan")
+    r = gdn.bwd(q, k, v, d, b, SCALE, dout, h0, dht)
+    keep = torch.ones(D, dtype=torch.bool, device=q.device)
+    keep[7] = False
+    assert torch.equal(r["dinitial_state"][:, 1, keep], clean["dinitial_state"][:, 1, keep])
+    assert torch.equal(r["dv"][:, :, 1, keep], clean["dv"][:, :, 1, keep]) and torch.equal(r["dv"][:, :, 0], clean["dv"][:, :, 0])
+    assert r["dinitial_state"][0, 1, 7].isnan().all() and r["dv"][:, :, 1, 7].isnan().all()
