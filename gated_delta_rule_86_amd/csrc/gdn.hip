@@ -25,6 +25,7 @@
 // exponential of a difference and at most 1.  The products run on bf16 MFMA with fp32 accumulation; q, k, v are
 // bf16 as they come, every other factor is cut into three bf16 terms, hi + mid + lo: the 24 bits of fp32.
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "gdn_internal.h"
@@ -166,10 +167,8 @@ __device__ __forceinline__ void load_lds(const void *base, uint32_t bytes, uint3
                      : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(off), "s"(r)
                      : "memory");
 }
-__device__ __forceinline__ uint32_t lds_address(const void *p)
-{
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)p;
-}
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+#define lds_base(array) ((uint32_t)(uintptr_t)(lds_byte *)(array))
 // Everything that this wave has in flight has arrived, and then the other waves' too.
 __device__ __forceinline__ void arrive()
 {
@@ -689,13 +688,13 @@ struct LdsWalk {
 // Half n of a tile straight into LDS: 4 rows an instruction, wave w of kWaves takes rows 4w .. and those 4 kWaves behind
 // them.  Rows behind the chunk lie beyond the descriptor and arrive as zeros.
 template <int kWaves>
-__device__ __forceinline__ void tile_half(const unsigned char *lds, const GdnTensor &x, const uint16_t *base, int64_t t0, int len,
+__device__ __forceinline__ void tile_half(uint32_t lds, const GdnTensor &x, const uint16_t *base, int64_t t0, int len,
                                           int n, int wave, int lane)
 {
     const uint32_t stride = (uint32_t)x.st * 2;
     const int row = 4 * wave + (lane >> 4);
     const uint32_t off = (uint32_t)(row + 4 * kWaves * n) * stride + (uint32_t)(((lane & 15) ^ swz(row)) << 4);
-    load_lds(base + t0 * x.st, len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u, off, lds_address(lds) + 1024 * (wave + kWaves * n));
+    load_lds(base + t0 * x.st, len > 0 ? (uint32_t)(len - 1) * stride + 256u : 0u, off, lds + 1024 * (wave + kWaves * n));
 }
 
 // Transposing read: lane i of each 16 lanes gives the address of 4 channels of token i / 4 and gets channel i of
@@ -841,8 +840,9 @@ __device__ __forceinline__ void rows_store(float *m, const f32x16 &x, int lane)
         m[(8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)) * kD + (lane & 31)] = x[i];
 }
 
+// at: where in LDS `lds` begins
 template <int kMode>
-__device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row, int64_t p, int64_t h)
+__device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, uint32_t at, int64_t row, int64_t p, int64_t h)
 {
     constexpr bool kOut = kMode == kModeOut, kValues = kMode != kModePhi;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31;
@@ -901,13 +901,13 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
             return;
         if (part < 2 * kTiles) {
             const int t = part >> 1;
-            tile_half<kWalkWaves>(lds.tile[buf][t], t == 0 ? a.k : t == 1 ? a.v : a.q, t == 0 ? pk : t == 1 ? pv : pq, n.t0, n.len,
+            tile_half<kWalkWaves>(at + kTile * (3 * buf + t), t == 0 ? a.k : t == 1 ? a.v : a.q, t == 0 ? pk : t == 1 ? pv : pq, n.t0, n.len,
                                   part & 1, wave, lane);
         } else {
             int i = wave + kWalkWaves * (part - 2 * kTiles);  // the last KiB by several waves, rather than a branch
             i = i < kBytes / 1024 ? i : kBytes / 1024 - 1;
             load_lds(a.rec + (n.slot * a.H + h) * a.rec_bytes, n.len ? kBytes : 0, (uint32_t)(1024 * i + 16 * lane),
-                     lds_address(lds.rec[buf]) + 1024 * i);
+                     at + (int)offsetof(LdsWalk, rec) + (int)sizeof(lds.rec[0]) * buf + 1024 * i);
         }
     };
     State S;
@@ -1090,14 +1090,16 @@ __device__ __forceinline__ void walk(const GdnArgs &a, LdsWalk &lds, int64_t row
     store_held();
 }
 
-// Workgroup b of a walk: head b % H of segment b / H
+// Workgroup b of a walk: segment b % (rows P) of head b / (rows P).  Neighbours run on different XCDs, so that each of them gets
+// its share of every head (how long a share or transition takes depends on the head's decays), and heads that share q and k
+// meet in one XCD's cache.
 struct Place {
     int64_t row, p, h;
 
     __device__ explicit Place(const GdnArgs &a)
     {
-        const uint32_t b = blockIdx.x, s = b / (uint32_t)a.H;
-        h = b - s * (uint32_t)a.H;
+        const uint32_t b = blockIdx.x, n = (uint32_t)(a.rows * a.P), s = b % n;
+        h = b / n;
         row = s / (uint32_t)a.P;
         p = s - (uint32_t)row * (uint32_t)a.P;
     }
@@ -1107,23 +1109,23 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_out_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
     const Place at(a);
-    walk<kModeOut>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
+    walk<kModeOut>(a, *reinterpret_cast<LdsWalk *>(raw), lds_base(raw), at.row, at.p, at.h);
 }
-// y = 0: shares, y = 1: transitions
+// y = 0: transitions, y = 1: shares: the former end at once where they count as 0, so that all long ones begin early
 __global__ __launch_bounds__(kWalkThreads, 2) void gdn_cut_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
     const Place at(a);
-    if (blockIdx.y == 0)
-        walk<kModeShare>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
+    if (blockIdx.y == 1)
+        walk<kModeShare>(a, *reinterpret_cast<LdsWalk *>(raw), lds_base(raw), at.row, at.p, at.h);
     else
-        walk<kModePhi>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
+        walk<kModePhi>(a, *reinterpret_cast<LdsWalk *>(raw), lds_base(raw), at.row, at.p, at.h);
 }
 __global__ __launch_bounds__(kWalkThreads, 2) void gdn_store_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
     const Place at(a);
-    walk<kModeStore>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
+    walk<kModeStore>(a, *reinterpret_cast<LdsWalk *>(raw), lds_base(raw), at.row, at.p, at.h);
 }
 
 // ----------------------------------------------------------------------------------- scan
@@ -1246,7 +1248,7 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
 // dL/dS from a sequence's end to its start, in the same layout; stores it after each block, and dw.
 
 template <bool kShare>
-__device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_t row, int64_t p, int64_t h)
+__device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, uint32_t at, int64_t row, int64_t p, int64_t h)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int v = 32 * wave + (lane & 31);
@@ -1293,13 +1295,13 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, int64_
             return;
         if (part < 6) {
             const int t = part >> 1;
-            tile_half<kWalkWaves>(lds.tile[buf][t], t == 0 ? a.k : t == 1 ? a.dout : a.q, t == 0 ? pk : t == 1 ? po : pq, n.t0, n.len,
+            tile_half<kWalkWaves>(at + kTile * (3 * buf + t), t == 0 ? a.k : t == 1 ? a.dout : a.q, t == 0 ? pk : t == 1 ? po : pq, n.t0, n.len,
                                   part & 1, wave, lane);
         } else {
             int i = wave + kWalkWaves * (part - 6);
             i = i < kBytes / 1024 ? i : kBytes / 1024 - 1;
             load_lds(a.rec + (n.slot * a.H + h) * a.rec_bytes + kGdnMat, n.len ? kBytes : 0, (uint32_t)(1024 * i + 16 * lane),
-                     lds_address(lds.rec[buf]) + 1024 * i);
+                     at + (int)offsetof(LdsWalk, rec) + (int)sizeof(lds.rec[0]) * buf + 1024 * i);
         }
     };
     State S;
@@ -1454,7 +1456,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_back_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
     const Place at(a);
-    walk_back<kShare>(a, *reinterpret_cast<LdsWalk *>(raw), at.row, at.p, at.h);
+    walk_back<kShare>(a, *reinterpret_cast<LdsWalk *>(raw), lds_base(raw), at.row, at.p, at.h);
 }
 
 // ------------------------------------------------------------------- gradients of a block
@@ -1499,12 +1501,12 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
     const int len = (int)(rest < kGB ? rest : kGB);
     const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGB, tok0 = row * a.T + t0;
     const int64_t slot = slot_of(begin, seq) + 2 * c;
-    tile_half<8>(s.k, a.k, head_base(a.k, row, head), t0, len, 0, wave, lane);
-    tile_half<8>(s.k, a.k, head_base(a.k, row, head), t0, len, 1, wave, lane);
-    tile_half<8>(s.q, a.q, head_base(a.q, row, head), t0, len, 0, wave, lane);
-    tile_half<8>(s.q, a.q, head_base(a.q, row, head), t0, len, 1, wave, lane);
-    tile_half<8>(s.o, a.dout, head_base(a.dout, row, head), t0, len, 0, wave, lane);
-    tile_half<8>(s.o, a.dout, head_base(a.dout, row, head), t0, len, 1, wave, lane);
+    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, k), a.k, head_base(a.k, row, head), t0, len, 0, wave, lane);
+    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, k), a.k, head_base(a.k, row, head), t0, len, 1, wave, lane);
+    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, q), a.q, head_base(a.q, row, head), t0, len, 0, wave, lane);
+    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, q), a.q, head_base(a.q, row, head), t0, len, 1, wave, lane);
+    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, o), a.dout, head_base(a.dout, row, head), t0, len, 0, wave, lane);
+    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, o), a.dout, head_base(a.dout, row, head), t0, len, 1, wave, lane);
     // the state's columns of this wave: lane = key channel, elements 8 x + j: value row 16 x + 8 h + j
     const int kg = wave & 3, kc = 32 * kg + column_of<true>(l32);
     const int64_t at = (block * a.H + head) * kD * kD;
