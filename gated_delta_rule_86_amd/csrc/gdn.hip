@@ -1461,35 +1461,42 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_back_kernel(GdnArgs a)
 
 // ------------------------------------------------------------------- gradients of a block
 //
-// One workgroup of 8 waves per (block of 64 tokens, head); the formulas hold for blocks of any length, r_t and dw_t are the
-// tokens' own.  w = beta r and dx = beta dw are cut into bf16 terms once, in LDS.  Waves 0 .. 3 form what the state before
-// the block gives to dq and dk, 32 key channels each (rows: channels, a lane's token is lane % 32); waves 4 .. 7 what its
-// gradient behind the block gives to dk, and the 32 x 32 tiles of P, P^T and G + G^T, which all reach the first four through
-// LDS in the place of the terms.
+// One workgroup of 4 waves per (block of 64 tokens, head), two of them on a CU, so that one computes while the other's loads
+// are on their way; the formulas hold for blocks of any length, r_t and dw_t are the tokens' own.  Each wave forms what the
+// state before the block and its gradient behind it give to dq and dk, 32 key channels each (rows: channels, a lane's token
+// is lane % 32): it takes them from memory, cut as they come.  w = beta r and dx = beta dw stay in LDS in fp32 and are cut
+// where they are used, which takes less room and time than their terms would.  Then the waves share out the 32 x 32 tiles of
+// P, P^T and G + G^T, which reach all of them through LDS, in the place of w and dx.
 
+// LDS: w and dx, 64 rows of 32 pieces of 16 bytes each, piece u of row t at u ^ (t % 16), and dout.  Behind the products with
+// them: the matrices (steps of 3 KiB), k, q, and what is below.
+constexpr int kGradX = kGB * 512, kGradO = 2 * kGradX, kGradLds = kGradO + kGB * 256;
+// P: columns tokens t, contraction sources, steps 0 .. 1 + 2 t; P^T: columns sources s, contraction tokens, steps 2 s .. 3; then, in
+// their place, G + G^T, all steps
+constexpr int kGradP = 0, kGradPT = 6, kGradMats = 12;
+constexpr int kGradK = kGradMats * 3072, kGradQ = kGradK + kGB * 256;
 struct LdsGrad {
-    unsigned char k[kGB * 256], q[kGB * 256], o[kGB * 256];
-    unsigned char w[3][kGB * 256], x[3][kGB * 256];  // terms of w and dx; then the matrices and dk's share
-    float bh[kGB], bl[kGB], from[kGB], tail[kGB];    // running sums of log2 decays as pairs, and their factors
-    float last;
-    float sums[4][kGB];   // q.dq of each wave's channels
+    float bh[4][kGB], bl[4][kGB];  // running sums of log2 decays as pairs, a copy for each wave
+    float sums[4][kGB];            // q.dq of each wave's channels
     float vdv[kGB];
-    float end[4];         // <dS, S_after>, a wave's share
+    float end[4];                  // <dS, S_after>, a wave's share
 };
-// Steps of the matrices in LDS (3 KiB each).  P: columns tokens t, contraction sources, steps 0 .. 1 + 2 t; P^T: columns sources s,
-// contraction tokens, steps 2 s .. 3; G + G^T all.
-constexpr int kGradP = 0, kGradPT = 6, kGradG = 12, kGradMats = 20;
+constexpr int kGradRest = kGradQ + kGB * 256;
+static_assert(kGradRest + sizeof(LdsGrad) <= kGradLds, "the second half reuses the first's room");
 
-__device__ __forceinline__ Terms row_terms(const unsigned char (*t)[kGB * 256], const Lanes &ln, int x, int block)
+// This wave's writes to LDS are done, and then the other waves'; loads from memory stay in flight.
+__device__ __forceinline__ void settle()
 {
-    return Terms{row_frag(t[0], ln, x, block), row_frag(t[1], ln, x, block), row_frag(t[2], ln, x, block)};
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
 }
 
-__global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
+__global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) unsigned char raw[];
-    LdsGrad &s = *reinterpret_cast<LdsGrad *>(raw);
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, h = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, kg = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, h = lane >> 5;
     const int64_t block = blockIdx.x / (uint32_t)a.H, head = blockIdx.x - (uint32_t)block * (uint32_t)a.H;
     if (a.status && *a.status != 0)
         return;
@@ -1501,316 +1508,317 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
     const int len = (int)(rest < kGB ? rest : kGB);
     const int64_t row = a.cu ? 0 : seq, t0 = (a.cu ? begin : 0) + c * kGB, tok0 = row * a.T + t0;
     const int64_t slot = slot_of(begin, seq) + 2 * c;
-    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, k), a.k, head_base(a.k, row, head), t0, len, 0, wave, lane);
-    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, k), a.k, head_base(a.k, row, head), t0, len, 1, wave, lane);
-    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, q), a.q, head_base(a.q, row, head), t0, len, 0, wave, lane);
-    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, q), a.q, head_base(a.q, row, head), t0, len, 1, wave, lane);
-    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, o), a.dout, head_base(a.dout, row, head), t0, len, 0, wave, lane);
-    tile_half<8>(lds_base(raw) + (int)offsetof(LdsGrad, o), a.dout, head_base(a.dout, row, head), t0, len, 1, wave, lane);
-    // the state's columns of this wave: lane = key channel, elements 8 x + j: value row 16 x + 8 h + j
-    const int kg = wave & 3, kc = 32 * kg + column_of<true>(l32);
-    const int64_t at = (block * a.H + head) * kD * kD;
-    // one lane offset for all of them, the rest sits in the instruction
-    const __amdgpu_buffer_rsrc_t rs = rsrc(a.before + at, kGdnStateBytes), rd = rsrc(a.dafter + at, kGdnStateBytes);
-    const int lane_at = 4 * (8 * h * kD + kc);
-    auto element = [&](__amdgpu_buffer_rsrc_t r, int i) {
-        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, 4 * kD * (16 * (i >> 3) + (i & 7)), 0));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // two rows an instruction; a chunk without tokens has none and arrives as zeros
+        const int n = kg + 4 * i, chunk = n >> 4, t = 2 * n + h;
+        const int64_t from = ((slot + chunk) * a.H + head) * kGC * kD;
+        const uint32_t off = (uint32_t)((t & 31) * 512 + ((l32 ^ (t & 15)) << 4)), bytes = len > kGC * chunk ? kGC * kD * 4 : 0;
+        load_lds(a.res + from, bytes, off, lds_base(raw) + 1024 * n);
+        load_lds(a.dwrite + from, bytes, off, lds_base(raw) + kGradX + 1024 * n);
+    }
+    auto load_tile = [&](const GdnTensor &x, int to) {
+        const uint16_t *p = head_base(x, row, head);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            tile_half<4>(lds_base(raw) + to, x, p, t0, len, n, kg, lane);
     };
-    float S[64];
-    if (wave < 4) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-            S[i] = element(rs, i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-            S[i] = element(rd, i);
-    }
-    if (wave == 7) {
-        const float dec = lane < len ? a.decay[(tok0 + lane) * a.H + head] : 0.0f;
-        const double b = running_sum64((double)clamp_decay(dec) * kLog2e64), last = of_lane(b, 63);
-        s.bh[lane] = (float)b;
-        s.bl[lane] = (float)(b - (double)(float)b);
-        s.from[lane] = __builtin_amdgcn_exp2f((float)b);
-        s.tail[lane] = __builtin_amdgcn_exp2f((float)(last - b));
-        if (lane == 0)
-            s.last = __builtin_amdgcn_exp2f((float)last);
-    }
-    // rows of r and dw: thread = token tid / 8, value channels 16 (tid % 8) ..
+    load_tile(a.dout, kGradO);
+    // rows of v: thread = token tid / 4, value channels 32 (tid % 4) ..
+    const int rt = tid >> 2, v0 = 32 * (tid & 3);
+    const bool on = rt < len;
+    u32x4 rv[4];
     {
-        const int t = tid >> 3, v0 = 16 * (tid & 7);
-        const bool on = t < len;
-        const int64_t from = ((slot + (t >> 5)) * a.H + head) * kGC * kD + (t & 31) * kD + v0;  // a chunk without tokens has no rows
-        const float *pr = a.res + (on ? from : (slot * a.H + head) * kGC * kD), *pw = a.dwrite + (pr - a.res);
-        const float be = on ? a.beta[(tok0 + t) * a.H + head] : 0.0f;
-        const uint16_t *pv = head_base(a.v, row, head) + (t0 + (on ? t : 0)) * a.v.st + v0;
-        const u32x4 vv[2] = {*reinterpret_cast<const u32x4 *>(pv), *reinterpret_cast<const u32x4 *>(pv + 8)};
-        float db = 0.0f, vd = 0.0f;
+        const u32x4 *pv = reinterpret_cast<const u32x4 *>(head_base(a.v, row, head) + (t0 + (on ? rt : 0)) * a.v.st + v0);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            f32x4 r[2], d[2], x[2];
+        for (int i = 0; i < 4; ++i)
+            rv[i] = pv[i];
+    }
+    const float rb = on ? a.beta[(tok0 + rt) * a.H + head] : 0.0f;
+    const float rg = lane < len ? a.decay[(tok0 + lane) * a.H + head] : 0.0f;
+    // the states' columns of this wave: lane = key channel, element 8 x + j: value row 16 x + 8 h + j
+    const int64_t at = (block * a.H + head) * kD * kD;
+    const __amdgpu_buffer_rsrc_t rs = rsrc(a.before + at, kGdnStateBytes), rd = rsrc(a.dafter + at, kGdnStateBytes);
+    const int lane_at = 4 * (8 * h * kD + 32 * kg + column_of<true>(l32));
+    struct Piece {
+        f32x4 a, b;
+    };
+    auto piece = [&](__amdgpu_buffer_rsrc_t r, int x) {
+        Piece y;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                r[e] = *reinterpret_cast<const f32x4 *>(pr + 8 * hf + 4 * e);
-                d[e] = *reinterpret_cast<const f32x4 *>(pw + 8 * hf + 4 * e);
-                if (!on)
-                    r[e] = d[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                x[e] = d[e] * be;
-                const f32x4 v4 = widen4(u32x2{vv[hf][2 * e], vv[hf][2 * e + 1]});
+        for (int j = 0; j < 4; ++j) {
+            y.a[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at + 4 * kD * j, 64 * kD * x, 0));
+            y.b[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane_at + 4 * kD * (4 + j), 64 * kD * x, 0));
+        }
+        return y;
+    };
+    // of each token in lane: its logarithm as a pair
+    const double b64 = running_sum64((double)clamp_decay(rg) * kLog2e64), last64 = of_lane(b64, 63);
+    const float bh = (float)b64, bl = (float)(b64 - (double)bh);
+    const float from1 = __builtin_amdgcn_exp2f((float)b64), tail1 = __builtin_amdgcn_exp2f((float)(last64 - b64));
+    const float last = __builtin_amdgcn_exp2f((float)last64);
+    arrive();
+    float vd = 0.0f;
+    {
+        float db = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    db = fmaf(d[e][i], r[e][i], db);
-                    vd = fmaf(x[e][i], v4[i], vd);
-                }
-                r[e] *= be;
+        for (int i = 0; i < 8; ++i) {  // scaled by beta in place
+            const int p = rt * 512 + (((8 * (tid & 3) + i) ^ (rt & 15)) << 4);
+            f32x4 r = *reinterpret_cast<const f32x4 *>(raw + p), d = *reinterpret_cast<const f32x4 *>(raw + kGradX + p);
+            if (!on)
+                r = d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const f32x4 x = d * rb, v4 = widen4(u32x2{rv[i >> 1][2 * (i & 1)], rv[i >> 1][2 * (i & 1) + 1]});
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                db = fmaf(d[e], r[e], db);
+                vd = fmaf(x[e], v4[e], vd);
             }
-            const int to = t * 256 + (((2 * (tid & 7) + hf) ^ swz(t)) << 4);
-            Terms y = cut8(r[0], r[1]);
-            *reinterpret_cast<u32x4 *>(s.w[0] + to) = y.h;
-            *reinterpret_cast<u32x4 *>(s.w[1] + to) = y.m;
-            *reinterpret_cast<u32x4 *>(s.w[2] + to) = y.l;
-            y = cut8(x[0], x[1]);
-            *reinterpret_cast<u32x4 *>(s.x[0] + to) = y.h;
-            *reinterpret_cast<u32x4 *>(s.x[1] + to) = y.m;
-            *reinterpret_cast<u32x4 *>(s.x[2] + to) = y.l;
-            if (on)
-                *reinterpret_cast<u32x4 *>(a.dv + ((tok0 + t) * a.H + head) * kD + v0 + 8 * hf) =
-                    u32x4{pack2(x[0][0], x[0][1]), pack2(x[0][2], x[0][3]), pack2(x[1][0], x[1][1]), pack2(x[1][2], x[1][3])};
+            *reinterpret_cast<f32x4 *>(raw + p) = r * rb;
+            *reinterpret_cast<f32x4 *>(raw + kGradX + p) = x;
+            rv[i >> 1][2 * (i & 1)] = pack2(x[0], x[1]);
+            rv[i >> 1][2 * (i & 1) + 1] = pack2(x[2], x[3]);
+        }
+        if (on) {
+            u32x4 *dv = reinterpret_cast<u32x4 *>(a.dv + ((tok0 + rt) * a.H + head) * kD + v0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dv[i] = rv[i];
         }
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {
+        for (int o = 2; o > 0; o >>= 1) {
             db += __shfl_xor(db, o);
             vd += __shfl_xor(vd, o);
         }
-        if ((tid & 7) == 0) {
-            s.vdv[t] = on ? vd : 0.0f;
-            if (on)
-                a.dbeta[(tok0 + t) * a.H + head] = db;
-        }
+        if (on && (tid & 3) == 0)
+            a.dbeta[(tok0 + rt) * a.H + head] = db;
     }
-    arrive();
-    const Lanes ln(lane);
-    auto terms_of = [&](int x) {
-        return cut8(f32x4{S[8 * x], S[8 * x + 1], S[8 * x + 2], S[8 * x + 3]},
-                    f32x4{S[8 * x + 4], S[8 * x + 5], S[8 * x + 6], S[8 * x + 7]});
-    };
-    // 16 channels 32 kg + 16 h .. of token 32 th + lane % 32
-    auto mine = [&](const unsigned char *tile, int th, float *y) {
+    Piece ps[2], pd[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = 32 * th + l32, piece = 4 * kg + 2 * h + e;
-            const u32x4 u = *reinterpret_cast<const u32x4 *>(tile + t * 256 + ((piece ^ swz(t)) << 4));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[8 * e + 2 * i] = lo_f(u[i]);
-                y[8 * e + 2 * i + 1] = hi_f(u[i]);
-            }
-        }
+    for (int x = 0; x < 2; ++x) {
+        ps[x] = piece(rs, x);
+        pd[x] = piece(rd, x);
+    }
+    settle();
+    Lanes ln(lane);
+    int row4 = l32 * 512 + (((2 * h) ^ (l32 & 15)) << 4);
+    // 8 values 16 x + 8 h .. of row 32 th + lane % 32 of w or dx
+    auto terms = [&](int which, int x, int th) {
+        const unsigned char *p = raw + which + 16384 * th + 256 * (x >> 2);
+        return cut8(*reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3)))),
+                    *reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3) + 16))));
     };
-    unsigned char *mats = s.w[0], *share = mats + kGradMats * 3072;
-    f32x16 dq[2], dk[2];
-    if (wave < 4) {
-        dq[0] = dq[1] = dk[0] = dk[1] = zero16();
+    float dot = 0.0f;  // <dS, S_after>, this lane's share
+    f32x16 dq[2], dk[2], put[4];
+    {
+        f32x16 dw[2];
+        dq[0] = dq[1] = dk[0] = dk[1] = dw[0] = dw[1] = zero16();
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const Terms c8 = terms_of(x);
+            const Piece s = ps[x & 1], d = pd[x & 1];
+            if (x < 6) {
+                ps[x & 1] = piece(rs, x + 2);
+                pd[x & 1] = piece(rd, x + 2);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                dot = fmaf(s.b[j], d.b[j], fmaf(s.a[j], d.a[j], dot));
+            __asm__ volatile("" : "+v"(dot));  // here: put off, it would keep the pieces
+            const Terms cs = cut8(s.a, s.b), cd = cut8(d.a, d.b);
 #pragma unroll
             for (int th = 0; th < 2; ++th) {
-                dq[th] = mfma3(c8, row_frag(s.o, ln, x, th), dq[th]);
-                dk[th] = mfma6(c8, row_terms(s.x, ln, x, th), dk[th]);
+                dq[th] = mfma3(cs, row_frag(raw + kGradO, ln, x, th), dq[th]);
+                dk[th] = mfma6(cs, terms(kGradX, x, th), dk[th]);
+                dw[th] = mfma6(cd, terms(0, x, th), dw[th]);
             }
             __builtin_amdgcn_sched_barrier(0);  // one step at a time: more of them in flight do not fit the registers
         }
+        dot *= last;
+        const uint16_t *pk = head_base(a.k, row, head);
 #pragma unroll
         for (int th = 0; th < 2; ++th) {
-            dq[th] *= a.scale * s.from[32 * th + l32];
-            dk[th] *= -s.from[32 * th + l32];
-        }
-        __syncthreads();
-    } else {
-        float dot = 0.0f;
+            const int t = 32 * th + l32;
+            const float from = __shfl(from1, t), tail = __shfl(tail1, t);
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(pk + (t0 + (t < len ? t : 0)) * a.k.st + 32 * kg + 16 * h);
+            const u32x4 k16[2] = {p[0], p[1]};
+            dq[th] *= a.scale * from;
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            dot = fmaf(S[i], element(rs, i), dot);
-        dot *= s.last;
-        dk[0] = dk[1] = zero16();
+            for (int i = 0; i < 16; ++i) {
+                const float y = dw[th][i] * tail;  // 0 behind the block
+                const uint32_t u = k16[i >> 3][(i & 7) >> 1];
+                dot = fmaf(y, i & 1 ? hi_f(u) : lo_f(u), dot);
+                dk[th][i] = y - from * dk[th][i];
+            }
+            __asm__ volatile("" : "+v"(dq[th]), "+v"(dk[th]), "+v"(dot));
+        }
+    }
+    // The tiles, unscaled: the product of rows of token tile i by rows of token tile j, and the transposed one of the same
+    // operands.  Their terms are cut anew, from places that the compiler cannot tell to be those above: kept from there they would
+    // not fit the registers.
+    __asm__ volatile("" : "+v"(row4), "+v"(ln.row));
+    auto g_pair = [&](int i, int j, f32x16 &y, f32x16 &yt) {
+        y = yt = zero16();
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const Terms c8 = terms_of(x);
-#pragma unroll
-            for (int th = 0; th < 2; ++th)
-                dk[th] = mfma6(c8, row_terms(s.w, ln, x, th), dk[th]);
+            const Terms w = terms(0, x, i), d = terms(kGradX, x, j);
+            y = mfma6(w, d, y);
+            yt = mfma6(d, w, yt);
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    auto p_pair = [&](int i, int j, f32x16 &y, f32x16 &yt) {
+        y = yt = zero16();
 #pragma unroll
-        for (int th = 0; th < 2; ++th) {
-            dk[th] *= s.tail[32 * th + l32];
-            float k16[16];
-            mine(s.k, th, k16);
+        for (int x = 0; x < 8; ++x) {
+            const Terms w = terms(0, x, i);
+            const u32x4 o = row_frag(raw + kGradO, ln, x, j);
+            y = mfma3(w, o, y);
+            yt = mfma3(o, w, yt);
+            if (x & 1)
+                __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // P(0, 1) or, transposed, P^T(1, 0)
+    auto p_far = [&](bool low) {
+        f32x16 y = zero16();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const Terms w = terms(0, x, 0);
+            const u32x4 o = row_frag(raw + kGradO, ln, x, 1);
+            y = low ? mfma3(w, o, y) : mfma3(o, w, y);
+            if (x & 1)
+                __builtin_amdgcn_sched_barrier(0);
+        }
+        return y;
+    };
+    // waves 0 .. 2: G and G^T of tiles 00, 11, 01; 3: the diagonal tiles of P and P^T; the others of P, P^T: waves 0 and 1
+    if (kg < 3)
+        g_pair(kg == 1, kg != 0, put[0], put[1]);
+    if (kg == 0) {
+        put[2] = p_far(true);
+    } else if (kg == 1) {
+        put[2] = p_far(false);
+    } else if (kg == 3) {
+        p_pair(0, 0, put[0], put[1]);
+        p_pair(1, 1, put[2], put[3]);
+    }
+    settle();  // w, dx and dout are read by no one
+    load_tile(a.k, kGradK);
+    load_tile(a.q, kGradQ);
+    LdsGrad &s = *reinterpret_cast<LdsGrad *>(raw + kGradRest);
+    s.bh[kg][lane] = bh;
+    s.bl[kg][lane] = bl;
+    if ((tid & 3) == 0)
+        s.vdv[rt] = on ? vd : 0.0f;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        dot += __shfl_xor(dot, o);
+    if (lane == 0)
+        s.end[kg] = dot;
+    // times f e^{b_t - b_u} for u <= t (strict: u < t), formed where it is used, and 0 elsewhere
+    auto scaled = [&](int rt, int ct, f32x16 d, float f, bool low, bool strict) {
+        const float ch = s.bh[kg][32 * ct + l32], cl = s.bl[kg][32 * ct + l32], sign = low ? 1.0f : -1.0f;
+        const int c0 = 32 * (ct - rt) + l32 - 4 * h, side = low ? 1 : -1;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const f32x4 rh = *reinterpret_cast<const f32x4 *>(&s.bh[kg][32 * rt + 8 * n + 4 * h]);
+            const f32x4 rl = *reinterpret_cast<const f32x4 *>(&s.bl[kg][32 * rt + 8 * n + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ahead = side * (c0 - (8 * n + i));  // of the source, in tokens
+                const float b = sign * ((ch - rh[i]) + (cl - rl[i]));
+                const float z = d[4 * n + i] * f * __builtin_amdgcn_exp2f(ahead >= 0 ? b : 0.0f);
+                d[4 * n + i] = ahead >= (strict ? 1 : 0) ? z : 0.0f;
+            }
+        }
+        return d;
+    };
+    auto store = [&](int step, const f32x16 &y) {
+        store_terms(raw, step, lane, cut8(y, 0));
+        store_terms(raw, step + 1, lane, cut8(y, 1));
+    };
+    if (kg == 0) {
+        store(kGradP + 2, scaled(0, 1, put[2], a.scale, true, false));
+    } else if (kg == 1) {
+        store(kGradPT + 2, scaled(1, 0, put[2], a.scale, false, false));
+    } else if (kg == 3) {
+        store(kGradP, scaled(0, 0, put[0], a.scale, true, false));
+        store(kGradPT, scaled(0, 0, put[1], a.scale, false, false));
+        store(kGradP + 4, scaled(1, 1, put[2], a.scale, true, false));
+        store(kGradPT + 4, scaled(1, 1, put[3], a.scale, false, false));
+    }
+    f32x16 g, gt;
+    if (kg < 3) {
+        g = scaled(kg == 1, kg != 0, put[0], -1.0f, true, true);
+        gt = scaled(kg != 0, kg == 1, put[1], -1.0f, false, true);
+        if (kg < 2)  // both triangles of one tile
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                dot = fmaf(dk[th][i], k16[i], dot);
-        }
+                g[i] = (i & 3) + 8 * (i >> 2) + 4 * h < l32 ? g[i] : gt[i];
+    }
+    arrive();  // P, P^T, k, q
+    auto key = [&](int tile, int st) { return col_frag(raw + tile + 8192 * (st >> 1), ln.out, kg, st & 1); };
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1)
-            dot += __shfl_xor(dot, o);
-        if (lane == 0)
-            s.end[kg] = dot;
-        // The tiles: rows of row tile rt (a lane's 16 in the order of a D tile), columns of column tile ct.  e^{b_t - b_u} for u <= t
-        // is formed where it is used.
-        auto tile = [&](int rt, int ct, const f32x16 &d, float f, bool low, f32x16 y) {  // low: rows are the sources
-            const float ch = s.bh[32 * ct + l32], cl = s.bl[32 * ct + l32];
+    for (int st = 0; st < 4; ++st) {  // 16 tokens each of the contraction
+        const u32x4 kc4 = key(kGradK, st), qc4 = key(kGradQ, st);
+#pragma unroll
+        for (int th = 0; th < 2; ++th) {
+            if (st < 2 + 2 * th)
+                dq[th] = mfma3(kc4, load_terms(raw, kGradP + 2 * th + st, lane), dq[th]);
+            if (st >= 2 * th)
+                dk[th] = mfma3(qc4, load_terms(raw, kGradPT + 2 * th + st, lane), dk[th]);
+        }
+    }
+    settle();
+    if (kg < 3)
+        store(kg == 2 ? 4 : 6 * kg, g);
+    if (kg == 2)
+        store(2, gt);
+    settle();
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+        const u32x4 kc4 = key(kGradK, st);
+#pragma unroll
+        for (int th = 0; th < 2; ++th)
+            dk[th] = mfma3(kc4, load_terms(raw, 4 * th + st, lane), dk[th]);
+    }
+#pragma unroll
+    for (int th = 0; th < 2; ++th) {
+        const int t = 32 * th + l32;
+        float y1 = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // 16 channels 32 kg + 16 h .. of token t
+            const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + kGradQ + t * 256 + (((4 * kg + 2 * h + e) ^ swz(t)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y1 = fmaf(dq[th][8 * e + 2 * i + 1], hi_f(u[i]), fmaf(dq[th][8 * e + 2 * i], lo_f(u[i]), y1));
+        }
+        y1 += __shfl_xor(y1, 32);
+        if (h == 0)
+            s.sums[kg][t] = y1;
+        if (t >= len)
+            continue;
+        const int64_t to = ((tok0 + t) * a.H + head) * kD + 32 * kg + 16 * h;
+        if (a.dq_h) {
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const f32x4 rh = *reinterpret_cast<const f32x4 *>(&s.bh[32 * rt + 8 * n + 4 * h]);
-                const f32x4 rl = *reinterpret_cast<const f32x4 *>(&s.bl[32 * rt + 8 * n + 4 * h]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rw = 32 * rt + 8 * n + 4 * h + i, cl_ = 32 * ct + l32;
-                    const float b = low ? (ch - rh[i]) + (cl - rl[i]) : (rh[i] - ch) + (rl[i] - cl);
-                    const bool on = low ? rw <= cl_ : rw >= cl_;
-                    const float z = d[4 * n + i] * (f * __builtin_amdgcn_exp2f(on ? b : 0.0f));
-                    // P with its diagonal; G without, one triangle at a time
-                    y[4 * n + i] = (f < 0.0f ? on && rw != cl_ : on) ? z : y[4 * n + i];
-                }
+                reinterpret_cast<f32x4 *>(a.dq_h + to)[n] = f32x4{dq[th][4 * n], dq[th][4 * n + 1], dq[th][4 * n + 2], dq[th][4 * n + 3]};
+                reinterpret_cast<f32x4 *>(a.dk_h + to)[n] = f32x4{dk[th][4 * n], dk[th][4 * n + 1], dk[th][4 * n + 2], dk[th][4 * n + 3]};
             }
-            return y;
-        };
-        f32x16 put[3];
-        int where[3] = {-1, -1, -1};
-        auto keep = [&](int n, int step, const f32x16 &y) {  // 2 steps each, written when the terms in LDS are done with
-            put[n] = y;
-            where[n] = step;
-        };
-        // P and P^T are scaled by a factor above 0 and G by -1; with a scale of 0 or below the sign is taken apart
-        auto p_low = [&](int rt, int ct) {
-            f32x16 d = zero16();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                d = mfma3(row_terms(s.w, ln, x, rt), row_frag(s.o, ln, x, ct), d);
-                if (x & 1)
-                    __builtin_amdgcn_sched_barrier(0);
-            }
-            return tile(rt, ct, d * a.scale, 1.0f, true, zero16());
-        };
-        auto p_high = [&](int rt, int ct) {
-            f32x16 d = zero16();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                d = mfma3(row_frag(s.o, ln, x, rt), row_terms(s.w, ln, x, ct), d);
-                if (x & 1)
-                    __builtin_amdgcn_sched_barrier(0);
-            }
-            return tile(rt, ct, d * a.scale, 1.0f, false, zero16());
-        };
-        auto g_low = [&](int rt, int ct, const f32x16 &y) {
-            f32x16 d = zero16();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                d = mfma6(row_terms(s.w, ln, x, rt), row_terms(s.x, ln, x, ct), d);
-                if (x & 1)
-                    __builtin_amdgcn_sched_barrier(0);
-            }
-            return tile(rt, ct, d, -1.0f, true, y);
-        };
-        auto g_high = [&](int rt, int ct, const f32x16 &y) {
-            f32x16 d = zero16();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                d = mfma6(row_terms(s.x, ln, x, rt), row_terms(s.w, ln, x, ct), d);
-                if (x & 1)
-                    __builtin_amdgcn_sched_barrier(0);
-            }
-            return tile(rt, ct, d, -1.0f, false, y);
-        };
-        if (kg < 2) {  // the diagonal tiles of G + G^T and of P
-            keep(0, kGradG + 4 * kg + 2 * kg, g_high(kg, kg, g_low(kg, kg, zero16())));
-            keep(1, kGradP + (kg ? 4 : 0), p_low(kg, kg));
-        } else if (kg == 2) {
-            keep(0, kGradG + 4, g_low(0, 1, zero16()));
-            keep(1, kGradG + 2, g_high(1, 0, zero16()));
-            keep(2, kGradP + 2, p_low(0, 1));
         } else {
-            keep(0, kGradPT, p_high(0, 0));
-            keep(1, kGradPT + 2, p_high(1, 0));
-            keep(2, kGradPT + 4, p_high(1, 1));
-        }
-        __syncthreads();  // the terms of w and dx are read by no one
 #pragma unroll
-        for (int n = 0; n < 3; ++n)
-            if (where[n] >= 0) {
-                store_terms(mats, where[n], lane, cut8(put[n], 0));
-                store_terms(mats, where[n] + 1, lane, cut8(put[n], 1));
-            }
-        f32x4 *y = reinterpret_cast<f32x4 *>(share + kg * 8192) + lane;
+            for (int n = 0; n < 2; ++n) {
+                u32x4 x, z;
 #pragma unroll
-        for (int th = 0; th < 2; ++th)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                y[64 * (4 * th + n)] = f32x4{dk[th][4 * n], dk[th][4 * n + 1], dk[th][4 * n + 2], dk[th][4 * n + 3]};
-    }
-    __syncthreads();
-    if (wave < 4) {
-        const f32x4 *y = reinterpret_cast<const f32x4 *>(share + kg * 8192) + lane;
-#pragma unroll
-        for (int th = 0; th < 2; ++th)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const f32x4 z = y[64 * (4 * th + n)];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dk[th][4 * n + i] += z[i];
-            }
-#pragma unroll
-        for (int st = 0; st < 4; ++st) {  // 16 tokens each of the contraction
-            const u32x4 kc4 = col_frag(s.k + 8192 * (st >> 1), ln.out, kg, st & 1);
-            const u32x4 qc4 = col_frag(s.q + 8192 * (st >> 1), ln.out, kg, st & 1);
-#pragma unroll
-            for (int th = 0; th < 2; ++th) {
-                if (st < 2 + 2 * th)
-                    dq[th] = mfma3(kc4, load_terms(mats, kGradP + 2 * th + st, lane), dq[th]);
-                if (st >= 2 * th)
-                    dk[th] = mfma3(qc4, load_terms(mats, kGradPT + 2 * th + st, lane), dk[th]);
-                dk[th] = mfma3(kc4, load_terms(mats, kGradG + 4 * th + st, lane), dk[th]);
-            }
-        }
-#pragma unroll
-        for (int th = 0; th < 2; ++th) {
-            float q16[16], y1 = 0.0f;
-            mine(s.q, th, q16);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                y1 = fmaf(dq[th][i], q16[i], y1);
-            y1 += __shfl_xor(y1, 32);
-            const int t = 32 * th + l32;
-            if (h == 0)
-                s.sums[kg][t] = y1;
-            if (t >= len)
-                continue;
-            const int64_t to = ((tok0 + t) * a.H + head) * kD + 32 * kg + 16 * h;
-            if (a.dq_h) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    reinterpret_cast<f32x4 *>(a.dq_h + to)[n] = f32x4{dq[th][4 * n], dq[th][4 * n + 1], dq[th][4 * n + 2], dq[th][4 * n + 3]};
-                    reinterpret_cast<f32x4 *>(a.dk_h + to)[n] = f32x4{dk[th][4 * n], dk[th][4 * n + 1], dk[th][4 * n + 2], dk[th][4 * n + 3]};
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = pack2(dq[th][8 * n + 2 * e], dq[th][8 * n + 2 * e + 1]);
+                    z[e] = pack2(dk[th][8 * n + 2 * e], dk[th][8 * n + 2 * e + 1]);
                 }
-            } else {
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    u32x4 x, z;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = pack2(dq[th][8 * n + 2 * e], dq[th][8 * n + 2 * e + 1]);
-                        z[e] = pack2(dk[th][8 * n + 2 * e], dk[th][8 * n + 2 * e + 1]);
-                    }
-                    reinterpret_cast<u32x4 *>(a.dq + to)[n] = x;
-                    reinterpret_cast<u32x4 *>(a.dk + to)[n] = z;
-                }
+                reinterpret_cast<u32x4 *>(a.dq + to)[n] = x;
+                reinterpret_cast<u32x4 *>(a.dk + to)[n] = z;
             }
         }
     }
-    __syncthreads();
-    if (wave != 0)
+    settle();
+    if (kg != 0)
         return;
     float qd = 0.0f, end = 0.0f;
 #pragma unroll
@@ -1820,11 +1828,8 @@ __global__ __launch_bounds__(512, 1) void gdn_grad_kernel(GdnArgs a)
     }
     const double each = lane < len ? (double)qd - (double)s.vdv[lane] : 0.0;
     const double upto = running_sum64(each), total = of_lane(upto, 63);  // by all lanes, those behind the block too
-    if (lane < len) {
-        const int64_t to = (tok0 + lane) * a.H + head;
-        const float gd = a.decay[to];
-        a.ddecay[to] = gd > kLowest && gd <= 0.0f ? (float)((total - upto) + each + (double)end) : 0.0f;
-    }
+    if (lane < len)
+        a.ddecay[(tok0 + lane) * a.H + head] = rg > kLowest && rg <= 0.0f ? (float)((total - upto) + each + (double)end) : 0.0f;
 }
 
 // ------------------------------------------------------------------------- cu_seqlens
@@ -2013,7 +2018,7 @@ hipError_t gdn_launch_bwd(const GdnArgs &a, int32_t *status, hipStream_t s)
     }
     hipLaunchKernelGGL(gdn_back_kernel<false>, dim3(grid), dim3(kWalkThreads), sizeof(LdsWalk), s, a);
     if (a.T > 0)
-        hipLaunchKernelGGL(gdn_grad_kernel, dim3((unsigned)(a.blocks * a.H)), dim3(512), sizeof(LdsGrad), s, a);
+        hipLaunchKernelGGL(gdn_grad_kernel, dim3((unsigned)(a.blocks * a.H)), dim3(256), kGradLds, s, a);
     e = hipGetLastError();
     if (e != hipSuccess || !a.dq_h || a.T == 0)
         return e;
