@@ -58,7 +58,7 @@ bool make_layout(const Sizes &z, bool bwd, kda::GdnLayout *L)
     const kda::GdnPlan &p = L->plan;
     L->slots = z.B * z.T / kda::kGC + z.n_seq + 1;
     L->blocks = z.B * z.T / kda::kGB + z.n_seq + 1;
-    // 64 threads for each record, 512 for each block, 256 for each segment and head, 4096 for each row and head
+    // 64 threads for each record, at most 512 for each block, 256 for each segment and head, 4096 for each row and head
     if (L->slots > (((int64_t)1 << 26) - 8) / z.H || (bwd && L->blocks > (((int64_t)1 << 23) - 8) / z.H) ||
         p.rows * p.P > (((int64_t)1 << 24) - 8) / z.H || (p.P > 1 && p.rows >= ((int64_t)1 << 20) / z.H))
         return false;
