@@ -6,7 +6,8 @@ import torch
 
 from gated_delta_rule_86_amd import blocknorm, gdn, qkrope
 
-from gdn_testutil import BF16_STEP, D, FP32_MAX, FP32_REL_L2, close_bf16, close_fp32, gdn_ref, inputs
+from gdn_testutil import (BF16_STEP, D, FP32_MAX, FP32_REL_L2, close_bf16, close_fp32, close_grads, gdn_ref, gdn_ref_bwd,
+                          inputs)
 from test_gpu_blocknorm import act, rms
 from test_gpu_qkrope import ref as rope_ref
 
@@ -284,3 +285,25 @@ def test_state_past_32_bits():
     gdn.fwd_recurrent(q, k, v, decay, beta, SCALE, out, state, state)
     torch.cuda.synchronize()
     assert torch.equal(out[-3:], o) and torch.equal(state[-3:], st)
+
+
+@pytest.mark.parametrize("cu", [None, [0, 1, 3100, 3100, 7500]], ids=["rows", "packed"])
+def test_long_segments_of_many_heads(cu):
+    """70 heads in segments of more than 1000 tokens, where heads that forget slowly are taken first, among the first 64 and
+    behind them: some heads of either kind against the reference."""
+    T, H, some = 7500, 70, [0, 31, 63, 66, 69]
+    N = 1 if cu is None else len(cu) - 1
+    q, k, v, decay, beta, n = inputs(1, T, H, H, 41)
+    decay = decay * torch.where(torch.arange(H, device="cuda") % 3 == 0, 1e-2, 1.0)
+    h0, dht, dout = n(N, H, D, D), n(N, H, D, D), n(1, T, H, D).bfloat16()
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int64, device="cuda")
+    out, ht = torch.empty_like(v), torch.empty_like(h0)
+    gdn.fwd(q, k, v, decay, beta, SCALE, out, h0, ht, c)
+    r = gdn.bwd(q, k, v, decay, beta, SCALE, dout, h0, dht, c)
+    args = [x[:, :, some].contiguous() for x in (q, k, v, decay, beta)]
+    ro, rs = gdn_ref(*args, SCALE, h0[:, some], cu)
+    close_bf16(out[:, :, some], ro, "out")
+    close_fp32(ht[:, some], rs, "final")
+    want = gdn_ref_bwd(*args, SCALE, dout[:, :, some], h0[:, some], dht[:, some], cu)
+    got = {x: r[x][:, :, some] for x in ("dq", "dk", "dv", "ddecay", "dbeta")}
+    close_grads(got | {"dinitial_state": r["dinitial_state"][:, some]}, want)
