@@ -15,6 +15,11 @@
 // registers of its lanes.  A lane owns 8 neighbouring channels (16 bytes of a 2-byte type); D / 8 lanes, rounded up to a
 // power of two, own a row of up to 512 channels, several rows in flight; longer rows take a workgroup of 256 or 512
 // threads with one or two pieces each, the next row's loads on their way while one is worked on.
+//
+// Measured (a copy of 512 MiB: 5.33 TB/s): residual forward, 16384 rows of 4096 bf16 channels, both norms: 104 us, 5.2 TB/s;
+// residual backward, 6002 rows of 2048, bf16 with an fp32 stream: 40 us, 5.7 TB/s of what reaches memory, and 5 for the sums;
+// gated backward, 131072 rows of 128: 35 us, 4.9 TB/s, and 4 for the sums: there a third of the issue slots are taken,
+// the exponential and the divisions of the gate among them; gated forward of 1024 rows: 6 us, the launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -24,6 +24,12 @@
 // Numbers: decays are used as min(max(g, -1000), 0); running sums of logarithms are fp64, a factor is the
 // exponential of a difference and at most 1.  The products run on bf16 MFMA with fp32 accumulation; q, k, v are
 // bf16 as they come, every other factor is cut into three bf16 terms, hi + mid + lo: the 24 bits of fp32.
+//
+// Passes: prep forms each chunk's triangular matrices; the cut walks each segment's share of the state at its end and its
+// transition, the scan the states there (few rows: the chip has room for 512 walks); the output walk starts from them.
+// Backwards the store walk keeps the state before each block of 64 tokens, the back walk its gradient behind it, and the
+// gradients of the blocks follow from the two.  Times below are of B=2 T=4096 H=16 (a), 38350 packed tokens H=32 Hk=16 (b) and
+// T=65536 H=8 (c).
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -119,7 +125,8 @@ __device__ __forceinline__ Terms cut8(const f32x16 &x, int s)
         cut2(x[8 * s + 2 * e], x[8 * s + 2 * e + 1], t, e);
     return t;
 }
-// products with an exact factor, and of two cut factors (the terms left out are below 2^-24 of the product)
+// products with an exact factor, and of two cut factors (what is left out, mid lo + lo mid + lo lo, comes to some 2^-23 of the
+// product: the cuts leave 2^-8 and 2^-16 of a factor behind on average)
 template <typename D>
 __device__ __forceinline__ D mfma3(u32x4 a, const Terms &b, D c)
 {
@@ -356,7 +363,8 @@ __device__ __forceinline__ double of_lane(double b, int lane)
 constexpr float kDead = -150.0f;
 
 // How many of the chunks [c_lo, c_hi) of a sequence, counted from the end (or from the start), a state has to pass until it counts
-// as 0; one more than all of them if it never does.  By a wave, 64 chunks at a time.
+// as 0; one more than all of them if it never does.  By a wave, 64 chunks at a time.  What lies beyond is left out of shares and
+// transitions: it is below what fp32 tells apart next to any state that the segment itself writes.
 template <bool kFromEnd>
 __device__ __forceinline__ int64_t live_chunks(const GdnArgs &a, int64_t slot0, int64_t c_lo, int64_t c_hi, int64_t h, int lane)
 {
@@ -384,16 +392,17 @@ constexpr int kVTail = 128;  // e^{L - b_s}
 constexpr int kVLast = 160;  // [0]: e^{L}
 
 // The terms of one step (16 of the contraction) of a 32 x 32 matrix, in the order of the lanes
+constexpr int kTermStep = 3 * 1024;
 __device__ __forceinline__ void store_terms(unsigned char *mat, int step, int lane, const Terms &t)
 {
-    u32x4 *p = reinterpret_cast<u32x4 *>(mat + step * 3072 + lane * 16);
+    u32x4 *p = reinterpret_cast<u32x4 *>(mat + step * kTermStep + lane * 16);
     p[0] = t.h;
     p[64] = t.m;
     p[128] = t.l;
 }
 __device__ __forceinline__ Terms load_terms(const unsigned char *mat, int step, int lane)
 {
-    const u32x4 *p = reinterpret_cast<const u32x4 *>(mat + step * 3072 + lane * 16);
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(mat + step * kTermStep + lane * 16);
     return Terms{p[0], p[64], p[128]};
 }
 
@@ -405,6 +414,8 @@ struct LdsPrep {
     float bh[kGC], bl[kGC], beta[kGC];
 };
 
+// Bound by memory, most of it the records that it writes: (a) 23 us, 5.5 TB/s; (b) 188 us, 4.8 TB/s; (c) 80 us, 4.5 TB/s.
+// Records of chunks of 64 tokens, two waves each, took 400 us in (b): four times the matrix to solve and to write.
 // One wave per (chunk, head), nothing shared between waves.  M = e^{b_t - b_s} k_t.k_s; N's two 16 x 16 blocks on the diagonal
 // are solved column by column, the block below them with fp32 matrix instructions:
 // N_10 = (1 - N_11 beta)(M_10 - M_10 beta N_00).
@@ -798,6 +809,14 @@ __device__ __forceinline__ void state_scale(State &S, float f)
 }
 
 // --------------------------------------------------------------------------- forward walk
+//
+// 32 value columns a wave on 32x32x16 matrix instructions, four waves a workgroup, two workgroups a CU; a chunk's tiles and record
+// come into one of two LDS buffers while the other is worked on, with one barrier a chunk.  Per chunk and wave of the output
+// walk: 96 matrix instructions (of 32 cycles), 750 other vector instructions, most of them cuts, 58 LDS reads.  A wave alone
+// on its SIMD issues one in 5.2 cycles, which is what bounds (a) with 256 workgroups (67 us, 4.2 us a chunk; the matrix
+// pipe busy 30 %) and (c) (262 us); two a SIMD reach 6.6 us for two chunks ((b): 537 us, matrix pipe 50 %, vector 59 %).
+// With products and cuts in the compiler's order (b) took 567 us; chunks of 64 tokens with one workgroup a CU made all of the
+// call's kernels 1307 us together, where these make 1180 in that order.
 
 constexpr int kModeOut = 0;    // out and final states
 constexpr int kModeShare = 1;  // a segment's share of the state at its end (F)
@@ -1162,7 +1181,9 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_store_kernel(GdnArgs a)
 // State at each cut: S_{p+1} = S_p Phi_p + F_p where segment p lies inside one sequence (else F_p is the state); backwards
 // (kRev) the gradients of the states at the cuts, dS_{p-1} = dS_p Phi_p^T + F_p.  A workgroup of 8 waves takes 16 value
 // columns of one row and head; wave w forms key channels 16w .. of each state and hands its terms to the others
-// through LDS.  The next step's Phi and F are on their way meanwhile.
+// through LDS.  The next step's Phi and F are on their way meanwhile.  A step takes some 2 us: each of a row's 8 workgroups
+// reads the whole of Phi, 64 KiB at some 15 bytes a cycle ((a) 18 us for 6 steps, (c) 64 for 30).  Two steps' loads on their
+// way took longer (20 and 73).
 template <bool kRev>
 __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
 {
@@ -1274,7 +1295,8 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
 
 // -------------------------------------------------------------------------- backward walk
 //
-// dL/dS from a sequence's end to its start, in the same layout; stores it after each block, and dw.
+// dL/dS from a sequence's end to its start, in the same layout; stores it after each block, and dw.  90 matrix instructions a
+// chunk; (a) 104 us, the store walk 85, each writing 134 MB of states.
 
 template <bool kShare>
 __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, uint32_t at, int64_t row, int64_t p, int64_t h)
@@ -1498,6 +1520,11 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_back_kernel(GdnArgs a)
 // is lane % 32): it takes them from memory, cut as they come.  w = beta r and dx = beta dw stay in LDS in fp32 and are cut
 // where they are used, which takes less room and time than their terms would.  Then the waves share out the 32 x 32 tiles of
 // P, P^T and G + G^T, which reach all of them through LDS, in the place of w and dx.
+//
+// 408 matrix and some 4800 other vector instructions a wave, three quarters of them cuts: issue bounds it (matrix pipe busy
+// 27 %, vector 44 %), then memory, 3.4 TB/s.  (a) 184 to 196 us.  One workgroup of 8 waves with the terms in LDS took 252 (its
+// 36000 cycles of loads and 29000 of products did not overlap: a CU takes in some 10 bytes a cycle), with tiles shared out evenly 230;
+// products and cuts interleaved by hand change nothing here.
 
 // LDS: w and dx, 64 rows of 32 pieces of 16 bytes each, piece u of row t at u ^ (t % 16), and dout.  Behind the products with
 // them: the matrices (steps of 3 KiB), k, q, and what is below.
@@ -1505,7 +1532,7 @@ constexpr int kGradX = kGB * 512, kGradO = 2 * kGradX, kGradLds = kGradO + kGB *
 // P: columns tokens t, contraction sources, steps 0 .. 1 + 2 t; P^T: columns sources s, contraction tokens, steps 2 s .. 3; then, in
 // their place, G + G^T, all steps
 constexpr int kGradP = 0, kGradPT = 6, kGradMats = 12;
-constexpr int kGradK = kGradMats * 3072, kGradQ = kGradK + kGB * 256;
+constexpr int kGradK = kGradMats * kTermStep, kGradQ = kGradK + kGB * 256;
 struct LdsGrad {
     float bh[4][kGB], bl[4][kGB];  // running sums of log2 decays as pairs, a copy for each wave
     float sums[4][kGB];            // q.dq of each wave's channels
@@ -1887,7 +1914,8 @@ __global__ __launch_bounds__(1024) void gdn_check_kernel(const int64_t *cu, int6
 //
 // One wave per (sequence, head, 32 rows of the state); lane = row % 8 * 8 + q holds 16 channels of 4 rows: 16-byte
 // pieces, interleaved with those of the row's other 7 lanes.  S q = S~ q + beta r (k.q), so one pass over the row
-// gives both dot products.  The state is read once and written once, which bounds it.
+// gives both dot products.  The state is read once and written once, which bounds it: 256 sequences of 32 heads, fp32
+// states, 206 us, 5.3 TB/s (a copy: 5.33).
 template <bool kF32>
 __global__ __launch_bounds__(256) void gdn_recurrent_kernel(GdnArgs a)
 {

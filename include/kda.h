@@ -418,8 +418,10 @@ size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, i
  *             in-place state carry and the handling of an invalid cu_seqlens (kda_fwd_device_status reads the
  *             status word of this workspace too).
  * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; out and bf16 final states are
- * rounded once.  A value that is not finite (or a NaN gate) reaches its own sequence and head alone, from the first token of its
- * chunk of 32 tokens on, and may last.  Deterministic: fixed summation orders, no atomics.
+ * rounded once.  Where a row is cut into segments (kda_gdn_fwd_workspace_size), a finite state that has passed transitions of a
+ * norm below 2^-150 in all counts as 0.  A value that is not finite (or a NaN gate) reaches its own sequence and head alone, from
+ * the first token of its chunk of 32 tokens on; in the state it lasts, in k or v it may be forgotten behind such transitions.
+ * Deterministic: fixed summation orders, no atomics.
  * Errors: KDA_ERR_NULL, _SHAPE (also sizes whose launch would hold 2^32 threads), _HEAD_DIM, _DTYPE, _SCALE, _ALIGN,
  * _WORKSPACE, _CU_SEQLENS, _HIP, _ALIAS, _HEADS, _STRIDE.
  */
@@ -443,8 +445,8 @@ kda_status kda_gdn_fwd_recurrent(const void *q, const void *k, const void *v, co
 
 /*
  * kda_gdn_fwd_workspace_size -- 256 bytes; 13 KiB per chunk of 32 tokens and head (T / 32 chunks in all, and one for each sequence);
- * where rows are cut into segments that run in parallel, three fp32 128 x 128 states per segment and head.  A function
- * of (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes.
+ * where rows are cut into segments that run in parallel, three fp32 128 x 128 states and a word per segment and head and a word
+ * per chunk and head.  A function of (B, T, H, N, has_cu_seqlens) alone.  Returns 0 for invalid sizes.
  */
 size_t kda_gdn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
 
@@ -471,7 +473,7 @@ kda_status kda_gdn_bwd(const void *q, const void *k, const void *v, const float 
 
 /*
  * kda_gdn_bwd_workspace_size -- 256 bytes; 51 KiB per chunk of 32 tokens and head (T / 32 chunks in all, and one for each sequence) and
- * 128 KiB per block of 64; where rows are cut, three fp32 128 x 128 states per segment and head; with Hk < H two fp32 [B, T, H, 128].
+ * 128 KiB per block of 64; where rows are cut, what kda_gdn_fwd_workspace_size says of that; with Hk < H two fp32 [B, T, H, 128].
  * Returns 0 for invalid sizes.
  */
 size_t kda_gdn_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int has_cu_seqlens);
