@@ -364,7 +364,7 @@ constexpr float kDead = -150.0f;
 
 // How many of the chunks [c_lo, c_hi) of a sequence, counted from the end (or from the start), a state has to pass until it counts
 // as 0; one more than all of them if it never does.  By a wave, 64 chunks at a time.  What lies beyond is left out of shares and
-// transitions: it is below what fp32 tells apart next to any state that the segment itself writes.
+// transitions: of a state of size 1 it is below the smallest fp32 number.
 template <bool kFromEnd>
 __device__ __forceinline__ int64_t live_chunks(const GdnArgs &a, int64_t slot0, int64_t c_lo, int64_t c_hi, int64_t h, int lane)
 {
@@ -1338,7 +1338,6 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, uint32
     Chunk ch = w.next(a);
     if (ch.len == 0)
         return;
-    const Lanes ln(lane);
     const uint16_t *pk = head_base(a.k, row, h), *po = head_base(a.dout, row, h), *pq = head_base(a.q, row, h);
     constexpr int kBytes = 2 * kGdnMat + kGdnVec, kLoads = 6 + (kBytes / 1024 + kWalkWaves - 1) / kWalkWaves;
     auto fetch = [&](int buf, const Chunk &n, int part) {  // in parts, as in the forward walk
@@ -1373,6 +1372,11 @@ __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, uint32
         const unsigned char *tk = lds.tile[buf][0], *to = lds.tile[buf][1], *tq = lds.tile[buf][2], *vec = lds.rec[buf],
                             *mt = vec + kGdnVec, *ma = mt + kGdnMat;
         const Chunk nx = w.next(a);
+        int l = tid & 63;
+        if constexpr (kShare)  // places formed anew: kept from chunk to chunk some would be in scratch, whose loads wait for the tiles'
+            __asm__ volatile("" : "+v"(l));
+        const int lane = l;
+        const Lanes ln(lane);
         arrive();  // this chunk's tiles and record are there; the other buffer is read by no one
         store_held();
         if (ch.first) {
