@@ -74,7 +74,7 @@ void set_sizes(kda::NormArgs *a, int64_t B, int64_t T, int64_t H, int64_t D)
     a->inv_t = T > 0 ? 1.0 / (double)T : 1.0;
 }
 
-// Outputs overlap no input and not each other; `same`: outputs that may be an input (same place, both contiguous).
+// Outputs overlap no input (callers leave out one that an output replaces in place) and not each other.
 bool clear(const Range *in, int n_in, const Range *out, int n_out)
 {
     for (int i = 0; i < n_out; ++i) {
@@ -88,8 +88,9 @@ bool clear(const Range *in, int n_in, const Range *out, int n_out)
     return true;
 }
 
-// Contiguous, as an output that takes its place has to be
-bool dense(const kda::NormView &v, int64_t D) { return v.flat && (v.sh == D || v.sh == 0); }
+// Contiguous, as an output that takes its place has to be: one row, or rows D apart (rows 0 apart are one row broadcast, which
+// every other workgroup still reads when the first output row is written)
+bool dense(const kda::NormView &v, const kda::NormArgs &a) { return a.rows == 1 || (v.flat && v.sh == a.D); }
 
 }  // namespace
 
@@ -122,7 +123,7 @@ kda_status kda_gated_norm(const void *x, const void *gate, const float *weight, 
         return KDA_ERR_ALIGN;
     const Range ro = range_of(out, (size_t)a.rows * (size_t)D * (size_t)size);
     // in place: each value of a row is read before any of the row is written, by the same lane
-    const bool over_x = out == x && dense(a.x, D), over_z = out == gate && dense(a.z, D);
+    const bool over_x = out == x && dense(a.x, a), over_z = out == gate && dense(a.z, a);
     const Range none = {0, 0};
     const Range in[] = {over_x ? none : rx, over_z ? none : rz, range_of(weight, (size_t)D * 4)};
     if (!clear(in, 3, &ro, 1))
@@ -228,7 +229,7 @@ kda_status kda_residual_norm(const void *x, const void *residual, const float *w
     const size_t values = (size_t)a.rows * (size_t)D, wb = (size_t)D * 4;
     const Range none = {0, 0};
     // in place: a row's values are in registers before any of it is written, by the threads that read them
-    const bool over_x = out == x && dense(a.x, D), over_z = residual_out == residual && dense(a.z, D);
+    const bool over_x = out == x && dense(a.x, a), over_z = residual_out == residual && dense(a.z, a);
     const Range out_r[] = {range_of(out, values * (size_t)size), range_of(residual_out, values * (size_t)rsize)};
     const Range w_in[] = {range_of(weight, wb), range_of(scale, wb), range_of(post_weight, wb)};
     const Range for_out[] = {over_x ? none : rx, rz}, for_res[] = {rx, over_z ? none : rz};
