@@ -18,8 +18,12 @@
 //   dq_t = scale e^{b_t} S^T dO_t + sum_s P_ts k_s,           P_ts = scale e^{b_t - b_s} dO_t.w_s  (s <= t),
 //   dk_s = tail_s dS^T w_s - e^{b_s} S^T dx_s + sum_t P_ts q_t + sum_t (G_ts + G_st) k_t,
 //                                                             G_ts = -e^{b_t - b_s} dx_t.w_s     (s < t),
-//   dg_t = sum over the chunk's u >= t of (q_u.dq_u - v_u.dv_u), plus <dS, S_after>,
-// since <dS~, S~> at a token is that at the next one plus what the token's read adds and its write takes.
+//   dg_t = <dS~_t, S~_t>, the sum of all that crosses the token:
+//     e^{L} <dS, S> + sum_{s < t} tail_s w_s.(dS k_s) + sum_{u >= t} e^{b_u} (scale dO_u.(S q_u) - dx_u.(S k_u))
+//     + sum_{s < t <= u} (P_us q_u.k_s + G_us k_u.k_s).
+// Every term has e^{g_t} in it and none is taken away again, so dg_t is as exact where a head forgets as where it remembers.
+// (The sums of q_u.dq_u - v_u.dv_u over u >= t are the same in exact arithmetic, but hold the token's own read and write,
+// which e^{g_t} does not scale: in fp32 nothing is left of dg_t below g_t = -16.)
 //
 // Numbers: decays are used as min(max(g, -1000), 0); running sums of logarithms are fp64, a factor is the
 // exponential of a difference and at most 1.  The products run on bf16 MFMA with fp32 accumulation; q, k, v are
@@ -1539,9 +1543,12 @@ constexpr int kGradP = 0, kGradPT = 6, kGradMats = 12;
 constexpr int kGradK = kGradMats * kTermStep, kGradQ = kGradK + kGB * 256;
 struct LdsGrad {
     float bh[4][kGB], bl[4][kGB];  // running sums of log2 decays as pairs, a copy for each wave
-    float sums[4][kGB];            // q.dq of each wave's channels
-    float vdv[kGB];
-    float end[4];                  // <dS, S_after>, a wave's share
+    // terms of dg (above): by source or token for each wave's channels, inside tiles 00 and 11 by token (of G and of P), and of
+    // tile 01 by its tokens and by its sources (of P and of G)
+    float writes[4][kGB], reads[4][kGB];
+    float inside[2][kGB];
+    float far_tok[2][kGC], far_src[2][kGC];
+    float end[4];                  // e^L <dS, S>, a wave's share
 };
 constexpr int kGradRest = kGradQ + kGB * 256;
 static_assert(kGradRest + sizeof(LdsGrad) <= kGradLds, "the second half reuses the first's room");
@@ -1585,16 +1592,9 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
             tile_half<4>(lds_base(raw) + to, x, p, t0, len, n, kg, lane);
     };
     load_tile(a.dout, kGradO);
-    // rows of v: thread = token tid / 4, value channels 32 (tid % 4) ..
+    // rows of dv: thread = token tid / 4, value channels 32 (tid % 4) ..
     const int rt = tid >> 2, v0 = 32 * (tid & 3);
     const bool on = rt < len;
-    u32x4 rv[4];
-    {
-        const u32x4 *pv = reinterpret_cast<const u32x4 *>(head_base(a.v, row, head) + (t0 + (on ? rt : 0)) * a.v.st + v0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            rv[i] = pv[i];
-    }
     const float rb = on ? a.beta[(tok0 + rt) * a.H + head] : 0.0f;
     const float rg = lane < len ? a.decay[(tok0 + lane) * a.H + head] : 0.0f;
     // the states' columns of this wave: lane = key channel, element 8 x + j: value row 16 x + 8 h + j
@@ -1619,21 +1619,19 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
     const float from1 = __builtin_amdgcn_exp2f((float)b64), tail1 = __builtin_amdgcn_exp2f((float)(last64 - b64));
     const float last = __builtin_amdgcn_exp2f((float)last64);
     arrive();
-    float vd = 0.0f;
     {
         float db = 0.0f;
+        u32x4 rv[4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // scaled by beta in place
             const int p = rt * 512 + (((8 * (tid & 3) + i) ^ (rt & 15)) << 4);
             f32x4 r = *reinterpret_cast<const f32x4 *>(raw + p), d = *reinterpret_cast<const f32x4 *>(raw + kGradX + p);
             if (!on)
                 r = d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            const f32x4 x = d * rb, v4 = widen4(u32x2{rv[i >> 1][2 * (i & 1)], rv[i >> 1][2 * (i & 1) + 1]});
+            const f32x4 x = d * rb;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 db = fmaf(d[e], r[e], db);
-                vd = fmaf(x[e], v4[e], vd);
-            }
             *reinterpret_cast<f32x4 *>(raw + p) = r * rb;
             *reinterpret_cast<f32x4 *>(raw + kGradX + p) = x;
             rv[i >> 1][2 * (i & 1)] = pack2(x[0], x[1]);
@@ -1646,10 +1644,8 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
                 dv[i] = rv[i];
         }
 #pragma unroll
-        for (int o = 2; o > 0; o >>= 1) {
+        for (int o = 2; o > 0; o >>= 1)
             db += __shfl_xor(db, o);
-            vd += __shfl_xor(vd, o);
-        }
         if (on && (tid & 3) == 0)
             a.dbeta[(tok0 + rt) * a.H + head] = db;
     }
@@ -1668,7 +1664,8 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
         return cut8(*reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3)))),
                     *reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3) + 16))));
     };
-    float dot = 0.0f;  // <dS, S_after>, this lane's share
+    float dot = 0.0f;  // <dS, S>, this lane's share
+    float writes[2], reads[2];
     f32x16 dq[2], dk[2], put[4];
     {
         f32x16 dw[2];
@@ -1694,22 +1691,29 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
             __builtin_amdgcn_sched_barrier(0);  // one step at a time: more of them in flight do not fit the registers
         }
         dot *= last;
-        const uint16_t *pk = head_base(a.k, row, head);
+        const uint16_t *pk = head_base(a.k, row, head), *pq = head_base(a.q, row, head);
 #pragma unroll
         for (int th = 0; th < 2; ++th) {
             const int t = 32 * th + l32;
             const float from = __shfl(from1, t), tail = __shfl(tail1, t);
-            const u32x4 *p = reinterpret_cast<const u32x4 *>(pk + (t0 + (t < len ? t : 0)) * a.k.st + 32 * kg + 16 * h);
-            const u32x4 k16[2] = {p[0], p[1]};
+            const int64_t at = t0 + (t < len ? t : 0);  // behind the block all sums are 0
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(pk + at * a.k.st + 32 * kg + 16 * h),
+                        *o = reinterpret_cast<const u32x4 *>(pq + at * a.q.st + 32 * kg + 16 * h);
+            const u32x4 k16[2] = {p[0], p[1]}, q16[2] = {o[0], o[1]};
             dq[th] *= a.scale * from;
+            float wk = 0.0f, rd = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float y = dw[th][i] * tail;  // 0 behind the block
-                const uint32_t u = k16[i >> 3][(i & 7) >> 1];
-                dot = fmaf(y, i & 1 ? hi_f(u) : lo_f(u), dot);
-                dk[th][i] = y - from * dk[th][i];
+                const float y = dw[th][i] * tail, z = from * dk[th][i];
+                const uint32_t uk = k16[i >> 3][(i & 7) >> 1], uq = q16[i >> 3][(i & 7) >> 1];
+                const float ke = i & 1 ? hi_f(uk) : lo_f(uk);
+                wk = fmaf(y, ke, wk);
+                rd = fmaf(dq[th][i], i & 1 ? hi_f(uq) : lo_f(uq), fmaf(-z, ke, rd));
+                dk[th][i] = y - z;
             }
-            __asm__ volatile("" : "+v"(dq[th]), "+v"(dk[th]), "+v"(dot));
+            writes[th] = wk + __shfl_xor(wk, 32);
+            reads[th] = rd + __shfl_xor(rd, 32);
+            __asm__ volatile("" : "+v"(dq[th]), "+v"(dk[th]), "+v"(writes[th]), "+v"(reads[th]));
         }
     }
     // The tiles, unscaled: the product of rows of token tile i by rows of token tile j, and the transposed one of the same
@@ -1768,8 +1772,13 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
     LdsGrad &s = *reinterpret_cast<LdsGrad *>(raw + kGradRest);
     s.bh[kg][lane] = bh;
     s.bl[kg][lane] = bl;
-    if ((tid & 3) == 0)
-        s.vdv[rt] = on ? vd : 0.0f;
+    if (h == 0) {
+#pragma unroll
+        for (int th = 0; th < 2; ++th) {
+            s.writes[kg][32 * th + l32] = writes[th];
+            s.reads[kg][32 * th + l32] = reads[th];
+        }
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
         dot += __shfl_xor(dot, o);
@@ -1798,13 +1807,17 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
         store_terms(raw, step + 1, lane, cut8(y, 1));
     };
     if (kg == 0) {
-        store(kGradP + 2, scaled(0, 1, put[2], a.scale, true, false));
+        put[2] = scaled(0, 1, put[2], a.scale, true, false);
+        store(kGradP + 2, put[2]);
     } else if (kg == 1) {
-        store(kGradPT + 2, scaled(1, 0, put[2], a.scale, false, false));
+        put[2] = scaled(1, 0, put[2], a.scale, false, false);
+        store(kGradPT + 2, put[2]);
     } else if (kg == 3) {
-        store(kGradP, scaled(0, 0, put[0], a.scale, true, false));
+        put[0] = scaled(0, 0, put[0], a.scale, true, false);
+        store(kGradP, put[0]);
         store(kGradPT, scaled(0, 0, put[1], a.scale, false, false));
-        store(kGradP + 4, scaled(1, 1, put[2], a.scale, true, false));
+        put[2] = scaled(1, 1, put[2], a.scale, true, false);
+        store(kGradP + 4, put[2]);
         store(kGradPT + 4, scaled(1, 1, put[3], a.scale, false, false));
     }
     f32x16 g, gt;
@@ -1817,6 +1830,68 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
                 g[i] = (i & 3) + 8 * (i >> 2) + 4 * h < l32 ? g[i] : gt[i];
     }
     arrive();  // P, P^T, k, q
+    // Terms of dg from tiles of P and G (rows: registers, columns: lane % 32), each times the dot products of the rows' and
+    // columns' tokens: rows of x by columns of y
+    auto dots = [&](f32x16 d, int x, int i, int y, int j) {
+        f32x16 c = zero16();
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+            c = mfma(row_frag(raw + x, ln, n, i), row_frag(raw + y, ln, n, j), c);
+        return d * c;
+    };
+    auto over_rows = [&](const f32x16 &d, float *to) {
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x += d[i];
+        x += __shfl_xor(x, 32);
+        if (h == 0)
+            to[l32] = x;
+    };
+    // for each token t of a tile on the diagonal the sum over rows s < t and columns u >= t
+    auto inside = [&](f32x16 d, float *to) {
+        float upto = 0.0f;  // rows before 8 n
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {  // d: the sum of the rows before this one, where the column is not before it
+            float own = 0.0f, part[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                part[i] = own;
+                own += d[4 * n + i];
+            }
+            const float other = __shfl_xor(own, 32), base = h ? upto + other : upto;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                d[4 * n + i] = 8 * n + 4 * h + i <= l32 ? base + part[i] : 0.0f;
+            upto += own + other;
+        }
+        // over the columns: at each step lanes in pairs keep one half of the rows each
+#pragma unroll
+        for (int o = 1, n = 8; n > 0; o <<= 1, n >>= 1)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool upper = lane & o;
+                const float keep = upper ? d[i + n] : d[i], give = upper ? d[i] : d[i + n];
+                d[i] = keep + __shfl_xor(give, o);
+            }
+        const float x = d[0] + __shfl_xor(d[0], 16);
+        const int i = 8 * (lane & 1) + 2 * (lane & 2) + ((lane >> 1) & 2) + ((lane >> 3) & 1);  // its row
+        if ((lane & 16) == 0)
+            to[8 * (i >> 2) + 4 * h + (i & 3)] = x;
+    };
+    if (kg == 0) {
+        over_rows(dots(put[2], kGradK, 0, kGradQ, 1), s.far_tok[0]);
+        inside(dots(g, kGradK, 0, kGradK, 0), s.inside[0]);
+    } else if (kg == 1) {
+        over_rows(dots(put[2], kGradQ, 1, kGradK, 0), s.far_src[0]);
+        inside(dots(g, kGradK, 1, kGradK, 1), s.inside[0] + kGC);
+    } else if (kg == 2) {
+        over_rows(dots(g, kGradK, 0, kGradK, 1), s.far_tok[1]);
+        over_rows(dots(gt, kGradK, 1, kGradK, 0), s.far_src[1]);
+    } else {
+        inside(dots(put[0], kGradK, 0, kGradQ, 0), s.inside[1]);
+        inside(dots(put[2], kGradK, 1, kGradQ, 1), s.inside[1] + kGC);
+    }
     auto key = [&](int tile, int st) { return col_frag(raw + tile + 8192 * (st >> 1), ln.out, kg, st & 1); };
 #pragma unroll
     for (int st = 0; st < 4; ++st) {  // 16 tokens each of the contraction
@@ -1845,17 +1920,6 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
 #pragma unroll
     for (int th = 0; th < 2; ++th) {
         const int t = 32 * th + l32;
-        float y1 = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {  // 16 channels 32 kg + 16 h .. of token t
-            const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + kGradQ + t * 256 + (((4 * kg + 2 * h + e) ^ swz(t)) << 4));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y1 = fmaf(dq[th][8 * e + 2 * i + 1], hi_f(u[i]), fmaf(dq[th][8 * e + 2 * i], lo_f(u[i]), y1));
-        }
-        y1 += __shfl_xor(y1, 32);
-        if (h == 0)
-            s.sums[kg][t] = y1;
         if (t >= len)
             continue;
         const int64_t to = ((tok0 + t) * a.H + head) * kD + 32 * kg + 16 * h;
@@ -1879,19 +1943,24 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
             }
         }
     }
-    settle();
     if (kg != 0)
         return;
-    float qd = 0.0f, end = 0.0f;
+    // dg: sums over the tokens before (without the lane's own) run forwards, those over tokens from the lane's on backwards, by
+    // lanes in the opposite order; of tile 01 in tokens of the upper half over its tokens, of the lower half over its sources
+    float end = 0.0f, written = 0.0f, read = 0.0f;
+    const int past = lane > 0 ? lane - 1 : 0, turned = 63 - lane;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        qd += s.sums[n][lane];
         end += s.end[n];
+        written += s.writes[n][past];
+        read += s.reads[n][turned];
     }
-    const double each = lane < len ? (double)qd - (double)s.vdv[lane] : 0.0;
-    const double upto = running_sum64(each), total = of_lane(upto, 63);  // by all lanes, those behind the block too
+    const float src = s.far_src[0][past & 31] + s.far_src[1][past & 31], tok = s.far_tok[0][turned & 31] + s.far_tok[1][turned & 31];
+    const double before = running_sum64(lane > 0 ? (double)written : 0.0) + running_sum32(lane > 0 && h == 0 ? (double)src : 0.0);
+    const double behind = running_sum64((double)read) + running_sum32(h == 0 ? (double)tok : 0.0);
+    const double dg = (double)end + before + __shfl(behind, turned) + (double)s.inside[0][lane] + (double)s.inside[1][lane];
     if (lane < len)
-        a.ddecay[(tok0 + lane) * a.H + head] = rg > kLowest && rg <= 0.0f ? (float)((total - upto) + each + (double)end) : 0.0f;
+        a.ddecay[(tok0 + lane) * a.H + head] = rg > kLowest && rg <= 0.0f ? (float)dg : 0.0f;
 }
 
 // ------------------------------------------------------------------------- cu_seqlens
