@@ -1691,28 +1691,27 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
             __builtin_amdgcn_sched_barrier(0);  // one step at a time: more of them in flight do not fit the registers
         }
         dot *= last;
-        const uint16_t *pk = head_base(a.k, row, head), *pq = head_base(a.q, row, head);
+        const uint16_t *pk = head_base(a.k, row, head);
 #pragma unroll
         for (int th = 0; th < 2; ++th) {
             const int t = 32 * th + l32;
             const float from = __shfl(from1, t), tail = __shfl(tail1, t);
             const int64_t at = t0 + (t < len ? t : 0);  // behind the block all sums are 0
-            const u32x4 *p = reinterpret_cast<const u32x4 *>(pk + at * a.k.st + 32 * kg + 16 * h),
-                        *o = reinterpret_cast<const u32x4 *>(pq + at * a.q.st + 32 * kg + 16 * h);
-            const u32x4 k16[2] = {p[0], p[1]}, q16[2] = {o[0], o[1]};
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(pk + at * a.k.st + 32 * kg + 16 * h);
+            const u32x4 k16[2] = {p[0], p[1]};
             dq[th] *= a.scale * from;
             float wk = 0.0f, rd = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float y = dw[th][i] * tail, z = from * dk[th][i];
-                const uint32_t uk = k16[i >> 3][(i & 7) >> 1], uq = q16[i >> 3][(i & 7) >> 1];
-                const float ke = i & 1 ? hi_f(uk) : lo_f(uk);
+                const uint32_t u = k16[i >> 3][(i & 7) >> 1];
+                const float ke = i & 1 ? hi_f(u) : lo_f(u);
                 wk = fmaf(y, ke, wk);
-                rd = fmaf(dq[th][i], i & 1 ? hi_f(uq) : lo_f(uq), fmaf(-z, ke, rd));
+                rd = fmaf(-z, ke, rd);
                 dk[th][i] = y - z;
             }
             writes[th] = wk + __shfl_xor(wk, 32);
-            reads[th] = rd + __shfl_xor(rd, 32);
+            reads[th] = rd;  // without dq.q yet
             __asm__ volatile("" : "+v"(dq[th]), "+v"(dk[th]), "+v"(writes[th]), "+v"(reads[th]));
         }
     }
@@ -1774,10 +1773,8 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
     s.bl[kg][lane] = bl;
     if (h == 0) {
 #pragma unroll
-        for (int th = 0; th < 2; ++th) {
+        for (int th = 0; th < 2; ++th)
             s.writes[kg][32 * th + l32] = writes[th];
-            s.reads[kg][32 * th + l32] = reads[th];
-        }
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
@@ -1879,6 +1876,21 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
         if ((lane & 16) == 0)
             to[8 * (i >> 2) + 4 * h + (i & 3)] = x;
     };
+#pragma unroll
+    for (int th = 0; th < 2; ++th) {
+        const int t = 32 * th + l32;
+        float x = reads[th];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // 16 channels 32 kg + 16 h .. of token t
+            const u32x4 u = *reinterpret_cast<const u32x4 *>(raw + kGradQ + t * 256 + (((4 * kg + 2 * h + e) ^ swz(t)) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x = fmaf(dq[th][8 * e + 2 * i + 1], hi_f(u[i]), fmaf(dq[th][8 * e + 2 * i], lo_f(u[i]), x));
+        }
+        x += __shfl_xor(x, 32);
+        if (h == 0)
+            s.reads[kg][t] = x;
+    }
     if (kg == 0) {
         over_rows(dots(put[2], kGradK, 0, kGradQ, 1), s.far_tok[0]);
         inside(dots(g, kGradK, 0, kGradK, 0), s.inside[0]);
