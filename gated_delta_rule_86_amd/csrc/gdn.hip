@@ -100,7 +100,12 @@ __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c)
 struct Terms {  // three bf16 terms of 8 floats
     u32x4 h, m, l;
 };
-// Two floats into word e of each term: the upper 16 bits, those of what they leave, and the rest, which has 8 bits: exact.
+// Cuts: x = h + m + l exactly, towards 0 (cut2, cut8) or to the nearest (cut2n, cut8n).  A product with a bf16 factor is whole either
+// way.  mfma6 leaves out m l + l m + l l of two cut factors, relative to the product (normal factors): both towards 0 2^-24.0 root mean
+// square and 2^-21.2 at most, always on the side of 0; one of them to the nearest 2^-25.7 and 2^-22.6, both 2^-27.4 and 2^-24.2, on
+// no side (a rounded fp32 product: 2^-25.2).  So one at least is: both where that costs nothing, in the walks the record's alone (the
+// other too makes the calls 1 to 2 % longer: v_cvt_pk_bf16_f32 for v_perm_b32).
+// Two floats into word e of each term: the upper 16 bits, those of what they leave, and the rest, which has 8 bits.
 __device__ __forceinline__ void cut2(float x, float y, Terms &t, int e)
 {
     constexpr uint32_t kUpper = 0x07060302u;  // the upper halves of two words
@@ -129,8 +134,32 @@ __device__ __forceinline__ Terms cut8(const f32x16 &x, int s)
         cut2(x[8 * s + 2 * e], x[8 * s + 2 * e + 1], t, e);
     return t;
 }
-// products with an exact factor, and of two cut factors (what is left out, mid lo + lo mid + lo lo, comes to some 2^-23 of the
-// product: the cuts leave 2^-8 and 2^-16 of a factor behind on average)
+// Two floats into word e of each term: the nearest bf16 value, that of what it leaves, and the rest, which has 8 bits with its sign.
+__device__ __forceinline__ void cut2n(float x, float y, Terms &t, int e)
+{
+    t.h[e] = pack2(x, y);
+    const float x1 = x - lo_f(t.h[e]), y1 = y - hi_f(t.h[e]);
+    t.m[e] = pack2(x1, y1);
+    t.l[e] = pack2(x1 - lo_f(t.m[e]), y1 - hi_f(t.m[e]));
+}
+__device__ __forceinline__ Terms cut8n(f32x4 a, f32x4 b)
+{
+    Terms t;
+    cut2n(a[0], a[1], t, 0);
+    cut2n(a[2], a[3], t, 1);
+    cut2n(b[0], b[1], t, 2);
+    cut2n(b[2], b[3], t, 3);
+    return t;
+}
+__device__ __forceinline__ Terms cut8n(const f32x16 &x, int s)
+{
+    Terms t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        cut2n(x[8 * s + 2 * e], x[8 * s + 2 * e + 1], t, e);
+    return t;
+}
+// products with an exact factor, and of two cut factors (one at least to the nearest)
 template <typename D>
 __device__ __forceinline__ D mfma3(u32x4 a, const Terms &b, D c)
 {
@@ -520,7 +549,7 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gdn_prep_kernel(GdnArgs a)
     }
 #pragma unroll
     for (int st = 0; st < 2; ++st)
-        store_terms(rec + (kBwd ? 2 : 1) * kGdnMat + kGdnVec, st, lane, cut8(qk, st));
+        store_terms(rec + (kBwd ? 2 : 1) * kGdnMat + kGdnVec, st, lane, cut8n(qk, st));
     __builtin_amdgcn_wave_barrier();
     // N's diagonal blocks: lanes of block lane / 16 % 2, column lane % 16; both halves of the wave do the same
     {
@@ -583,9 +612,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void gdn_prep_kernel(GdnArgs a)
                     y[e][i] = u0 + i > l32 ? -s.n[(u0 + i) * kNRow + l32] * bb[i] : u0 + i == l32 ? 1.0f : 0.0f;
             }
         }
-        store_terms(rec, st, lane, cut8(x[0], x[1]));
+        store_terms(rec, st, lane, cut8n(x[0], x[1]));
         if constexpr (kBwd)
-            store_terms(rec + kGdnMat + kGdnVec, st, lane, cut8(y[0], y[1]));
+            store_terms(rec + kGdnMat + kGdnVec, st, lane, cut8n(y[0], y[1]));
     }
 }
 
@@ -1235,8 +1264,8 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
     bool have = false;  // `own` is the state that segment p begins (ends) with
     auto share_terms = [&]() {
         Terms t;
-        cut2(own[0], own[1], t, 0);
-        cut2(own[2], own[3], t, 1);
+        cut2n(own[0], own[1], t, 0);
+        cut2n(own[2], own[3], t, 1);
         const int x = wave >> 1, e = 2 * (wave & 1);
         *reinterpret_cast<u32x2 *>(&terms[cur][0][x][lane][e]) = u32x2{t.h[0], t.h[1]};
         *reinterpret_cast<u32x2 *>(&terms[cur][1][x][lane][e]) = u32x2{t.m[0], t.m[1]};
@@ -1274,7 +1303,7 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
                 Terms ft[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    ft[x] = cut8(f[2 * x], f[2 * x + 1]);
+                    ft[x] = cut8n(f[2 * x], f[2 * x + 1]);
                 own = acc;
                 if (next == 1)
                     fetch(p + dir);
@@ -1661,7 +1690,7 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
     // 8 values 16 x + 8 h .. of row 32 th + lane % 32 of w or dx
     auto terms = [&](int which, int x, int th) {
         const unsigned char *p = raw + which + 16384 * th + 256 * (x >> 2);
-        return cut8(*reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3)))),
+        return cut8n(*reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3)))),
                     *reinterpret_cast<const f32x4 *>(p + (row4 ^ (64 * (x & 3) + 16))));
     };
     float dot = 0.0f;  // <dS, S>, this lane's share
@@ -1681,7 +1710,7 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
             for (int j = 0; j < 4; ++j)
                 dot = fmaf(s.b[j], d.b[j], fmaf(s.a[j], d.a[j], dot));
             __asm__ volatile("" : "+v"(dot));  // here: put off, it would keep the pieces
-            const Terms cs = cut8(s.a, s.b), cd = cut8(d.a, d.b);
+            const Terms cs = cut8n(s.a, s.b), cd = cut8n(d.a, d.b);
 #pragma unroll
             for (int th = 0; th < 2; ++th) {
                 dq[th] = mfma3(cs, row_frag(raw + kGradO, ln, x, th), dq[th]);
