@@ -2004,26 +2004,6 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
         a.ddecay[(tok0 + lane) * a.H + head] = rg > kLowest && rg <= 0.0f ? (float)dg : 0.0f;
 }
 
-// ------------------------------------------------------------------------- cu_seqlens
-
-// The walks trust cu_seqlens, so nothing may run on one that leads out of the tensors.
-__global__ __launch_bounds__(1024) void gdn_check_kernel(const int64_t *cu, int64_t N, int64_t T, int32_t *status)
-{
-    __shared__ int bits;
-    if (threadIdx.x == 0)
-        bits = (cu[0] != 0 ? 1 : 0) | (cu[N] != T ? 4 : 0);
-    __syncthreads();
-    int mine = 0;
-    for (int64_t n = threadIdx.x; n < N; n += 1024)
-        if (cu[n + 1] < cu[n])
-            mine = 2;
-    if (mine)
-        atomicOr(&bits, mine);
-    __syncthreads();
-    if (threadIdx.x == 0)
-        *status = bits;
-}
-
 // ------------------------------------------------------------------- token by token
 //
 // One wave per (sequence, head, 32 rows of the state); lane = row % 8 * 8 + q holds 16 channels of 4 rows: 16-byte
@@ -2145,11 +2125,10 @@ __global__ __launch_bounds__(256) void gdn_recurrent_kernel(GdnArgs a)
         }
 }
 
+// The walks trust cu_seqlens, so nothing may run on one that leads out of the tensors.
 hipError_t launch_check(const GdnArgs &a, int32_t *status, hipStream_t s)
 {
-    if (a.cu)
-        hipLaunchKernelGGL(gdn_check_kernel, dim3(1), dim3(1024), 0, s, a.cu, a.N, a.T, status);
-    return hipGetLastError();
+    return a.cu ? lin_launch_check(a.cu, a.N, a.T, status, s) : hipSuccess;
 }
 
 }  // namespace
