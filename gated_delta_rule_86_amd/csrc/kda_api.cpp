@@ -7,22 +7,16 @@
 
 #include <hip/hip_runtime.h>
 
+#include "host_checks.h"
 #include "kda.h"
 #include "kda_internal.h"
 
 namespace {
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void *p, size_t bytes)
-{
-    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+using kda::aligned;
+using kda::overlap;
+using kda::Range;
+using kda::range_of;
 
 size_t state_elem_bytes(kda_state_dtype d) { return d == KDA_STATE_BF16 ? 2 : 4; }
 

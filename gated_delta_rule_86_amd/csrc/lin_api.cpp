@@ -7,50 +7,29 @@
 
 #include <hip/hip_runtime.h>
 
+#include "host_checks.h"
 #include "kda.h"
 #include "lin_internal.h"
 
 namespace {
 
+using kda::aligned;
+using kda::check_cu;
+using kda::dtype_ok;
 using kda::kD;
+using kda::overlap;
+using kda::Range;
+using kda::range_of;
+using kda::set_tensor;
+using kda::state_bytes;
+using Sizes = kda::HeadSizes;
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void *p, size_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, p ? lo + bytes : lo};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-constexpr int64_t kMaxTokenStride = (int64_t)1 << 24;  // elements: 64 rows stay below 2^31 bytes
-constexpr int64_t kMaxElems = (int64_t)1 << 46;
-
-struct Sizes {
-    int64_t B, T, Hk, H, N, n_seq;
-    bool varlen;
-};
-
-// B, T, Hk, H, N, K, V and the sizes that follow from them
 kda_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, bool varlen, Sizes *z)
 {
-    if (B < 1 || T < 0 || H < 1)
-        return KDA_ERR_SHAPE;
-    if (Hk < 1 || H % Hk != 0)
-        return KDA_ERR_HEADS;
-    if (varlen ? (B != 1 || N < 1) : (N != 0 && N != B))
-        return KDA_ERR_SHAPE;
-    if (H > ((int64_t)1 << 16) || T >= ((int64_t)1 << 35) || T > ((int64_t)1 << 40) / B ||
-        B * T > kMaxElems / (H * kD))
-        return KDA_ERR_SHAPE;
-    const int64_t n_seq = varlen ? N : B;
-    if (n_seq >= ((int64_t)1 << 29) || n_seq > (((int64_t)1 << 31) - 64) / (4 * H))
-        return KDA_ERR_SHAPE;
-    *z = Sizes{B, T, Hk, H, N, n_seq, varlen};
-    return KDA_OK;
+    const kda_status st = kda::check_head_sizes(B, T, Hk, H, N, varlen, z);
+    if (st != KDA_OK)
+        return st;
+    return z->n_seq >= ((int64_t)1 << 29) || z->n_seq > (((int64_t)1 << 31) - 64) / (4 * H) ? KDA_ERR_SHAPE : KDA_OK;
 }
 
 bool make_layout(const Sizes &z, bool bwd, bool ddecay, kda::LinLayout *L)
@@ -93,45 +72,6 @@ bool make_layout(const Sizes &z, bool bwd, bool ddecay, kda::LinLayout *L)
     }
     L->total = off;
     return true;
-}
-
-bool dtype_ok(kda_state_dtype d) { return d == KDA_STATE_NONE || d == KDA_STATE_BF16 || d == KDA_STATE_FP32; }
-
-size_t state_bytes(kda_state_dtype d) { return kda::kLinStateBytes / (d == KDA_STATE_BF16 ? 2 : 1); }
-
-// One strided input [B, T, heads, 128]; strides in elements (batch, token, head), NULL = contiguous.
-kda_status set_tensor(const void *p, const int64_t *st, const Sizes &z, int64_t heads, kda::LinTensor *t, Range *r)
-{
-    t->p = static_cast<const uint16_t *>(p);
-    t->share = z.H / heads;
-    t->sb = st ? st[0] : z.T * heads * kD;
-    t->st = st ? st[1] : heads * kD;
-    t->sh = st ? st[2] : kD;
-    if (t->sb < 0 || t->st < 0 || t->sh < 0 || t->sb % 8 || t->st % 8 || t->sh % 8 || t->st > kMaxTokenStride ||
-        t->sb > kMaxElems || t->sh > kMaxElems)
-        return KDA_ERR_STRIDE;
-    if (z.T == 1)
-        t->st = kD;  // never a step, but the kernels take a row's end from it
-    if (!aligned(p, 16))
-        return KDA_ERR_ALIGN;
-    if (z.T > kMaxElems / (t->st + 1) || (z.T > 1 && t->st < kD))  // tokens' rows do not overlap
-        return KDA_ERR_STRIDE;
-    const size_t last = (size_t)(z.B - 1) * (size_t)t->sb + (size_t)(z.T - 1) * (size_t)t->st +
-                        (size_t)(heads - 1) * (size_t)t->sh + kD;
-    *r = range_of(p, z.T > 0 ? last * 2 : 0);
-    return KDA_OK;
-}
-
-kda_status check_cu(const int64_t *cu, const int64_t *host, const Sizes &z)
-{
-    if (!cu || !host)
-        return KDA_OK;
-    if (host[0] != 0 || host[z.N] != z.T)
-        return KDA_ERR_CU_SEQLENS;
-    for (int64_t i = 0; i < z.N; ++i)
-        if (host[i + 1] < host[i])
-            return KDA_ERR_CU_SEQLENS;
-    return KDA_OK;
 }
 
 // Everything that the forward entry points check; fills role 0 and the sizes.

@@ -6,24 +6,17 @@
 
 #include <hip/hip_runtime.h>
 
+#include "host_checks.h"
 #include "kda.h"
 #include "norm_internal.h"
 
 namespace {
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-constexpr int64_t kMaxElems = (int64_t)1 << 46;
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void *p, size_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, p ? lo + bytes : lo};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+using kda::aligned;
+using kda::kMaxElems;
+using kda::overlap;
+using kda::Range;
+using kda::range_of;
 
 int size_of(int dtype) { return dtype == KDA_DTYPE_FP32 ? 4 : 2; }
 bool dtype_ok(int d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32 || d == KDA_DTYPE_FP16; }

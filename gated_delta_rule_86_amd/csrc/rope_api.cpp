@@ -7,14 +7,14 @@
 
 #include <hip/hip_runtime.h>
 
+#include "host_checks.h"
 #include "kda.h"
 #include "rope_internal.h"
 
 namespace {
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-constexpr int64_t kMaxElems = (int64_t)1 << 46;
+using kda::aligned;
+using kda::kMaxElems;
 
 struct Span {  // a strided view and the bytes it touches
     uintptr_t lo, hi;
