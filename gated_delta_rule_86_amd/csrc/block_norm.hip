@@ -17,9 +17,11 @@
 // threads with one or two pieces each, the next row's loads on their way while one is worked on.
 //
 // Measured (a copy of 512 MiB: 5.33 TB/s): residual forward, 16384 rows of 4096 bf16 channels, both norms: 104 us, 5.2 TB/s;
-// residual backward, 6002 rows of 2048, bf16 with an fp32 stream: 40 us, 5.7 TB/s of what reaches memory, and 5 for the sums;
-// gated backward, 131072 rows of 128: 35 us, 4.9 TB/s, and 4 for the sums: there a third of the issue slots are taken,
-// the exponential and the divisions of the gate among them; gated forward of 1024 rows: 6 us, the launch.
+// residual backward, 6002 rows of 2048, bf16 with an fp32 stream: 43 us, 5.3 TB/s, and 5 for the sums; 16384 rows of 4096 with
+// both norms and their sums 178 us, 4.5 TB/s (without the norm behind the block 166), with an fp32 stream 240, 5.0 TB/s;
+// gated backward, 131072 rows of 128: 34 us, 4.9 TB/s, and 4 for the sums: there a third of the issue slots are taken,
+// the exponential and the divisions of the gate among them; gated forward of 1024 rows: 6 us, the launch; of 131072 rows
+// 24 us, 4.2 TB/s, of 524288 77 us, 5.2 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -33,7 +33,9 @@
 // transition, the scan the states there (few rows: the chip has room for 512 walks); the output walk starts from them.
 // Backwards the store walk keeps the state before each block of 64 tokens, the back walk its gradient behind it, and the
 // gradients of the blocks follow from the two.  Times below are of B=2 T=4096 H=16 (a), 38350 packed tokens H=32 Hk=16 (b) and
-// T=65536 H=8 (c).
+// T=65536 H=8 (c), on a card at speed (after some 30 passes), with the decays that such models start training from: two thirds of the
+// heads forget within a segment, and their transitions and most of their shares are left out.  Where every head remembers, the
+// cut takes 70 us for 62 in (a), 569 for 289 in (b), 256 for 167 in (c), and each scan a fifth more.
 #include <hip/hip_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -102,7 +104,7 @@ struct Terms {  // three bf16 terms of 8 floats
 };
 // Cuts: x = h + m + l exactly, towards 0 (cut2, cut8) or to the nearest (cut2n, cut8n).  A product with a bf16 factor is whole either
 // way.  mfma6 leaves out m l + l m + l l of two cut factors, relative to the product (normal factors): both towards 0 2^-24.0 root mean
-// square and 2^-21.2 at most, always on the side of 0; one of them to the nearest 2^-25.7 and 2^-22.6, both 2^-27.4 and 2^-24.2, on
+// square and 2^-21 at most, always on the side of 0; one of them to the nearest 2^-25.7 and 2^-22.4, both 2^-27.4 and 2^-24, on
 // no side (a rounded fp32 product: 2^-25.2).  So one at least is: both where that costs nothing, in the walks the record's alone (the
 // other too makes the calls 1 to 2 % longer: v_cvt_pk_bf16_f32 for v_perm_b32).
 // Two floats into word e of each term: the upper 16 bits, those of what they leave, and the rest, which has 8 bits.
@@ -447,8 +449,8 @@ struct LdsPrep {
     float bh[kGC], bl[kGC], beta[kGC];
 };
 
-// Bound by memory, most of it the records that it writes: (a) 23 us, 5.5 TB/s; (b) 188 us, 4.8 TB/s; (c) 80 us, 4.5 TB/s.
-// Records of chunks of 64 tokens, two waves each, took 400 us in (b): four times the matrix to solve and to write.
+// Bound by memory, most of it the records that it writes: (a) 25 us, 5.1 TB/s; (b) 169 us, 5.3 TB/s; (c) 70 us, 5.1 TB/s.
+// Records of chunks of 64 tokens, two waves each, took 2.2 times as long in (b): four times the matrix to solve and to write.
 // One wave per (chunk, head), nothing shared between waves.  M = e^{b_t - b_s} k_t.k_s; N's two 16 x 16 blocks on the diagonal
 // are solved column by column, the block below them with fp32 matrix instructions:
 // N_10 = (1 - N_11 beta)(M_10 - M_10 beta N_00).
@@ -846,10 +848,10 @@ __device__ __forceinline__ void state_scale(State &S, float f)
 // 32 value columns a wave on 32x32x16 matrix instructions, four waves a workgroup, two workgroups a CU; a chunk's tiles and record
 // come into one of two LDS buffers while the other is worked on, with one barrier a chunk.  Per chunk and wave of the output
 // walk: 96 matrix instructions (of 32 cycles), 750 other vector instructions, most of them cuts, 58 LDS reads.  A wave alone
-// on its SIMD issues one in 5.2 cycles, which is what bounds (a) with 256 workgroups (67 us, 4.2 us a chunk; the matrix
-// pipe busy 30 %) and (c) (262 us); two a SIMD reach 6.6 us for two chunks ((b): 537 us, matrix pipe 50 %, vector 59 %).
-// With products and cuts in the compiler's order (b) took 567 us; chunks of 64 tokens with one workgroup a CU made all of the
-// call's kernels 1307 us together, where these make 1180 in that order.
+// on its SIMD issues in 61 % of its cycles, which is what bounds (a) with 256 workgroups (62 us, 3.9 us a chunk; the matrix
+// pipe busy 31 %) and (c) (212 us, 40 %); two a SIMD reach some 6 us for two chunks ((b): 462 us, matrix pipe 49 %, vector 58 %).
+// With products and cuts in the compiler's order (b) took 12 % longer; chunks of 64 tokens with one workgroup a CU made all
+// of the call's kernels together 11 % longer than these in that order.
 
 constexpr int kModeOut = 0;    // out and final states
 constexpr int kModeShare = 1;  // a segment's share of the state at its end (F)
@@ -1215,7 +1217,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_store_kernel(GdnArgs a)
 // (kRev) the gradients of the states at the cuts, dS_{p-1} = dS_p Phi_p^T + F_p.  A workgroup of 8 waves takes 16 value
 // columns of one row and head; wave w forms key channels 16w .. of each state and hands its terms to the others
 // through LDS.  The next step's Phi and F are on their way meanwhile.  A step takes some 2 us: each of a row's 8 workgroups
-// reads the whole of Phi, 64 KiB at some 15 bytes a cycle ((a) 18 us for 6 steps, (c) 64 for 30).  Two steps' loads on their
+// reads the whole of Phi, 64 KiB at some 15 bytes a cycle ((a) 18 us for 6 steps, (c) 59 for 30).  Two steps' loads on their
 // way took longer (20 and 73).
 template <bool kRev>
 __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
@@ -1329,7 +1331,7 @@ __global__ __launch_bounds__(512) void gdn_scan_kernel(GdnArgs a)
 // -------------------------------------------------------------------------- backward walk
 //
 // dL/dS from a sequence's end to its start, in the same layout; stores it after each block, and dw.  90 matrix instructions a
-// chunk; (a) 99 us, the store walk 81, each writing 134 MB of states, and shares 72.
+// chunk; (a) 85 us, the store walk 69, each writing 134 MB of states, and shares 61.
 
 template <bool kShare>
 __device__ __forceinline__ void walk_back(const GdnArgs &a, LdsWalk &lds, uint32_t at, int64_t row, int64_t p, int64_t h)
@@ -1558,10 +1560,12 @@ __global__ __launch_bounds__(kWalkThreads, 2) void gdn_back_kernel(GdnArgs a)
 // where they are used, which takes less room and time than their terms would.  Then the waves share out the 32 x 32 tiles of
 // P, P^T and G + G^T, which reach all of them through LDS, in the place of w and dx.
 //
-// 408 matrix and some 4800 other vector instructions a wave, three quarters of them cuts: issue bounds it (matrix pipe busy
-// 27 %, vector 44 %), then memory, 3.4 TB/s.  (a) 184 to 196 us.  One workgroup of 8 waves with the terms in LDS took 252 (its
-// 36000 cycles of loads and 29000 of products did not overlap: a CU takes in some 10 bytes a cycle), with tiles shared out evenly 230;
-// products and cuts interleaved by hand change nothing here.
+// 414 matrix and some 5250 other vector instructions a wave, three quarters of them cuts: issue bounds it (matrix pipe busy
+// 26 %, vector 46 %), then memory, 3.4 TB/s.  (a) 184 us, some 5 of them what ddecay's terms add to the sums of q.dq - v.dv (the
+// reads of v saved).  One workgroup of 8 waves with the terms in LDS took 37 % longer (its 36000 cycles of loads and 29000 of
+// products did not overlap: a CU takes in some 10 bytes a cycle), with tiles shared out evenly 25 %; products and cuts
+// interleaved by hand change nothing here, ddecay's products beside those of P (no branches) or its sums over lanes by
+// DPP in place of LDS permutes do not either or make it slower (call 522 and 545 us).
 
 // LDS: w and dx, 64 rows of 32 pieces of 16 bytes each, piece u of row t at u ^ (t % 16), and dout.  Behind the products with
 // them: the matrices (steps of 3 KiB), k, q, and what is below.
@@ -2009,7 +2013,7 @@ __global__ __launch_bounds__(256, 2) void gdn_grad_kernel(GdnArgs a)
 // One wave per (sequence, head, 32 rows of the state); lane = row % 8 * 8 + q holds 16 channels of 4 rows: 16-byte
 // pieces, interleaved with those of the row's other 7 lanes.  S q = S~ q + beta r (k.q), so one pass over the row
 // gives both dot products.  The state is read once and written once, which bounds it: 256 sequences of 32 heads, fp32
-// states, 206 us, 5.3 TB/s (a copy: 5.33).
+// states, 207 us, 5.2 TB/s (a copy: 5.33); bf16 states 110 us, 5.0 TB/s.
 template <bool kF32>
 __global__ __launch_bounds__(256) void gdn_recurrent_kernel(GdnArgs a)
 {

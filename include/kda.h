@@ -376,7 +376,9 @@ size_t kda_lin_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, in
  *   dq, dk        bf16 [B, T, Hk, 128], dv bf16 [B, T, H, 128], contiguous, 16-byte aligned, fully
  *                 written; heads that share a q/k head are summed in fp32 and rounded once.
  *   ddecay        NULL (not wanted) or fp32, of decay's shape; a per-head decay's is summed over
- *                 all tokens.  0 where decay lies outside (-1000, 0].  Products as in kda_lin_fwd.  Asking for
+ *                 all tokens.  0 where decay lies outside (-1000, 0].  It is a sum of differences that hold the token's own
+ *                 write, so its error is some 1e-7 of q.dq, whatever the decay: a percent of a token's ddecay at a decay
+ *                 of -8, all of it from -14 on (kda_gdn_bwd's keeps its digits).  Products as in kda_lin_fwd.  Asking for
  *                 it changes the order of dq's and dk's fp32 sums, so single values may round differently.
  *   dinitial_state  NULL or fp32 [N, H, 128, 128], 16-byte aligned (also when initial_state is NULL).
  *   workspace     kda_lin_bwd_workspace_size(..., ddecay != NULL) bytes, 256-byte aligned.
@@ -418,7 +420,7 @@ size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, i
  *             in-place state carry and the handling of an invalid cu_seqlens (kda_fwd_device_status reads the
  *             status word of this workspace too).
  * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; a product of two factors of more than 8 bits
- * leaves out 2^-25.7 of itself root mean square, 2^-22.6 at most, on no side.  out and bf16 final states are rounded once.  Where a row is cut into segments (kda_gdn_fwd_workspace_size), a finite state that has passed transitions of a
+ * leaves out 2^-25.7 of itself root mean square, 2^-22.4 at most, on no side.  out and bf16 final states are rounded once.  Where a row is cut into segments (kda_gdn_fwd_workspace_size), a finite state that has passed transitions of a
  * norm below 2^-150 in all counts as 0.  A value that is not finite (or a NaN gate) reaches its own sequence and head alone, from
  * the first token of its chunk of 32 tokens on; in the state it lasts, in k or v it may be forgotten behind such transitions.
  * Deterministic: fixed summation orders, no atomics.

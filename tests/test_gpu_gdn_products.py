@@ -6,7 +6,7 @@ of 24 bits.  Column 1 becomes -s + beta_0 s.
 
 What may be off, with e = 2^-24, relative to |s|: the product's sum and the three steps that add the terms of a write to the state round
 to the nearest at full size, by at most e each with either sign (steps before them are 2^-7 and less in size); what a product
-leaves out is at most 2^-22.6.  One value: 4 e + 2^-22.6 < 2^-21.  The roundings are evenly spread within half a step, e / sqrt(3) root
+leaves out is at most 2^-22.4.  One value: 4 e + 2^-22.4 < 2^-21.  The roundings are evenly spread within half a step, e / sqrt(3) root
 mean square at the most, sqrt(4 / 3) e together with their signs independent, and what is left out 2^-25.7: below 1.3 e.  The mean
 over n independent samples is then within six times 1.3 e / sqrt(n).  Terms cut towards zero in both factors leave out mid lo + lo
 mid + lo lo always on the same side: 2^-25 of |s| in the mean, ten times that."""
