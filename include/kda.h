@@ -419,10 +419,12 @@ size_t kda_lin_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t H, i
  *             (256-byte aligned, kda_gdn_fwd_workspace_size bytes) and stream: as in kda_fwd, including the
  *             in-place state carry and the handling of an invalid cu_seqlens (kda_fwd_device_status reads the
  *             status word of this workspace too).
- * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; a product of two factors of more than 8 bits
- * leaves out 2^-25.7 of itself root mean square, 2^-22.4 at most, on no side.  out and bf16 final states are rounded once.  Where a row is cut into segments (kda_gdn_fwd_workspace_size), a finite state that has passed transitions of a
- * norm below 2^-150 in all counts as 0.  A value that is not finite (or a NaN gate) reaches its own sequence and head alone, from
- * the first token of its chunk of 32 tokens on; in the state it lasts, in k or v it may be forgotten behind such transitions.
+ * Products take 24 bits of every factor and sum in fp32, whatever the states' dtypes; a product of two factors of more
+ * than 8 bits leaves out 2^-25.7 of itself root mean square, 2^-22.4 at most, on no side.  out and bf16 final states are
+ * rounded once.  Where a row is cut into segments (kda_gdn_fwd_workspace_size), a finite state that has passed
+ * transitions of a norm below 2^-150 in all counts as 0.  A value that is not finite (or a NaN gate) reaches its own
+ * sequence and head alone, from the first token of its chunk of 32 tokens on; in the state it lasts, in k or v it may be
+ * forgotten behind such transitions.
  * Deterministic: fixed summation orders, no atomics.
  * Errors: KDA_ERR_NULL, _SHAPE (also sizes whose launch would hold 2^32 threads), _HEAD_DIM, _DTYPE, _SCALE, _ALIGN,
  * _WORKSPACE, _CU_SEQLENS, _HIP, _ALIAS, _HEADS, _STRIDE.
@@ -459,14 +461,15 @@ size_t kda_gdn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t N, in
  *   dfinal_state  NULL (zero) or fp32 [N, H, 128, 128], 16-byte aligned: dL/dfinal_state.
  *   dq, dk        bf16 [B, T, Hk, 128], dv bf16 [B, T, H, 128], contiguous, 16-byte aligned, fully
  *                 written; heads that share a q/k head are summed in fp32 and rounded once.
- *   ddecay, dbeta fp32 [B, T, H], fully written.  ddecay is 0 where decay lies outside (-1000, 0].  It is the sum of what crosses
- *                 its token, all of it scaled by e^decay and so are its errors (some 1e-6 of the sizes of the summands); 0 below about -87.
+ *   ddecay, dbeta fp32 [B, T, H], fully written.  ddecay is 0 where decay lies outside (-1000, 0].  It is the sum of
+ *                 what crosses its token, all of it scaled by e^decay, and so are its errors (some 1e-6 of the sizes of
+ *                 the summands); 0 below about -87.
  *   dinitial_state  NULL or fp32 [N, H, 128, 128], 16-byte aligned (also when initial_state is NULL).
  *   workspace     kda_gdn_bwd_workspace_size(...) bytes, 256-byte aligned.
- * Products as in kda_gdn_fwd.  A value that is not finite reaches the gradients of its own sequence alone, one of v, dout, a gate or a
- * state there those of its value head (dq and dk are sums over the heads that share a q/k head): any of their tokens up to the end of its
- * block of 64, and behind it where kda_gdn_fwd passes it on; beyond transitions of a norm below 2^-150 it may be forgotten.
- * Outputs must not overlap inputs or each other (KDA_ERR_ALIAS).  An invalid cu_seqlens
+ * Products as in kda_gdn_fwd.  A value that is not finite reaches the gradients of its own sequence alone, one of v, dout, a
+ * gate or a state there those of its value head (dq and dk are sums over the heads that share a q/k head): any of their
+ * tokens up to the end of its block of 64, and behind it where kda_gdn_fwd passes it on; beyond transitions of a norm below
+ * 2^-150 it may be forgotten.  Outputs must not overlap inputs or each other (KDA_ERR_ALIAS).  An invalid cu_seqlens
  * found on the device leaves dq, dk, dv, ddecay and dbeta unwritten and makes dinitial_state = dfinal_state (or 0).
  * Deterministic.
  */
